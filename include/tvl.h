@@ -4,7 +4,9 @@
  * decode (single pass or split-K with a log-sum-exp merge), the two fused
  * into one decode-step call, and chunked causal prefill over a cached
  * prefix; around them the rotary embedding fused into the write, block
- * copies for copy-on-write, and a host block allocator.
+ * copies for copy-on-write, and a host block allocator.  Two ways to hold
+ * more context: a cache in 4 bits (write, expand, copy, decode) and attention
+ * with a sliding window and sinks (decode, prefill, release of old blocks).
  *
  * Sources of the method (web pages on tiny-vLLM and nano-vLLM):
  *   [tiny-vllm README]  "tiny-vllm" README, Korean translation: feature list
@@ -285,6 +287,100 @@ tvl_status tvl_copy_blocks(void* k_cache, void* v_cache, const int32_t* src,
                            const int32_t* dst, int n, int num_kv_heads,
                            int head_dim, int block_size, int num_blocks,
                            void* stream);
+
+/*
+ * The 4-bit cache.  One array holds K and V; a row (one token, one KV head, K
+ * or V) is 64 codes of 4 bits and two bf16 numbers s, z, and stands for
+ * s * code + z.  z is the row's minimum, s = (maximum - z) / 15 rounded up to
+ * bf16, code = min(15, rint((x - z) / s)) (ties to even; s = 0 gives code 0),
+ * so every value is kept within s / 2.  A row that is not finite, or whose
+ * range is not, stands for NaN.  Layout: uint8 [NB, bs / 16, Hkv, 1152]; the
+ * 1152 bytes of 16 tokens of a head are K codes [16][32], V codes [16][32]
+ * (dimension d in byte d / 2, even d in the low half), K (s, z) [16][2] and V
+ * (s, z) [16][2] in bf16.  72 bytes a token and KV head, 3.56 times fewer than
+ * in bf16.  Slots, block tables and the allocator are those of the bf16 cache.
+ * Supported: D == 64, bs in {16, 32, 64, 128}, any Hkv.
+ */
+
+/*
+ * Write into the 4-bit cache, with the rotary embedding fused when positions
+ * are given: as tvl_rope_paged_kv_write (q rotated in place, K rotated and
+ * rounded to bf16), then every K and V row of a token with slot_mapping[t] >=
+ * 0 is quantised into that slot.  positions == NULL: no rotation, and q must
+ * be NULL.  Each output row depends on its input row alone.
+ *   q : bf16 [T, Hq, D] or NULL; k_new, v_new : bf16 [T, Hkv, D]
+ *   cache : uint8, written in place; slot_mapping : int32 [T]
+ *   positions : int32 [T] >= 0, or NULL
+ * The rotation is within one bf16 ulp of the double-precision definition plus
+ * 2^-21 * (|x_i| + |x_{i+D/2}|).  A slot >= NB * bs is skipped and sets
+ * TVL_DEV_BAD_SLOT; a row that is not finite sets TVL_DEV_NONFINITE.
+ */
+tvl_status tvl_kv4_write(void* q, const void* k_new, const void* v_new, void* cache,
+                         const int32_t* slot_mapping, const int32_t* positions, int num_tokens,
+                         int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                         int num_blocks, float rope_theta, void* stream);
+
+/*
+ * Expands blocks of the 4-bit cache to bf16: for i in [0, n), block dst[i] of
+ * k_cache and v_cache (bf16 [out_blocks, bs, Hkv, D]) becomes s * code + z of
+ * block src[i], rounded once.  This is how a prefill attends to a prefix held
+ * in 4 bits: expand the prefix's blocks, then call a prefill over the bf16
+ * blocks.  Destinations must be distinct; ids out of range are skipped and
+ * set TVL_DEV_BAD_BLOCK_ID.
+ */
+tvl_status tvl_kv4_expand_blocks(void* k_cache, void* v_cache, const void* cache,
+                                 const int32_t* src, const int32_t* dst, int n, int num_kv_heads,
+                                 int head_dim, int block_size, int num_blocks, int out_blocks,
+                                 void* stream);
+
+/* tvl_copy_blocks for the 4-bit cache: block dst[i] becomes a copy of src[i]. */
+tvl_status tvl_kv4_copy_blocks(void* cache, const int32_t* src, const int32_t* dst, int n,
+                               int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                               void* stream);
+
+/*
+ * Visibility in the windowed calls.  The query at position p sees the cached
+ * tokens j <= p with j > p - window or j < sinks: the last `window` tokens,
+ * itself included, and the first `sinks`.  window == 0: no window, every j <=
+ * p is seen (sinks then has no effect).  Blocks that hold no visible token
+ * are not read, and their block table entries may hold anything (see
+ * tvl_allocator_trim).
+ */
+
+/* Workspace of the two decode calls below, for the current device (its SM
+ * count), whatever the batch; written to *bytes. */
+tvl_status tvl_window_decode_workspace_size(int num_q_heads, int num_kv_heads, int head_dim,
+                                            size_t* bytes);
+
+/*
+ * Decode attention over the 4-bit cache: as tvl_paged_attention_decode, with
+ * the rows' values s * code + z taken unrounded, and an optional window.
+ * fp32 accumulation; P is carried in two fp16 halves (22 bits).  The visible
+ * 16-token groups are balanced over one CTA per SM and merged by log-sum-exp;
+ * results do not vary from call to call.
+ *   out : float32 [S, Hq, D]; q : bf16 [S, Hq, D]; cache : see above
+ * context_lens[s] == 0 gives a zero row.  Two launches; no allocation.
+ * Supported: D == 64, G from 1 to 8, bs in {16, 32, 64, 128}, any Hkv,
+ * |q| < 2^100, NB * bs < 2^31.
+ */
+tvl_status tvl_kv4_attention_decode(float* out, const void* q, const void* cache,
+                                    const int32_t* block_tables, const int32_t* context_lens,
+                                    int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                    int block_size, int num_blocks, int max_blocks_per_seq,
+                                    float scale, int window, int sinks, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
+ * Decode attention with a window over the bf16 caches: the same call on the
+ * layout of tvl_paged_attention_decode.  P is carried in two bf16 halves (16
+ * bits).  Slots of a read block that are not visible may hold anything, NaN
+ * included.
+ */
+tvl_status tvl_paged_attention_window_decode(
+    float* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, int max_blocks_per_seq,
+    float scale, int window, int sinks, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Host block allocator: the CPU control plane that hands out the physical

@@ -9,10 +9,12 @@ been built, every call raises ``TvlError``.
 Functions (same names as the C entry points, without the ``tvl_`` prefix):
   paged_kv_write, paged_attention_decode, paged_attention_decode_workspace_size,
   paged_decode_step, paged_attention_prefill, rope_paged_kv_write,
-  copy_blocks, get_device_status, version.
+  copy_blocks, get_device_status, version; on the 4-bit cache kv4_write,
+  kv4_expand_blocks, kv4_copy_blocks, kv4_attention_decode; with a window and
+  sinks paged_attention_window_decode, window_decode_workspace_size.
 
-Bound calls (``bind_paged_decode_step``, ``bind_paged_attention_decode``,
-``bind_paged_attention_prefill``, ``bind_paged_kv_write``) check their
+Bound calls (``bind_`` before the name of a write, decode, prefill or
+``kv4_expand_blocks`` call) check their
 tensors once and return a callable that re-issues the same C call -- same
 pointers, sizes and stream -- with one ctypes call and no further checks.
 They are for loops that call the library with the same buffers every step
@@ -35,6 +37,10 @@ __all__ = [
     "DEV_BAD_QUERY_LEN", "DEV_TIMEOUT", "DEV_NONFINITE", "selftest_bounded_wait",
     "paged_decode_step", "BoundCall", "bind_paged_decode_step", "bind_paged_attention_decode",
     "bind_paged_attention_prefill", "bind_paged_kv_write",
+    "kv4_cache_shape", "kv4_write", "kv4_expand_blocks", "kv4_copy_blocks",
+    "kv4_attention_decode", "paged_attention_window_decode", "window_decode_workspace_size",
+    "bind_kv4_write", "bind_kv4_expand_blocks", "bind_kv4_attention_decode",
+    "bind_paged_attention_window_decode",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -98,6 +104,18 @@ def _load():
             lib.tvl_rope_paged_kv_write.restype = I
             lib.tvl_copy_blocks.argtypes = [P, P, P, P, I, I, I, I, I, P]
             lib.tvl_copy_blocks.restype = I
+            lib.tvl_kv4_write.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, F, P]
+            lib.tvl_kv4_expand_blocks.argtypes = [P, P, P, P, P, I, I, I, I, I, I, P]
+            lib.tvl_kv4_copy_blocks.argtypes = [P, P, P, I, I, I, I, I, P]
+            lib.tvl_window_decode_workspace_size.argtypes = [I, I, I, ctypes.POINTER(SZ)]
+            lib.tvl_kv4_attention_decode.argtypes = [
+                P, P, P, P, P, I, I, I, I, I, I, I, F, I, I, P, SZ, P]
+            lib.tvl_paged_attention_window_decode.argtypes = [
+                P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, I, P, SZ, P]
+            for name in ("tvl_kv4_write", "tvl_kv4_expand_blocks", "tvl_kv4_copy_blocks",
+                         "tvl_window_decode_workspace_size", "tvl_kv4_attention_decode",
+                         "tvl_paged_attention_window_decode"):
+                getattr(lib, name).restype = I
             I32P = ctypes.POINTER(ctypes.c_int32)
             IP = ctypes.POINTER(ctypes.c_int)
             lib.tvl_allocator_create.argtypes = [I, I, ctypes.POINTER(P)]
@@ -395,6 +413,216 @@ def bind_paged_attention_prefill(out, q, query_start_loc, k_cache, v_cache, bloc
     """paged_attention_prefill, checked once; returns a BoundCall."""
     return BoundCall(*_prep_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables,
                                     context_lens, scale, max_q_len, stream))
+
+
+KV4_RECORD_BYTES = 1152      # 16 tokens of one KV head in the 4-bit cache
+
+
+def kv4_cache_shape(num_blocks, num_kv_heads, block_size):
+    """Shape of a 4-bit cache tensor (uint8): [NB, bs / 16, Hkv, 1152]."""
+    if block_size % 16:
+        raise ValueError(f"block_size {block_size} is not a multiple of 16")
+    return (num_blocks, block_size // 16, num_kv_heads, KV4_RECORD_BYTES)
+
+
+def _need_kv4(cache, dev=None):
+    """Checks a 4-bit cache tensor; returns (num_blocks, block_size, num_kv_heads)."""
+    _need(cache, "cache", torch.uint8, 4, dev)
+    nb, chunks, hkv, rec = cache.shape
+    if rec != KV4_RECORD_BYTES:
+        raise ValueError(f"cache must be [NB, bs / 16, Hkv, {KV4_RECORD_BYTES}], got "
+                         f"{tuple(cache.shape)}")
+    return nb, chunks * 16, hkv
+
+
+def _prep_kv4_write(k_new, v_new, cache, slot_mapping, q, positions, rope_theta, stream):
+    nb, bs, hkv = _need_kv4(cache)
+    dev = cache.get_device()
+    _need(k_new, "k_new", torch.bfloat16, 3, dev)
+    _need(v_new, "v_new", torch.bfloat16, 3, dev)
+    _need(slot_mapping, "slot_mapping", torch.int32, 1, dev)
+    t, d, hq = slot_mapping.shape[0], k_new.shape[2], 0
+    if k_new.shape != (t, hkv, d) or v_new.shape != k_new.shape:
+        raise ValueError(f"k_new/v_new must be [{t}, {hkv}, D]")
+    if positions is not None:
+        _need(positions, "positions", torch.int32, 1, dev)
+        if positions.shape[0] != t:
+            raise ValueError("positions must be [T]")
+    if q is not None:
+        if positions is None:
+            raise ValueError("q is given without positions to rotate it by")
+        _need(q, "q", torch.bfloat16, 3, dev)
+        if q.shape[0] != t or q.shape[2] != d:
+            raise ValueError("q must be [T, Hq, D]")
+        hq = q.shape[1]
+    with _on_device(dev):
+        args = (_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(cache), _ptr(slot_mapping),
+                _ptr(positions), t, hq, hkv, d, bs, nb, float(rope_theta), _stream(stream))
+    return dev, _load().tvl_kv4_write, args, (q, k_new, v_new, cache, slot_mapping, positions)
+
+
+def kv4_write(k_new, v_new, cache, slot_mapping, q=None, positions=None, rope_theta=500000.0,
+              stream=None) -> None:
+    """4-bit cache (uint8, kv4_cache_shape) <- k_new/v_new bf16 [T, Hkv, D],
+    quantised, at rows slot_mapping int32 [T] (negative = skip).  With
+    positions (int32 [T]) q (in place; may be None) and K are rotated first."""
+    dev, fn, args, _ = _prep_kv4_write(k_new, v_new, cache, slot_mapping, q, positions,
+                                       rope_theta, stream)
+    with _on_device(dev):
+        _check(fn(*args))
+
+
+def bind_kv4_write(k_new, v_new, cache, slot_mapping, q=None, positions=None,
+                   rope_theta=500000.0, stream=None):
+    """kv4_write, checked once; returns a BoundCall."""
+    return BoundCall(*_prep_kv4_write(k_new, v_new, cache, slot_mapping, q, positions,
+                                      rope_theta, stream))
+
+
+def _prep_kv4_expand(k_cache, v_cache, cache, src, dst, stream):
+    nb, bs, hkv = _need_kv4(cache)
+    dev = cache.get_device()
+    _need(k_cache, "k_cache", torch.bfloat16, 4, dev)
+    _need(v_cache, "v_cache", torch.bfloat16, 4, dev)
+    _need(src, "src", torch.int32, 1, dev)
+    _need(dst, "dst", torch.int32, 1, dev)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst differ in length")
+    if v_cache.shape != k_cache.shape or tuple(k_cache.shape[1:3]) != (bs, hkv):
+        raise ValueError(f"k_cache/v_cache must be [blocks, {bs}, {hkv}, D]")
+    with _on_device(dev):
+        args = (_ptr(k_cache), _ptr(v_cache), _ptr(cache), _ptr(src), _ptr(dst), src.numel(), hkv,
+                k_cache.shape[3], bs, nb, k_cache.shape[0], _stream(stream))
+    return dev, _load().tvl_kv4_expand_blocks, args, (k_cache, v_cache, cache, src, dst)
+
+
+def kv4_expand_blocks(k_cache, v_cache, cache, src, dst, stream=None) -> None:
+    """Block dst[i] of the bf16 caches <- the values of block src[i] of the
+    4-bit cache (int32 CUDA tensors [n]; distinct destinations)."""
+    dev, fn, args, _ = _prep_kv4_expand(k_cache, v_cache, cache, src, dst, stream)
+    with _on_device(dev):
+        _check(fn(*args))
+
+
+def bind_kv4_expand_blocks(k_cache, v_cache, cache, src, dst, stream=None):
+    """kv4_expand_blocks, checked once; returns a BoundCall."""
+    return BoundCall(*_prep_kv4_expand(k_cache, v_cache, cache, src, dst, stream))
+
+
+def kv4_copy_blocks(cache, src, dst, stream=None) -> None:
+    """Block dst[i] of the 4-bit cache <- block src[i] (int32 CUDA tensors
+    [n]); bit-exact; the pairs must not overlap."""
+    nb, bs, hkv = _need_kv4(cache)
+    dev = cache.get_device()
+    _need(src, "src", torch.int32, 1, dev)
+    _need(dst, "dst", torch.int32, 1, dev)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst differ in length")
+    with _on_device(dev):
+        _check(_load().tvl_kv4_copy_blocks(_ptr(cache), _ptr(src), _ptr(dst), src.numel(), hkv, 64,
+                                           bs, nb, _stream(stream)))
+
+
+def window_decode_workspace_size(num_q_heads, num_kv_heads, head_dim=64) -> int:
+    """Bytes of workspace the 4-bit and the windowed decode need on the current
+    device (tvl_window_decode_workspace_size); remembered per device and heads."""
+    key = (torch.cuda.current_device() if torch.cuda.is_available() else -1, "window",
+           num_q_heads, num_kv_heads, head_dim)
+    hit = _ws_sizes.get(key)
+    if hit is not None:
+        return hit
+    out = ctypes.c_size_t(0)
+    _check(_load().tvl_window_decode_workspace_size(num_q_heads, num_kv_heads, head_dim,
+                                                    ctypes.byref(out)))
+    _ws_sizes[key] = int(out.value)
+    return int(out.value)
+
+
+def _prep_window_decode(out, q, caches, nb, bs, hkv, block_tables, context_lens, scale, window,
+                        sinks, workspace, stream):
+    """Checks shared by the 4-bit and the windowed decode; `caches` is the
+    4-bit cache alone or the two bf16 caches."""
+    dev = caches[0].get_device()
+    _need(q, "q", torch.bfloat16, 3, dev)
+    _need(out, "out", torch.float32, 3, dev)
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    s, hq, d = q.shape
+    if out.shape != q.shape:
+        raise ValueError("out and q shapes differ")
+    if block_tables.shape[0] != s or context_lens.shape[0] != s:
+        raise ValueError("block_tables / context_lens must have num_seqs rows")
+    with _on_device(dev):
+        if workspace is None:
+            workspace = torch.empty(window_decode_workspace_size(hq, hkv, d), dtype=torch.uint8,
+                                    device=dev)
+        _need(workspace, "workspace", torch.uint8, 1, dev)
+        args = (_ptr(out), _ptr(q), *(_ptr(c) for c in caches), _ptr(block_tables),
+                _ptr(context_lens), s, hq, hkv, d, bs, nb, block_tables.shape[1], float(scale),
+                int(window), int(sinks), _ptr(workspace), workspace.numel(), _stream(stream))
+    lib = _load()
+    fn = (lib.tvl_kv4_attention_decode if len(caches) == 1
+          else lib.tvl_paged_attention_window_decode)
+    return dev, fn, args, (out, q, *caches, block_tables, context_lens, workspace)
+
+
+def _prep_kv4_decode(out, q, cache, block_tables, context_lens, scale, window, sinks, workspace,
+                     stream):
+    nb, bs, hkv = _need_kv4(cache)
+    return _prep_window_decode(out, q, (cache,), nb, bs, hkv, block_tables, context_lens, scale,
+                               window, sinks, workspace, stream)
+
+
+def _prep_bf16_window_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, window,
+                             sinks, workspace, stream):
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4, k_cache.get_device())
+    nb, bs, hkv, d = k_cache.shape
+    if v_cache.shape != k_cache.shape or q.shape[-1] != d:
+        raise ValueError("inconsistent q / cache shapes")
+    return _prep_window_decode(out, q, (k_cache, v_cache), nb, bs, hkv, block_tables,
+                               context_lens, scale, window, sinks, workspace, stream)
+
+
+def kv4_attention_decode(out, q, cache, block_tables, context_lens, scale, window=0, sinks=0,
+                         workspace=None, stream=None):
+    """out fp32 [S, Hq, D] <- decode attention of q bf16 [S, Hq, D] over the
+    4-bit cache; with window > 0 over the last `window` tokens and the first
+    `sinks`.  workspace: uint8 CUDA tensor (allocated here when None)."""
+    dev, fn, args, _ = _prep_kv4_decode(out, q, cache, block_tables, context_lens, scale, window,
+                                        sinks, workspace, stream)
+    with _on_device(dev):
+        _check(fn(*args))
+    return out
+
+
+def bind_kv4_attention_decode(out, q, cache, block_tables, context_lens, scale, window=0, sinks=0,
+                              workspace=None, stream=None):
+    """kv4_attention_decode, checked once (a workspace of None is allocated
+    here once); returns a BoundCall."""
+    return BoundCall(*_prep_kv4_decode(out, q, cache, block_tables, context_lens, scale, window,
+                                       sinks, workspace, stream))
+
+
+def paged_attention_window_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale,
+                                  window, sinks=0, workspace=None, stream=None):
+    """out fp32 [S, Hq, D] <- paged decode attention of q bf16 [S, Hq, D] over
+    the last `window` tokens and the first `sinks` (window 0: all tokens)."""
+    dev, fn, args, _ = _prep_bf16_window_decode(out, q, k_cache, v_cache, block_tables,
+                                                context_lens, scale, window, sinks, workspace,
+                                                stream)
+    with _on_device(dev):
+        _check(fn(*args))
+    return out
+
+
+def bind_paged_attention_window_decode(out, q, k_cache, v_cache, block_tables, context_lens,
+                                       scale, window, sinks=0, workspace=None, stream=None):
+    """paged_attention_window_decode, checked once (a workspace of None is
+    allocated here once); returns a BoundCall."""
+    return BoundCall(*_prep_bf16_window_decode(out, q, k_cache, v_cache, block_tables,
+                                               context_lens, scale, window, sinks, workspace,
+                                               stream))
 
 
 class BoundCall:

@@ -450,4 +450,247 @@ tvl_status tvl_paged_attention_prefill(float* out, const void* q, const int32_t*
   return TVL_OK;
 }
 
+// ------------------------------------------------------------ 4-bit cache
+
+namespace {
+
+bool kv4_block_size(int bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
+
+tvl_status kv4_sizes(int num_kv_heads, int head_dim, int block_size, int num_blocks) {
+  if (num_kv_heads <= 0 || num_blocks <= 0)
+    return fail(TVL_ERR_INVALID_ARG, "num_kv_heads and num_blocks must be positive");
+  if (head_dim != 64) return fail(TVL_ERR_UNSUPPORTED, "head_dim %d (supported: 64)", head_dim);
+  if (!kv4_block_size(block_size))
+    return fail(TVL_ERR_UNSUPPORTED, "block_size %d (4-bit cache: 16, 32, 64, 128)", block_size);
+  return TVL_OK;
+}
+
+}  // namespace
+
+tvl_status tvl_kv4_write(void* q, const void* k_new, const void* v_new, void* cache,
+                         const int32_t* slot_mapping, const int32_t* positions, int num_tokens,
+                         int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                         int num_blocks, float rope_theta, void* stream) {
+  if (num_tokens < 0) return fail(TVL_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+  if (num_q_heads < 0) return fail(TVL_ERR_INVALID_ARG, "num_q_heads %d < 0", num_q_heads);
+  tvl_status st = kv4_sizes(num_kv_heads, head_dim, block_size, num_blocks);
+  if (st != TVL_OK) return st;
+  if (positions && (!(rope_theta > 1.0f) || !std::isfinite(rope_theta)))
+    return fail(TVL_ERR_INVALID_ARG, "rope_theta must be finite and > 1");
+  if (q && !positions) return fail(TVL_ERR_INVALID_ARG, "q given without positions to rotate it by");
+  if (q && num_q_heads == 0) return fail(TVL_ERR_INVALID_ARG, "q given with no query heads");
+  if (!cache) return fail(TVL_ERR_INVALID_ARG, "null cache pointer");
+  if (!aligned16(cache)) return fail(TVL_ERR_INVALID_ARG, "cache must be 16-byte aligned");
+  if (num_tokens == 0) return TVL_OK;
+  if (!k_new || !v_new || !slot_mapping) return fail(TVL_ERR_INVALID_ARG, "null input pointer");
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(q))
+    return fail(TVL_ERR_INVALID_ARG, "q, k_new and v_new must be 16-byte aligned");
+  uint32_t* word = nullptr;
+  st = status_word(&word);
+  if (st != TVL_OK) return st;
+  tvl::Kv4WriteArgs a;
+  a.q = q;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.cache = cache;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_slots = static_cast<long long>(num_blocks) * block_size;
+  a.rope_theta = rope_theta;
+  a.status = word;
+  cudaError_t e = tvl::launch_kv4_write(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv4_write launch");
+  return TVL_OK;
+}
+
+tvl_status tvl_kv4_expand_blocks(void* k_cache, void* v_cache, const void* cache,
+                                 const int32_t* src, const int32_t* dst, int n, int num_kv_heads,
+                                 int head_dim, int block_size, int num_blocks, int out_blocks,
+                                 void* stream) {
+  if (n < 0) return fail(TVL_ERR_INVALID_ARG, "n %d < 0", n);
+  tvl_status st = kv4_sizes(num_kv_heads, head_dim, block_size, num_blocks);
+  if (st != TVL_OK) return st;
+  if (out_blocks <= 0) return fail(TVL_ERR_INVALID_ARG, "out_blocks %d <= 0", out_blocks);
+  if (n == 0) return TVL_OK;
+  if (!k_cache || !v_cache || !cache || !src || !dst)
+    return fail(TVL_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(cache))
+    return fail(TVL_ERR_INVALID_ARG, "cache pointers must be 16-byte aligned");
+  uint32_t* word = nullptr;
+  st = status_word(&word);
+  if (st != TVL_OK) return st;
+  tvl::Kv4ExpandArgs a;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.cache = cache;
+  a.src = src;
+  a.dst = dst;
+  a.n = n;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.out_blocks = out_blocks;
+  a.status = word;
+  cudaError_t e = tvl::launch_kv4_expand(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv4_expand launch");
+  return TVL_OK;
+}
+
+tvl_status tvl_kv4_copy_blocks(void* cache, const int32_t* src, const int32_t* dst, int n,
+                               int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                               void* stream) {
+  if (n < 0) return fail(TVL_ERR_INVALID_ARG, "n %d < 0", n);
+  tvl_status st = kv4_sizes(num_kv_heads, head_dim, block_size, num_blocks);
+  if (st != TVL_OK) return st;
+  if (n == 0) return TVL_OK;
+  if (!cache || !src || !dst) return fail(TVL_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(cache)) return fail(TVL_ERR_INVALID_ARG, "cache must be 16-byte aligned");
+  uint32_t* word = nullptr;
+  st = status_word(&word);
+  if (st != TVL_OK) return st;
+  tvl::CopyBlocksArgs a;
+  a.k_cache = cache;
+  a.v_cache = nullptr;
+  a.src = src;
+  a.dst = dst;
+  a.n = n;
+  a.block_bytes = static_cast<long long>(block_size) * num_kv_heads * 72;
+  a.num_blocks = num_blocks;
+  a.status = word;
+  cudaError_t e = tvl::launch_copy_blocks(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv4_copy_blocks launch");
+  return TVL_OK;
+}
+
+// ------------------------------------- decode with a window, or in 4 bits
+
+namespace {
+
+tvl_status window_heads(int hq, int hkv, int d) {
+  if (hq <= 0 || hkv <= 0) return fail(TVL_ERR_INVALID_ARG, "head counts must be positive");
+  if (hq % hkv != 0)
+    return fail(TVL_ERR_INVALID_ARG, "num_q_heads %d not a multiple of num_kv_heads %d", hq, hkv);
+  if (d != 64) return fail(TVL_ERR_UNSUPPORTED, "head_dim %d (supported: 64)", d);
+  if (hq / hkv > 8) return fail(TVL_ERR_UNSUPPORTED, "GQA group %d (supported: 1 to 8)", hq / hkv);
+  if (hkv / tvl::window_heads_per_cta(hkv) > 65535)
+    return fail(TVL_ERR_UNSUPPORTED, "num_kv_heads %d", hkv);
+  return TVL_OK;
+}
+
+// One CTA per SM, shared by the groups of KV heads that a CTA owns.
+tvl_status window_ctas(int hkv, int* ctas) {
+  int sms = 0;
+  tvl_status st = sm_count(&sms);
+  if (st != TVL_OK) return st;
+  const int groups = hkv / tvl::window_heads_per_cta(hkv);
+  *ctas = sms / groups < 1 ? 1 : sms / groups;
+  return TVL_OK;
+}
+
+tvl_status window_decode_impl(float* out, const void* q, const void* k_cache, const void* v_cache,
+                              const void* kv4, const int32_t* block_tables,
+                              const int32_t* context_lens, int num_seqs, int num_q_heads,
+                              int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                              int max_blocks_per_seq, float scale, int window, int sinks,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  if (num_seqs < 0) return fail(TVL_ERR_INVALID_ARG, "num_seqs %d < 0", num_seqs);
+  if (max_blocks_per_seq <= 0 || num_blocks <= 0)
+    return fail(TVL_ERR_INVALID_ARG, "num_blocks and max_blocks_per_seq must be positive");
+  if (!kv4_block_size(block_size))
+    return fail(TVL_ERR_UNSUPPORTED, "block_size %d (supported: 16, 32, 64, 128)", block_size);
+  if (static_cast<long long>(num_blocks) * block_size > INT_MAX ||
+      static_cast<long long>(max_blocks_per_seq) * block_size > INT_MAX - 127)
+    return fail(TVL_ERR_UNSUPPORTED, "more than 2^31 - 1 token slots");
+  if (window < 0 || sinks < 0)
+    return fail(TVL_ERR_INVALID_ARG, "window %d and sinks %d must not be negative", window, sinks);
+  if (!std::isfinite(scale)) return fail(TVL_ERR_INVALID_ARG, "scale is not finite");
+  tvl_status st = window_heads(num_q_heads, num_kv_heads, head_dim);
+  if (st != TVL_OK) return st;
+  if (num_seqs == 0) return TVL_OK;
+  if (!out || !q || (!kv4 && (!k_cache || !v_cache)) || !block_tables || !context_lens)
+    return fail(TVL_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(kv4))
+    return fail(TVL_ERR_INVALID_ARG, "out, q and the caches must be 16-byte aligned");
+  if (!workspace) return fail(TVL_ERR_WORKSPACE, "null workspace");
+  if (!aligned16(workspace)) return fail(TVL_ERR_INVALID_ARG, "workspace not 16-byte aligned");
+  int ctas = 0;
+  st = window_ctas(num_kv_heads, &ctas);
+  if (st != TVL_OK) return st;
+  const size_t need = tvl::window_workspace_bytes(ctas, num_q_heads);
+  if (workspace_bytes < need)
+    return fail(TVL_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  uint32_t* word = nullptr;
+  st = status_word(&word);
+  if (st != TVL_OK) return st;
+  tvl::WindowDecodeArgs a;
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.kv4 = kv4;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.window = window;
+  a.sinks = sinks;
+  a.scale = scale;
+  a.ctas = ctas;
+  a.workspace = workspace;
+  a.status = word;
+  cudaError_t e = tvl::launch_window_decode(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "window decode launch");
+  return TVL_OK;
+}
+
+}  // namespace
+
+tvl_status tvl_window_decode_workspace_size(int num_q_heads, int num_kv_heads, int head_dim,
+                                            size_t* bytes) {
+  if (!bytes) return fail(TVL_ERR_INVALID_ARG, "null bytes pointer");
+  tvl_status st = window_heads(num_q_heads, num_kv_heads, head_dim);
+  if (st != TVL_OK) return st;
+  int ctas = 0;
+  st = window_ctas(num_kv_heads, &ctas);
+  if (st != TVL_OK) return st;
+  *bytes = tvl::window_workspace_bytes(ctas, num_q_heads);
+  return TVL_OK;
+}
+
+tvl_status tvl_kv4_attention_decode(float* out, const void* q, const void* cache,
+                                    const int32_t* block_tables, const int32_t* context_lens,
+                                    int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                    int block_size, int num_blocks, int max_blocks_per_seq,
+                                    float scale, int window, int sinks, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  if (num_seqs > 0 && !cache) return fail(TVL_ERR_INVALID_ARG, "null cache pointer");
+  return window_decode_impl(out, q, nullptr, nullptr, cache, block_tables, context_lens, num_seqs,
+                            num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                            max_blocks_per_seq, scale, window, sinks, workspace, workspace_bytes,
+                            stream);
+}
+
+tvl_status tvl_paged_attention_window_decode(float* out, const void* q, const void* k_cache,
+                                             const void* v_cache, const int32_t* block_tables,
+                                             const int32_t* context_lens, int num_seqs,
+                                             int num_q_heads, int num_kv_heads, int head_dim,
+                                             int block_size, int num_blocks,
+                                             int max_blocks_per_seq, float scale, int window,
+                                             int sinks, void* workspace, size_t workspace_bytes,
+                                             void* stream) {
+  return window_decode_impl(out, q, k_cache, v_cache, nullptr, block_tables, context_lens,
+                            num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                            max_blocks_per_seq, scale, window, sinks, workspace, workspace_bytes,
+                            stream);
+}
+
 }  // extern "C"

@@ -57,11 +57,11 @@ cudaError_t launch_rope_kv_write(const RopeKvWriteArgs& a, cudaStream_t stream);
 
 struct CopyBlocksArgs {
   void* k_cache;
-  void* v_cache;
+  void* v_cache;           // null: one cache only (the 4-bit cache)
   const int32_t* src;
   const int32_t* dst;
   int n;
-  long long block_bytes;   // bs * Hkv * D * 2
+  long long block_bytes;   // bs * Hkv * D * 2 (4-bit: bs * Hkv * 72)
   int num_blocks;
   uint32_t* status;
 };
@@ -137,6 +137,55 @@ struct PrefillArgs {
   int num_sms;            // the persistent grid's size bound
 };
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
+
+// ------------------------------------------------------------ 4-bit cache
+
+struct Kv4WriteArgs {
+  void* q;                 // rotated in place when positions are given; may be null
+  const void* k_new;
+  const void* v_new;
+  void* cache;
+  const int32_t* slot_mapping;
+  const int32_t* positions;   // null: no rotation
+  int num_tokens, num_q_heads, num_kv_heads, block_size;
+  long long num_slots;
+  float rope_theta;
+  uint32_t* status;
+};
+cudaError_t launch_kv4_write(const Kv4WriteArgs& a, cudaStream_t stream);
+
+struct Kv4ExpandArgs {
+  void* k_cache;           // bf16, written
+  void* v_cache;
+  const void* cache;
+  const int32_t* src;      // blocks of the 4-bit cache
+  const int32_t* dst;      // blocks of the bf16 caches
+  int n, num_kv_heads, block_size, num_blocks, out_blocks;
+  uint32_t* status;
+};
+cudaError_t launch_kv4_expand(const Kv4ExpandArgs& a, cudaStream_t stream);
+
+// ---------------------------------------- decode with a window, or in 4 bits
+
+struct WindowDecodeArgs {
+  float* out;
+  const void* q;
+  const void* k_cache;     // bf16 caches, or null
+  const void* v_cache;
+  const void* kv4;         // the 4-bit cache, or null
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  int num_seqs, num_q_heads, num_kv_heads, block_size, num_blocks, max_blocks_per_seq;
+  int window, sinks;       // window 0: every cached token is visible
+  float scale;
+  int ctas;                // CTAs per KV-head group
+  void* workspace;
+  uint32_t* status;
+};
+// KV heads one CTA owns: the largest divisor of num_kv_heads up to 8.
+int window_heads_per_cta(int num_kv_heads);
+size_t window_workspace_bytes(int ctas, int num_q_heads);
+cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream);
 
 // Sets the calling thread's tvl_last_error() text.
 void set_last_error(const char* msg);

@@ -1,0 +1,273 @@
+// kv4.cu -- writing rows into the 4-bit paged cache and expanding its blocks
+// back to bf16 (the layout is kv4.cuh's).
+//
+// Write: for each token, optionally the rotary embedding of its q heads (in
+// place) and of its new K heads, then each K and V row x (64 values) becomes
+//   z = min x,  s = bf16 rounded up of (max x - z) / 15,
+//   c_d = min(15, rint((x_d - z) / s))   (ties to even; s = 0: all 0),
+// so |s c_d + z - x_d| <= s / 2.  s is rounded up, so the largest value needs
+// no code above 15; the division is IEEE's, because bf16 inputs make exact ties
+// common and a product with 1 / s would break them either way.
+//
+// Bound: HBM bandwidth for a prefill chunk (per token 256 Hkv bytes in, 72 Hkv
+// out, and q both ways), latency for a decode step.  Eight lanes hold a row, 16
+// bytes each; a warp takes 16 rows of a token (q, K and V rows in one list)
+// with all loads in flight, so a token with 48 rows is spread over three warps
+// and a decode step of 64 tokens over 192.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "device.cuh"
+#include "kernels.h"
+#include "kv4.cuh"
+
+namespace tvl {
+namespace {
+
+constexpr int kD = 64;
+constexpr int kWarps = 4;              // per CTA
+constexpr int kRowsPerWarp = 16;
+constexpr unsigned kFull = 0xffffffffu;
+
+// theta^(-2i/D) / (2 pi) in units of 2^-64 turns: position times this, modulo
+// 2^64, is the angle reduced exactly, whatever the position.
+struct RopeTurns {
+  unsigned long long f[kD / 2];
+};
+
+struct WriteParams {
+  __nv_bfloat16* q;
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  uint8_t* cache;
+  const int32_t* slots;
+  const int32_t* positions;     // null: no rotation
+  int num_tokens, hq, hkv, block_size, parts;
+  long long num_slots;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__global__ void __launch_bounds__(kWarps * 32)
+    kv4_write_kernel(const WriteParams p, const RopeTurns turns) {
+  __shared__ float2 trig[kWarps][kD / 2];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long id = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  const long long t = id / p.parts;
+  if (t >= p.num_tokens) return;
+  const int row0 = static_cast<int>(id - t * p.parts) * kRowsPerWarp + (lane >> 3);
+  const int c = lane & 7;
+  const int rows = p.hq + 2 * p.hkv;
+  constexpr int kIt = kRowsPerWarp / 4;
+
+  uint4 w[kIt];
+#pragma unroll
+  for (int i = 0; i < kIt; ++i) {
+    const int r = row0 + 4 * i;
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (r < rows) {
+      const __nv_bfloat16* src = r < p.hq            ? p.q + (t * p.hq + r) * kD
+                                 : r < p.hq + p.hkv ? p.k_new + (t * p.hkv + r - p.hq) * kD
+                                                     : p.v_new + (t * p.hkv + r - p.hq - p.hkv) * kD;
+      w[i] = __ldcs(reinterpret_cast<const uint4*>(src) + c);
+    }
+  }
+  const long long slot = p.slots[t];
+  if (p.positions != nullptr) {
+    // lane i: pair i's angle in (-1/2, 1/2] turns, then its sine and cosine
+    const unsigned long long a =
+        static_cast<unsigned long long>(static_cast<long long>(p.positions[t])) * turns.f[lane];
+    float sn, cs;
+    sincospif(__ll2float_rn(static_cast<long long>(a)) * 1.0842021724855044e-19f, &sn, &cs);  // 2^-63
+    trig[warp][lane] = make_float2(cs, sn);
+    __syncwarp();
+  }
+  const bool store = slot >= 0 && slot < p.num_slots;
+  if (slot >= p.num_slots && lane == 0) report(p.status, TVL_DEV_BAD_SLOT);
+  // records of the token's 16-token group, one a head; its place in them
+  const int tok = static_cast<int>(slot & (kRecTokens - 1));
+  uint8_t* group = p.cache + (store ? slot / kRecTokens : 0) * p.hkv * kRecBytes;
+
+#pragma unroll
+  for (int i = 0; i < kIt; ++i) {
+    const int r = row0 + 4 * i;
+    float x[8];
+    {
+      const float2 f0 = bf16x2_to_float2(w[i].x), f1 = bf16x2_to_float2(w[i].y);
+      const float2 f2 = bf16x2_to_float2(w[i].z), f3 = bf16x2_to_float2(w[i].w);
+      x[0] = f0.x; x[1] = f0.y; x[2] = f1.x; x[3] = f1.y;
+      x[4] = f2.x; x[5] = f2.y; x[6] = f3.x; x[7] = f3.y;
+    }
+    if (p.positions != nullptr) {
+      // lane c's partner in the pairs (d, d + 32) is lane c ^ 4
+      uint4 o;
+      o.x = __shfl_xor_sync(kFull, w[i].x, 4);
+      o.y = __shfl_xor_sync(kFull, w[i].y, 4);
+      o.z = __shfl_xor_sync(kFull, w[i].z, 4);
+      o.w = __shfl_xor_sync(kFull, w[i].w, 4);
+      if (r < p.hq + p.hkv) {
+        const float sign = c < 4 ? -1.f : 1.f;
+        const float2 f[4] = {bf16x2_to_float2(o.x), bf16x2_to_float2(o.y), bf16x2_to_float2(o.z),
+                             bf16x2_to_float2(o.w)};
+        const float2* tr = &trig[warp][8 * (c & 3)];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 cs = tr[j];
+          const float other = (j & 1) ? f[j >> 1].y : f[j >> 1].x;
+          x[j] = fmaf(x[j], cs.x, sign * (other * cs.y));
+        }
+        uint4 y;
+        y.x = pack_bf16(x[0], x[1]);
+        y.y = pack_bf16(x[2], x[3]);
+        y.z = pack_bf16(x[4], x[5]);
+        y.w = pack_bf16(x[6], x[7]);
+        if (r < p.hq) reinterpret_cast<uint4*>(p.q + (t * p.hq + r) * kD)[c] = y;
+        // the K that is quantised is the bf16 row the bf16 cache would hold
+        const float2 g0 = bf16x2_to_float2(y.x), g1 = bf16x2_to_float2(y.y);
+        const float2 g2 = bf16x2_to_float2(y.z), g3 = bf16x2_to_float2(y.w);
+        x[0] = g0.x; x[1] = g0.y; x[2] = g1.x; x[3] = g1.y;
+        x[4] = g2.x; x[5] = g2.y; x[6] = g3.x; x[7] = g3.y;
+      }
+    }
+    float mn = x[0], mx = x[0];
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      mn = fminf(mn, x[j]);
+      mx = fmaxf(mx, x[j]);
+      bad |= !(fabsf(x[j]) < INFINITY);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      mn = fminf(mn, __shfl_xor_sync(kFull, mn, o));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    }
+    const float range = mx - mn;
+    bad |= !(range < INFINITY);
+    const bool row_bad = ((__ballot_sync(kFull, bad) >> (lane & 24)) & 0xffu) != 0;
+    if (!store || r < p.hq || r >= rows) continue;
+    uint32_t code = 0;
+    uint32_t sz = 0x7fc07fc0u;          // a row that is not finite stands for NaN
+    if (!row_bad) {
+      const uint32_t sb = (__float_as_uint(__fdiv_rn(range, 15.0f)) + 0xffffu) & 0xffff0000u;
+      const float s = __uint_as_float(sb);
+      sz = (sb >> 16) | (__float_as_uint(mn) & 0xffff0000u);
+      if (s > 0.f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int v = __float2int_rn(__fdiv_rn(x[j] - mn, s));
+          code |= static_cast<uint32_t>(min(v, 15)) << (4 * j);
+        }
+      }
+    } else if (c == 0) {
+      report(p.status, TVL_DEV_NONFINITE);
+    }
+    const bool is_v = r >= p.hq + p.hkv;
+    uint8_t* rec = group + (r - p.hq - (is_v ? p.hkv : 0)) * kRecBytes;
+    reinterpret_cast<uint32_t*>(rec + (is_v ? kRecV : 0) + tok * kRowCodes)[c] = code;
+    if (c == 0) reinterpret_cast<uint32_t*>(rec + (is_v ? kRecVMeta : kRecKMeta))[tok] = sz;
+  }
+}
+
+// One warp per record: its 16 K rows and 16 V rows, four at a time (eight
+// lanes a row, 4 bytes of codes in, 16 bytes of bf16 out), the codes of all
+// eight steps in flight.
+__global__ void __launch_bounds__(kWarps * 32)
+    kv4_expand_kernel(__nv_bfloat16* k_cache, __nv_bfloat16* v_cache, const uint8_t* cache,
+                      const int32_t* src, const int32_t* dst, long long records, int hkv, int cpb,
+                      int src_blocks, int dst_blocks, uint32_t* status) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long id = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  if (id >= records) return;
+  const int h = static_cast<int>(id % hkv);
+  const long long rest = id / hkv;
+  const int sub = static_cast<int>(rest % cpb);
+  const long long i = rest / cpb;
+  const int from = src[i], to = dst[i];
+  if (from < 0 || from >= src_blocks || to < 0 || to >= dst_blocks) {
+    if (lane == 0) report(status, TVL_DEV_BAD_BLOCK_ID);
+    return;
+  }
+  const uint8_t* rec = cache + ((static_cast<long long>(from) * cpb + sub) * hkv + h) * kRecBytes;
+  const int c = lane & 7, g = lane >> 3;
+  uint32_t code[8], sz[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {          // k < 4: K rows, else V rows
+    const int tok = (k & 3) * 4 + g;
+    code[k] = __ldcs(reinterpret_cast<const uint32_t*>(rec + (k < 4 ? 0 : kRecV) + tok * kRowCodes) + c);
+    sz[k] = __ldcs(reinterpret_cast<const uint32_t*>(rec + (k < 4 ? kRecKMeta : kRecVMeta)) + tok);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int tok = (k & 3) * 4 + g;
+    const float2 m = bf16x2_to_float2(sz[k]);
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      y[j] = fmaf(m.x, static_cast<float>((code[k] >> (4 * j)) & 15u), m.y);
+    __nv_bfloat16* out = (k < 4 ? k_cache : v_cache) +
+                         ((static_cast<long long>(to) * cpb + sub) * kRecTokens + tok) * hkv * kD + h * kD;
+    reinterpret_cast<uint4*>(out)[c] = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                                  pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+  }
+}
+
+const RopeTurns& rope_turns(float theta) {
+  static thread_local float have = 0.f;
+  static thread_local RopeTurns t = {};
+  if (have != theta) {
+    for (int i = 0; i < kD / 2; ++i)
+      t.f[i] = static_cast<unsigned long long>(
+          std::llrint(std::pow(static_cast<double>(theta), -2.0 * i / kD) / 6.283185307179586476925 *
+                      4611686018427387904.0)) << 2;      // 2^62 steps a turn, then 2^64
+    have = theta;
+  }
+  return t;
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_write(const Kv4WriteArgs& a, cudaStream_t stream) {
+  if (a.num_tokens == 0) return cudaSuccess;
+  WriteParams p;
+  p.q = static_cast<__nv_bfloat16*>(a.q);
+  p.k_new = static_cast<const __nv_bfloat16*>(a.k_new);
+  p.v_new = static_cast<const __nv_bfloat16*>(a.v_new);
+  p.cache = static_cast<uint8_t*>(a.cache);
+  p.slots = a.slot_mapping;
+  p.positions = a.positions;
+  p.num_tokens = a.num_tokens;
+  p.hq = a.q && a.positions ? a.num_q_heads : 0;
+  p.hkv = a.num_kv_heads;
+  p.block_size = a.block_size;
+  p.parts = (p.hq + 2 * p.hkv + kRowsPerWarp - 1) / kRowsPerWarp;
+  p.num_slots = a.num_slots;
+  p.status = a.status;
+  const long long warps = static_cast<long long>(a.num_tokens) * p.parts;
+  static const RopeTurns none = {};
+  return launch_pdl(kv4_write_kernel, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)),
+                    dim3(kWarps * 32), 0, stream, p,
+                    a.positions ? rope_turns(a.rope_theta) : none);
+}
+
+cudaError_t launch_kv4_expand(const Kv4ExpandArgs& a, cudaStream_t stream) {
+  if (a.n == 0) return cudaSuccess;
+  const int cpb = a.block_size / kRecTokens;
+  const long long records = static_cast<long long>(a.n) * cpb * a.num_kv_heads;
+  return launch_pdl(kv4_expand_kernel, dim3(static_cast<unsigned>((records + kWarps - 1) / kWarps)),
+                    dim3(kWarps * 32), 0, stream, static_cast<__nv_bfloat16*>(a.k_cache),
+                    static_cast<__nv_bfloat16*>(a.v_cache), static_cast<const uint8_t*>(a.cache),
+                    a.src, a.dst, records, a.num_kv_heads, cpb, a.num_blocks, a.out_blocks,
+                    a.status);
+}
+
+}  // namespace tvl

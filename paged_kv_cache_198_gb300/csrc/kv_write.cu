@@ -137,7 +137,7 @@ cudaError_t launch_rope_kv_write(const RopeKvWriteArgs& a, cudaStream_t stream) 
 
 cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, cudaStream_t stream) {
   if (a.n == 0) return cudaSuccess;
-  return launch_pdl(copy_blocks_kernel, dim3(a.n, 2), dim3(256), 0, stream,
+  return launch_pdl(copy_blocks_kernel, dim3(a.n, a.v_cache ? 2 : 1), dim3(256), 0, stream,
                     static_cast<uint4*>(a.k_cache), static_cast<uint4*>(a.v_cache), a.src, a.dst,
                     a.block_bytes / 16, a.num_blocks, a.status);
 }

@@ -1,0 +1,1138 @@
+// window_decode.cu -- decode attention on the tensor cores, over a bf16 or a
+// 4-bit paged cache, with an optional sliding window and sinks.
+//
+// What it computes: for each sequence s (one query token at position ctx - 1)
+// and query head h,
+//   out[s,h,:] = sum_j softmax_j(scale * q[s,h,:] . K_j) V_j
+// over the visible tokens j < ctx: all of them without a window, else those
+// with j >= ctx - window or j < sinks.
+//
+// Bound: every visible K/V byte is read once, so HBM bandwidth -- provided
+// that the arithmetic keeps up.  At 4 bits an SM is handed a 16-token record
+// of one head (1152 bytes) every 26 cycles (6.8 TB/s, 152 SMs, 1.9 GHz), 104
+// issue slots of each of its four schedulers; one fp32 FMA per (value, query
+// head) would need 256 for four heads.  So both products run on mma.sync
+// m16n8k16 with the tokens (Q K^T) or the dimensions (P V) as the 16 rows and
+// the query heads of the GQA group as the 8 columns; the operands come straight
+// from shared memory into registers, with no dequantised copy.
+//
+// 4-bit codes as operands.  A code in the low bits of a 16-bit word is the
+// fp16 subnormal c * 2^-24, in bits 4..7 it is 16 c * 2^-24: one AND turns two
+// codes into an operand register, and the factors 2^24 and 16 go into q and the
+// final scale.  The k order of a product is free, so lane t of a row takes
+// the row's dimensions 16 t .. 16 t + 15 as one 8-byte load.  Per row
+//   scale q . K_j = s_j (q . c_j) F + z_j sum(q),
+// and for V the weight p_j s_j multiplies c_j - 8 (one packed subtract) while
+// p_j (z_j + 8 s_j) is summed in fp32 beside it: centred codes keep the long
+// sum as small as the output, so fp32 accumulation loses nothing to
+// cancellation.  q (bf16) is exact in fp16 after a power-of-two scale.
+//
+// P in two halves.  The weights p are fp32; hi + lo, two 16-bit numbers, keep
+// 22 (fp16) or 16 (bf16) bits of them, so the fp32 output carries no rounding
+// of P.  With four query heads or fewer the lo halves ride in columns 4..7 of
+// the same product at no cost; with five to eight they take a second one.
+//
+// Work split.  The visible 16-token chunks of all sequences form one line, cut
+// into equal ranges, one CTA per SM and KV-head group, each sequence start
+// counted as `seg_weight` chunks more.  A range's piece of a sequence is a
+// segment; one that covers its whole sequence writes the output, any other a
+// partial (m, l, acc) record; the CTA that holds a split sequence's first
+// chunk lists it for merge_kernel.
+//
+// CTA.  One producer warp fills a ring of shared-memory stages (bulk copies
+// of whole 16-token runs of the 4-bit cache, swizzled tensor copies of the
+// bf16 one), one mbarrier each; up to 16 consumer warps, `wph` per KV head,
+// take the chunks of a stage in turn.  The warps of a head combine at a segment's
+// end through shared memory.  All waits are bounded.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <mutex>
+
+#include "device.cuh"
+#include "kernels.h"
+#include "kv4.cuh"
+#include "tc.cuh"
+
+namespace tvl {
+namespace {
+
+constexpr int kD = 64;
+constexpr int kChunk = 16;
+constexpr int kMaxWarps = 16;                 // consumer warps
+constexpr int kThreads = (kMaxWarps + 1) * 32;
+constexpr uint32_t kBf16Tile = kChunk * kD * 2;   // one head's K (or V) of a chunk
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kMaxVScale = 128.0f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr uint32_t kSmemLimit = 227 * 1024;
+constexpr int kCombPitch = 72;                // floats a head of a warp hands over: 64 + m, l
+
+enum Format : int { kBf16 = 0, k4Bit = 1 };
+enum : int { kSegFirst = 1, kSegLast = 2, kTerminate = 4 };
+
+// chunks a warp takes from a stage at once (independent work in flight)
+template <int F>
+__host__ __device__ constexpr int chunks_per_warp() { return F == k4Bit ? 2 : 1; }
+
+struct alignas(16) StageMeta {
+  int seq, record, flags, n;   // n: chunks in the stage
+  int v0, ns, delta, ctx;      // first virtual chunk; sink chunks; token chunk = v + (v >= ns) * delta
+};
+
+struct Params {
+  float* out;
+  const __nv_bfloat16* q;
+  const uint8_t* kv4;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  int num_seqs, hq, hkv, group, num_blocks, max_blocks;
+  int cpb_log2;          // log2 of the 16-token chunks in a block
+  int window, sinks;     // window 0: none
+  int hpc, wph, cps, stages;
+  uint32_t stage_bytes, kv_bytes;
+  float scale_log2;
+  int ctas, seg_weight;
+  float* ws_m;           // records [2 * ctas][hq]
+  float* ws_l;
+  float* ws_acc;
+  int4* ws_split;        // per CTA: the split sequence it starts (seq or -1, first record, last CTA)
+  long long* ws_total;   // length of the cost line
+  uint32_t* status;
+};
+
+struct Layout {
+  uint32_t meta, bars, comb, sched, total;
+};
+
+__host__ __device__ inline uint32_t align_up(uint32_t x, uint32_t a) { return (x + a - 1) / a * a; }
+
+__host__ __device__ inline Layout make_layout(int stages, uint32_t stage_bytes, int hpc, int wph,
+                                              int group) {
+  Layout l;
+  uint32_t off = stages * stage_bytes;
+  l.meta = off;
+  off += stages * sizeof(StageMeta);
+  l.bars = off;                                        // full, empty; comb full, empty per head
+  off += (2 * stages + 2 * hpc) * 8;
+  l.comb = align_up(off, 16);
+  off = l.comb + (wph - 1) * hpc * group * kCombPitch * 4;
+  l.sched = align_up(off, 16);
+  off = l.sched + 64 + 32 * 8;
+  l.total = off;
+  return l;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Weight of a partial result with reference maximum m under the common one.
+// m = -inf with anything in it means scores that were all NaN: kept as NaN.
+__device__ __forceinline__ float weight_of(float m, float common) {
+  return m == -INFINITY ? 1.f : ex2(m - common);
+}
+
+__device__ __forceinline__ int load_ctx(const Params& p, int s) {
+  int c = p.context_lens[s];
+  const long long cap = static_cast<long long>(p.max_blocks) << (p.cpb_log2 + 4);
+  if (c < 0 || c > cap) {
+    report(p.status, TVL_DEV_BAD_CONTEXT_LEN);
+    c = c < 0 ? 0 : static_cast<int>(cap);
+  }
+  return c;
+}
+
+// The visible chunks of a sequence: ns chunks from 0 (sinks), then the window's
+// from w0.  Virtual chunk v is token chunk v for v < ns, else v - ns + w0.
+struct Visible {
+  int ns, delta, n;
+};
+__device__ __forceinline__ Visible visible_of(const Params& p, int ctx) {
+  const int first = p.window > 0 && ctx > p.window ? ctx - p.window : 0;
+  const int w0 = first / kChunk;
+  const int sc = p.sinks / kChunk + (p.sinks % kChunk != 0 ? 1 : 0);
+  Visible v;
+  v.ns = min(sc, w0);
+  v.delta = w0 - v.ns;
+  v.n = (ctx + kChunk - 1) / kChunk - v.delta;
+  return v;
+}
+__device__ __forceinline__ long long seq_cost(int n, int w) { return n > 0 ? n + w : 0; }
+
+// ------------------------------------------------------------------ schedule
+
+struct Schedule {
+  int seq0, v0;          // first sequence and virtual chunk
+  int seq_end, v_end;    // ends before chunk v_end of sequence seq_end
+  long long total, hi;   // the cost line's length, this CTA's end on it
+};
+
+__device__ void block_scan(long long v, long long& incl, long long& total, long long* tmp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) tmp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    long long w = lane < nw ? tmp[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(kFull, w, o);
+      if (lane >= o) w += y;
+    }
+    if (lane < nw) tmp[lane] = w;
+  }
+  __syncthreads();
+  incl = x + (warp > 0 ? tmp[warp - 1] : 0);
+  total = tmp[nw - 1];
+  __syncthreads();
+}
+
+// Every thread sums the costs of a contiguous slice of the sequences; one
+// scan places the slices on the line, and the threads whose slices hold this
+// CTA's two ends walk them again.
+__device__ void make_schedule(const Params& p, Schedule* sc, long long* tmp) {
+  const int tid = threadIdx.x, cta = blockIdx.x, w = p.seg_weight;
+  const int per = (p.num_seqs + blockDim.x - 1) / blockDim.x;
+  const int s_lo = min(p.num_seqs, tid * per), s_hi = min(p.num_seqs, s_lo + per);
+  long long mine = 0;
+  for (int s = s_lo; s < s_hi; ++s) mine += seq_cost(visible_of(p, load_ctx(p, s)).n, w);
+  if (tid == 0) {
+    sc->seq0 = sc->seq_end = p.num_seqs;
+    sc->v0 = sc->v_end = 0;
+  }
+  long long incl, total;
+  block_scan(mine, incl, total, tmp);      // its barriers order the initial values
+  const long long excl = incl - mine;
+  const long long lo = total * cta / p.ctas, hi = total * (cta + 1) / p.ctas;
+  auto locate = [&](long long x, int& seq, int& v) {
+    long long run = excl;
+    for (int s = s_lo; s < s_hi; ++s) {
+      const long long c = seq_cost(visible_of(p, load_ctx(p, s)).n, w);
+      if (x < run + c) {
+        seq = s;
+        v = static_cast<int>(x - run - w > 0 ? x - run - w : 0);
+        return;
+      }
+      run += c;
+    }
+  };
+  if (mine > 0 && excl <= lo && lo < incl) locate(lo, sc->seq0, sc->v0);
+  if (mine > 0 && excl <= hi && hi < incl) locate(hi, sc->seq_end, sc->v_end);
+  if (tid == 0) {
+    sc->total = total;
+    sc->hi = hi;
+  }
+}
+
+// ------------------------------------------------------------------ producer
+
+struct Segment {
+  int s, v, e, ctx, ns, delta, n, record;
+};
+
+template <int F>
+__device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, const Layout& L,
+                         const CUtensorMap* tm_k, const CUtensorMap* tm_v) {
+  const int lane = threadIdx.x & 31;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars);
+  uint64_t* empty = full + p.stages;
+  StageMeta* meta = reinterpret_cast<StageMeta*>(smem + L.meta);
+  const int hpc = p.hpc, h0 = blockIdx.z * hpc, cta = blockIdx.x;
+  const uint32_t chunk_bytes = hpc * (F == k4Bit ? kRecBytes : 2 * kBf16Tile);
+  const uint32_t q_bytes = hpc * p.group * kD * 2;
+  const uint64_t stream_policy = policy_evict_first();
+  const uint64_t keep_policy = policy_evict_last();
+  if (F == kBf16 && lane == 0) {
+    prefetch_tensormap(tm_k);
+    prefetch_tensormap(tm_v);
+  }
+
+  int st = 0, filled = 0;        // next stage; stages filled so far, capped
+  uint32_t ph = 0;               // parity of the fill before the next one of stage st
+  bool ok = true;
+  auto acquire = [&]() {
+    bool good = true;
+    if (filled >= p.stages && lane == 0) good = mbar_wait(&empty[st], ph ^ 1);
+    ok = __shfl_sync(kFull, good ? 1 : 0, 0) != 0;
+    return ok;
+  };
+  auto advance_stage = [&]() {
+    if (filled < p.stages) ++filled;
+    if (++st == p.stages) {
+      st = 0;
+      ph ^= 1;
+    }
+  };
+
+  // lane i: the context length of sequence win + i
+  int win = -64, win_ctx = 0;
+  // The segment that starts at chunk v of sequence s or after it; false: none left.
+  auto find = [&](int s, int v, bool first, Segment& g) {
+    for (;; ++s, v = 0) {
+      if (s >= p.num_seqs || s > sc.seq_end || (s == sc.seq_end && v >= sc.v_end)) return false;
+      if (s < win || s >= win + 32) {
+        win = s;
+        win_ctx = s + lane < p.num_seqs ? load_ctx(p, s + lane) : 0;
+      }
+      g.ctx = __shfl_sync(kFull, win_ctx, s - win);
+      const Visible vis = visible_of(p, g.ctx);
+      if (v >= vis.n) continue;
+      g.s = s;
+      g.v = v;
+      g.e = s == sc.seq_end ? min(sc.v_end, vis.n) : vis.n;
+      g.ns = vis.ns;
+      g.delta = vis.delta;
+      g.n = vis.n;
+      g.record = v == 0 && g.e == vis.n ? -1 : 2 * cta + (first ? 0 : 1);
+      return true;
+    }
+  };
+  // this lane's block table entry: chunk vb + lane of the segment
+  auto entry = [&](const Segment& g, int vb) {
+    const int v = vb + lane;
+    if (v >= g.e) return 0;
+    const int c = v < g.ns ? v : v + g.delta;
+    return p.block_tables[static_cast<long long>(g.s) * p.max_blocks + (c >> p.cpb_log2)];
+  };
+
+  int4 split = make_int4(-1, 0, 0, 0);
+  Segment g;
+  bool have = find(sc.seq0, sc.v0, true, g);
+  int tbl = have ? entry(g, g.v) : 0;
+  while (have && ok) {
+    if (g.v == 0 && g.e < g.n) {
+      // a split sequence's first piece: it ends at this CTA's end of the
+      // line, and the sequence's last chunk lies g.n - g.e - 1 places on
+      const long long x = sc.hi + (g.n - g.e) - 1;
+      split = make_int4(g.s, g.record, static_cast<int>(((x + 1) * p.ctas - 1) / sc.total), 0);
+    }
+    Segment nx;
+    const bool have_next = find(g.s, g.e, false, nx);
+    for (int vb = g.v; vb < g.e && ok; vb += 32) {
+      // the next 32 entries (of this segment or the next) are fetched while
+      // this batch's copies are issued
+      const int ntbl = vb + 32 < g.e ? entry(g, vb + 32) : (have_next ? entry(nx, nx.v) : 0);
+      for (int v = vb; v < g.e && v < vb + 32; v += p.cps) {
+        const int n = min(p.cps, g.e - v);
+        if (!acquire()) break;
+        uint8_t* base = smem + static_cast<size_t>(st) * p.stage_bytes;
+        const bool first = v == g.v;
+        if (lane == 0) {
+          StageMeta m;
+          m.seq = g.s;
+          m.record = g.record;
+          m.flags = (first ? kSegFirst : 0) | (v + n == g.e ? kSegLast : 0);
+          m.n = n;
+          m.v0 = v;
+          m.ns = g.ns;
+          m.delta = g.delta;
+          m.ctx = g.ctx;
+          meta[st] = m;
+          mbar_arrive_expect_tx(&full[st], n * chunk_bytes + (first ? q_bytes : 0));
+        }
+        int page = __shfl_sync(kFull, tbl, (v - vb + lane) & 31);   // orders lane 0's arrive, too
+        if (lane < n) {
+          if (page < 0 || page >= p.num_blocks) {
+            report(p.status, TVL_DEV_BAD_BLOCK_ID);
+            page = 0;
+          }
+          const int vv = v + lane;
+          const int c = vv < g.ns ? vv : vv + g.delta;
+          const int sub = c & ((1 << p.cpb_log2) - 1);
+          const long long chunk = (static_cast<long long>(page) << p.cpb_log2) + sub;
+          if (F == k4Bit) {
+            bulk_load(base + lane * chunk_bytes, p.kv4 + (chunk * p.hkv + h0) * kRecBytes,
+                      chunk_bytes, &full[st], stream_policy);
+          } else {
+            const int tok = static_cast<int>(chunk * kChunk);
+            const uint32_t half = hpc * kBf16Tile;
+            tma_load_3d(base + lane * half, tm_k, 0, tok, h0, &full[st]);
+            tma_load_3d(base + p.kv_bytes / 2 + lane * half, tm_v, 0, tok, h0, &full[st]);
+          }
+        }
+        if (first && lane == 31)
+          bulk_load(base + p.kv_bytes,
+                    p.q + (static_cast<size_t>(g.s) * p.hq + static_cast<size_t>(h0) * p.group) * kD,
+                    q_bytes, &full[st], keep_policy);
+        advance_stage();
+      }
+      tbl = ntbl;
+    }
+    g = nx;
+    have = have_next;
+  }
+  if (blockIdx.z == 0 && lane == 0) {
+    p.ws_split[cta] = split;
+    if (cta == 0) *p.ws_total = sc.total;
+  }
+  if (ok && acquire()) {
+    if (lane == 0) {
+      meta[st].flags = kTerminate;
+      mbar_arrive(&full[st]);
+    }
+    advance_stage();
+  } else if (lane == 0) {
+    report(p.status, kDevTimeout);
+  }
+  // copies in flight land before the CTA may exit: the last fill of each stage
+  if (lane == 0) {
+    for (int i = 0; i < filled; ++i) {
+      if (--st < 0) {
+        st = p.stages - 1;
+        ph ^= 1;
+      }
+      if (!mbar_wait(&full[st], ph)) report(p.status, kDevTimeout);
+    }
+  }
+}
+
+// ----------------------------------------------------------------- consumers
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// the 8 x 8 matrix of 16-bit elements held one row per lane quad, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float2 meta_sz(uint32_t w) { return bf16x2_to_float2(w); }
+
+template <int F>
+__device__ __forceinline__ uint32_t pack16(float2 v) {
+  if constexpr (F == k4Bit) {
+    const __half2 h = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+template <int F>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+  if constexpr (F == k4Bit) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return bf16x2_to_float2(w);
+}
+
+// Row r of the 16 rows of a product is token row_token(r) of the chunk.  With
+// 4-bit rows of 32 bytes this order leaves both the K loads (8 bytes a lane,
+// rows 0..3 and 4..7 a half warp each) and the V loads (4 bytes a lane, rows of
+// one parity together) free of bank conflicts: tokens of a group differ mod 4.
+template <int F>
+__device__ __forceinline__ int row_token(int r) {   // r < 8
+  if (F == kBf16) return r;
+  return (0x57463120 >> (4 * r)) & 7;               // 0 2 1 3 6 4 7 5
+}
+
+// A lane (g = lane / 4, t = lane % 4) holds columns 2 t and 2 t + 1: `x`, `y`.
+struct State {
+  uint32_t qf[4][2];   // q as the column operand
+  float acc[4][4];     // output rows, see out_dim
+  float2 m, l, zs;     // reference maximum (log2), sum of p, sum of p (z + 8 s)
+  float2 qsum;         // 4-bit: sum(q) * scale_log2
+  float kf;            // 4-bit: factor of q . c
+  float vs;            // 4-bit: power of two on the V scales
+};
+
+// acc[i][0..1] is output dimension out_dim(i, 0), acc[i][2..3] out_dim(i, 1)
+template <int F>
+__device__ __forceinline__ int out_dim(int g, int i, int half) {
+  return F == k4Bit ? 8 * g + 2 * i + half : 16 * i + 8 * half + g;
+}
+
+template <int F, bool kLoCols>
+__device__ __forceinline__ void load_q(State& st, const Params& p, const uint8_t* qbase) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int h = kLoCols ? (g & 3) : g;
+  const bool live = h < p.group;
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(qbase + (live ? h : 0) * (kD * 2));
+  if constexpr (F == kBf16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      st.qf[i][0] = live ? q[8 * i + t] : 0u;
+      st.qf[i][1] = live ? q[8 * i + t + 4] : 0u;
+    }
+  } else {
+    float v[16];
+    float sum = 0.f, mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = bf16x2_to_float2(live ? q[8 * t + i] : 0u);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+      sum += f.x + f.y;
+      if (fabsf(f.x) < INFINITY) mx = fmaxf(mx, fabsf(f.x));
+      if (fabsf(f.y) < INFINITY) mx = fmaxf(mx, fabsf(f.y));
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    sum += __shfl_xor_sync(kFull, sum, 1);
+    sum += __shfl_xor_sync(kFull, sum, 2);
+    st.qsum.x = __shfl_sync(kFull, sum, 8 * t) * p.scale_log2;
+    st.qsum.y = __shfl_sync(kFull, sum, 8 * t + 4) * p.scale_log2;
+    // the largest |q| of the group to [2^14, 2^15): exact in fp16 for every
+    // element down to 2^-28 of it (a bf16 has 8 significant bits)
+    int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+    e = max(-100, min(100, e));
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+    const float up16 = up * 0.0625f;
+    st.kf = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 10 + e) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = (i >> 1) * 8 + (i & 1) * 2;
+      st.qf[i][0] = pack16<k4Bit>(make_float2(v[d] * up, v[d + 4] * up));
+      st.qf[i][1] = pack16<k4Bit>(make_float2(v[d + 1] * up16, v[d + 5] * up16));
+    }
+  }
+}
+
+// NCH chunks of the warp's head; chunk i starts at token tok0[i] and lies at
+// kb[i] (4-bit: the record; bf16: the K tile, with the V tile v_off behind).
+template <int F, bool kLoCols, int NCH, bool kMasked>
+__device__ __forceinline__ void process(State& st, const Params& p, const uint8_t* const (&kb)[NCH],
+                                        uint32_t v_off, const int (&tok0)[NCH], int ctx) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int r0 = row_token<F>(g), r1 = 8 + r0;
+  const int first = p.window > 0 && ctx > p.window ? ctx - p.window : 0;
+  auto seen = [&](int tok) { return tok < ctx && (tok >= first || tok < p.sinks); };
+
+  // --- scores: c[0..1] row g, c[2..3] row g + 8
+  float2 x[NCH][2];
+#pragma unroll
+  for (int ch = 0; ch < NCH; ++ch) {
+    float c[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (F == k4Bit) {
+      const uint2 a = *reinterpret_cast<const uint2*>(kb[ch] + r0 * kRowCodes + t * 8);
+      const uint2 b = *reinterpret_cast<const uint2*>(kb[ch] + r1 * kRowCodes + t * 8);
+      const float2 m0 = meta_sz(*reinterpret_cast<const uint32_t*>(kb[ch] + kRecKMeta + r0 * 4));
+      const float2 m1 = meta_sz(*reinterpret_cast<const uint32_t*>(kb[ch] + kRecKMeta + r1 * 4));
+      constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
+      mma_f16(c, a.x & kLo, b.x & kLo, a.x & kHi, b.x & kHi, st.qf[0][0], st.qf[0][1]);
+      mma_f16(c, (a.x >> 8) & kLo, (b.x >> 8) & kLo, (a.x >> 8) & kHi, (b.x >> 8) & kHi,
+              st.qf[1][0], st.qf[1][1]);
+      mma_f16(c, a.y & kLo, b.y & kLo, a.y & kHi, b.y & kHi, st.qf[2][0], st.qf[2][1]);
+      mma_f16(c, (a.y >> 8) & kLo, (b.y >> 8) & kLo, (a.y >> 8) & kHi, (b.y >> 8) & kHi,
+              st.qf[3][0], st.qf[3][1]);
+      const float s0 = m0.x * st.kf, s1 = m1.x * st.kf;
+      x[ch][0] = __ffma2_rn(make_float2(c[0], c[1]), make_float2(s0, s0),
+                            __fmul2_rn(st.qsum, make_float2(m0.y, m0.y)));
+      x[ch][1] = __ffma2_rn(make_float2(c[2], c[3]), make_float2(s1, s1),
+                            __fmul2_rn(st.qsum, make_float2(m1.y, m1.y)));
+    } else {
+      const uint32_t base = smem_addr(kb[ch]);
+      const int row = (lane & 7) + (lane & 8);          // matrices 1 and 3: rows 8..15
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t a[4];
+        ldsm4(a, base + row * 128 + (((2 * i + (lane >> 4)) ^ (row & 7)) << 4));
+        mma_bf16(c, a[0], a[1], a[2], a[3], st.qf[i][0], st.qf[i][1]);
+      }
+      const float2 sl = make_float2(p.scale_log2, p.scale_log2);
+      x[ch][0] = __fmul2_rn(make_float2(c[0], c[1]), sl);
+      x[ch][1] = __fmul2_rn(make_float2(c[2], c[3]), sl);
+    }
+    if (kMasked) {
+      if (!seen(tok0[ch] + r0)) x[ch][0] = make_float2(-INFINITY, -INFINITY);
+      if (!seen(tok0[ch] + r1)) x[ch][1] = make_float2(-INFINITY, -INFINITY);
+    }
+  }
+  // --- 4-bit: the V rows' scales (an unseen row: all zero)
+  float2 mv[NCH][2];
+  if constexpr (F == k4Bit) {
+#pragma unroll
+    for (int ch = 0; ch < NCH; ++ch) {
+      mv[ch][0] = meta_sz(*reinterpret_cast<const uint32_t*>(kb[ch] + kRecVMeta + r0 * 4));
+      mv[ch][1] = meta_sz(*reinterpret_cast<const uint32_t*>(kb[ch] + kRecVMeta + r1 * 4));
+      if (kMasked) {
+        if (!seen(tok0[ch] + r0)) mv[ch][0] = make_float2(0.f, 0.f);
+        if (!seen(tok0[ch] + r1)) mv[ch][1] = make_float2(0.f, 0.f);
+      }
+    }
+  }
+  // --- online softmax: the reference moves only when a score passes it by 2^8
+  // (exact, one reference scales numerator and denominator)
+  float2 mx = x[0][0];
+  float sv = 0.f;
+#pragma unroll
+  for (int ch = 0; ch < NCH; ++ch)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      mx.x = fmaxf(mx.x, x[ch][r].x);
+      mx.y = fmaxf(mx.y, x[ch][r].y);
+      if (F == k4Bit) sv = fmaxf(sv, mv[ch][r].x);
+    }
+  const bool up = fmaxf(mx.x - st.m.x, mx.y - st.m.y) > kRescaleLog2;
+  if (__any_sync(kFull, up || (F == k4Bit && sv * st.vs > kMaxVScale))) {
+    float f_v = 1.f;
+    if (F == k4Bit) {
+      // the V scales' power of two: the largest seen to [32, 64)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) sv = fmaxf(sv, __shfl_xor_sync(kFull, sv, o));
+      if (st.vs == 0.f || sv * st.vs > kMaxVScale) {
+        int e = static_cast<int>(__float_as_uint(sv) >> 23) - 127;
+        e = max(-100, min(100, e));
+        const float vs = __uint_as_float(static_cast<uint32_t>(127 + 5 - e) << 23);
+        f_v = st.vs == 0.f ? 0.f : vs / st.vs;
+        st.vs = vs;
+      }
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      mx.x = fmaxf(mx.x, __shfl_xor_sync(kFull, mx.x, o));
+      mx.y = fmaxf(mx.y, __shfl_xor_sync(kFull, mx.y, o));
+    }
+    mx.x = fmaxf(mx.x, st.m.x);
+    mx.y = fmaxf(mx.y, st.m.y);
+    float2 f = make_float2(ex2(st.m.x - mx.x), ex2(st.m.y - mx.y));
+    st.m = mx;
+    st.l = __fmul2_rn(st.l, f);
+    st.zs = __fmul2_rn(st.zs, f);
+    f.x *= f_v;
+    f.y *= f_v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      st.acc[i][0] *= f.x;
+      st.acc[i][1] *= f.y;
+      st.acc[i][2] *= f.x;
+      st.acc[i][3] *= f.y;
+    }
+  }
+  const float2 nm = make_float2(-st.m.x, -st.m.y);
+#pragma unroll
+  for (int ch = 0; ch < NCH; ++ch) {
+    // --- weights, as the column operand of P V: rows of the transposed matrix
+    // are the heads, its columns the tokens
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float2 d = __fadd2_rn(x[ch][r], nm);
+      float2 w = make_float2(ex2(d.x), ex2(d.y));
+      st.l = __fadd2_rn(st.l, w);
+      if constexpr (F == k4Bit) {
+        const float zc = fmaf(8.f, mv[ch][r].x, mv[ch][r].y);
+        st.zs = __ffma2_rn(w, make_float2(zc, zc), st.zs);
+        const float sc = mv[ch][r].x * st.vs;
+        w = __fmul2_rn(w, make_float2(sc, sc));
+      }
+      hi[r] = pack16<F>(w);
+      const float2 back = unpack16<F>(hi[r]);
+      lo[r] = pack16<F>(make_float2(w.x - back.x, w.y - back.y));
+      if (kLoCols && t >= 2) hi[r] = lo[r];
+      hi[r] = transpose8(hi[r]);
+      if (!kLoCols) lo[r] = transpose8(lo[r]);
+    }
+    // --- O^T += V^T P^T
+    if constexpr (F == k4Bit) {
+      const uint8_t* vb = kb[ch] + kRecV + g * 4;
+      const int ta = row_token<F>(2 * t), tb = row_token<F>(2 * t + 1);
+      const uint32_t y0 = *reinterpret_cast<const uint32_t*>(vb + ta * kRowCodes);
+      const uint32_t y1 = *reinterpret_cast<const uint32_t*>(vb + tb * kRowCodes);
+      const uint32_t y2 = *reinterpret_cast<const uint32_t*>(vb + (8 + ta) * kRowCodes);
+      const uint32_t y3 = *reinterpret_cast<const uint32_t*>(vb + (8 + tb) * kRowCodes);
+      // two tokens' codes of one dimension side by side
+      const uint32_t w0[2] = {__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632)};
+      const uint32_t w1[2] = {__byte_perm(y2, y3, 0x5410), __byte_perm(y2, y3, 0x7632)};
+      constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
+      constexpr uint32_t k8 = 0x00080008u, k128 = 0x00800080u;   // 8 and 128 times 2^-24
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t u0 = (i & 1) ? w0[i >> 1] >> 8 : w0[i >> 1];
+        const uint32_t u1 = (i & 1) ? w1[i >> 1] >> 8 : w1[i >> 1];
+        const uint32_t a0 = half2_sub(u0 & kLo, k8), a1 = half2_sub(u0 & kHi, k128);
+        const uint32_t a2 = half2_sub(u1 & kLo, k8), a3 = half2_sub(u1 & kHi, k128);
+        mma_f16(st.acc[i], a0, a1, a2, a3, hi[0], hi[1]);
+        if (!kLoCols) mma_f16(st.acc[i], a0, a1, a2, a3, lo[0], lo[1]);
+      }
+    } else {
+      const uint32_t base = smem_addr(kb[ch] + v_off);
+      const int tok = (lane & 7) + ((lane >> 4) << 3);  // matrices 2 and 3: tokens 8..15
+      uint32_t keep[2] = {kFull, kFull};
+      if (kMasked) {                                    // unseen slots may hold anything
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          keep[r] = (seen(tok0[ch] + 8 * r + 2 * t) ? 0x0000ffffu : 0u) |
+                    (seen(tok0[ch] + 8 * r + 2 * t + 1) ? 0xffff0000u : 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t a[4];
+        ldsm4_t(a, base + tok * 128 + (((2 * i + ((lane >> 3) & 1)) ^ (tok & 7)) << 4));
+        if (kMasked) {
+          a[0] &= keep[0];
+          a[1] &= keep[0];
+          a[2] &= keep[1];
+          a[3] &= keep[1];
+        }
+        mma_bf16(st.acc[i], a[0], a[1], a[2], a[3], hi[0], hi[1]);
+        if (!kLoCols) mma_bf16(st.acc[i], a[0], a[1], a[2], a[3], lo[0], lo[1]);
+      }
+    }
+  }
+}
+
+// Ends a segment.  Sums the lanes' shares; with several warps a head, the
+// others hand (m, l, o) to warp 0 of the head, which stores the output or the
+// record.  False: a bounded wait ran out.
+template <int F, bool kLoCols>
+__device__ bool finish(State& st, const Params& p, uint8_t* smem, const Layout& L, int h, int w,
+                       int seg, int seq, int record) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint64_t* cfull = reinterpret_cast<uint64_t*>(smem + L.bars) + 2 * p.stages;
+  uint64_t* cempty = cfull + p.hpc;
+  float* comb = reinterpret_cast<float*>(smem + L.comb);
+  const int G = p.group;
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    st.l.x += __shfl_xor_sync(kFull, st.l.x, o);
+    st.l.y += __shfl_xor_sync(kFull, st.l.y, o);
+    if (F == k4Bit) {
+      st.zs.x += __shfl_xor_sync(kFull, st.zs.x, o);
+      st.zs.y += __shfl_xor_sync(kFull, st.zs.y, o);
+    }
+  }
+  float o[2][8];       // [column][2 i + half]: dimension out_dim(g, i, half)
+  const float f0 = F == k4Bit ? 16777216.f / st.vs : 1.f;
+  const float f1 = F == k4Bit ? f0 * 0.0625f : 1.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (kLoCols) st.acc[i][k] += __shfl_xor_sync(kFull, st.acc[i][k], 2);
+    o[0][2 * i] = fmaf(st.acc[i][0], f0, F == k4Bit ? st.zs.x : 0.f);
+    o[1][2 * i] = fmaf(st.acc[i][1], f0, F == k4Bit ? st.zs.y : 0.f);
+    o[0][2 * i + 1] = fmaf(st.acc[i][2], f1, F == k4Bit ? st.zs.x : 0.f);
+    o[1][2 * i + 1] = fmaf(st.acc[i][3], f1, F == k4Bit ? st.zs.y : 0.f);
+  }
+  const float m[2] = {st.m.x, st.m.y}, l[2] = {st.l.x, st.l.y};
+  if (w > 0) {
+    if (seg > 0 && !mbar_wait(&cempty[h], (seg - 1) & 1)) return false;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int hg = 2 * t + j;
+      if (hg >= G || (kLoCols && t >= 2)) continue;
+      float* dst = comb + (((w - 1) * p.hpc + h) * G + hg) * kCombPitch;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dst[out_dim<F>(g, i >> 1, i & 1)] = o[j][i];
+      if (g == 0) {
+        dst[64] = m[j];
+        dst[65] = l[j];
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&cfull[h]);
+    return true;
+  }
+  if (p.wph > 1 && !mbar_wait(&cfull[h], seg & 1)) return false;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int hg = 2 * t + j;
+    if (hg >= G || (kLoCols && t >= 2)) continue;
+    float mm = m[j], ll = l[j];
+    for (int i = 1; i < p.wph; ++i) {
+      const float* src = comb + (((i - 1) * p.hpc + h) * G + hg) * kCombPitch;
+      const float mi = src[64];
+      const float li = src[65];
+      if (mi == -INFINITY && li == 0.f) continue;   // it had no chunk of the segment
+      const float mn = fmaxf(mm, mi);
+      const float fa = weight_of(mm, mn), fb = weight_of(mi, mn);
+      mm = mn;
+      ll = ll * fa + li * fb;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        o[j][k] = o[j][k] * fa + src[out_dim<F>(g, k >> 1, k & 1)] * fb;
+    }
+    const float sc = record < 0 ? 1.0f / ll : 1.0f;
+    const long long row =
+        static_cast<long long>(record < 0 ? seq : record) * p.hq + (blockIdx.z * p.hpc + h) * G + hg;
+    float* dst = (record < 0 ? p.out : p.ws_acc) + row * kD;
+    if constexpr (F == k4Bit) {
+      float4* d4 = reinterpret_cast<float4*>(dst + 8 * g);
+      d4[0] = make_float4(o[j][0] * sc, o[j][1] * sc, o[j][2] * sc, o[j][3] * sc);
+      d4[1] = make_float4(o[j][4] * sc, o[j][5] * sc, o[j][6] * sc, o[j][7] * sc);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dst[out_dim<F>(g, k >> 1, k & 1)] = o[j][k] * sc;
+    }
+    if (record >= 0 && g == 0) {
+      p.ws_m[row] = mm;
+      p.ws_l[row] = ll;
+    }
+  }
+  __syncwarp();
+  if (p.wph > 1 && lane == 0) mbar_arrive(&cempty[h]);
+  return true;
+}
+
+template <int F, bool kLoCols>
+__device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int h = warp % p.hpc, w = warp / p.hpc;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars);
+  uint64_t* empty = full + p.stages;
+  const StageMeta* meta = reinterpret_cast<const StageMeta*>(smem + L.meta);
+  constexpr int NC = chunks_per_warp<F>();
+  const uint32_t tile = F == k4Bit ? kRecBytes : kBf16Tile;
+
+  State st;
+  int seg = 0, stage = 0;
+  uint32_t ph = 0;
+  for (;;) {
+    if (!mbar_wait(&full[stage], ph)) {
+      if (lane == 0) report(p.status, kDevTimeout);
+      return;
+    }
+    const StageMeta md = meta[stage];
+    if (md.flags & kTerminate) return;
+    const uint8_t* base = smem + static_cast<size_t>(stage) * p.stage_bytes;
+    if (md.flags & kSegFirst) {
+      load_q<F, kLoCols>(st, p, base + p.kv_bytes + h * p.group * (kD * 2));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) st.acc[i][k] = 0.f;
+      st.m = make_float2(-INFINITY, -INFINITY);
+      st.l = st.zs = make_float2(0.f, 0.f);
+      st.vs = 0.f;
+    }
+    const int first = p.window > 0 && md.ctx > p.window ? md.ctx - p.window : 0;
+    auto token_of = [&](int j) {
+      const int v = md.v0 + j;
+      return (v < md.ns ? v : v + md.delta) * kChunk;
+    };
+    auto whole = [&](int tok) {
+      return tok + kChunk <= md.ctx && (tok >= first || tok + kChunk <= p.sinks);
+    };
+    const uint32_t v_off = p.kv_bytes / 2;
+    int j = w;
+    if constexpr (NC == 2) {
+      if (j + p.wph < md.n) {
+        const uint8_t* kb[2] = {base + (j * p.hpc + h) * tile, base + ((j + p.wph) * p.hpc + h) * tile};
+        const int tok[2] = {token_of(j), token_of(j + p.wph)};
+        if (whole(tok[0]) && whole(tok[1]))
+          process<F, kLoCols, 2, false>(st, p, kb, v_off, tok, md.ctx);
+        else
+          process<F, kLoCols, 2, true>(st, p, kb, v_off, tok, md.ctx);
+        j = md.n;
+      }
+    }
+    if (j < md.n) {
+      const uint8_t* kb[1] = {base + (j * p.hpc + h) * tile};
+      const int tok[1] = {token_of(j)};
+      if (whole(tok[0]))
+        process<F, kLoCols, 1, false>(st, p, kb, v_off, tok, md.ctx);
+      else
+        process<F, kLoCols, 1, true>(st, p, kb, v_off, tok, md.ctx);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[stage]);
+    if (md.flags & kSegLast) {
+      if (!finish<F, kLoCols>(st, p, smem, L, h, w, seg, md.seq, md.record)) {
+        if (lane == 0) report(p.status, kDevTimeout);
+        return;
+      }
+      ++seg;
+    }
+    if (++stage == p.stages) {
+      stage = 0;
+      ph ^= 1;
+    }
+  }
+}
+
+template <int F, bool kLoCols>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  // 128-byte-swizzled tiles repeat every 1024 bytes
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const Layout L = make_layout(p.stages, p.stage_bytes, p.hpc, p.wph, p.group);
+  Schedule* sched = reinterpret_cast<Schedule*>(smem + L.sched);
+  long long* tmp = reinterpret_cast<long long*>(smem + L.sched + 64);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int consumers = p.hpc * p.wph;
+  if (tid == 0) {
+    uint64_t* b = reinterpret_cast<uint64_t*>(smem + L.bars);
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&b[i], 1);
+      mbar_init(&b[p.stages + i], consumers);
+    }
+    for (int i = 0; i < p.hpc; ++i) {
+      mbar_init(&b[2 * p.stages + i], p.wph > 1 ? p.wph - 1 : 1);
+      mbar_init(&b[2 * p.stages + p.hpc + i], 1);
+    }
+    fence_barrier_init();
+  }
+  grid_dependency_wait();        // inputs may come from the preceding kernel
+  grid_dependents_launch();
+  make_schedule(p, sched, tmp);
+  __syncthreads();
+  const Schedule sc = *sched;
+  if (warp == consumers) {
+    producer<F>(p, sc, smem, L, &tm_k, &tm_v);
+  } else {
+    // empty contexts have no chunk and so no segment: zero rows, dealt out
+    const int n = p.hpc * p.group * kD;
+    for (int s = blockIdx.x; s < p.num_seqs; s += p.ctas) {
+      if (p.context_lens[s] > 0) continue;
+      float* dst = p.out + (static_cast<long long>(s) * p.hq + blockIdx.z * p.hpc * p.group) * kD;
+      for (int i = tid; i < n; i += consumers * 32) dst[i] = 0.f;
+    }
+    consumer<F, kLoCols>(p, smem, L);
+  }
+}
+
+// --------------------------------------------------------------------- merge
+
+constexpr int kMergeHeads = 4;
+constexpr int kMergeParts = 4;
+constexpr int kMergeBatch = 16;
+
+// The records of the split sequence that starts in CTA blockIdx.x, if there
+// is one: its own, and the first record of every CTA up to the sequence's
+// last.  Four warps a head take a quarter of them each, 16 records' loads in
+// flight:  out = sum_r 2^(m_r - M) acc_r / sum_r 2^(m_r - M) l_r,  M = max m_r.
+__global__ void __launch_bounds__(kMergeHeads * kMergeParts * 32)
+    window_merge_kernel(float* out, const float* ws_m, const float* ws_l, const float* ws_acc,
+                        const int4* ws_split, const long long* ws_total, int hq, int ctas) {
+  __shared__ float pm[kMergeParts][kMergeHeads], pl[kMergeParts][kMergeHeads];
+  __shared__ float po[kMergeParts][kMergeHeads][kD];
+  grid_dependency_wait();
+  const int4 sp = ws_split[blockIdx.x];
+  if (sp.x < 0) return;
+  const long long total = *ws_total;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int hw = warp % kMergeHeads, part = warp / kMergeHeads;
+  const int h = blockIdx.y * kMergeHeads + hw;
+  const bool live = h < hq;
+  const int c0 = blockIdx.x, n = sp.z - c0 + 1;
+  const int k_lo = n * part / kMergeParts, k_hi = n * (part + 1) / kMergeParts;
+  float mx = -INFINITY, den = 0.f, o0 = 0.f, o1 = 0.f;
+  for (int k0 = k_lo; live && k0 < k_hi; k0 += kMergeBatch) {
+    float mv[kMergeBatch], lv[kMergeBatch], a0[kMergeBatch], a1[kMergeBatch];
+    float mb = mx;
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const int k = k0 + u;
+      const long long c = c0 + k;
+      // a CTA whose range is empty (fewer chunks than CTAs) wrote no record
+      const bool has = k < k_hi && (k == 0 || total * c / ctas < total * (c + 1) / ctas);
+      mv[u] = -INFINITY;
+      lv[u] = a0[u] = a1[u] = 0.f;
+      if (has) {
+        const long long row = (k == 0 ? sp.y : 2 * c) * hq + h;
+        mv[u] = ws_m[row];
+        lv[u] = ws_l[row];
+        a0[u] = ws_acc[row * kD + lane];
+        a1[u] = ws_acc[row * kD + lane + 32];
+      }
+      mb = fmaxf(mb, mv[u]);
+    }
+    const float f = weight_of(mx, mb);             // nothing summed yet: all zero
+    den *= f;
+    o0 *= f;
+    o1 *= f;
+    mx = mb;
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const float w = weight_of(mv[u], mx);        // no record: all zero
+      den = fmaf(w, lv[u], den);
+      o0 = fmaf(w, a0[u], o0);
+      o1 = fmaf(w, a1[u], o1);
+    }
+  }
+  if (lane == 0) {
+    pm[part][hw] = mx;
+    pl[part][hw] = den;
+  }
+  po[part][hw][lane] = o0;
+  po[part][hw][lane + 32] = o1;
+  __syncthreads();
+  if (part != 0 || !live) return;
+  float mm = -INFINITY;
+  for (int i = 0; i < kMergeParts; ++i) mm = fmaxf(mm, pm[i][hw]);
+  den = o0 = o1 = 0.f;
+  for (int i = 0; i < kMergeParts; ++i) {
+    const float w = weight_of(pm[i][hw], mm);
+    den = fmaf(w, pl[i][hw], den);
+    o0 = fmaf(w, po[i][hw][lane], o0);
+    o1 = fmaf(w, po[i][hw][lane + 32], o1);
+  }
+  const float inv = 1.0f / den;
+  float* dst = out + (static_cast<long long>(sp.x) * hq + h) * kD;
+  dst[lane] = o0 * inv;
+  dst[lane + 32] = o1 * inv;
+}
+
+// --------------------------------------------------------------------- host
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    cudaDriverEntryPointQueryResult q;
+    void* f = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// The bf16 cache as [Hkv][NB * bs tokens][64]: one box is a 16-token chunk of
+// the CTA's heads, in shared memory head after head, 16 swizzled rows each.
+bool cache_map(CUtensorMap* m, const void* base, int hkv, long long tokens, int hpc) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(tokens),
+                              static_cast<cuuint64_t>(hkv)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hkv) * kD * 2, kD * 2};
+  const cuuint32_t box[3] = {kD, kChunk, static_cast<cuuint32_t>(hpc)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int F, bool kLoCols>
+cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, dim3 grid,
+                     uint32_t smem, cudaStream_t stream) {
+  auto kern = window_decode_kernel<F, kLoCols>;
+  static PerDeviceOnce once;
+  cudaError_t e = once.run([&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, grid, dim3((p.hpc * p.wph + 1) * 32), smem, stream, tk, tv, p);
+}
+
+// Warps per KV head: a power of two, up to 16 consumer warps in all.
+int warps_per_head(int hpc) {
+  int w = 1;
+  while (2 * w * hpc <= kMaxWarps) w *= 2;
+  return w;
+}
+
+}  // namespace
+
+int window_heads_per_cta(int num_kv_heads) {
+  for (int h = 8; h > 1; --h)
+    if (num_kv_heads % h == 0) return h;
+  return 1;
+}
+
+// m and l [2 ctas, hq], acc [2 ctas, hq, D], split [ctas], total: each part on
+// a 256-byte boundary
+size_t window_workspace_bytes(int ctas, int num_q_heads) {
+  const size_t rows = 2 * static_cast<size_t>(ctas) * num_q_heads;
+  const size_t a = (rows * 4 + 255) / 256 * 256;
+  return 2 * a + rows * kD * 4 + (static_cast<size_t>(ctas) * 16 + 255) / 256 * 256 + 256;
+}
+
+cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream) {
+  if (a.num_seqs == 0) return cudaSuccess;
+  const bool four = a.kv4 != nullptr;
+  Params p;
+  p.out = a.out;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.kv4 = static_cast<const uint8_t*>(a.kv4);
+  p.block_tables = a.block_tables;
+  p.context_lens = a.context_lens;
+  p.num_seqs = a.num_seqs;
+  p.hq = a.num_q_heads;
+  p.hkv = a.num_kv_heads;
+  p.group = a.num_q_heads / a.num_kv_heads;
+  p.num_blocks = a.num_blocks;
+  p.max_blocks = a.max_blocks_per_seq;
+  p.cpb_log2 = 0;
+  while ((kChunk << p.cpb_log2) < a.block_size) ++p.cpb_log2;
+  p.window = a.window;
+  p.sinks = a.window > 0 ? a.sinks : 0;
+  p.hpc = window_heads_per_cta(a.num_kv_heads);
+  p.wph = warps_per_head(p.hpc);
+  p.cps = p.wph * (four ? chunks_per_warp<k4Bit>() : chunks_per_warp<kBf16>());
+  p.kv_bytes = p.cps * p.hpc * (four ? kRecBytes : 2 * kBf16Tile);
+  p.stage_bytes = align_up(p.kv_bytes + p.hpc * p.group * kD * 2, 1024);
+  const uint32_t fixed = make_layout(0, p.stage_bytes, p.hpc, p.wph, p.group).total + 1024 + 16;
+  int stages = static_cast<int>((kSmemLimit - fixed) / (p.stage_bytes + sizeof(StageMeta) + 16));
+  p.stages = stages > 8 ? 8 : stages;
+  if (p.stages < 2) return cudaErrorInvalidConfiguration;
+  p.scale_log2 = a.scale * kLog2e;
+  p.ctas = a.ctas;
+  p.seg_weight = 2;
+  p.status = a.status;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const size_t rows = 2 * static_cast<size_t>(a.ctas) * a.num_q_heads;
+  const size_t ab = (rows * 4 + 255) / 256 * 256;
+  p.ws_m = reinterpret_cast<float*>(ws);
+  p.ws_l = reinterpret_cast<float*>(ws + ab);
+  p.ws_acc = reinterpret_cast<float*>(ws + 2 * ab);
+  p.ws_split = reinterpret_cast<int4*>(ws + 2 * ab + rows * kD * 4);
+  p.ws_total = reinterpret_cast<long long*>(ws + 2 * ab + rows * kD * 4 +
+                                            (static_cast<size_t>(a.ctas) * 16 + 255) / 256 * 256);
+  CUtensorMap tk = {}, tv = {};
+  if (!four) {
+    const long long tokens = static_cast<long long>(a.num_blocks) * a.block_size;
+    if (!cache_map(&tk, a.k_cache, a.num_kv_heads, tokens, p.hpc) ||
+        !cache_map(&tv, a.v_cache, a.num_kv_heads, tokens, p.hpc))
+      return cudaErrorInvalidValue;
+  }
+  const uint32_t smem = make_layout(p.stages, p.stage_bytes, p.hpc, p.wph, p.group).total + 1024;
+  const dim3 grid(a.ctas, 1, a.num_kv_heads / p.hpc);
+  cudaError_t e;
+  if (four)
+    e = p.group <= 4 ? launch_t<k4Bit, true>(tk, tv, p, grid, smem, stream)
+                     : launch_t<k4Bit, false>(tk, tv, p, grid, smem, stream);
+  else
+    e = p.group <= 4 ? launch_t<kBf16, true>(tk, tv, p, grid, smem, stream)
+                     : launch_t<kBf16, false>(tk, tv, p, grid, smem, stream);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(window_merge_kernel,
+                    dim3(a.ctas, (a.num_q_heads + kMergeHeads - 1) / kMergeHeads),
+                    dim3(kMergeHeads * kMergeParts * 32), 0, stream, a.out, p.ws_m, p.ws_l,
+                    p.ws_acc, p.ws_split, p.ws_total, a.num_q_heads, a.ctas);
+}
+
+}  // namespace tvl
