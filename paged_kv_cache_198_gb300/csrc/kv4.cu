@@ -43,7 +43,7 @@ struct WriteParams {
   uint8_t* cache;
   const int32_t* slots;
   const int32_t* positions;     // null: no rotation
-  int num_tokens, hq, hkv, block_size, parts;
+  int num_tokens, hq, hkv, parts_q;
   long long num_slots;
   uint32_t* status;
 };
@@ -53,19 +53,51 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// A row's eight values of this lane, as four pairs.
+struct Eight {
+  float2 v[4];
+};
+__device__ __forceinline__ Eight widen(uint4 w) {
+  return {{bf16x2_to_float2(w.x), bf16x2_to_float2(w.y), bf16x2_to_float2(w.z),
+           bf16x2_to_float2(w.w)}};
+}
+__device__ __forceinline__ uint4 narrow(const Eight& x) {
+  return make_uint4(pack_bf16(x.v[0].x, x.v[0].y), pack_bf16(x.v[1].x, x.v[1].y),
+                    pack_bf16(x.v[2].x, x.v[2].y), pack_bf16(x.v[3].x, x.v[3].y));
+}
+
+// This lane's share of the rotation: dimensions 8 c .. 8 c + 7 of a row, whose
+// partners (d, d + 32) are lane c ^ 4's; sn carries the sign.
+struct Turn {
+  float2 cs[4], sn[4];
+};
+__device__ __forceinline__ uint4 rotate(uint4 w, const Turn& t) {
+  uint4 o;
+  o.x = __shfl_xor_sync(kFull, w.x, 4);
+  o.y = __shfl_xor_sync(kFull, w.y, 4);
+  o.z = __shfl_xor_sync(kFull, w.z, 4);
+  o.w = __shfl_xor_sync(kFull, w.w, 4);
+  Eight x = widen(w);
+  const Eight y = widen(o);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x.v[j] = __ffma2_rn(x.v[j], t.cs[j], __fmul2_rn(y.v[j], t.sn[j]));
+  return narrow(x);
+}
+
+// blockIdx.y: the token's part -- parts_q of 16 q rows, then 16 K and V rows each.
 __global__ void __launch_bounds__(kWarps * 32)
     kv4_write_kernel(const WriteParams p, const RopeTurns turns) {
   __shared__ float2 trig[kWarps][kD / 2];
   grid_dependency_wait();
   grid_dependents_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long id = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  const long long t = id / p.parts;
+  const long long t = static_cast<long long>(blockIdx.x) * kWarps + warp;
   if (t >= p.num_tokens) return;
-  const int row0 = static_cast<int>(id - t * p.parts) * kRowsPerWarp + (lane >> 3);
   const int c = lane & 7;
-  const int rows = p.hq + 2 * p.hkv;
   constexpr int kIt = kRowsPerWarp / 4;
+  const bool is_q = static_cast<int>(blockIdx.y) < p.parts_q;
+  const int row0 = (blockIdx.y - (is_q ? 0 : p.parts_q)) * kRowsPerWarp + (lane >> 3);
+  const int rows = is_q ? p.hq : 2 * p.hkv;
 
   uint4 w[kIt];
 #pragma unroll
@@ -73,76 +105,65 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int r = row0 + 4 * i;
     w[i] = make_uint4(0, 0, 0, 0);
     if (r < rows) {
-      const __nv_bfloat16* src = r < p.hq            ? p.q + (t * p.hq + r) * kD
-                                 : r < p.hq + p.hkv ? p.k_new + (t * p.hkv + r - p.hq) * kD
-                                                     : p.v_new + (t * p.hkv + r - p.hq - p.hkv) * kD;
+      const __nv_bfloat16* src = is_q        ? p.q + (t * p.hq + r) * kD
+                                 : r < p.hkv ? p.k_new + (t * p.hkv + r) * kD
+                                             : p.v_new + (t * p.hkv + r - p.hkv) * kD;
       w[i] = __ldcs(reinterpret_cast<const uint4*>(src) + c);
     }
   }
-  const long long slot = p.slots[t];
+  Turn turn;
   if (p.positions != nullptr) {
-    // lane i: pair i's angle in (-1/2, 1/2] turns, then its sine and cosine
+    // lane i: pair i's angle in [-1/2, 1/2) turns, then its sine and cosine
     const unsigned long long a =
         static_cast<unsigned long long>(static_cast<long long>(p.positions[t])) * turns.f[lane];
     float sn, cs;
     sincospif(__ll2float_rn(static_cast<long long>(a)) * 1.0842021724855044e-19f, &sn, &cs);  // 2^-63
     trig[warp][lane] = make_float2(cs, sn);
     __syncwarp();
+    const float4* tr = reinterpret_cast<const float4*>(&trig[warp][8 * (c & 3)]);
+    const float sign = c < 4 ? -1.f : 1.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 f = tr[j];
+      turn.cs[j] = make_float2(f.x, f.z);
+      turn.sn[j] = make_float2(f.y * sign, f.w * sign);
+    }
   }
-  const bool store = slot >= 0 && slot < p.num_slots;
-  if (slot >= p.num_slots && lane == 0) report(p.status, TVL_DEV_BAD_SLOT);
+  if (is_q) {
+#pragma unroll
+    for (int i = 0; i < kIt; ++i) {
+      const int r = row0 + 4 * i;
+      const uint4 y = rotate(w[i], turn);
+      if (r < rows) reinterpret_cast<uint4*>(p.q + (t * p.hq + r) * kD)[c] = y;
+    }
+    return;
+  }
+  const long long slot = p.slots[t];
+  if (slot < 0) return;
+  if (slot >= p.num_slots) {
+    if (lane == 0) report(p.status, TVL_DEV_BAD_SLOT);
+    return;
+  }
   // records of the token's 16-token group, one a head; its place in them
   const int tok = static_cast<int>(slot & (kRecTokens - 1));
-  uint8_t* group = p.cache + (store ? slot / kRecTokens : 0) * p.hkv * kRecBytes;
-
+  uint8_t* group = p.cache + slot / kRecTokens * p.hkv * kRecBytes;
 #pragma unroll
   for (int i = 0; i < kIt; ++i) {
     const int r = row0 + 4 * i;
-    float x[8];
-    {
-      const float2 f0 = bf16x2_to_float2(w[i].x), f1 = bf16x2_to_float2(w[i].y);
-      const float2 f2 = bf16x2_to_float2(w[i].z), f3 = bf16x2_to_float2(w[i].w);
-      x[0] = f0.x; x[1] = f0.y; x[2] = f1.x; x[3] = f1.y;
-      x[4] = f2.x; x[5] = f2.y; x[6] = f3.x; x[7] = f3.y;
-    }
+    const bool is_v = r >= p.hkv;
     if (p.positions != nullptr) {
-      // lane c's partner in the pairs (d, d + 32) is lane c ^ 4
-      uint4 o;
-      o.x = __shfl_xor_sync(kFull, w[i].x, 4);
-      o.y = __shfl_xor_sync(kFull, w[i].y, 4);
-      o.z = __shfl_xor_sync(kFull, w[i].z, 4);
-      o.w = __shfl_xor_sync(kFull, w[i].w, 4);
-      if (r < p.hq + p.hkv) {
-        const float sign = c < 4 ? -1.f : 1.f;
-        const float2 f[4] = {bf16x2_to_float2(o.x), bf16x2_to_float2(o.y), bf16x2_to_float2(o.z),
-                             bf16x2_to_float2(o.w)};
-        const float2* tr = &trig[warp][8 * (c & 3)];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 cs = tr[j];
-          const float other = (j & 1) ? f[j >> 1].y : f[j >> 1].x;
-          x[j] = fmaf(x[j], cs.x, sign * (other * cs.y));
-        }
-        uint4 y;
-        y.x = pack_bf16(x[0], x[1]);
-        y.y = pack_bf16(x[2], x[3]);
-        y.z = pack_bf16(x[4], x[5]);
-        y.w = pack_bf16(x[6], x[7]);
-        if (r < p.hq) reinterpret_cast<uint4*>(p.q + (t * p.hq + r) * kD)[c] = y;
-        // the K that is quantised is the bf16 row the bf16 cache would hold
-        const float2 g0 = bf16x2_to_float2(y.x), g1 = bf16x2_to_float2(y.y);
-        const float2 g2 = bf16x2_to_float2(y.z), g3 = bf16x2_to_float2(y.w);
-        x[0] = g0.x; x[1] = g0.y; x[2] = g1.x; x[3] = g1.y;
-        x[4] = g2.x; x[5] = g2.y; x[6] = g3.x; x[7] = g3.y;
-      }
+      // the K that is quantised is the bf16 row the bf16 cache would hold
+      const uint4 y = rotate(w[i], turn);
+      if (!is_v) w[i] = y;
     }
-    float mn = x[0], mx = x[0];
-    bool bad = false;
+    const Eight e = widen(w[i]);
+    const float x[8] = {e.v[0].x, e.v[0].y, e.v[1].x, e.v[1].y, e.v[2].x, e.v[2].y, e.v[3].x, e.v[3].y};
+    float mn = x[0], mx = x[0], fin = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       mn = fminf(mn, x[j]);
       mx = fmaxf(mx, x[j]);
-      bad |= !(fabsf(x[j]) < INFINITY);
+      fin = fmaf(x[j], 0.f, fin);              // 0 unless something is not finite
     }
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
@@ -150,9 +171,9 @@ __global__ void __launch_bounds__(kWarps * 32)
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
     }
     const float range = mx - mn;
-    bad |= !(range < INFINITY);
+    const bool bad = !(range < INFINITY) || fin != 0.f;      // NaN != 0
     const bool row_bad = ((__ballot_sync(kFull, bad) >> (lane & 24)) & 0xffu) != 0;
-    if (!store || r < p.hq || r >= rows) continue;
+    if (r >= rows) continue;
     uint32_t code = 0;
     uint32_t sz = 0x7fc07fc0u;          // a row that is not finite stands for NaN
     if (!row_bad) {
@@ -169,8 +190,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     } else if (c == 0) {
       report(p.status, TVL_DEV_NONFINITE);
     }
-    const bool is_v = r >= p.hq + p.hkv;
-    uint8_t* rec = group + (r - p.hq - (is_v ? p.hkv : 0)) * kRecBytes;
+    uint8_t* rec = group + (r - (is_v ? p.hkv : 0)) * kRecBytes;
     reinterpret_cast<uint32_t*>(rec + (is_v ? kRecV : 0) + tok * kRowCodes)[c] = code;
     if (c == 0) reinterpret_cast<uint32_t*>(rec + (is_v ? kRecVMeta : kRecKMeta))[tok] = sz;
   }
@@ -248,13 +268,12 @@ cudaError_t launch_kv4_write(const Kv4WriteArgs& a, cudaStream_t stream) {
   p.num_tokens = a.num_tokens;
   p.hq = a.q && a.positions ? a.num_q_heads : 0;
   p.hkv = a.num_kv_heads;
-  p.block_size = a.block_size;
-  p.parts = (p.hq + 2 * p.hkv + kRowsPerWarp - 1) / kRowsPerWarp;
+  p.parts_q = (p.hq + kRowsPerWarp - 1) / kRowsPerWarp;
+  const int parts_kv = (2 * p.hkv + kRowsPerWarp - 1) / kRowsPerWarp;
   p.num_slots = a.num_slots;
   p.status = a.status;
-  const long long warps = static_cast<long long>(a.num_tokens) * p.parts;
   static const RopeTurns none = {};
-  return launch_pdl(kv4_write_kernel, dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps)),
+  return launch_pdl(kv4_write_kernel, dim3((a.num_tokens + kWarps - 1) / kWarps, p.parts_q + parts_kv),
                     dim3(kWarps * 32), 0, stream, p,
                     a.positions ? rope_turns(a.rope_theta) : none);
 }

@@ -72,7 +72,7 @@ constexpr uint32_t kSmemLimit = 227 * 1024;
 constexpr int kCombPitch = 72;                // floats a head of a warp hands over: 64 + m, l
 
 enum Format : int { kBf16 = 0, k4Bit = 1 };
-enum : int { kSegFirst = 1, kSegLast = 2, kTerminate = 4 };
+enum : int { kSegFirst = 1, kSegLast = 2, kTerminate = 4, kPartial = 8 };
 
 // chunks a warp takes from a stage at once (independent work in flight)
 template <int F>
@@ -99,7 +99,9 @@ struct Params {
   float* ws_m;           // records [2 * ctas][hq]
   float* ws_l;
   float* ws_acc;
-  int4* ws_split;        // per CTA: the split sequence it starts (seq or -1, first record, last CTA)
+  int4* ws_split;        // split sequences: (seq or -1, first record, first CTA, last CTA); entry
+                         // per sequence, or per CTA that holds the first chunk when there are
+                         // more sequences than CTAs
   long long* ws_total;   // length of the cost line
   uint32_t* status;
 };
@@ -238,7 +240,7 @@ __device__ void make_schedule(const Params& p, Schedule* sc, long long* tmp) {
 // ------------------------------------------------------------------ producer
 
 struct Segment {
-  int s, v, e, ctx, ns, delta, n, record;
+  int s, v, e, ctx, ns, delta, n, record, window;
 };
 
 template <int F>
@@ -294,6 +296,7 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
       g.ns = vis.ns;
       g.delta = vis.delta;
       g.n = vis.n;
+      g.window = p.window > 0 ? min(p.window, g.ctx) : g.ctx;
       g.record = v == 0 && g.e == vis.n ? -1 : 2 * cta + (first ? 0 : 1);
       return true;
     }
@@ -306,6 +309,7 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
     return p.block_tables[static_cast<long long>(g.s) * p.max_blocks + (c >> p.cpb_log2)];
   };
 
+  const bool by_seq = p.num_seqs <= p.ctas && blockIdx.z == 0;
   int4 split = make_int4(-1, 0, 0, 0);
   Segment g;
   bool have = find(sc.seq0, sc.v0, true, g);
@@ -315,8 +319,10 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
       // a split sequence's first piece: it ends at this CTA's end of the
       // line, and the sequence's last chunk lies g.n - g.e - 1 places on
       const long long x = sc.hi + (g.n - g.e) - 1;
-      split = make_int4(g.s, g.record, static_cast<int>(((x + 1) * p.ctas - 1) / sc.total), 0);
+      split = make_int4(g.s, g.record, cta, static_cast<int>(((x + 1) * p.ctas - 1) / sc.total));
     }
+    if (by_seq && g.v == 0 && lane == 0)
+      p.ws_split[g.s] = g.e < g.n ? split : make_int4(-1, 0, 0, 0);
     Segment nx;
     const bool have_next = find(g.s, g.e, false, nx);
     for (int vb = g.v; vb < g.e && ok; vb += 32) {
@@ -328,11 +334,18 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
         if (!acquire()) break;
         uint8_t* base = smem + static_cast<size_t>(st) * p.stage_bytes;
         const bool first = v == g.v;
+        const int vv = v + lane;
+        const int c = vv < g.ns ? vv : vv + g.delta;
+        const bool whole = c * kChunk + kChunk <= g.ctx &&
+                           (c * kChunk >= g.ctx - g.window || c * kChunk + kChunk <= p.sinks);
+        const bool all = __all_sync(kFull, lane >= n || whole);
+        int page = __shfl_sync(kFull, tbl, (v - vb + lane) & 31);
         if (lane == 0) {
           StageMeta m;
           m.seq = g.s;
           m.record = g.record;
-          m.flags = (first ? kSegFirst : 0) | (v + n == g.e ? kSegLast : 0);
+          m.flags = (first ? kSegFirst : 0) | (v + n == g.e ? kSegLast : 0) |
+                    (all && n == p.cps ? 0 : kPartial);
           m.n = n;
           m.v0 = v;
           m.ns = g.ns;
@@ -341,14 +354,12 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
           meta[st] = m;
           mbar_arrive_expect_tx(&full[st], n * chunk_bytes + (first ? q_bytes : 0));
         }
-        int page = __shfl_sync(kFull, tbl, (v - vb + lane) & 31);   // orders lane 0's arrive, too
+        __syncwarp();
         if (lane < n) {
           if (page < 0 || page >= p.num_blocks) {
             report(p.status, TVL_DEV_BAD_BLOCK_ID);
             page = 0;
           }
-          const int vv = v + lane;
-          const int c = vv < g.ns ? vv : vv + g.delta;
           const int sub = c & ((1 << p.cpb_log2) - 1);
           const long long chunk = (static_cast<long long>(page) << p.cpb_log2) + sub;
           if (F == k4Bit) {
@@ -373,7 +384,7 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
     have = have_next;
   }
   if (blockIdx.z == 0 && lane == 0) {
-    p.ws_split[cta] = split;
+    if (!by_seq) p.ws_split[cta] = split;
     if (cta == 0) *p.ws_total = sc.total;
   }
   if (ok && acquire()) {
@@ -413,6 +424,24 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the same with a zero accumulator in
+__device__ __forceinline__ void mma_f16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                           uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ float2 add2(float a0, float a1, float b0, float b1) {
+  return __fadd2_rn(make_float2(a0, a1), make_float2(b0, b1));
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -431,9 +460,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
+// 2 a + b on fp16 pairs
+__device__ __forceinline__ uint32_t half2_twice_plus(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(0x40004000u), "r"(b));
   return d;
 }
 __device__ __forceinline__ float2 meta_sz(uint32_t w) { return bf16x2_to_float2(w); }
@@ -540,14 +570,14 @@ __device__ __forceinline__ void process(State& st, const Params& p, const uint8_
   float2 x[NCH][2];
 #pragma unroll
   for (int ch = 0; ch < NCH; ++ch) {
-    float c[4] = {0.f, 0.f, 0.f, 0.f};
+    float c[4];
     if constexpr (F == k4Bit) {
       const uint2 a = *reinterpret_cast<const uint2*>(kb[ch] + r0 * kRowCodes + t * 8);
       const uint2 b = *reinterpret_cast<const uint2*>(kb[ch] + r1 * kRowCodes + t * 8);
       const float2 m0 = meta_sz(*reinterpret_cast<const uint32_t*>(kb[ch] + kRecKMeta + r0 * 4));
       const float2 m1 = meta_sz(*reinterpret_cast<const uint32_t*>(kb[ch] + kRecKMeta + r1 * 4));
       constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
-      mma_f16(c, a.x & kLo, b.x & kLo, a.x & kHi, b.x & kHi, st.qf[0][0], st.qf[0][1]);
+      mma_f16_0(c, a.x & kLo, b.x & kLo, a.x & kHi, b.x & kHi, st.qf[0][0], st.qf[0][1]);
       mma_f16(c, (a.x >> 8) & kLo, (b.x >> 8) & kLo, (a.x >> 8) & kHi, (b.x >> 8) & kHi,
               st.qf[1][0], st.qf[1][1]);
       mma_f16(c, a.y & kLo, b.y & kLo, a.y & kHi, b.y & kHi, st.qf[2][0], st.qf[2][1]);
@@ -565,7 +595,14 @@ __device__ __forceinline__ void process(State& st, const Params& p, const uint8_
       for (int i = 0; i < 4; ++i) {
         uint32_t a[4];
         ldsm4(a, base + row * 128 + (((2 * i + (lane >> 4)) ^ (row & 7)) << 4));
-        mma_bf16(c, a[0], a[1], a[2], a[3], st.qf[i][0], st.qf[i][1]);
+        // four sums of 16 products, added in fp32 with rounding to nearest: the
+        // tensor core's own accumulation truncates
+        float d[4];
+        mma_bf16_0(i == 0 ? c : d, a[0], a[1], a[2], a[3], st.qf[i][0], st.qf[i][1]);
+        if (i > 0) {
+          const float2 e0 = add2(c[0], c[1], d[0], d[1]), e1 = add2(c[2], c[3], d[2], d[3]);
+          c[0] = e0.x; c[1] = e0.y; c[2] = e1.x; c[3] = e1.y;
+        }
       }
       const float2 sl = make_float2(p.scale_log2, p.scale_log2);
       x[ch][0] = __fmul2_rn(make_float2(c[0], c[1]), sl);
@@ -638,25 +675,31 @@ __device__ __forceinline__ void process(State& st, const Params& p, const uint8_
     }
   }
   const float2 nm = make_float2(-st.m.x, -st.m.y);
+  float sum[4][4];
 #pragma unroll
   for (int ch = 0; ch < NCH; ++ch) {
     // --- weights, as the column operand of P V: rows of the transposed matrix
     // are the heads, its columns the tokens
-    uint32_t hi[2], lo[2];
+    uint32_t hi[2], lo[2], lo2[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const float2 d = __fadd2_rn(x[ch][r], nm);
       float2 w = make_float2(ex2(d.x), ex2(d.y));
       st.l = __fadd2_rn(st.l, w);
       if constexpr (F == k4Bit) {
-        const float zc = fmaf(8.f, mv[ch][r].x, mv[ch][r].y);
+        const float zc = fmaf(7.5f, mv[ch][r].x, mv[ch][r].y);
         st.zs = __ffma2_rn(w, make_float2(zc, zc), st.zs);
         const float sc = mv[ch][r].x * st.vs;
         w = __fmul2_rn(w, make_float2(sc, sc));
       }
       hi[r] = pack16<F>(w);
-      const float2 back = unpack16<F>(hi[r]);
-      lo[r] = pack16<F>(make_float2(w.x - back.x, w.y - back.y));
+      float2 back = unpack16<F>(hi[r]);
+      w = make_float2(w.x - back.x, w.y - back.y);
+      lo[r] = pack16<F>(w);
+      if (F == kBf16) {
+        back = unpack16<F>(lo[r]);
+        lo2[r] = transpose8(pack16<F>(make_float2(w.x - back.x, w.y - back.y)));
+      }
       if (kLoCols && t >= 2) hi[r] = lo[r];
       hi[r] = transpose8(hi[r]);
       if (!kLoCols) lo[r] = transpose8(lo[r]);
@@ -673,15 +716,18 @@ __device__ __forceinline__ void process(State& st, const Params& p, const uint8_
       const uint32_t w0[2] = {__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632)};
       const uint32_t w1[2] = {__byte_perm(y2, y3, 0x5410), __byte_perm(y2, y3, 0x7632)};
       constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
-      constexpr uint32_t k8 = 0x00080008u, k128 = 0x00800080u;   // 8 and 128 times 2^-24
+      constexpr uint32_t k15 = 0x800f800fu, k240 = 0x80f080f0u;   // -15 and -240 times 2^-24
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t u0 = (i & 1) ? w0[i >> 1] >> 8 : w0[i >> 1];
         const uint32_t u1 = (i & 1) ? w1[i >> 1] >> 8 : w1[i >> 1];
-        const uint32_t a0 = half2_sub(u0 & kLo, k8), a1 = half2_sub(u0 & kHi, k128);
-        const uint32_t a2 = half2_sub(u1 & kLo, k8), a3 = half2_sub(u1 & kHi, k128);
-        mma_f16(st.acc[i], a0, a1, a2, a3, hi[0], hi[1]);
-        if (!kLoCols) mma_f16(st.acc[i], a0, a1, a2, a3, lo[0], lo[1]);
+        const uint32_t a0 = half2_twice_plus(u0 & kLo, k15), a1 = half2_twice_plus(u0 & kHi, k240);
+        const uint32_t a2 = half2_twice_plus(u1 & kLo, k15), a3 = half2_twice_plus(u1 & kHi, k240);
+        if (ch == 0)
+          mma_f16_0(sum[i], a0, a1, a2, a3, hi[0], hi[1]);
+        else
+          mma_f16(sum[i], a0, a1, a2, a3, hi[0], hi[1]);
+        if (!kLoCols) mma_f16(sum[i], a0, a1, a2, a3, lo[0], lo[1]);
       }
     } else {
       const uint32_t base = smem_addr(kb[ch] + v_off);
@@ -703,11 +749,25 @@ __device__ __forceinline__ void process(State& st, const Params& p, const uint8_
           a[2] &= keep[1];
           a[3] &= keep[1];
         }
-        mma_bf16(st.acc[i], a[0], a[1], a[2], a[3], hi[0], hi[1]);
-        if (!kLoCols) mma_bf16(st.acc[i], a[0], a[1], a[2], a[3], lo[0], lo[1]);
+        if (ch == 0)
+          mma_bf16_0(sum[i], a[0], a[1], a[2], a[3], hi[0], hi[1]);
+        else
+          mma_bf16(sum[i], a[0], a[1], a[2], a[3], hi[0], hi[1]);
+        if (!kLoCols) mma_bf16(sum[i], a[0], a[1], a[2], a[3], lo[0], lo[1]);
+        mma_bf16(sum[i], a[0], a[1], a[2], a[3], lo2[0], lo2[1]);
       }
     }
   }
+  // The tensor core truncates what it accumulates, which over a long context
+  // would pull the sums towards zero; across chunks they add up here, rounded.
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      const float2 e = add2(st.acc[i][k], st.acc[i][k + 1], sum[i][k], sum[i][k + 1]);
+      st.acc[i][k] = e.x;
+      st.acc[i][k + 1] = e.y;
+    }
 }
 
 // Ends a segment.  Sums the lanes' shares; with several warps a head, the
@@ -731,7 +791,7 @@ __device__ bool finish(State& st, const Params& p, uint8_t* smem, const Layout& 
     }
   }
   float o[2][8];       // [column][2 i + half]: dimension out_dim(g, i, half)
-  const float f0 = F == k4Bit ? 16777216.f / st.vs : 1.f;
+  const float f0 = F == k4Bit ? 8388608.f / st.vs : 1.f;
   const float f1 = F == k4Bit ? f0 * 0.0625f : 1.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -823,6 +883,7 @@ __device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
     }
     const StageMeta md = meta[stage];
     if (md.flags & kTerminate) return;
+    const uint32_t v_off = p.kv_bytes / 2;
     const uint8_t* base = smem + static_cast<size_t>(stage) * p.stage_bytes;
     if (md.flags & kSegFirst) {
       load_q<F, kLoCols>(st, p, base + p.kv_bytes + h * p.group * (kD * 2));
@@ -834,34 +895,26 @@ __device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
       st.l = st.zs = make_float2(0.f, 0.f);
       st.vs = 0.f;
     }
-    const int first = p.window > 0 && md.ctx > p.window ? md.ctx - p.window : 0;
-    auto token_of = [&](int j) {
-      const int v = md.v0 + j;
-      return (v < md.ns ? v : v + md.delta) * kChunk;
-    };
-    auto whole = [&](int tok) {
-      return tok + kChunk <= md.ctx && (tok >= first || tok + kChunk <= p.sinks);
-    };
-    const uint32_t v_off = p.kv_bytes / 2;
-    int j = w;
-    if constexpr (NC == 2) {
-      if (j + p.wph < md.n) {
-        const uint8_t* kb[2] = {base + (j * p.hpc + h) * tile, base + ((j + p.wph) * p.hpc + h) * tile};
-        const int tok[2] = {token_of(j), token_of(j + p.wph)};
-        if (whole(tok[0]) && whole(tok[1]))
-          process<F, kLoCols, 2, false>(st, p, kb, v_off, tok, md.ctx);
-        else
-          process<F, kLoCols, 2, true>(st, p, kb, v_off, tok, md.ctx);
-        j = md.n;
+    const uint8_t* kb0 = base + (w * p.hpc + h) * tile;      // the warp's first chunk
+    const uint32_t step = p.wph * p.hpc * tile;              // to its next
+    if (!(md.flags & kPartial)) {
+      const uint8_t* kb[NC];
+      int tok[NC];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        kb[i] = kb0 + i * step;
+        tok[i] = 0;
       }
-    }
-    if (j < md.n) {
-      const uint8_t* kb[1] = {base + (j * p.hpc + h) * tile};
-      const int tok[1] = {token_of(j)};
-      if (whole(tok[0]))
-        process<F, kLoCols, 1, false>(st, p, kb, v_off, tok, md.ctx);
-      else
+      process<F, kLoCols, NC, false>(st, p, kb, v_off, tok, md.ctx);
+    } else {
+      // a short stage, or one with slots that are not visible
+      for (int j = w; j < md.n; j += p.wph) {
+        const int v = md.v0 + j;
+        const uint8_t* kb[1] = {kb0};
+        const int tok[1] = {(v < md.ns ? v : v + md.delta) * kChunk};
         process<F, kLoCols, 1, true>(st, p, kb, v_off, tok, md.ctx);
+        kb0 += step;
+      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[stage]);
@@ -916,6 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = p.hpc * p.group * kD;
     for (int s = blockIdx.x; s < p.num_seqs; s += p.ctas) {
       if (p.context_lens[s] > 0) continue;
+      if (tid == 0 && blockIdx.z == 0 && p.num_seqs <= p.ctas) p.ws_split[s] = make_int4(-1, 0, 0, 0);
       float* dst = p.out + (static_cast<long long>(s) * p.hq + blockIdx.z * p.hpc * p.group) * kD;
       for (int i = tid; i < n; i += consumers * 32) dst[i] = 0.f;
     }
@@ -925,43 +979,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // --------------------------------------------------------------------- merge
 
-constexpr int kMergeHeads = 4;
-constexpr int kMergeParts = 4;
-constexpr int kMergeBatch = 16;
+constexpr int kMergeWarps = 16;
+constexpr int kMergeBatch = 8;
 
-// The records of the split sequence that starts in CTA blockIdx.x, if there
-// is one: its own, and the first record of every CTA up to the sequence's
-// last.  Four warps a head take a quarter of them each, 16 records' loads in
-// flight:  out = sum_r 2^(m_r - M) acc_r / sum_r 2^(m_r - M) l_r,  M = max m_r.
-__global__ void __launch_bounds__(kMergeHeads * kMergeParts * 32)
+// Entry blockIdx.x of the list of split sequences: the sequence's record in
+// its first CTA, and the first record of every CTA up to its last.  `parts`
+// warps a head take a share of them each, 8 records' loads in flight:
+//   out = sum_r 2^(m_r - M) acc_r / sum_r 2^(m_r - M) l_r,  M = max m_r.
+// 64 registers: two full CTAs an SM, so a batch of many short merges is
+// resident at once.
+__global__ void __launch_bounds__(kMergeWarps * 32, 2)
     window_merge_kernel(float* out, const float* ws_m, const float* ws_l, const float* ws_acc,
-                        const int4* ws_split, const long long* ws_total, int hq, int ctas) {
-  __shared__ float pm[kMergeParts][kMergeHeads], pl[kMergeParts][kMergeHeads];
-  __shared__ float po[kMergeParts][kMergeHeads][kD];
+                        const int4* ws_split, const long long* ws_total, int hq, int ctas,
+                        int parts) {
+  __shared__ float pm[kMergeWarps], pl[kMergeWarps], po[kMergeWarps][kD];
   grid_dependency_wait();
   const int4 sp = ws_split[blockIdx.x];
   if (sp.x < 0) return;
   const long long total = *ws_total;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int hw = warp % kMergeHeads, part = warp / kMergeHeads;
-  const int h = blockIdx.y * kMergeHeads + hw;
+  const int heads = static_cast<int>(blockDim.x) / (32 * parts);
+  const int hw = warp / parts, part = warp - hw * parts;
+  const int h = blockIdx.y * heads + hw;
   const bool live = h < hq;
-  const int c0 = blockIdx.x, n = sp.z - c0 + 1;
-  const int k_lo = n * part / kMergeParts, k_hi = n * (part + 1) / kMergeParts;
+  const int c0 = sp.z, n = sp.w - c0 + 1;
+  const bool dense = total >= ctas;         // every CTA holds chunks
+  const int few = static_cast<int>(total);  // used when total < ctas
   float mx = -INFINITY, den = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int k0 = k_lo; live && k0 < k_hi; k0 += kMergeBatch) {
+  for (int k0 = part * kMergeBatch; live && k0 < n; k0 += parts * kMergeBatch) {
     float mv[kMergeBatch], lv[kMergeBatch], a0[kMergeBatch], a1[kMergeBatch];
     float mb = mx;
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const int k = k0 + u;
-      const long long c = c0 + k;
+      const int k = k0 + u, c = c0 + k;
       // a CTA whose range is empty (fewer chunks than CTAs) wrote no record
-      const bool has = k < k_hi && (k == 0 || total * c / ctas < total * (c + 1) / ctas);
+      const bool has = k < n && (k == 0 || dense || few * c / ctas < few * (c + 1) / ctas);
       mv[u] = -INFINITY;
       lv[u] = a0[u] = a1[u] = 0.f;
       if (has) {
-        const long long row = (k == 0 ? sp.y : 2 * c) * hq + h;
+        const long long row = static_cast<long long>(k == 0 ? sp.y : 2 * c) * hq + h;
         mv[u] = ws_m[row];
         lv[u] = ws_l[row];
         a0[u] = ws_acc[row * kD + lane];
@@ -982,23 +1038,26 @@ __global__ void __launch_bounds__(kMergeHeads * kMergeParts * 32)
       o1 = fmaf(w, a1[u], o1);
     }
   }
-  if (lane == 0) {
-    pm[part][hw] = mx;
-    pl[part][hw] = den;
+  if (parts > 1) {
+    if (lane == 0) {
+      pm[warp] = mx;
+      pl[warp] = den;
+    }
+    po[warp][lane] = o0;
+    po[warp][lane + 32] = o1;
+    __syncthreads();
+    if (part != 0) return;
+    mx = -INFINITY;
+    for (int i = 0; i < parts; ++i) mx = fmaxf(mx, pm[warp + i]);
+    den = o0 = o1 = 0.f;
+    for (int i = 0; i < parts; ++i) {
+      const float w = weight_of(pm[warp + i], mx);
+      den = fmaf(w, pl[warp + i], den);
+      o0 = fmaf(w, po[warp + i][lane], o0);
+      o1 = fmaf(w, po[warp + i][lane + 32], o1);
+    }
   }
-  po[part][hw][lane] = o0;
-  po[part][hw][lane + 32] = o1;
-  __syncthreads();
-  if (part != 0 || !live) return;
-  float mm = -INFINITY;
-  for (int i = 0; i < kMergeParts; ++i) mm = fmaxf(mm, pm[i][hw]);
-  den = o0 = o1 = 0.f;
-  for (int i = 0; i < kMergeParts; ++i) {
-    const float w = weight_of(pm[i][hw], mm);
-    den = fmaf(w, pl[i][hw], den);
-    o0 = fmaf(w, po[i][hw][lane], o0);
-    o1 = fmaf(w, po[i][hw][lane + 32], o1);
-  }
+  if (!live) return;
   const float inv = 1.0f / den;
   float* dst = out + (static_cast<long long>(sp.x) * hq + h) * kD;
   dst[lane] = o0 * inv;
@@ -1129,10 +1188,16 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
     e = p.group <= 4 ? launch_t<kBf16, true>(tk, tv, p, grid, smem, stream)
                      : launch_t<kBf16, false>(tk, tv, p, grid, smem, stream);
   if (e != cudaSuccess) return e;
+  // a sequence has about 1 + ctas / num_seqs records: one warp a head and
+  // batch of 8, up to 16
+  int parts = 1;
+  while (parts < kMergeWarps && parts * kMergeBatch * a.num_seqs < a.ctas) parts *= 2;
+  const int heads = parts < 4 ? 4 : kMergeWarps / parts;
   return launch_pdl(window_merge_kernel,
-                    dim3(a.ctas, (a.num_q_heads + kMergeHeads - 1) / kMergeHeads),
-                    dim3(kMergeHeads * kMergeParts * 32), 0, stream, a.out, p.ws_m, p.ws_l,
-                    p.ws_acc, p.ws_split, p.ws_total, a.num_q_heads, a.ctas);
+                    dim3(a.num_seqs < a.ctas ? a.num_seqs : a.ctas,
+                         (a.num_q_heads + heads - 1) / heads),
+                    dim3(heads * parts * 32), 0, stream, a.out, p.ws_m, p.ws_l, p.ws_acc,
+                    p.ws_split, p.ws_total, a.num_q_heads, a.ctas, parts);
 }
 
 }  // namespace tvl
