@@ -383,6 +383,23 @@ tvl_status tvl_paged_attention_window_decode(
     float scale, int window, int sinks, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Chunked causal prefill with a window: as tvl_paged_attention_prefill
+ * (queries are the last Lq tokens of each sequence; same arguments, limits,
+ * device checks and reports), with each row's visible keys as above and the
+ * output in bfloat16.  Blocks that no row of a 128-row query tile sees are not
+ * read for it.  P and V enter the P.V product as fp16, as there; a V value
+ * beyond the fp16 range or not finite spoils the rows of the query tiles that
+ * see it, and sets TVL_DEV_NONFINITE; values no row of a tile sees do not.
+ *   out : bf16 [Tq, Hq, D]; MB * bs <= 2^30 - 256
+ */
+tvl_status tvl_paged_attention_window_prefill(
+    void* out, const void* q, const int32_t* query_start_loc, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+    int total_q_tokens, int max_q_len, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, int max_blocks_per_seq, float scale, int window, int sinks,
+    void* stream);
+
+/*
  * Host block allocator: the CPU control plane that hands out the physical
  * blocks and slots the kernels read [nano-vLLM guide ch. 2 (control plane vs
  * data plane), ch. 4 "PagedAttention" (block allocator, no fragmentation

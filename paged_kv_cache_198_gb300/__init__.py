@@ -11,7 +11,8 @@ Functions (same names as the C entry points, without the ``tvl_`` prefix):
   paged_decode_step, paged_attention_prefill, rope_paged_kv_write,
   copy_blocks, get_device_status, version; on the 4-bit cache kv4_write,
   kv4_expand_blocks, kv4_copy_blocks, kv4_attention_decode; with a window and
-  sinks paged_attention_window_decode, window_decode_workspace_size.
+  sinks paged_attention_window_decode, window_decode_workspace_size,
+  paged_attention_window_prefill.
 
 Bound calls (``bind_`` before the name of a write, decode, prefill or
 ``kv4_expand_blocks`` call) check their
@@ -40,7 +41,8 @@ __all__ = [
     "kv4_cache_shape", "kv4_write", "kv4_expand_blocks", "kv4_copy_blocks",
     "kv4_attention_decode", "paged_attention_window_decode", "window_decode_workspace_size",
     "bind_kv4_write", "bind_kv4_expand_blocks", "bind_kv4_attention_decode",
-    "bind_paged_attention_window_decode",
+    "bind_paged_attention_window_decode", "paged_attention_window_prefill",
+    "bind_paged_attention_window_prefill",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -112,6 +114,9 @@ def _load():
                 P, P, P, P, P, I, I, I, I, I, I, I, F, I, I, P, SZ, P]
             lib.tvl_paged_attention_window_decode.argtypes = [
                 P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, I, P, SZ, P]
+            lib.tvl_paged_attention_window_prefill.argtypes = [
+                P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, I, P]
+            lib.tvl_paged_attention_window_prefill.restype = I
             for name in ("tvl_kv4_write", "tvl_kv4_expand_blocks", "tvl_kv4_copy_blocks",
                          "tvl_window_decode_workspace_size", "tvl_kv4_attention_decode",
                          "tvl_paged_attention_window_decode"):
@@ -372,12 +377,13 @@ def bind_paged_decode_step(out, q, k_new, v_new, k_cache, v_cache, block_tables,
 
 
 def _prep_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables, context_lens, scale,
-                  max_q_len, stream):
+                  max_q_len, stream, window=None, sinks=0):
+    """`window` None: the plain prefill (fp32 out); else the windowed one (bf16 out)."""
     _need(k_cache, "k_cache", torch.bfloat16, 4)
     dev = k_cache.get_device()
     _need(v_cache, "v_cache", torch.bfloat16, 4, dev)
     _need(q, "q", torch.bfloat16, 3, dev)
-    _need(out, "out", torch.float32, 3, dev)
+    _need(out, "out", torch.float32 if window is None else torch.bfloat16, 3, dev)
     _need(query_start_loc, "query_start_loc", torch.int32, 1, dev)
     _need(block_tables, "block_tables", torch.int32, 2, dev)
     _need(context_lens, "context_lens", torch.int32, 1, dev)
@@ -392,8 +398,11 @@ def _prep_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables, conte
     with _on_device(dev):
         args = (_ptr(out), _ptr(q), _ptr(query_start_loc), _ptr(k_cache), _ptr(v_cache),
                 _ptr(block_tables), _ptr(context_lens), s, tq, int(max_q_len), hq, hkv, d, bs,
-                nb, mb, float(scale), _stream(stream))
+                nb, mb, float(scale))
+        args += (() if window is None else (int(window), int(sinks))) + (_stream(stream),)
     keep = (out, q, query_start_loc, k_cache, v_cache, block_tables, context_lens)
+    if window is not None:
+        return dev, _load().tvl_paged_attention_window_prefill, args, keep
     return dev, _load().tvl_paged_attention_prefill, args, keep
 
 
@@ -623,6 +632,26 @@ def bind_paged_attention_window_decode(out, q, k_cache, v_cache, block_tables, c
     return BoundCall(*_prep_bf16_window_decode(out, q, k_cache, v_cache, block_tables,
                                                context_lens, scale, window, sinks, workspace,
                                                stream))
+
+
+def paged_attention_window_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables,
+                                   context_lens, scale, max_q_len, window, sinks=0, stream=None):
+    """out bf16 [Tq, Hq, D] <- causal attention of the last Lq tokens of each
+    sequence, each row over its last `window` tokens and the first `sinks`
+    (window 0: all earlier tokens)."""
+    dev, fn, args, _ = _prep_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables,
+                                     context_lens, scale, max_q_len, stream, int(window), sinks)
+    with _on_device(dev):
+        _check(fn(*args))
+    return out
+
+
+def bind_paged_attention_window_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables,
+                                        context_lens, scale, max_q_len, window, sinks=0,
+                                        stream=None):
+    """paged_attention_window_prefill, checked once; returns a BoundCall."""
+    return BoundCall(*_prep_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables,
+                                    context_lens, scale, max_q_len, stream, int(window), sinks))
 
 
 class BoundCall:

@@ -395,13 +395,14 @@ tvl_status tvl_paged_decode_step(float* out, const void* q, const void* k_new,
                      stream);
 }
 
-tvl_status tvl_paged_attention_prefill(float* out, const void* q, const int32_t* query_start_loc,
-                                       const void* k_cache, const void* v_cache,
-                                       const int32_t* block_tables, const int32_t* context_lens,
-                                       int num_seqs, int total_q_tokens, int max_q_len,
-                                       int num_q_heads, int num_kv_heads, int head_dim,
-                                       int block_size, int num_blocks, int max_blocks_per_seq,
-                                       float scale, void* stream) {
+namespace {
+
+tvl_status prefill_impl(void* out, const void* q, const int32_t* query_start_loc,
+                        const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                        const int32_t* context_lens, int num_seqs, int total_q_tokens,
+                        int max_q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                        int block_size, int num_blocks, int max_blocks_per_seq, float scale,
+                        bool windowed, int window, int sinks, void* stream) {
   if (num_seqs < 0 || total_q_tokens < 0 || max_q_len < 0)
     return fail(TVL_ERR_INVALID_ARG, "negative size");
   tvl_status st = check_heads(num_q_heads, num_kv_heads, head_dim);
@@ -443,11 +444,44 @@ tvl_status tvl_paged_attention_prefill(float* out, const void* q, const int32_t*
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.scale = scale;
   a.status = word;
+  a.windowed = windowed;
+  a.window = window;
+  a.sinks = sinks;
   st = sm_count(&a.num_sms);
   if (st != TVL_OK) return st;
   cudaError_t e = tvl::launch_prefill(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
   return TVL_OK;
+}
+
+}  // namespace
+
+tvl_status tvl_paged_attention_prefill(float* out, const void* q, const int32_t* query_start_loc,
+                                       const void* k_cache, const void* v_cache,
+                                       const int32_t* block_tables, const int32_t* context_lens,
+                                       int num_seqs, int total_q_tokens, int max_q_len,
+                                       int num_q_heads, int num_kv_heads, int head_dim,
+                                       int block_size, int num_blocks, int max_blocks_per_seq,
+                                       float scale, void* stream) {
+  return prefill_impl(out, q, query_start_loc, k_cache, v_cache, block_tables, context_lens,
+                      num_seqs, total_q_tokens, max_q_len, num_q_heads, num_kv_heads, head_dim,
+                      block_size, num_blocks, max_blocks_per_seq, scale, false, 0, 0, stream);
+}
+
+tvl_status tvl_paged_attention_window_prefill(
+    void* out, const void* q, const int32_t* query_start_loc, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+    int total_q_tokens, int max_q_len, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, int max_blocks_per_seq, float scale, int window, int sinks,
+    void* stream) {
+  if (window < 0 || sinks < 0)
+    return fail(TVL_ERR_INVALID_ARG, "window %d and sinks %d must not be negative", window, sinks);
+  if (static_cast<long long>(max_blocks_per_seq) * block_size > (1 << 30) - 256)
+    return fail(TVL_ERR_UNSUPPORTED, "a block table of more than 2^30 - 256 tokens");
+  return prefill_impl(out, q, query_start_loc, k_cache, v_cache, block_tables, context_lens,
+                      num_seqs, total_q_tokens, max_q_len, num_q_heads, num_kv_heads, head_dim,
+                      block_size, num_blocks, max_blocks_per_seq, scale, true, window, sinks,
+                      stream);
 }
 
 // ------------------------------------------------------------ 4-bit cache

@@ -123,7 +123,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_selftest_wait(uint32_t* status, cudaStream_t stream);
 
 struct PrefillArgs {
-  float* out;
+  void* out;              // fp32 [Tq, Hq, D]; windowed: bf16
   const void* q;
   const int32_t* query_start_loc;
   const void* k_cache;
@@ -135,6 +135,8 @@ struct PrefillArgs {
   float scale;
   uint32_t* status;
   int num_sms;            // the persistent grid's size bound
+  bool windowed;          // bf16 output, and the window and sinks below
+  int window, sinks;      // window 0: none
 };
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 

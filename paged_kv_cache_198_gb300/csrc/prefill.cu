@@ -48,6 +48,16 @@
 // 2^-11 relative (bf16 would cost 2^-8) -- the fp32-accumulated result stays
 // within 2e-3 of the exact attention even for rows with few keys.
 // TMEM (per head h): S_h 128 columns, O_h 64, P_h 64 (fp16 pairs).
+//
+// Sliding window and sinks (kWin): row p sees the keys j <= p with j > p -
+// window or j < sinks.  A unit's keys are then a list of physical blocks --
+// the sink blocks, then those from the first row's window on -- laid end to
+// end in key tiles; key u of that list is key u of the sequence, or u + delta
+// behind the sink blocks, so the mask of a row is again a pair of ranges of u.
+// Gaps are cut out per block, not per 128-key tile: a window of 1024 behind
+// four sinks is nine or ten tiles of 128 keys, where whole tiles would be ten
+// or eleven.  The output is bf16 (P's fp16 rounding, 2^-11, is below the
+// output's, 2^-8), staged as one swizzled 128-byte row.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -123,13 +133,14 @@ struct Barriers {
 static_assert(sizeof(Barriers) <= 512, "barrier area");
 
 struct Params {
-  float* out;
+  void* out;             // fp32, or bf16 (kWin)
   const int32_t* query_start_loc;
   const int32_t* block_tables;
   const int32_t* context_lens;
   int num_seqs, total_q, hq, hkv, group, bs, num_blocks, max_blocks, n_qtiles;
   float scale_log2;
   uint32_t* status;
+  int window, sinks;     // kWin; window 0: none
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -172,10 +183,20 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, co
 // Every role of the CTA derives the same units in the same order.
 struct Unit {
   int s, h0, q0, row0, rows, pos_first, ctx, n_kv;
+  int sb, delta;   // kWin: sink blocks; tokens left out behind them
   bool valid;      // rows to compute and consistent lengths
   bool bad;        // the sequence's lengths are inconsistent (reported, skipped)
   bool bad_ctx;    // the inconsistency is a context past the table's capacity
 };
+
+// The key list of a query tile whose rows start at position pos_first: sb sink
+// blocks, then the blocks from the first row's window on, delta tokens later.
+__device__ __forceinline__ void window_blocks(const Params& p, int pos_first, int& sb, int& delta) {
+  const int first = p.window > 0 ? max(0, pos_first - p.window + 1) : 0;
+  const int w0 = first / p.bs;
+  sb = min(p.sinks / p.bs + (p.sinks % p.bs != 0 ? 1 : 0), w0);
+  delta = (w0 - sb) * p.bs;
+}
 
 // Index of the k-th unit of CTA c among G: the units in longest-first order
 // are dealt to the CTAs row by row, every other row reversed (c, 2G-1-c,
@@ -189,7 +210,7 @@ __device__ __forceinline__ long long unit_index(int k, int c, int G) {
 // `tab`, the order and the items' lengths come from shared memory (tab[0..K)
 // rank -> item, then K-strided q0, Lq and context per item); without it the
 // order is the item order and the lengths are read from global memory.
-template <int NH, int K>
+template <int NH, int K, bool kWin>
 __device__ __forceinline__ void unit_info(const Params& p, const int* tab, int u, Unit& x) {
   const int pairs = p.hq / NH;
   const int rank = u / pairs;
@@ -225,18 +246,22 @@ __device__ __forceinline__ void unit_info(const Params& p, const int* tab, int u
   x.rows = min(kBM, lq - x.row0);
   x.pos_first = x.ctx - lq + x.row0;
   x.n_kv = (x.pos_first + x.rows - 1) / kBN + 1;
+  if constexpr (kWin) {
+    window_blocks(p, x.pos_first, x.sb, x.delta);
+    x.n_kv = (x.pos_first + x.rows - 1 - x.delta) / kBN + 1;
+  }
 }
 
 // The first unit of this CTA at or after index k that has work; k moves to
 // it.  With kWarp it is called by whole warps and the fields go through
 // lane 0, so that the compiler sees them warp-uniform (fewer registers).
-template <int NH, int K, bool kWarp>
+template <int NH, int K, bool kWarp, bool kWin>
 __device__ __forceinline__ bool next_valid_unit(const Params& p, const int* tab, int& k, Unit& x) {
   const int n_units = p.num_seqs * p.n_qtiles * (p.hq / NH);
   for (;; ++k) {
     const long long u = unit_index(k, blockIdx.x, gridDim.x);
     if (u >= n_units) return false;
-    unit_info<NH, K>(p, tab, static_cast<int>(u), x);
+    unit_info<NH, K, kWin>(p, tab, static_cast<int>(u), x);
     if (!kWarp) {
       if (x.valid) return true;
       continue;
@@ -251,10 +276,14 @@ __device__ __forceinline__ bool next_valid_unit(const Params& p, const int* tab,
   x.pos_first = __shfl_sync(kFull, x.pos_first, 0);
   x.ctx = __shfl_sync(kFull, x.ctx, 0);
   x.n_kv = __shfl_sync(kFull, x.n_kv, 0);
+  if constexpr (kWin) {
+    x.sb = __shfl_sync(kFull, x.sb, 0);
+    x.delta = __shfl_sync(kFull, x.delta, 0);
+  }
   return true;
 }
 
-template <int NH>
+template <int NH, bool kWin>
 __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                    const __grid_constant__ CUtensorMap tm_k,
@@ -296,6 +325,11 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
       const int ci = p.context_lens[si];
       const int last = ci - lqi + min((qt + 1) * kBM, lqi);   // keys seen
       key = qt * kBM >= lqi ? 0 : (last + kBN - 1) / kBN;
+      if constexpr (kWin) {
+        int sb, delta;
+        window_blocks(p, ci - lqi + qt * kBM, sb, delta);
+        if (key > 0) key = (last - delta + kBN - 1) / kBN;
+      }
       keys[i] = key;
       t[K + i] = qa;
       t[2 * K + i] = lqi;
@@ -313,7 +347,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
     tab = t;
   }
   auto next_unit = [&](int& k, Unit& x) -> bool {
-    return next_valid_unit<NH, K, true>(p, tab, k, x);
+    return next_valid_unit<NH, K, true, kWin>(p, tab, k, x);
   };
 
   if (threadIdx.x == 0) {
@@ -386,7 +420,8 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(&B->kv_full[st], 2 * kTileBytes);
         __syncwarp();
         for (int b = lane; b < boxes; b += 32) {
-          const int lb = j * boxes + b;                 // logical block
+          int lb = j * boxes + b;                       // logical block
+          if constexpr (kWin) lb += lb < x.sb ? 0 : x.delta / p.bs;
           int phys = p.num_blocks;                      // out of range: zero fill
           if (lb < nblk) {
             phys = table[lb];
@@ -431,7 +466,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
       bool ok = true;
       for (int k = 0; ok; ++k) {
         Unit x;
-        if (!next_valid_unit<NH, K, false>(p, tab, k, x)) break;
+        if (!next_valid_unit<NH, K, false, kWin>(p, tab, k, x)) break;
         for (int j = 0; ok && j < x.n_kv; ++j, ++gt) {
           if (is_qk) {
             ok = wait_or_abort(&B->kv_full[st], ph, p);
@@ -492,7 +527,14 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
 #pragma unroll 4
         for (int e = t; e < static_cast<int>(kTileBytes / 16); e += 32) {
           uint4 w = *reinterpret_cast<const uint4*>(vt + e * 16);
-          if (j * kBN + (e >> 3) < x.ctx) {
+          bool live = j * kBN + (e >> 3) < x.ctx;
+          if constexpr (kWin) {
+            // keys that no row of the unit sees become 0 as well
+            const int u = j * kBN + (e >> 3);
+            live = u < x.ctx - x.delta &&
+                   (u < p.sinks || p.window == 0 || u > x.pos_first - p.window - x.delta);
+          }
+          if (live) {
             w.x = bf16x2_to_half2(w.x);
             w.y = bf16x2_to_half2(w.y);
             w.z = bf16x2_to_half2(w.z);
@@ -529,9 +571,11 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
       // it again there, and no registers held through the tile loop)
       if (lane == 0) B->ustash[warp] = make_int4(x.rows, x.q0 + x.row0, x.h0, 0);
       __syncwarp();
-      const int qpos = x.pos_first + r;
-      const int pos_first = x.pos_first;
-      const int ctx = x.ctx;
+      // kWin: positions in the unit's key list
+      const int delta = kWin ? x.delta : 0;
+      const int qpos = x.pos_first - delta + r;
+      const int pos_first = x.pos_first - delta;
+      const int ctx = x.ctx - delta;
       const int n_kv = x.n_kv;
       float m_used = -INFINITY;                         // reference maximum (log2 units)
       float2 l2 = make_float2(0.f, 0.f);
@@ -551,21 +595,35 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         if (lane == 0) mbar_arrive(&B->s_free[hh]);
 
         // Tiles on the causal diagonal or past the context need the mask.
-        const bool masked = (key0 + kBN - 1 > pos_first) || (key0 + kBN > ctx);
+        bool masked = (key0 + kBN - 1 > pos_first) || (key0 + kBN > ctx);
+        if constexpr (kWin)
+          masked |= p.window > 0 && key0 <= pos_first + kBM - 1 - p.window && key0 + kBN > p.sinks;
         const int limit = min(qpos, ctx - 1) - key0;    // last visible column
+        // kWin: columns below `low` are visible only below `sink`.  Bit e of
+        // hidden(cc): column 32 cc + e of this row is masked
+        const int low = kWin && p.window > 0 ? qpos - p.window + 1 - key0 : -0x40000000;
+        const int sink = p.sinks - key0;
+        auto below = [](int n) -> uint32_t {            // bits 0 .. n - 1
+          return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+        };
+        auto hidden = [&](int cc) -> uint32_t {
+          return ~below(limit + 1 - 32 * cc) | (below(low - 32 * cc) & ~below(sink - 32 * cc));
+        };
         // row maximum of the scaled scores of this tile
         auto tile_max = [&]() -> float {
           float mt;
           if (masked) {
             mt = -INFINITY;
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc)
+            for (int cc = 0; cc < 4; ++cc) {
+              const uint32_t hid = kWin ? hidden(cc) : 0u;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 float v = __uint_as_float(sr[cc][e]) * p.scale_log2;
-                if (cc * 32 + e > limit) v = -INFINITY;
+                if (kWin ? (hid >> e & 1u) != 0 : cc * 32 + e > limit) v = -INFINITY;
                 mt = fmaxf(mt, v);
               }
+            }
           } else if (p.scale_log2 >= 0.f) {
             float mx = -INFINITY;
 #pragma unroll
@@ -592,17 +650,19 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
           float2 tsum = make_float2(0.f, 0.f);
           if (masked) {
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc)
+            for (int cc = 0; cc < 4; ++cc) {
+              const uint32_t hid = kWin ? hidden(cc) : 0u;
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 float2 v = make_float2(__uint_as_float(sr[cc][e]), __uint_as_float(sr[cc][e + 1]));
                 v = __ffma2_rn(v, sl2, nm2);
-                if (cc * 32 + e > limit) v.x = -INFINITY;
-                if (cc * 32 + e + 1 > limit) v.y = -INFINITY;
+                if (kWin ? (hid >> e & 1u) != 0 : cc * 32 + e > limit) v.x = -INFINITY;
+                if (kWin ? (hid >> e & 2u) != 0 : cc * 32 + e + 1 > limit) v.y = -INFINITY;
                 const float2 pv = make_float2(ex2(v.x), ex2(v.y));
                 tsum = __fadd2_rn(tsum, pv);
                 pk[cc >> 1][(cc & 1) * 16 + e / 2] = pack_half2(pv.x, pv.y);
               }
+            }
           } else {
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc)
@@ -629,10 +689,13 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
           tsum = make_p(m_used == -INFINITY ? 0.f : m_used);
           const float ts = tsum.x + tsum.y;
           move = !(ts <= 60000.f);
+          // a window may leave a row without a key in its first tiles: it has
+          // no reference yet (and O and l are 0)
+          if constexpr (kWin) move |= m_used == -INFINITY;
           if (__any_sync(kFull, move)) {
             if (move) {
               const float m_new = fmaxf(m_used, tile_max());
-              f = ex2(m_used - m_new);
+              f = kWin && m_new == -INFINITY ? 1.f : ex2(m_used - m_new);
               m_used = m_new;
             }
             tsum = make_p(m_used == -INFINITY ? 0.f : m_used);
@@ -686,11 +749,28 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
       // so spend only the staging on the unit's 64 KB of fp32 output.
       const int r0 = wi * 32;                           // the warp's first row
       const int nrows = min(32, us.x - r0);             // rows of it inside the unit
+      // kWin: a bf16 row is one 128-byte row of the same swizzled layout.
       uint8_t* st_head = smem + C::kStageOff + hh * (kBM * kD * 4);
+      auto bf16x8 = [&](const uint32_t* v, float k) -> uint4 {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * i]) * k,
+                                                         __uint_as_float(v[2 * i + 1]) * k);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+      };
       if (lane == 0) bulk_wait_read();                  // its last stores have read the rows
       __syncwarp();
       const float inv = 1.0f / (l2.x + l2.y);
       if (lane < nrows) {
+        if constexpr (kWin) {
+#pragma unroll
+          for (int jc = 0; jc < 8; ++jc)
+            *reinterpret_cast<uint4*>(st_head + r * 128 + ((jc ^ (r & 7)) << 4)) =
+                bf16x8(&o[jc >> 2][8 * (jc & 3)], inv);
+        } else {
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -700,6 +780,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
                             __uint_as_float(o[half][4 * jc + 1]) * inv,
                             __uint_as_float(o[half][4 * jc + 2]) * inv,
                             __uint_as_float(o[half][4 * jc + 3]) * inv);
+        }
         // A row that is not finite: a V value beyond the fp16 range of the
         // P.V product (bf16 holds values past 65504), or non-finite inputs.
         // The sum of the unnormalised row carries any inf or NaN.
@@ -719,6 +800,9 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
       const int full = nrows >= 32 ? 32 : (nrows >= 16 ? 16 : 0);   // rows in whole 16-row groups
       if (lane == 0 && full > 0) {
         for (int g = 0; g < full; g += 16)
+          if constexpr (kWin) {
+            tma_store_3d(&tm_o, st_head + (r0 + g) * 128, 0, us.z + hh, us.y + r0 + g);
+          } else
 #pragma unroll
           for (int half = 0; half < 2; ++half)
             tma_store_3d(&tm_o, st_head + half * (kBM * 128) + (r0 + g) * 128, half * 32, us.z + hh,
@@ -728,8 +812,13 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
       if (lane >= full && lane < nrows) {
         // a row outside the whole 16-row groups (a unit shorter than 128
         // rows): straight from registers
-        float4* dst = reinterpret_cast<float4*>(
-            p.out + (static_cast<long long>(us.y + r) * p.hq + us.z + hh) * kD);
+        const long long at = (static_cast<long long>(us.y + r) * p.hq + us.z + hh) * kD;
+        if constexpr (kWin) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at);
+#pragma unroll
+          for (int jc = 0; jc < 8; ++jc) dst[jc] = bf16x8(&o[jc >> 2][8 * (jc & 3)], inv);
+        } else {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
@@ -737,6 +826,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
             dst[cc * 8 + e / 4] =
                 make_float4(__uint_as_float(o[cc][e]) * inv, __uint_as_float(o[cc][e + 1]) * inv,
                             __uint_as_float(o[cc][e + 2]) * inv, __uint_as_float(o[cc][e + 3]) * inv);
+        }
       }
     }
     if (lane == 0) bulk_wait_all();                     // the output stores are complete
@@ -746,7 +836,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         const long long u = unit_index(k, c, G);
         if (u >= n_units) break;
         Unit x;
-        unit_info<NH, K>(p, tab, static_cast<int>(u), x);
+        unit_info<NH, K, kWin>(p, tab, static_cast<int>(u), x);
         if (x.bad) report(p.status, x.bad_ctx ? TVL_DEV_BAD_CONTEXT_LEN : TVL_DEV_BAD_QUERY_LEN);
       }
     }
@@ -787,7 +877,7 @@ bool make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims
   return r == CUDA_SUCCESS;
 }
 
-template <int NH>
+template <int NH, bool kWin>
 cudaError_t launch_nh(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       const CUtensorMap& to, const Params& p, int num_seqs, int num_sms,
                       cudaStream_t stream) {
@@ -796,12 +886,12 @@ cudaError_t launch_nh(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   // register split fits the registers the block is launched with
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
-    cudaError_t r = cudaFuncSetAttribute(prefill_kernel<NH>,
+    cudaError_t r = cudaFuncSetAttribute(prefill_kernel<NH, kWin>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::kSmemBytes);
     if (r != cudaSuccess || NH != 2) return r;
     cudaFuncAttributes fa;
-    r = cudaFuncGetAttributes(&fa, prefill_kernel<NH>);
+    r = cudaFuncGetAttributes(&fa, prefill_kernel<NH, kWin>);
     if (r != cudaSuccess) return r;
     if (fa.numRegs * C::kThreads < 2 * 128 * kRegsSoftmax + 128 * kRegsAux) {
       set_last_error("prefill kernel register allocation smaller than its register split");
@@ -818,7 +908,7 @@ cudaError_t launch_nh(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   // behind a kernel that is still draining, they started over that kernel's
   // tail and the last to start set the end (chunked prefill after the paged
   // write: 176 us per step against 157 us).
-  prefill_kernel<NH><<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, p);
+  prefill_kernel<NH, kWin><<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, p);
   return cudaGetLastError();
 }
 
@@ -831,9 +921,12 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD),
                                 static_cast<cuuint64_t>(a.num_q_heads),
                                 static_cast<cuuint64_t>(a.total_q_tokens)};
-    const cuuint64_t strides[2] = {kD * 4, static_cast<cuuint64_t>(a.num_q_heads) * kD * 4};
-    const cuuint32_t box[3] = {32, 1, 16};
-    if (!make_map(&to, a.out, 3, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
+    // (windowed: bf16 [Tq, Hq, D], 16-row x 64-column tiles)
+    const cuuint64_t elt = a.windowed ? 2 : 4;
+    const cuuint64_t strides[2] = {kD * elt, static_cast<cuuint64_t>(a.num_q_heads) * kD * elt};
+    const cuuint32_t box[3] = {a.windowed ? 64u : 32u, 1, 16};
+    if (!make_map(&to, a.out, 3, dims, strides, box,
+                  a.windowed ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
       return cudaErrorInvalidValue;
   }
   {
@@ -872,8 +965,16 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   p.n_qtiles = (a.max_q_len + kBM - 1) / kBM;
   p.scale_log2 = a.scale * kLog2e;
   p.status = a.status;
-  if (p.group >= 2) return launch_nh<2>(tq, tk, tv, to, p, a.num_seqs, a.num_sms, stream);
-  return launch_nh<1>(tq, tk, tv, to, p, a.num_seqs, a.num_sms, stream);
+  // a window or sinks past the table's capacity act as the capacity (and keep
+  // the mask's arithmetic inside 32 bits)
+  const int cap = a.max_blocks_per_seq * a.block_size;
+  p.window = a.window < cap ? a.window : cap;
+  p.sinks = a.window == 0 ? 0 : a.sinks < cap ? a.sinks : cap;
+  if (a.windowed)
+    return p.group >= 2 ? launch_nh<2, true>(tq, tk, tv, to, p, a.num_seqs, a.num_sms, stream)
+                        : launch_nh<1, true>(tq, tk, tv, to, p, a.num_seqs, a.num_sms, stream);
+  if (p.group >= 2) return launch_nh<2, false>(tq, tk, tv, to, p, a.num_seqs, a.num_sms, stream);
+  return launch_nh<1, false>(tq, tk, tv, to, p, a.num_seqs, a.num_sms, stream);
 }
 
 }  // namespace tvl

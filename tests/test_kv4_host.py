@@ -135,3 +135,18 @@ def test_plain_cache_packs_what_it_unpacks():
     # dimension d of token t: byte 32 t + d / 2 of the record, low half first
     b = cache[1, 1, 0, 512 + 32 * 5 + 9]
     assert codes[1, 1, 16 + 5, 0, 18] == (b & 15) and codes[1, 1, 16 + 5, 0, 19] == (b >> 4)
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(window=-1), "INVALID_ARG"), (dict(sinks=-2), "INVALID_ARG"), (dict(d=128), "UNSUPPORTED"),
+    (dict(bs=24), "UNSUPPORTED"), (dict(hq=6), "UNSUPPORTED"), (dict(mb=1 << 26), "UNSUPPORTED"),
+    (dict(out=None), "INVALID_ARG"), (dict(out=D16 + 8), "INVALID_ARG"), (dict(maxq=0), "INVALID_ARG"),
+    (dict(scale=float("nan")), "INVALID_ARG"), (dict(s=-1), "INVALID_ARG"), (dict(s=70000), "UNSUPPORTED")])
+def test_window_prefill_refusals(tvl, bad, want):
+    a = dict(out=D16, q=D16, qsl=D16, kc=D16, vc=D16, tab=D16, ctx=D16, s=2, tq=10, maxq=8, hq=8, hkv=2,
+             d=64, bs=16, nb=64, mb=8, scale=0.125, window=32, sinks=4)
+    a.update(bad)
+    rc = tvl._load().tvl_paged_attention_window_prefill(
+        a["out"], a["q"], a["qsl"], a["kc"], a["vc"], a["tab"], a["ctx"], a["s"], a["tq"], a["maxq"], a["hq"],
+        a["hkv"], a["d"], a["bs"], a["nb"], a["mb"], a["scale"], a["window"], a["sinks"], None)
+    assert rc == getattr(tvl, "ERR_" + want)
