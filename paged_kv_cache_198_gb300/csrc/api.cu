@@ -610,18 +610,7 @@ tvl_status window_heads(int hq, int hkv, int d) {
     return fail(TVL_ERR_INVALID_ARG, "num_q_heads %d not a multiple of num_kv_heads %d", hq, hkv);
   if (d != 64) return fail(TVL_ERR_UNSUPPORTED, "head_dim %d (supported: 64)", d);
   if (hq / hkv > 8) return fail(TVL_ERR_UNSUPPORTED, "GQA group %d (supported: 1 to 8)", hq / hkv);
-  if (hkv / tvl::window_heads_per_cta(hkv) > 65535)
-    return fail(TVL_ERR_UNSUPPORTED, "num_kv_heads %d", hkv);
-  return TVL_OK;
-}
-
-// One CTA per SM, shared by the groups of KV heads that a CTA owns.
-tvl_status window_ctas(int hkv, int* ctas) {
-  int sms = 0;
-  tvl_status st = sm_count(&sms);
-  if (st != TVL_OK) return st;
-  const int groups = hkv / tvl::window_heads_per_cta(hkv);
-  *ctas = sms / groups < 1 ? 1 : sms / groups;
+  if (hkv > 65535) return fail(TVL_ERR_UNSUPPORTED, "num_kv_heads %d > 65535", hkv);
   return TVL_OK;
 }
 
@@ -652,10 +641,11 @@ tvl_status window_decode_impl(float* out, const void* q, const void* k_cache, co
     return fail(TVL_ERR_INVALID_ARG, "out, q and the caches must be 16-byte aligned");
   if (!workspace) return fail(TVL_ERR_WORKSPACE, "null workspace");
   if (!aligned16(workspace)) return fail(TVL_ERR_INVALID_ARG, "workspace not 16-byte aligned");
-  int ctas = 0;
-  st = window_ctas(num_kv_heads, &ctas);
+  int sms = 0;
+  st = sm_count(&sms);
   if (st != TVL_OK) return st;
-  const size_t need = tvl::window_workspace_bytes(ctas, num_q_heads);
+  const size_t need =
+      tvl::window_workspace_bytes(tvl::window_max_ctas(num_kv_heads, sms), num_q_heads);
   if (workspace_bytes < need)
     return fail(TVL_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   uint32_t* word = nullptr;
@@ -678,7 +668,7 @@ tvl_status window_decode_impl(float* out, const void* q, const void* k_cache, co
   a.window = window;
   a.sinks = sinks;
   a.scale = scale;
-  a.ctas = ctas;
+  a.sms = sms;
   a.workspace = workspace;
   a.status = word;
   cudaError_t e = tvl::launch_window_decode(a, static_cast<cudaStream_t>(stream));
@@ -693,10 +683,10 @@ tvl_status tvl_window_decode_workspace_size(int num_q_heads, int num_kv_heads, i
   if (!bytes) return fail(TVL_ERR_INVALID_ARG, "null bytes pointer");
   tvl_status st = window_heads(num_q_heads, num_kv_heads, head_dim);
   if (st != TVL_OK) return st;
-  int ctas = 0;
-  st = window_ctas(num_kv_heads, &ctas);
+  int sms = 0;
+  st = sm_count(&sms);
   if (st != TVL_OK) return st;
-  *bytes = tvl::window_workspace_bytes(ctas, num_q_heads);
+  *bytes = tvl::window_workspace_bytes(tvl::window_max_ctas(num_kv_heads, sms), num_q_heads);
   return TVL_OK;
 }
 

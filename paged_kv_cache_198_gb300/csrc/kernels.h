@@ -180,12 +180,12 @@ struct WindowDecodeArgs {
   int num_seqs, num_q_heads, num_kv_heads, block_size, num_blocks, max_blocks_per_seq;
   int window, sinks;       // window 0: every cached token is visible
   float scale;
-  int ctas;                // CTAs per KV-head group
+  int sms;                 // of the device
   void* workspace;
   uint32_t* status;
 };
-// KV heads one CTA owns: the largest divisor of num_kv_heads up to 8.
-int window_heads_per_cta(int num_kv_heads);
+// The most CTAs that share one KV-head group's work (sizes the workspace).
+int window_max_ctas(int num_kv_heads, int sms);
 size_t window_workspace_bytes(int ctas, int num_q_heads);
 cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream);
 

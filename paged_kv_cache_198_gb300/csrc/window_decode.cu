@@ -61,10 +61,8 @@ namespace {
 
 constexpr int kD = 64;
 constexpr int kChunk = 16;
-constexpr int kMaxWarps = 16;                 // consumer warps
-constexpr int kThreads = (kMaxWarps + 1) * 32;
 constexpr uint32_t kBf16Tile = kChunk * kD * 2;   // one head's K (or V) of a chunk
-constexpr float kRescaleLog2 = 8.0f;
+constexpr float kMaxSum = 256.0f;             // a lane's weights under the reference maximum
 constexpr float kMaxVScale = 128.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kFull = 0xffffffffu;
@@ -75,8 +73,12 @@ enum Format : int { kBf16 = 0, k4Bit = 1 };
 enum : int { kSegFirst = 1, kSegLast = 2, kTerminate = 4, kPartial = 8 };
 
 // chunks a warp takes from a stage at once (independent work in flight)
-template <int F>
-__host__ __device__ constexpr int chunks_per_warp() { return F == k4Bit ? 2 : 1; }
+template <int F, bool kLoCols>
+__host__ __device__ constexpr int chunks_per_warp() { return F == k4Bit ? (kLoCols ? 4 : 2) : 1; }
+template <int F, bool kLoCols>
+__host__ __device__ constexpr int max_warps() { return F == k4Bit && kLoCols ? 12 : 16; }
+template <int F, bool kLoCols>
+__host__ __device__ constexpr int max_heads() { return F == k4Bit && kLoCols ? 4 : 8; }
 
 struct alignas(16) StageMeta {
   int seq, record, flags, n;   // n: chunks in the stage
@@ -92,7 +94,7 @@ struct Params {
   int num_seqs, hq, hkv, group, num_blocks, max_blocks;
   int cpb_log2;          // log2 of the 16-token chunks in a block
   int window, sinks;     // window 0: none
-  int hpc, wph, cps, stages;
+  int hpc, wph, cps, batch, stages;
   uint32_t stage_bytes, kv_bytes;
   float scale_log2;
   int ctas, seg_weight;
@@ -325,11 +327,11 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
       p.ws_split[g.s] = g.e < g.n ? split : make_int4(-1, 0, 0, 0);
     Segment nx;
     const bool have_next = find(g.s, g.e, false, nx);
-    for (int vb = g.v; vb < g.e && ok; vb += 32) {
-      // the next 32 entries (of this segment or the next) are fetched while
+    for (int vb = g.v; vb < g.e && ok; vb += p.batch) {
+      // the next batch's entries (of this segment or the next) are fetched while
       // this batch's copies are issued
-      const int ntbl = vb + 32 < g.e ? entry(g, vb + 32) : (have_next ? entry(nx, nx.v) : 0);
-      for (int v = vb; v < g.e && v < vb + 32; v += p.cps) {
+      const int ntbl = vb + p.batch < g.e ? entry(g, vb + p.batch) : (have_next ? entry(nx, nx.v) : 0);
+      for (int v = vb; v < g.e && v < vb + p.batch; v += p.cps) {
         const int n = min(p.cps, g.e - v);
         if (!acquire()) break;
         uint8_t* base = smem + static_cast<size_t>(st) * p.stage_bytes;
@@ -497,6 +499,7 @@ __device__ __forceinline__ int row_token(int r) {   // r < 8
 // A lane (g = lane / 4, t = lane % 4) holds columns 2 t and 2 t + 1: `x`, `y`.
 struct State {
   uint32_t qf[4][2];   // q as the column operand
+  uint32_t qg[4][2];   // 4-bit, up to four heads: qf has columns 0..3, qg columns 4..7
   float acc[4][4];     // output rows, see out_dim
   float2 m, l, zs;     // reference maximum (log2), sum of p, sum of p (z + 8 s)
   float2 qsum;         // 4-bit: sum(q) * scale_log2
@@ -552,222 +555,349 @@ __device__ __forceinline__ void load_q(State& st, const Params& p, const uint8_t
       const int d = (i >> 1) * 8 + (i & 1) * 2;
       st.qf[i][0] = pack16<k4Bit>(make_float2(v[d] * up, v[d + 4] * up));
       st.qf[i][1] = pack16<k4Bit>(make_float2(v[d + 1] * up16, v[d + 5] * up16));
+      if (kLoCols) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          st.qg[i][k] = g >= 4 ? st.qf[i][k] : 0u;
+          if (g >= 4) st.qf[i][k] = 0u;
+        }
+      }
     }
   }
 }
 
-// NCH chunks of the warp's head; chunk i starts at token tok0[i] and lies at
-// kb[i] (4-bit: the record; bf16: the K tile, with the V tile v_off behind).
-template <int F, bool kLoCols, int NCH, bool kMasked>
-__device__ __forceinline__ void process(State& st, const Params& p, const uint8_t* const (&kb)[NCH],
-                                        uint32_t v_off, const int (&tok0)[NCH], int ctx) {
+// Moves the reference maximum to cover the scores x (two columns a lane), and,
+// on the 4-bit cache, the power of two on the V scales to cover sv; everything
+// summed so far is rescaled.  One reference scales numerator and denominator,
+// so the result does not depend on when this happens.
+template <int F, bool kPair>
+__device__ __forceinline__ void move_reference(State& st, float2 mx, float sv) {
+  float f_v = 1.f;
+  constexpr int kFirst = kPair ? 2 : 4;      // a pair's two chunks share the columns' reference
+  if (F == k4Bit) {
+#pragma unroll
+    for (int o = kFirst; o < 32; o <<= 1) sv = fmaxf(sv, __shfl_xor_sync(kFull, sv, o));
+    if (st.vs == 0.f || sv * st.vs > kMaxVScale) {
+      int e = static_cast<int>(__float_as_uint(sv) >> 23) - 127;   // the largest to [32, 64)
+      e = max(-100, min(100, e));
+      const float vs = __uint_as_float(static_cast<uint32_t>(127 + 5 - e) << 23);
+      f_v = st.vs == 0.f ? 0.f : vs / st.vs;
+      st.vs = vs;
+    }
+  }
+#pragma unroll
+  for (int o = kFirst; o < 32; o <<= 1) {
+    mx.x = fmaxf(mx.x, __shfl_xor_sync(kFull, mx.x, o));
+    mx.y = fmaxf(mx.y, __shfl_xor_sync(kFull, mx.y, o));
+  }
+  mx.x = fmaxf(mx.x, st.m.x);
+  mx.y = fmaxf(mx.y, st.m.y);
+  float2 f = make_float2(ex2(st.m.x - mx.x), ex2(st.m.y - mx.y));
+  st.m = mx;
+  st.l = __fmul2_rn(st.l, f);
+  st.zs = __fmul2_rn(st.zs, f);
+  f.x *= f_v;
+  f.y *= f_v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    st.acc[i][0] *= f.x;
+    st.acc[i][1] *= f.y;
+    st.acc[i][2] *= f.x;
+    st.acc[i][3] *= f.y;
+  }
+}
+
+__device__ __forceinline__ void add_to(float (&acc)[4], const float (&sum)[4]) {
+  // The tensor core truncates what it accumulates, which over a long context
+  // would pull the sums towards zero; across stages they add up here, rounded.
+  const float2 a = add2(acc[0], acc[1], sum[0], sum[1]), b = add2(acc[2], acc[3], sum[2], sum[3]);
+  acc[0] = a.x;
+  acc[1] = a.y;
+  acc[2] = b.x;
+  acc[3] = b.y;
+}
+
+__device__ __forceinline__ uint32_t lds32(const uint8_t* p) {
+  return *reinterpret_cast<const uint32_t*>(p);
+}
+
+constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
+constexpr uint32_t k15 = 0x800f800fu, k240 = 0x80f080f0u;     // -15 and -240 times 2^-24
+
+// Scores of a 4-bit chunk's 16 rows: c = q . codes
+__device__ __forceinline__ void codes_dot(float (&c)[4], const uint8_t* rec, const uint32_t (&qf)[4][2],
+                                          int r0, int t) {
+  const uint2 a = *reinterpret_cast<const uint2*>(rec + r0 * kRowCodes + t * 8);
+  const uint2 b = *reinterpret_cast<const uint2*>(rec + (8 + r0) * kRowCodes + t * 8);
+  mma_f16_0(c, a.x & kLo, b.x & kLo, a.x & kHi, b.x & kHi, qf[0][0], qf[0][1]);
+  mma_f16(c, (a.x >> 8) & kLo, (b.x >> 8) & kLo, (a.x >> 8) & kHi, (b.x >> 8) & kHi, qf[1][0],
+          qf[1][1]);
+  mma_f16(c, a.y & kLo, b.y & kLo, a.y & kHi, b.y & kHi, qf[2][0], qf[2][1]);
+  mma_f16(c, (a.y >> 8) & kLo, (b.y >> 8) & kLo, (a.y >> 8) & kHi, (b.y >> 8) & kHi, qf[3][0],
+          qf[3][1]);
+}
+
+// The V codes of this lane's four tokens and eight dimensions, two tokens'
+// codes of a dimension side by side: w[0..1] tokens (0, 1), w[2..3] tokens (8, 9)
+// of the product's k order; byte pairs of dimensions 0..3 and 4..7.
+__device__ __forceinline__ void load_v(uint32_t (&w)[4], const uint8_t* rec, int g, int t) {
+  const uint8_t* vb = rec + kRecV + g * 4;
+  const int ta = row_token<k4Bit>(2 * t) * kRowCodes, tb = row_token<k4Bit>(2 * t + 1) * kRowCodes;
+  const uint32_t y0 = lds32(vb + ta), y1 = lds32(vb + tb);
+  const uint32_t y2 = lds32(vb + ta + 8 * kRowCodes), y3 = lds32(vb + tb + 8 * kRowCodes);
+  w[0] = __byte_perm(y0, y1, 0x5410);
+  w[1] = __byte_perm(y0, y1, 0x7632);
+  w[2] = __byte_perm(y2, y3, 0x5410);
+  w[3] = __byte_perm(y2, y3, 0x7632);
+}
+// rows 2 i, 2 i + 1 of the lane's dimensions as the row operand, codes centred
+__device__ __forceinline__ void v_operand(uint32_t (&a)[4], const uint32_t (&w)[4], int i) {
+  const uint32_t u0 = (i & 1) ? w[i >> 1] >> 8 : w[i >> 1];
+  const uint32_t u1 = (i & 1) ? w[2 + (i >> 1)] >> 8 : w[2 + (i >> 1)];
+  a[0] = half2_twice_plus(u0 & kLo, k15);
+  a[1] = half2_twice_plus(u0 & kHi, k240);
+  a[2] = half2_twice_plus(u1 & kLo, k15);
+  a[3] = half2_twice_plus(u1 & kHi, k240);
+}
+
+// NP pairs of chunks, A and B, of a 4-bit head with at most four query heads.
+// The product has eight columns; A's scores are formed in columns 0..3 (q is
+// zero in the others) and B's in columns 4..7, so one pass of the softmax
+// arithmetic serves both.  For P V the lo halves cross over (lane ^ 2): A's
+// operand is (hi A, lo A), B's is (lo B, hi B); columns n and n + 4 are added
+// at the segment's end.  tok: the first token of this lane's chunk of each pair.
+template <int NP, bool kMasked>
+__device__ __forceinline__ void process_pairs(State& st, const Params& p, const uint8_t* const (&ra)[NP],
+                                              const uint8_t* const (&rb)[NP], const int (&tok)[NP],
+                                              int ctx) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int r0 = row_token<F>(g), r1 = 8 + r0;
+  const bool second = t >= 2;
+  const int r0 = row_token<k4Bit>(g);
+  float2 x0[NP], x1[NP], v0[NP], v1[NP], w0[NP], w1[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const uint8_t* mine = second ? rb[i] : ra[i];
+    const float2 k0 = meta_sz(lds32(mine + kRecKMeta + r0 * 4));
+    const float2 k1 = meta_sz(lds32(mine + kRecKMeta + r0 * 4 + 32));
+    v0[i] = meta_sz(lds32(mine + kRecVMeta + r0 * 4));
+    v1[i] = meta_sz(lds32(mine + kRecVMeta + r0 * 4 + 32));
+    float a[4], b[4];
+    codes_dot(a, ra[i], st.qf, r0, t);
+    codes_dot(b, rb[i], st.qg, r0, t);
+    add_to(a, b);            // each is zero in the other's columns
+    const float s0 = k0.x * st.kf, s1 = k1.x * st.kf;
+    x0[i] = make_float2(fmaf(a[0], s0, st.qsum.x * k0.y), fmaf(a[1], s0, st.qsum.y * k0.y));
+    x1[i] = make_float2(fmaf(a[2], s1, st.qsum.x * k1.y), fmaf(a[3], s1, st.qsum.y * k1.y));
+    if (kMasked) {
+      const int first = p.window > 0 && ctx > p.window ? ctx - p.window : 0;
+      const int k = tok[i] + r0;
+      if (!(k < ctx && (k >= first || k < p.sinks))) {
+        x0[i] = make_float2(-INFINITY, -INFINITY);
+        v0[i] = make_float2(0.f, 0.f);
+      }
+      if (!(k + 8 < ctx && (k + 8 >= first || k + 8 < p.sinks))) {
+        x1[i] = make_float2(-INFINITY, -INFINITY);
+        v1[i] = make_float2(0.f, 0.f);
+      }
+    }
+  }
+  float2 sum;
+  auto weights = [&]() {
+    const float2 nm = make_float2(-st.m.x, -st.m.y);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const float2 d0 = __fadd2_rn(x0[i], nm), d1 = __fadd2_rn(x1[i], nm);
+      w0[i] = make_float2(ex2(d0.x), ex2(d0.y));
+      w1[i] = make_float2(ex2(d1.x), ex2(d1.y));
+      sum = i == 0 ? __fadd2_rn(w0[0], w1[0]) : __fadd2_rn(sum, __fadd2_rn(w0[i], w1[i]));
+    }
+  };
+  weights();
+  float sv = fmaxf(v0[0].x, v1[0].x);
+#pragma unroll
+  for (int i = 1; i < NP; ++i) sv = fmaxf(sv, fmaxf(v0[i].x, v1[i].x));
+  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) <= kMaxSum) || sv * st.vs > kMaxVScale)) {
+    float2 mx = x0[0];
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      mx = make_float2(fmaxf(mx.x, fmaxf(x0[i].x, x1[i].x)), fmaxf(mx.y, fmaxf(x0[i].y, x1[i].y)));
+    move_reference<k4Bit, true>(st, mx, sv);
+    weights();
+  }
+  st.l = __fadd2_rn(st.l, sum);
+  uint32_t oa[NP][2], ob[NP][2];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const float z0 = fmaf(7.5f, v0[i].x, v0[i].y), z1 = fmaf(7.5f, v1[i].x, v1[i].y);
+    st.zs.x = fmaf(w1[i].x, z1, fmaf(w0[i].x, z0, st.zs.x));
+    st.zs.y = fmaf(w1[i].y, z1, fmaf(w0[i].y, z0, st.zs.y));
+    const float e0 = v0[i].x * st.vs, e1 = v1[i].x * st.vs;
+    w0[i] = make_float2(w0[i].x * e0, w0[i].y * e0);
+    w1[i] = make_float2(w1[i].x * e1, w1[i].y * e1);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float2 w = r == 0 ? w0[i] : w1[i];
+      const uint32_t hi = pack16<k4Bit>(w);
+      const float2 back = unpack16<k4Bit>(hi);
+      const uint32_t lo =
+          __shfl_xor_sync(kFull, pack16<k4Bit>(make_float2(w.x - back.x, w.y - back.y)), 2);
+      oa[i][r] = transpose8(second ? lo : hi);
+      ob[i][r] = transpose8(second ? hi : lo);
+    }
+  }
+  float d[4][4];
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    uint32_t wa[4], wb[4];
+    load_v(wa, ra[k], g, t);
+    load_v(wb, rb[k], g, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t a[4];
+      v_operand(a, wa, i);
+      if (k == 0)
+        mma_f16_0(d[i], a[0], a[1], a[2], a[3], oa[k][0], oa[k][1]);
+      else
+        mma_f16(d[i], a[0], a[1], a[2], a[3], oa[k][0], oa[k][1]);
+      v_operand(a, wb, i);
+      mma_f16(d[i], a[0], a[1], a[2], a[3], ob[k][0], ob[k][1]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) add_to(st.acc[i], d[i]);
+}
+
+// One chunk: the bf16 cache, and the 4-bit cache with more than four query
+// heads.  4-bit: `chunk` is the record; bf16: the K tile, the V tile v_off
+// behind.
+template <int F, bool kLoCols, bool kMasked>
+__device__ __forceinline__ void process(State& st, const Params& p, const uint8_t* chunk,
+                                        uint32_t v_off, int tok0, int ctx) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int r0 = row_token<F>(g);
   const int first = p.window > 0 && ctx > p.window ? ctx - p.window : 0;
   auto seen = [&](int tok) { return tok < ctx && (tok >= first || tok < p.sinks); };
 
-  // --- scores: c[0..1] row g, c[2..3] row g + 8
-  float2 x[NCH][2];
-#pragma unroll
-  for (int ch = 0; ch < NCH; ++ch) {
-    float c[4];
-    if constexpr (F == k4Bit) {
-      const uint2 a = *reinterpret_cast<const uint2*>(kb[ch] + r0 * kRowCodes + t * 8);
-      const uint2 b = *reinterpret_cast<const uint2*>(kb[ch] + r1 * kRowCodes + t * 8);
-      const float2 m0 = meta_sz(*reinterpret_cast<const uint32_t*>(kb[ch] + kRecKMeta + r0 * 4));
-      const float2 m1 = meta_sz(*reinterpret_cast<const uint32_t*>(kb[ch] + kRecKMeta + r1 * 4));
-      constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
-      mma_f16_0(c, a.x & kLo, b.x & kLo, a.x & kHi, b.x & kHi, st.qf[0][0], st.qf[0][1]);
-      mma_f16(c, (a.x >> 8) & kLo, (b.x >> 8) & kLo, (a.x >> 8) & kHi, (b.x >> 8) & kHi,
-              st.qf[1][0], st.qf[1][1]);
-      mma_f16(c, a.y & kLo, b.y & kLo, a.y & kHi, b.y & kHi, st.qf[2][0], st.qf[2][1]);
-      mma_f16(c, (a.y >> 8) & kLo, (b.y >> 8) & kLo, (a.y >> 8) & kHi, (b.y >> 8) & kHi,
-              st.qf[3][0], st.qf[3][1]);
-      const float s0 = m0.x * st.kf, s1 = m1.x * st.kf;
-      x[ch][0] = __ffma2_rn(make_float2(c[0], c[1]), make_float2(s0, s0),
-                            __fmul2_rn(st.qsum, make_float2(m0.y, m0.y)));
-      x[ch][1] = __ffma2_rn(make_float2(c[2], c[3]), make_float2(s1, s1),
-                            __fmul2_rn(st.qsum, make_float2(m1.y, m1.y)));
-    } else {
-      const uint32_t base = smem_addr(kb[ch]);
-      const int row = (lane & 7) + (lane & 8);          // matrices 1 and 3: rows 8..15
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t a[4];
-        ldsm4(a, base + row * 128 + (((2 * i + (lane >> 4)) ^ (row & 7)) << 4));
-        // four sums of 16 products, added in fp32 with rounding to nearest: the
-        // tensor core's own accumulation truncates
-        float d[4];
-        mma_bf16_0(i == 0 ? c : d, a[0], a[1], a[2], a[3], st.qf[i][0], st.qf[i][1]);
-        if (i > 0) {
-          const float2 e0 = add2(c[0], c[1], d[0], d[1]), e1 = add2(c[2], c[3], d[2], d[3]);
-          c[0] = e0.x; c[1] = e0.y; c[2] = e1.x; c[3] = e1.y;
-        }
-      }
-      const float2 sl = make_float2(p.scale_log2, p.scale_log2);
-      x[ch][0] = __fmul2_rn(make_float2(c[0], c[1]), sl);
-      x[ch][1] = __fmul2_rn(make_float2(c[2], c[3]), sl);
-    }
-    if (kMasked) {
-      if (!seen(tok0[ch] + r0)) x[ch][0] = make_float2(-INFINITY, -INFINITY);
-      if (!seen(tok0[ch] + r1)) x[ch][1] = make_float2(-INFINITY, -INFINITY);
-    }
-  }
-  // --- 4-bit: the V rows' scales (an unseen row: all zero)
-  float2 mv[NCH][2];
+  // --- scores: x[0] row g, x[1] row g + 8
+  float2 x[2], mv[2];
   if constexpr (F == k4Bit) {
-#pragma unroll
-    for (int ch = 0; ch < NCH; ++ch) {
-      mv[ch][0] = meta_sz(*reinterpret_cast<const uint32_t*>(kb[ch] + kRecVMeta + r0 * 4));
-      mv[ch][1] = meta_sz(*reinterpret_cast<const uint32_t*>(kb[ch] + kRecVMeta + r1 * 4));
-      if (kMasked) {
-        if (!seen(tok0[ch] + r0)) mv[ch][0] = make_float2(0.f, 0.f);
-        if (!seen(tok0[ch] + r1)) mv[ch][1] = make_float2(0.f, 0.f);
-      }
-    }
-  }
-  // --- online softmax: the reference moves only when a score passes it by 2^8
-  // (exact, one reference scales numerator and denominator)
-  float2 mx = x[0][0];
-  float sv = 0.f;
-#pragma unroll
-  for (int ch = 0; ch < NCH; ++ch)
+    float c[4];
+    codes_dot(c, chunk, st.qf, r0, t);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      mx.x = fmaxf(mx.x, x[ch][r].x);
-      mx.y = fmaxf(mx.y, x[ch][r].y);
-      if (F == k4Bit) sv = fmaxf(sv, mv[ch][r].x);
+      const float2 m = meta_sz(lds32(chunk + kRecKMeta + (r0 + 8 * r) * 4));
+      mv[r] = meta_sz(lds32(chunk + kRecVMeta + (r0 + 8 * r) * 4));
+      const float s = m.x * st.kf;
+      x[r] = make_float2(fmaf(c[2 * r], s, st.qsum.x * m.y), fmaf(c[2 * r + 1], s, st.qsum.y * m.y));
     }
-  const bool up = fmaxf(mx.x - st.m.x, mx.y - st.m.y) > kRescaleLog2;
-  if (__any_sync(kFull, up || (F == k4Bit && sv * st.vs > kMaxVScale))) {
-    float f_v = 1.f;
-    if (F == k4Bit) {
-      // the V scales' power of two: the largest seen to [32, 64)
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) sv = fmaxf(sv, __shfl_xor_sync(kFull, sv, o));
-      if (st.vs == 0.f || sv * st.vs > kMaxVScale) {
-        int e = static_cast<int>(__float_as_uint(sv) >> 23) - 127;
-        e = max(-100, min(100, e));
-        const float vs = __uint_as_float(static_cast<uint32_t>(127 + 5 - e) << 23);
-        f_v = st.vs == 0.f ? 0.f : vs / st.vs;
-        st.vs = vs;
-      }
-    }
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      mx.x = fmaxf(mx.x, __shfl_xor_sync(kFull, mx.x, o));
-      mx.y = fmaxf(mx.y, __shfl_xor_sync(kFull, mx.y, o));
-    }
-    mx.x = fmaxf(mx.x, st.m.x);
-    mx.y = fmaxf(mx.y, st.m.y);
-    float2 f = make_float2(ex2(st.m.x - mx.x), ex2(st.m.y - mx.y));
-    st.m = mx;
-    st.l = __fmul2_rn(st.l, f);
-    st.zs = __fmul2_rn(st.zs, f);
-    f.x *= f_v;
-    f.y *= f_v;
+  } else {
+    float c[4];
+    const uint32_t base = smem_addr(chunk);
+    const int row = (lane & 7) + (lane & 8);          // matrices 1 and 3: rows 8..15
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      st.acc[i][0] *= f.x;
-      st.acc[i][1] *= f.y;
-      st.acc[i][2] *= f.x;
-      st.acc[i][3] *= f.y;
+      uint32_t a[4];
+      ldsm4(a, base + row * 128 + (((2 * i + (lane >> 4)) ^ (row & 7)) << 4));
+      // four sums of 16 products, added with rounding (see add_to)
+      float d[4];
+      mma_bf16_0(i == 0 ? c : d, a[0], a[1], a[2], a[3], st.qf[i][0], st.qf[i][1]);
+      if (i > 0) add_to(c, d);
     }
+    const float2 sl = make_float2(p.scale_log2, p.scale_log2);
+    x[0] = __fmul2_rn(make_float2(c[0], c[1]), sl);
+    x[1] = __fmul2_rn(make_float2(c[2], c[3]), sl);
+    mv[0] = mv[1] = make_float2(0.f, 0.f);
   }
-  const float2 nm = make_float2(-st.m.x, -st.m.y);
-  float sum[4][4];
+  if (kMasked) {
 #pragma unroll
-  for (int ch = 0; ch < NCH; ++ch) {
-    // --- weights, as the column operand of P V: rows of the transposed matrix
-    // are the heads, its columns the tokens
-    uint32_t hi[2], lo[2], lo2[2];
+    for (int r = 0; r < 2; ++r)
+      if (!seen(tok0 + r0 + 8 * r)) {
+        x[r] = make_float2(-INFINITY, -INFINITY);
+        mv[r] = make_float2(0.f, 0.f);
+      }
+  }
+  // --- online softmax
+  float2 w[2], sum;
+  auto weights = [&]() {
+    const float2 nm = make_float2(-st.m.x, -st.m.y);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const float2 d = __fadd2_rn(x[ch][r], nm);
-      float2 w = make_float2(ex2(d.x), ex2(d.y));
-      st.l = __fadd2_rn(st.l, w);
-      if constexpr (F == k4Bit) {
-        const float zc = fmaf(7.5f, mv[ch][r].x, mv[ch][r].y);
-        st.zs = __ffma2_rn(w, make_float2(zc, zc), st.zs);
-        const float sc = mv[ch][r].x * st.vs;
-        w = __fmul2_rn(w, make_float2(sc, sc));
-      }
-      hi[r] = pack16<F>(w);
-      float2 back = unpack16<F>(hi[r]);
-      w = make_float2(w.x - back.x, w.y - back.y);
-      lo[r] = pack16<F>(w);
-      if (F == kBf16) {
-        back = unpack16<F>(lo[r]);
-        lo2[r] = transpose8(pack16<F>(make_float2(w.x - back.x, w.y - back.y)));
-      }
-      if (kLoCols && t >= 2) hi[r] = lo[r];
-      hi[r] = transpose8(hi[r]);
-      if (!kLoCols) lo[r] = transpose8(lo[r]);
+      const float2 d = __fadd2_rn(x[r], nm);
+      w[r] = make_float2(ex2(d.x), ex2(d.y));
     }
-    // --- O^T += V^T P^T
+    sum = __fadd2_rn(w[0], w[1]);
+  };
+  weights();
+  const float sv = fmaxf(mv[0].x, mv[1].x);
+  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) <= kMaxSum) || (F == k4Bit && sv * st.vs > kMaxVScale))) {
+    move_reference<F, false>(st, make_float2(fmaxf(x[0].x, x[1].x), fmaxf(x[0].y, x[1].y)), sv);
+    weights();
+  }
+  st.l = __fadd2_rn(st.l, sum);
+  // --- weights as the column operand of P V: rows of the transposed matrix are
+  // the heads, its columns the tokens
+  uint32_t hi[2], lo[2], lo2[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
     if constexpr (F == k4Bit) {
-      const uint8_t* vb = kb[ch] + kRecV + g * 4;
-      const int ta = row_token<F>(2 * t), tb = row_token<F>(2 * t + 1);
-      const uint32_t y0 = *reinterpret_cast<const uint32_t*>(vb + ta * kRowCodes);
-      const uint32_t y1 = *reinterpret_cast<const uint32_t*>(vb + tb * kRowCodes);
-      const uint32_t y2 = *reinterpret_cast<const uint32_t*>(vb + (8 + ta) * kRowCodes);
-      const uint32_t y3 = *reinterpret_cast<const uint32_t*>(vb + (8 + tb) * kRowCodes);
-      // two tokens' codes of one dimension side by side
-      const uint32_t w0[2] = {__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632)};
-      const uint32_t w1[2] = {__byte_perm(y2, y3, 0x5410), __byte_perm(y2, y3, 0x7632)};
-      constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
-      constexpr uint32_t k15 = 0x800f800fu, k240 = 0x80f080f0u;   // -15 and -240 times 2^-24
+      const float zc = fmaf(7.5f, mv[r].x, mv[r].y), sc = mv[r].x * st.vs;
+      st.zs.x = fmaf(w[r].x, zc, st.zs.x);
+      st.zs.y = fmaf(w[r].y, zc, st.zs.y);
+      w[r].x *= sc;
+      w[r].y *= sc;
+    }
+    hi[r] = pack16<F>(w[r]);
+    float2 back = unpack16<F>(hi[r]);
+    const float2 rest = make_float2(w[r].x - back.x, w[r].y - back.y);
+    lo[r] = pack16<F>(rest);
+    if (F == kBf16) {
+      back = unpack16<F>(lo[r]);
+      lo2[r] = transpose8(pack16<F>(make_float2(rest.x - back.x, rest.y - back.y)));
+    }
+    if (kLoCols && t >= 2) hi[r] = lo[r];
+    hi[r] = transpose8(hi[r]);
+    if (!kLoCols) lo[r] = transpose8(lo[r]);
+  }
+  // --- O^T += V^T P^T
+  if constexpr (F == k4Bit) {
+    uint32_t wv[4];
+    load_v(wv, chunk, g, t);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t u0 = (i & 1) ? w0[i >> 1] >> 8 : w0[i >> 1];
-        const uint32_t u1 = (i & 1) ? w1[i >> 1] >> 8 : w1[i >> 1];
-        const uint32_t a0 = half2_twice_plus(u0 & kLo, k15), a1 = half2_twice_plus(u0 & kHi, k240);
-        const uint32_t a2 = half2_twice_plus(u1 & kLo, k15), a3 = half2_twice_plus(u1 & kHi, k240);
-        if (ch == 0)
-          mma_f16_0(sum[i], a0, a1, a2, a3, hi[0], hi[1]);
-        else
-          mma_f16(sum[i], a0, a1, a2, a3, hi[0], hi[1]);
-        if (!kLoCols) mma_f16(sum[i], a0, a1, a2, a3, lo[0], lo[1]);
-      }
-    } else {
-      const uint32_t base = smem_addr(kb[ch] + v_off);
-      const int tok = (lane & 7) + ((lane >> 4) << 3);  // matrices 2 and 3: tokens 8..15
-      uint32_t keep[2] = {kFull, kFull};
-      if (kMasked) {                                    // unseen slots may hold anything
+    for (int i = 0; i < 4; ++i) {
+      uint32_t a[4];
+      float o[4];
+      v_operand(a, wv, i);
+      mma_f16_0(o, a[0], a[1], a[2], a[3], hi[0], hi[1]);
+      mma_f16(o, a[0], a[1], a[2], a[3], lo[0], lo[1]);
+      add_to(st.acc[i], o);
+    }
+  } else {
+    const uint32_t base = smem_addr(chunk + v_off);
+    const int tok = (lane & 7) + ((lane >> 4) << 3);  // matrices 2 and 3: tokens 8..15
+    uint32_t keep[2] = {kFull, kFull};
+    if (kMasked) {                                    // unseen slots may hold anything
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          keep[r] = (seen(tok0[ch] + 8 * r + 2 * t) ? 0x0000ffffu : 0u) |
-                    (seen(tok0[ch] + 8 * r + 2 * t + 1) ? 0xffff0000u : 0u);
-      }
+      for (int r = 0; r < 2; ++r)
+        keep[r] = (seen(tok0 + 8 * r + 2 * t) ? 0x0000ffffu : 0u) |
+                  (seen(tok0 + 8 * r + 2 * t + 1) ? 0xffff0000u : 0u);
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t a[4];
-        ldsm4_t(a, base + tok * 128 + (((2 * i + ((lane >> 3) & 1)) ^ (tok & 7)) << 4));
-        if (kMasked) {
-          a[0] &= keep[0];
-          a[1] &= keep[0];
-          a[2] &= keep[1];
-          a[3] &= keep[1];
-        }
-        if (ch == 0)
-          mma_bf16_0(sum[i], a[0], a[1], a[2], a[3], hi[0], hi[1]);
-        else
-          mma_bf16(sum[i], a[0], a[1], a[2], a[3], hi[0], hi[1]);
-        if (!kLoCols) mma_bf16(sum[i], a[0], a[1], a[2], a[3], lo[0], lo[1]);
-        mma_bf16(sum[i], a[0], a[1], a[2], a[3], lo2[0], lo2[1]);
+    for (int i = 0; i < 4; ++i) {
+      uint32_t a[4];
+      float o[4];
+      ldsm4_t(a, base + tok * 128 + (((2 * i + ((lane >> 3) & 1)) ^ (tok & 7)) << 4));
+      if (kMasked) {
+        a[0] &= keep[0];
+        a[1] &= keep[0];
+        a[2] &= keep[1];
+        a[3] &= keep[1];
       }
+      mma_bf16_0(o, a[0], a[1], a[2], a[3], hi[0], hi[1]);
+      if (!kLoCols) mma_bf16(o, a[0], a[1], a[2], a[3], lo[0], lo[1]);
+      mma_bf16(o, a[0], a[1], a[2], a[3], lo2[0], lo2[1]);
+      add_to(st.acc[i], o);
     }
   }
-  // The tensor core truncates what it accumulates, which over a long context
-  // would pull the sums towards zero; across chunks they add up here, rounded.
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int k = 0; k < 4; k += 2) {
-      const float2 e = add2(st.acc[i][k], st.acc[i][k + 1], sum[i][k], sum[i][k + 1]);
-      st.acc[i][k] = e.x;
-      st.acc[i][k + 1] = e.y;
-    }
 }
 
 // Ends a segment.  Sums the lanes' shares; with several warps a head, the
@@ -781,8 +911,9 @@ __device__ bool finish(State& st, const Params& p, uint8_t* smem, const Layout& 
   uint64_t* cempty = cfull + p.hpc;
   float* comb = reinterpret_cast<float*>(smem + L.comb);
   const int G = p.group;
+  constexpr bool kPair = F == k4Bit && kLoCols;
 #pragma unroll
-  for (int o = 4; o < 32; o <<= 1) {
+  for (int o = kPair ? 2 : 4; o < 32; o <<= 1) {
     st.l.x += __shfl_xor_sync(kFull, st.l.x, o);
     st.l.y += __shfl_xor_sync(kFull, st.l.y, o);
     if (F == k4Bit) {
@@ -870,22 +1001,26 @@ __device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars);
   uint64_t* empty = full + p.stages;
   const StageMeta* meta = reinterpret_cast<const StageMeta*>(smem + L.meta);
-  constexpr int NC = chunks_per_warp<F>();
-  const uint32_t tile = F == k4Bit ? kRecBytes : kBf16Tile;
+  constexpr bool kPair = F == k4Bit && kLoCols;
+  constexpr int NC = chunks_per_warp<F, kLoCols>();
+  constexpr uint32_t kTile = F == k4Bit ? kRecBytes : kBf16Tile;
+  const uint32_t mine = (w * p.hpc + h) * kTile;           // the warp's first chunk in a stage
+  const uint32_t step = p.wph * p.hpc * kTile;             // to its next
+  const uint32_t v_off = p.kv_bytes / 2;
 
   State st;
   int seg = 0, stage = 0;
   uint32_t ph = 0;
+  const uint8_t* base = smem;
   for (;;) {
     if (!mbar_wait(&full[stage], ph)) {
       if (lane == 0) report(p.status, kDevTimeout);
       return;
     }
-    const StageMeta md = meta[stage];
-    if (md.flags & kTerminate) return;
-    const uint32_t v_off = p.kv_bytes / 2;
-    const uint8_t* base = smem + static_cast<size_t>(stage) * p.stage_bytes;
-    if (md.flags & kSegFirst) {
+    const StageMeta& md = meta[stage];
+    const int flags = md.flags;
+    if (flags & kTerminate) return;
+    if (flags & kSegFirst) {
       load_q<F, kLoCols>(st, p, base + p.kv_bytes + h * p.group * (kD * 2));
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -895,45 +1030,62 @@ __device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
       st.l = st.zs = make_float2(0.f, 0.f);
       st.vs = 0.f;
     }
-    const uint8_t* kb0 = base + (w * p.hpc + h) * tile;      // the warp's first chunk
-    const uint32_t step = p.wph * p.hpc * tile;              // to its next
-    if (!(md.flags & kPartial)) {
-      const uint8_t* kb[NC];
-      int tok[NC];
+    if (!(flags & kPartial)) {
+      if constexpr (kPair) {
+        constexpr int NP = NC / 2;
+        const uint8_t *ra[NP], *rb[NP];
+        int tok[NP];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        kb[i] = kb0 + i * step;
-        tok[i] = 0;
+        for (int i = 0; i < NP; ++i) {
+          ra[i] = base + mine + 2 * i * step;
+          rb[i] = ra[i] + step;
+          tok[i] = 0;
+        }
+        process_pairs<NP, false>(st, p, ra, rb, tok, 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          process<F, kLoCols, false>(st, p, base + mine + i * step, v_off, 0, 0);
       }
-      process<F, kLoCols, NC, false>(st, p, kb, v_off, tok, md.ctx);
     } else {
       // a short stage, or one with slots that are not visible
-      for (int j = w; j < md.n; j += p.wph) {
-        const int v = md.v0 + j;
-        const uint8_t* kb[1] = {kb0};
-        const int tok[1] = {(v < md.ns ? v : v + md.delta) * kChunk};
-        process<F, kLoCols, 1, true>(st, p, kb, v_off, tok, md.ctx);
-        kb0 += step;
+      const int n = md.n, ctx = md.ctx, v0 = md.v0, ns = md.ns, delta = md.delta;
+      auto token_of = [&](int j) { return (v0 + j < ns ? v0 + j : v0 + j + delta) * kChunk; };
+      if constexpr (kPair) {
+        for (int j = w, i = 0; j < n; j += 2 * p.wph, ++i) {
+          // without a second chunk the first stands in for it, all unseen
+          const bool two = j + p.wph < n;
+          const uint8_t* ra[1] = {base + mine + 2 * i * step};
+          const uint8_t* rb[1] = {ra[0] + (two ? step : 0)};
+          const int tok[1] = {(lane & 2) == 0 ? token_of(j) : two ? token_of(j + p.wph) : 0x7fffff00};
+          process_pairs<1, true>(st, p, ra, rb, tok, ctx);
+        }
+      } else {
+        for (int j = w, i = 0; j < n; j += p.wph, ++i)
+          process<F, kLoCols, true>(st, p, base + mine + i * step, v_off, token_of(j), ctx);
       }
     }
+    const int seq = md.seq, record = md.record;
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[stage]);
-    if (md.flags & kSegLast) {
-      if (!finish<F, kLoCols>(st, p, smem, L, h, w, seg, md.seq, md.record)) {
+    if (flags & kSegLast) {
+      if (!finish<F, kLoCols>(st, p, smem, L, h, w, seg, seq, record)) {
         if (lane == 0) report(p.status, kDevTimeout);
         return;
       }
       ++seg;
     }
+    base += p.stage_bytes;
     if (++stage == p.stages) {
       stage = 0;
       ph ^= 1;
+      base = smem;
     }
   }
 }
 
 template <int F, bool kLoCols>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((max_warps<F, kLoCols>() + 1) * 32, 1)
     window_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -1107,19 +1259,29 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const Params&
   return launch_pdl(kern, grid, dim3((p.hpc * p.wph + 1) * 32), smem, stream, tk, tv, p);
 }
 
-// Warps per KV head: a power of two, up to 16 consumer warps in all.
-int warps_per_head(int hpc) {
-  int w = 1;
-  while (2 * w * hpc <= kMaxWarps) w *= 2;
-  return w;
+// KV heads one CTA owns: the largest divisor up to `most`.
+int heads_per_cta(int num_kv_heads, int most) {
+  int h = most;
+  while (num_kv_heads % h != 0) --h;
+  return h;
+}
+
+// The CTA's shape for a format and group size.
+template <int F, bool kLoCols>
+void shape(Params& p) {
+  p.hpc = heads_per_cta(p.hkv, max_heads<F, kLoCols>());
+  constexpr int nc = chunks_per_warp<F, kLoCols>();
+  p.wph = max_warps<F, kLoCols>() / p.hpc;
+  if (p.wph * nc > 32) p.wph = 32 / nc;       // a lane of the producer per chunk of a stage
+  p.cps = p.wph * nc;
+  p.batch = 32 / p.cps * p.cps;
 }
 
 }  // namespace
 
-int window_heads_per_cta(int num_kv_heads) {
-  for (int h = 8; h > 1; --h)
-    if (num_kv_heads % h == 0) return h;
-  return 1;
+int window_max_ctas(int num_kv_heads, int sms) {
+  const int c = sms / (num_kv_heads / heads_per_cta(num_kv_heads, 8));
+  return c < 1 ? 1 : c;
 }
 
 // m and l [2 ctas, hq], acc [2 ctas, hq, D], split [ctas], total: each part on
@@ -1149,9 +1311,13 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
   while ((kChunk << p.cpb_log2) < a.block_size) ++p.cpb_log2;
   p.window = a.window;
   p.sinks = a.window > 0 ? a.sinks : 0;
-  p.hpc = window_heads_per_cta(a.num_kv_heads);
-  p.wph = warps_per_head(p.hpc);
-  p.cps = p.wph * (four ? chunks_per_warp<k4Bit>() : chunks_per_warp<kBf16>());
+  const bool lo_cols = p.group <= 4;
+  if (!four)
+    lo_cols ? shape<kBf16, true>(p) : shape<kBf16, false>(p);
+  else
+    lo_cols ? shape<k4Bit, true>(p) : shape<k4Bit, false>(p);
+  const int groups = p.hkv / p.hpc;
+  p.ctas = a.sms / groups < 1 ? 1 : a.sms / groups;
   p.kv_bytes = p.cps * p.hpc * (four ? kRecBytes : 2 * kBf16Tile);
   p.stage_bytes = align_up(p.kv_bytes + p.hpc * p.group * kD * 2, 1024);
   const uint32_t fixed = make_layout(0, p.stage_bytes, p.hpc, p.wph, p.group).total + 1024 + 16;
@@ -1159,18 +1325,17 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
   p.stages = stages > 8 ? 8 : stages;
   if (p.stages < 2) return cudaErrorInvalidConfiguration;
   p.scale_log2 = a.scale * kLog2e;
-  p.ctas = a.ctas;
   p.seg_weight = 2;
   p.status = a.status;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  const size_t rows = 2 * static_cast<size_t>(a.ctas) * a.num_q_heads;
+  const size_t rows = 2 * static_cast<size_t>(p.ctas) * a.num_q_heads;
   const size_t ab = (rows * 4 + 255) / 256 * 256;
   p.ws_m = reinterpret_cast<float*>(ws);
   p.ws_l = reinterpret_cast<float*>(ws + ab);
   p.ws_acc = reinterpret_cast<float*>(ws + 2 * ab);
   p.ws_split = reinterpret_cast<int4*>(ws + 2 * ab + rows * kD * 4);
   p.ws_total = reinterpret_cast<long long*>(ws + 2 * ab + rows * kD * 4 +
-                                            (static_cast<size_t>(a.ctas) * 16 + 255) / 256 * 256);
+                                            (static_cast<size_t>(p.ctas) * 16 + 255) / 256 * 256);
   CUtensorMap tk = {}, tv = {};
   if (!four) {
     const long long tokens = static_cast<long long>(a.num_blocks) * a.block_size;
@@ -1179,25 +1344,25 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
       return cudaErrorInvalidValue;
   }
   const uint32_t smem = make_layout(p.stages, p.stage_bytes, p.hpc, p.wph, p.group).total + 1024;
-  const dim3 grid(a.ctas, 1, a.num_kv_heads / p.hpc);
+  const dim3 grid(p.ctas, 1, groups);
   cudaError_t e;
   if (four)
-    e = p.group <= 4 ? launch_t<k4Bit, true>(tk, tv, p, grid, smem, stream)
+    e = lo_cols ? launch_t<k4Bit, true>(tk, tv, p, grid, smem, stream)
                      : launch_t<k4Bit, false>(tk, tv, p, grid, smem, stream);
   else
-    e = p.group <= 4 ? launch_t<kBf16, true>(tk, tv, p, grid, smem, stream)
+    e = lo_cols ? launch_t<kBf16, true>(tk, tv, p, grid, smem, stream)
                      : launch_t<kBf16, false>(tk, tv, p, grid, smem, stream);
   if (e != cudaSuccess) return e;
   // a sequence has about 1 + ctas / num_seqs records: one warp a head and
   // batch of 8, up to 16
   int parts = 1;
-  while (parts < kMergeWarps && parts * kMergeBatch * a.num_seqs < a.ctas) parts *= 2;
+  while (parts < kMergeWarps && parts * kMergeBatch * a.num_seqs < p.ctas) parts *= 2;
   const int heads = parts < 4 ? 4 : kMergeWarps / parts;
   return launch_pdl(window_merge_kernel,
-                    dim3(a.num_seqs < a.ctas ? a.num_seqs : a.ctas,
+                    dim3(a.num_seqs < p.ctas ? a.num_seqs : p.ctas,
                          (a.num_q_heads + heads - 1) / heads),
                     dim3(heads * parts * 32), 0, stream, a.out, p.ws_m, p.ws_l, p.ws_acc,
-                    p.ws_split, p.ws_total, a.num_q_heads, a.ctas, parts);
+                    p.ws_split, p.ws_total, a.num_q_heads, p.ctas, parts);
 }
 
 }  // namespace tvl
