@@ -76,9 +76,9 @@ enum : int { kSegFirst = 1, kSegLast = 2, kTerminate = 4, kPartial = 8 };
 template <int F, bool kLoCols>
 __host__ __device__ constexpr int chunks_per_warp() { return F == k4Bit ? (kLoCols ? 4 : 2) : 1; }
 template <int F, bool kLoCols>
-__host__ __device__ constexpr int max_warps() { return F == k4Bit && kLoCols ? 12 : 16; }
+__host__ __device__ constexpr int max_warps() { return F == k4Bit ? 12 : 16; }
 template <int F, bool kLoCols>
-__host__ __device__ constexpr int max_heads() { return F == k4Bit && kLoCols ? 4 : 8; }
+__host__ __device__ constexpr int max_heads() { return F == k4Bit ? 4 : 8; }
 
 struct alignas(16) StageMeta {
   int seq, record, flags, n;   // n: chunks in the stage
@@ -94,10 +94,11 @@ struct Params {
   int num_seqs, hq, hkv, group, num_blocks, max_blocks;
   int cpb_log2;          // log2 of the 16-token chunks in a block
   int window, sinks;     // window 0: none
-  int hpc, wph, cps, batch, stages;
+  int hpc, wph, cps, first_cps, batch, stages;   // first_cps: chunks of a CTA's first stage
   uint32_t stage_bytes, kv_bytes;
   float scale_log2;
   int ctas, seg_weight;
+  int small;             // schedule_small serves
   float* ws_m;           // records [2 * ctas][hq]
   float* ws_l;
   float* ws_acc;
@@ -202,10 +203,56 @@ __device__ void block_scan(long long v, long long& incl, long long& total, long 
   __syncthreads();
 }
 
+// A batch of at most one sequence a thread whose line surely fits 32 bits times
+// the CTAs (the host checks): one scan, each warp adding up the totals of those
+// before it, and the threads whose sequences hold the CTA's two ends record
+// them.  Every thread whose sequence has chunks in the range prefetches their
+// block table entries for the producer.
+__device__ __forceinline__ void schedule_small(const Params& p, Schedule* sc, int* tmp) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  const int w = p.seg_weight;
+  Visible vis = {0, 0, 0};
+  if (tid < p.num_seqs) vis = visible_of(p, load_ctx(p, tid));
+  const int mine = vis.n > 0 ? vis.n + w : 0;
+  int x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) tmp[warp] = x;
+  if (tid == 0) {
+    sc->seq0 = sc->seq_end = p.num_seqs;
+    sc->v0 = sc->v_end = 0;
+  }
+  __syncthreads();
+  const int part = lane < nw ? tmp[lane] : 0;
+  const int total = __reduce_add_sync(kFull, part);
+  const int excl = __reduce_add_sync(kFull, lane < warp ? part : 0) + x - mine;
+  const int lo = static_cast<uint32_t>(total) * blockIdx.x / static_cast<uint32_t>(p.ctas);
+  const int hi = static_cast<uint32_t>(total) * (blockIdx.x + 1) / static_cast<uint32_t>(p.ctas);
+  if (mine > 0 && excl <= lo && lo < excl + mine) {
+    sc->seq0 = tid;
+    sc->v0 = max(0, lo - excl - w);
+  }
+  if (mine > 0 && excl <= hi && hi < excl + mine) {
+    sc->seq_end = tid;
+    sc->v_end = max(0, hi - excl - w);
+  }
+  if (tid == 0) {
+    sc->total = total;
+    sc->hi = hi;
+  }
+  const int a = max(0, lo - excl - w), b = min(vis.n, hi - excl - w);
+  const int32_t* row = p.block_tables + static_cast<long long>(tid) * p.max_blocks;
+  for (int v = a; v < b; v += 32 << p.cpb_log2)
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(row + ((v < vis.ns ? v : v + vis.delta) >> p.cpb_log2)));
+}
+
 // Every thread sums the costs of a contiguous slice of the sequences; one
 // scan places the slices on the line, and the threads whose slices hold this
 // CTA's two ends walk them again.
-__device__ void make_schedule(const Params& p, Schedule* sc, long long* tmp) {
+__device__ __noinline__ void make_schedule(const Params& p, Schedule* sc, long long* tmp) {
   const int tid = threadIdx.x, cta = blockIdx.x, w = p.seg_weight;
   const int per = (p.num_seqs + blockDim.x - 1) / blockDim.x;
   const int s_lo = min(p.num_seqs, tid * per), s_hi = min(p.num_seqs, s_lo + per);
@@ -262,7 +309,7 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
     prefetch_tensormap(tm_v);
   }
 
-  int st = 0, filled = 0;        // next stage; stages filled so far, capped
+  int st = 0, filled = 0, it = 0;   // next stage; stages filled so far, capped; fills
   uint32_t ph = 0;               // parity of the fill before the next one of stage st
   bool ok = true;
   auto acquire = [&]() {
@@ -331,8 +378,8 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
       // the next batch's entries (of this segment or the next) are fetched while
       // this batch's copies are issued
       const int ntbl = vb + p.batch < g.e ? entry(g, vb + p.batch) : (have_next ? entry(nx, nx.v) : 0);
-      for (int v = vb; v < g.e && v < vb + p.batch; v += p.cps) {
-        const int n = min(p.cps, g.e - v);
+      for (int v = vb; v < g.e && v < vb + p.batch;) {
+        const int n = min(min(it == 0 ? p.first_cps : p.cps, vb + p.batch - v), g.e - v);
         if (!acquire()) break;
         uint8_t* base = smem + static_cast<size_t>(st) * p.stage_bytes;
         const bool first = v == g.v;
@@ -378,6 +425,8 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
           bulk_load(base + p.kv_bytes,
                     p.q + (static_cast<size_t>(g.s) * p.hq + static_cast<size_t>(h0) * p.group) * kD,
                     q_bytes, &full[st], keep_policy);
+        v += n;
+        ++it;
         advance_stage();
       }
       tbl = ntbl;
@@ -767,30 +816,108 @@ __device__ __forceinline__ void process_pairs(State& st, const Params& p, const 
   for (int i = 0; i < 4; ++i) add_to(st.acc[i], d[i]);
 }
 
-// One chunk: the bf16 cache, and the 4-bit cache with more than four query
-// heads.  4-bit: `chunk` is the record; bf16: the K tile, the V tile v_off
-// behind.
-template <int F, bool kLoCols, bool kMasked>
-__device__ __forceinline__ void process(State& st, const Params& p, const uint8_t* chunk,
-                                        uint32_t v_off, int tok0, int ctx) {
+// N chunks of a 4-bit head with five to eight query heads; tok: their first
+// tokens.  Every column is a query head, and the lo halves take products of
+// their own.
+template <int N, bool kMasked>
+__device__ __forceinline__ void process_wide(State& st, const Params& p, const uint8_t* const (&rec)[N],
+                                             const int (&tok)[N], int ctx) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int r0 = row_token<F>(g);
+  const int r0 = row_token<k4Bit>(g);
+  float2 x[N][2], mv[N][2], w[N][2];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float c[4];
+    codes_dot(c, rec[i], st.qf, r0, t);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float2 m = meta_sz(lds32(rec[i] + kRecKMeta + (r0 + 8 * r) * 4));
+      mv[i][r] = meta_sz(lds32(rec[i] + kRecVMeta + (r0 + 8 * r) * 4));
+      const float s = m.x * st.kf;
+      x[i][r] = make_float2(fmaf(c[2 * r], s, st.qsum.x * m.y), fmaf(c[2 * r + 1], s, st.qsum.y * m.y));
+      if (kMasked) {
+        const int first = p.window > 0 && ctx > p.window ? ctx - p.window : 0;
+        const int k = tok[i] + r0 + 8 * r;
+        if (!(k < ctx && (k >= first || k < p.sinks))) {
+          x[i][r] = make_float2(-INFINITY, -INFINITY);
+          mv[i][r] = make_float2(0.f, 0.f);
+        }
+      }
+    }
+  }
+  float2 sum;
+  auto weights = [&]() {
+    const float2 nm = make_float2(-st.m.x, -st.m.y);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float2 d = __fadd2_rn(x[i][r], nm);
+        w[i][r] = make_float2(ex2(d.x), ex2(d.y));
+        sum = i + r == 0 ? w[0][0] : __fadd2_rn(sum, w[i][r]);
+      }
+    }
+  };
+  weights();
+  float sv = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) sv = fmaxf(sv, fmaxf(mv[i][0].x, mv[i][1].x));
+  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) <= kMaxSum) || sv * st.vs > kMaxVScale)) {
+    float2 mx = x[0][0];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      mx = make_float2(fmaxf(mx.x, fmaxf(x[i][0].x, x[i][1].x)), fmaxf(mx.y, fmaxf(x[i][0].y, x[i][1].y)));
+    move_reference<k4Bit, false>(st, mx, sv);
+    weights();
+  }
+  st.l = __fadd2_rn(st.l, sum);
+  uint32_t hi[N][2], lo[N][2];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float zc = fmaf(7.5f, mv[i][r].x, mv[i][r].y), sc = mv[i][r].x * st.vs;
+      st.zs.x = fmaf(w[i][r].x, zc, st.zs.x);
+      st.zs.y = fmaf(w[i][r].y, zc, st.zs.y);
+      const float2 v = make_float2(w[i][r].x * sc, w[i][r].y * sc);
+      const uint32_t h = pack16<k4Bit>(v);
+      const float2 back = unpack16<k4Bit>(h);
+      hi[i][r] = transpose8(h);
+      lo[i][r] = transpose8(pack16<k4Bit>(make_float2(v.x - back.x, v.y - back.y)));
+    }
+  float d[4][4];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    uint32_t wv[4];
+    load_v(wv, rec[k], g, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t a[4];
+      v_operand(a, wv, i);
+      if (k == 0)
+        mma_f16_0(d[i], a[0], a[1], a[2], a[3], hi[k][0], hi[k][1]);
+      else
+        mma_f16(d[i], a[0], a[1], a[2], a[3], hi[k][0], hi[k][1]);
+      mma_f16(d[i], a[0], a[1], a[2], a[3], lo[k][0], lo[k][1]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) add_to(st.acc[i], d[i]);
+}
+
+// One chunk of the bf16 cache: `chunk` is the K tile, the V tile lies v_off
+// behind.  P is three bf16 parts: hi and lo share the columns with up to four
+// query heads, and take a product each with more.
+template <bool kLoCols, bool kMasked>
+__device__ __forceinline__ void process_bf16(State& st, const Params& p, const uint8_t* chunk,
+                                             uint32_t v_off, int tok0, int ctx) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int first = p.window > 0 && ctx > p.window ? ctx - p.window : 0;
   auto seen = [&](int tok) { return tok < ctx && (tok >= first || tok < p.sinks); };
 
   // --- scores: x[0] row g, x[1] row g + 8
-  float2 x[2], mv[2];
-  if constexpr (F == k4Bit) {
-    float c[4];
-    codes_dot(c, chunk, st.qf, r0, t);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float2 m = meta_sz(lds32(chunk + kRecKMeta + (r0 + 8 * r) * 4));
-      mv[r] = meta_sz(lds32(chunk + kRecVMeta + (r0 + 8 * r) * 4));
-      const float s = m.x * st.kf;
-      x[r] = make_float2(fmaf(c[2 * r], s, st.qsum.x * m.y), fmaf(c[2 * r + 1], s, st.qsum.y * m.y));
-    }
-  } else {
+  float2 x[2];
+  {
     float c[4];
     const uint32_t base = smem_addr(chunk);
     const int row = (lane & 7) + (lane & 8);          // matrices 1 and 3: rows 8..15
@@ -806,15 +933,11 @@ __device__ __forceinline__ void process(State& st, const Params& p, const uint8_
     const float2 sl = make_float2(p.scale_log2, p.scale_log2);
     x[0] = __fmul2_rn(make_float2(c[0], c[1]), sl);
     x[1] = __fmul2_rn(make_float2(c[2], c[3]), sl);
-    mv[0] = mv[1] = make_float2(0.f, 0.f);
   }
   if (kMasked) {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
-      if (!seen(tok0 + r0 + 8 * r)) {
-        x[r] = make_float2(-INFINITY, -INFINITY);
-        mv[r] = make_float2(0.f, 0.f);
-      }
+      if (!seen(tok0 + g + 8 * r)) x[r] = make_float2(-INFINITY, -INFINITY);
   }
   // --- online softmax
   float2 w[2], sum;
@@ -828,9 +951,9 @@ __device__ __forceinline__ void process(State& st, const Params& p, const uint8_
     sum = __fadd2_rn(w[0], w[1]);
   };
   weights();
-  const float sv = fmaxf(mv[0].x, mv[1].x);
-  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) <= kMaxSum) || (F == k4Bit && sv * st.vs > kMaxVScale))) {
-    move_reference<F, false>(st, make_float2(fmaxf(x[0].x, x[1].x), fmaxf(x[0].y, x[1].y)), sv);
+  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) <= kMaxSum))) {
+    move_reference<kBf16, false>(
+        st, make_float2(fmaxf(x[0].x, x[1].x), fmaxf(x[0].y, x[1].y)), 0.f);
     weights();
   }
   st.l = __fadd2_rn(st.l, sum);
@@ -839,64 +962,42 @@ __device__ __forceinline__ void process(State& st, const Params& p, const uint8_
   uint32_t hi[2], lo[2], lo2[2];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    if constexpr (F == k4Bit) {
-      const float zc = fmaf(7.5f, mv[r].x, mv[r].y), sc = mv[r].x * st.vs;
-      st.zs.x = fmaf(w[r].x, zc, st.zs.x);
-      st.zs.y = fmaf(w[r].y, zc, st.zs.y);
-      w[r].x *= sc;
-      w[r].y *= sc;
-    }
-    hi[r] = pack16<F>(w[r]);
-    float2 back = unpack16<F>(hi[r]);
+    hi[r] = pack16<kBf16>(w[r]);
+    float2 back = unpack16<kBf16>(hi[r]);
     const float2 rest = make_float2(w[r].x - back.x, w[r].y - back.y);
-    lo[r] = pack16<F>(rest);
-    if (F == kBf16) {
-      back = unpack16<F>(lo[r]);
-      lo2[r] = transpose8(pack16<F>(make_float2(rest.x - back.x, rest.y - back.y)));
-    }
+    lo[r] = pack16<kBf16>(rest);
+    back = unpack16<kBf16>(lo[r]);
+    lo2[r] = transpose8(pack16<kBf16>(make_float2(rest.x - back.x, rest.y - back.y)));
     if (kLoCols && t >= 2) hi[r] = lo[r];
     hi[r] = transpose8(hi[r]);
     if (!kLoCols) lo[r] = transpose8(lo[r]);
   }
+  if (kLoCols && g >= 4) lo2[0] = lo2[1] = 0u;        // columns 4..7 hold the lo parts' sums
   // --- O^T += V^T P^T
-  if constexpr (F == k4Bit) {
-    uint32_t wv[4];
-    load_v(wv, chunk, g, t);
+  const uint32_t base = smem_addr(chunk + v_off);
+  const int tok = (lane & 7) + ((lane >> 4) << 3);    // matrices 2 and 3: tokens 8..15
+  uint32_t keep[2] = {kFull, kFull};
+  if (kMasked) {                                      // unseen slots may hold anything
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t a[4];
-      float o[4];
-      v_operand(a, wv, i);
-      mma_f16_0(o, a[0], a[1], a[2], a[3], hi[0], hi[1]);
-      mma_f16(o, a[0], a[1], a[2], a[3], lo[0], lo[1]);
-      add_to(st.acc[i], o);
-    }
-  } else {
-    const uint32_t base = smem_addr(chunk + v_off);
-    const int tok = (lane & 7) + ((lane >> 4) << 3);  // matrices 2 and 3: tokens 8..15
-    uint32_t keep[2] = {kFull, kFull};
-    if (kMasked) {                                    // unseen slots may hold anything
+    for (int r = 0; r < 2; ++r)
+      keep[r] = (seen(tok0 + 8 * r + 2 * t) ? 0x0000ffffu : 0u) |
+                (seen(tok0 + 8 * r + 2 * t + 1) ? 0xffff0000u : 0u);
+  }
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-        keep[r] = (seen(tok0 + 8 * r + 2 * t) ? 0x0000ffffu : 0u) |
-                  (seen(tok0 + 8 * r + 2 * t + 1) ? 0xffff0000u : 0u);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t a[4];
+    float o[4];
+    ldsm4_t(a, base + tok * 128 + (((2 * i + ((lane >> 3) & 1)) ^ (tok & 7)) << 4));
+    if (kMasked) {
+      a[0] &= keep[0];
+      a[1] &= keep[0];
+      a[2] &= keep[1];
+      a[3] &= keep[1];
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t a[4];
-      float o[4];
-      ldsm4_t(a, base + tok * 128 + (((2 * i + ((lane >> 3) & 1)) ^ (tok & 7)) << 4));
-      if (kMasked) {
-        a[0] &= keep[0];
-        a[1] &= keep[0];
-        a[2] &= keep[1];
-        a[3] &= keep[1];
-      }
-      mma_bf16_0(o, a[0], a[1], a[2], a[3], hi[0], hi[1]);
-      if (!kLoCols) mma_bf16(o, a[0], a[1], a[2], a[3], lo[0], lo[1]);
-      mma_bf16(o, a[0], a[1], a[2], a[3], lo2[0], lo2[1]);
-      add_to(st.acc[i], o);
-    }
+    mma_bf16_0(o, a[0], a[1], a[2], a[3], hi[0], hi[1]);
+    if (!kLoCols) mma_bf16(o, a[0], a[1], a[2], a[3], lo[0], lo[1]);
+    mma_bf16(o, a[0], a[1], a[2], a[3], lo2[0], lo2[1]);
+    add_to(st.acc[i], o);
   }
 }
 
@@ -1030,6 +1131,7 @@ __device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
       st.l = st.zs = make_float2(0.f, 0.f);
       st.vs = 0.f;
     }
+    const uint8_t* at = base + mine;
     if (!(flags & kPartial)) {
       if constexpr (kPair) {
         constexpr int NP = NC / 2;
@@ -1037,32 +1139,58 @@ __device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
         int tok[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          ra[i] = base + mine + 2 * i * step;
+          ra[i] = at + 2 * i * step;
           rb[i] = ra[i] + step;
           tok[i] = 0;
         }
         process_pairs<NP, false>(st, p, ra, rb, tok, 0);
+      } else if constexpr (F == k4Bit) {
+        const uint8_t* rec[NC];
+        int tok[NC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          rec[i] = at + i * step;
+          tok[i] = 0;
+        }
+        process_wide<NC, false>(st, p, rec, tok, 0);
       } else {
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
-          process<F, kLoCols, false>(st, p, base + mine + i * step, v_off, 0, 0);
+        for (int i = 0; i < NC; ++i) process_bf16<kLoCols, false>(st, p, at + i * step, v_off, 0, 0);
       }
     } else {
       // a short stage, or one with slots that are not visible
       const int n = md.n, ctx = md.ctx, v0 = md.v0, ns = md.ns, delta = md.delta;
       auto token_of = [&](int j) { return (v0 + j < ns ? v0 + j : v0 + j + delta) * kChunk; };
+      const int cnt = n > w ? (n - w + p.wph - 1) / p.wph : 0;      // the warp's chunks
+      // a missing chunk of a group is stood in for by the first, all unseen
+      auto rec_of = [&](int i) { return at + (i < cnt ? i : 0) * step; };
+      auto tok_of = [&](int i) { return i < cnt ? token_of(w + i * p.wph) : 0x7fffff00; };
       if constexpr (kPair) {
-        for (int j = w, i = 0; j < n; j += 2 * p.wph, ++i) {
-          // without a second chunk the first stands in for it, all unseen
-          const bool two = j + p.wph < n;
-          const uint8_t* ra[1] = {base + mine + 2 * i * step};
-          const uint8_t* rb[1] = {ra[0] + (two ? step : 0)};
-          const int tok[1] = {(lane & 2) == 0 ? token_of(j) : two ? token_of(j + p.wph) : 0x7fffff00};
+        if (cnt > 2) {
+          const uint8_t* ra[2] = {rec_of(0), rec_of(2)};
+          const uint8_t* rb[2] = {rec_of(1), rec_of(3)};
+          const int o = (lane & 2) >> 1;
+          const int tok[2] = {tok_of(o), tok_of(2 + o)};
+          process_pairs<2, true>(st, p, ra, rb, tok, ctx);
+        } else if (cnt > 0) {
+          const uint8_t* ra[1] = {rec_of(0)};
+          const uint8_t* rb[1] = {rec_of(1)};
+          const int tok[1] = {tok_of((lane & 2) >> 1)};
           process_pairs<1, true>(st, p, ra, rb, tok, ctx);
         }
+      } else if constexpr (F == k4Bit) {
+        if (cnt > 1) {
+          const uint8_t* rec[2] = {rec_of(0), rec_of(1)};
+          const int tok[2] = {tok_of(0), tok_of(1)};
+          process_wide<2, true>(st, p, rec, tok, ctx);
+        } else if (cnt > 0) {
+          const uint8_t* rec[1] = {rec_of(0)};
+          const int tok[1] = {tok_of(0)};
+          process_wide<1, true>(st, p, rec, tok, ctx);
+        }
       } else {
-        for (int j = w, i = 0; j < n; j += p.wph, ++i)
-          process<F, kLoCols, true>(st, p, base + mine + i * step, v_off, token_of(j), ctx);
+        for (int i = 0; i < cnt; ++i)
+          process_bf16<kLoCols, true>(st, p, rec_of(i), v_off, tok_of(i), ctx);
       }
     }
     const int seq = md.seq, record = md.record;
@@ -1111,7 +1239,10 @@ __global__ void __launch_bounds__((max_warps<F, kLoCols>() + 1) * 32, 1)
   }
   grid_dependency_wait();        // inputs may come from the preceding kernel
   grid_dependents_launch();
-  make_schedule(p, sched, tmp);
+  if (p.small)
+    schedule_small(p, sched, reinterpret_cast<int*>(tmp));
+  else
+    make_schedule(p, sched, tmp);
   __syncthreads();
   const Schedule sc = *sched;
   if (warp == consumers) {
@@ -1145,6 +1276,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 2)
                         const int4* ws_split, const long long* ws_total, int hq, int ctas,
                         int parts) {
   __shared__ float pm[kMergeWarps], pl[kMergeWarps], po[kMergeWarps][kD];
+  grid_dependents_launch();        // the next kernel waits for this one's memory itself
   grid_dependency_wait();
   const int4 sp = ws_split[blockIdx.x];
   if (sp.x < 0) return;
@@ -1274,6 +1406,7 @@ void shape(Params& p) {
   p.wph = max_warps<F, kLoCols>() / p.hpc;
   if (p.wph * nc > 32) p.wph = 32 / nc;       // a lane of the producer per chunk of a stage
   p.cps = p.wph * nc;
+  p.first_cps = nc == 4 ? 2 * p.wph : p.wph;
   p.batch = 32 / p.cps * p.cps;
 }
 
@@ -1325,7 +1458,9 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
   p.stages = stages > 8 ? 8 : stages;
   if (p.stages < 2) return cudaErrorInvalidConfiguration;
   p.scale_log2 = a.scale * kLog2e;
-  p.seg_weight = 2;
+  p.seg_weight = four ? 10 : 2;
+  const long long longest = (static_cast<long long>(a.max_blocks_per_seq) << p.cpb_log2) + p.seg_weight;
+  p.small = a.num_seqs <= (p.hpc * p.wph + 1) * 32 && longest * a.num_seqs * (p.ctas + 1) < (1LL << 31);
   p.status = a.status;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const size_t rows = 2 * static_cast<size_t>(p.ctas) * a.num_q_heads;
