@@ -6,8 +6,8 @@
 //   z = min x,  s = bf16 rounded up of (max x - z) / 15,
 //   c_d = min(15, rint((x_d - z) / s))   (ties to even; s = 0: all 0),
 // so |s c_d + z - x_d| <= s / 2.  s is rounded up, so the largest value needs
-// no code above 15; the division is IEEE's, because bf16 inputs make exact ties
-// common and a product with 1 / s would break them either way.
+// no code above 15.  bf16 inputs make exact ties common, so the quotient's
+// rounding is the exact one (row_codes).
 //
 // Bound: HBM bandwidth for a prefill chunk (per token 256 Hkv bytes in, 72 Hkv
 // out, and q both ways), latency for a decode step.  Eight lanes hold a row, 16
@@ -84,7 +84,52 @@ __device__ __forceinline__ uint4 rotate(uint4 w, const Turn& t) {
   return narrow(x);
 }
 
-// blockIdx.y: the token's part -- parts_q of 16 q rows, then 16 K and V rows each.
+// A row's (s, z) from its extremes, and the codes of this lane's eight values.
+//
+// c = rint((x - z) / s), ties to even, without a division a value: t = d * inv
+// rounded to an integer is off by at most one, and only next to a tie (inv is
+// within 2^-24 of 1 / s and d / s <= 15).  The residual e = d - t s is exact, so
+// |e| > s / 2, or = with t odd, says that the other neighbour is the nearer or
+// the even one.  Rows whose scale is too small for 1 / s take the division.
+__device__ __forceinline__ uint32_t row_codes(const Eight& x, float mn, float s) {
+  constexpr float kMagic = 12582912.f;             // 1.5 * 2^23: adding it rounds to an integer
+  if (s < 1e-36f) {
+    uint32_t code = 0;
+    if (s > 0.f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = (j & 1) ? x.v[j >> 1].y : x.v[j >> 1].x;
+        code |= static_cast<uint32_t>(min(__float2int_rn(__fdiv_rn(v - mn, s)), 15)) << (4 * j);
+      }
+    }
+    return code;
+  }
+  const float inv = __fdiv_rn(1.0f, s), half = 0.5f * s;
+  float c[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 d = __fadd2_rn(x.v[j], make_float2(-mn, -mn));
+    const float2 t = __ffma2_rn(d, make_float2(inv, inv), make_float2(kMagic, kMagic));
+    const float2 r = __fadd2_rn(t, make_float2(-kMagic, -kMagic));
+    const float2 e = __ffma2_rn(r, make_float2(-s, -s), d);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float ev = k ? e.y : e.x;
+      const int odd = __float_as_int(k ? t.y : t.x) & 1;
+      // over > 0, or = +0 with an odd code
+      const float over = fabsf(ev) - half;
+      const bool fix = __float_as_int(over) + odd > 0;
+      c[2 * j + k] = (k ? r.y : r.x) + (fix ? copysignf(1.0f, ev) : 0.0f);
+    }
+  }
+  // four codes are exact in one float: c0 + 16 c1 + 256 c2 + 4096 c3
+  const float lo = fmaf(4096.f, c[3], fmaf(256.f, c[2], fmaf(16.f, c[1], c[0]))) + kMagic;
+  const float hi = fmaf(4096.f, c[7], fmaf(256.f, c[6], fmaf(16.f, c[5], c[4]))) + kMagic;
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
+}
+
+// Block (x, y): 4 tokens, and of each the 16-row part y: parts_q of q rows, then
+// K and V rows.
 __global__ void __launch_bounds__(kWarps * 32)
     kv4_write_kernel(const WriteParams p, const RopeTurns turns) {
   __shared__ float2 trig[kWarps][kD / 2];
@@ -112,7 +157,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
   }
   Turn turn;
-  if (p.positions != nullptr) {
+  const bool rope = p.positions != nullptr && row0 - (lane >> 3) < (is_q ? p.hq : p.hkv);
+  if (rope) {
     // lane i: pair i's angle in [-1/2, 1/2) turns, then its sine and cosine
     const unsigned long long a =
         static_cast<unsigned long long>(static_cast<long long>(p.positions[t])) * turns.f[lane];
@@ -151,19 +197,19 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int i = 0; i < kIt; ++i) {
     const int r = row0 + 4 * i;
     const bool is_v = r >= p.hkv;
-    if (p.positions != nullptr) {
+    if (rope && r - (lane >> 3) < p.hkv) {       // the step holds a K row
       // the K that is quantised is the bf16 row the bf16 cache would hold
       const uint4 y = rotate(w[i], turn);
       if (!is_v) w[i] = y;
     }
-    const Eight e = widen(w[i]);
-    const float x[8] = {e.v[0].x, e.v[0].y, e.v[1].x, e.v[1].y, e.v[2].x, e.v[2].y, e.v[3].x, e.v[3].y};
-    float mn = x[0], mx = x[0], fin = 0.f;
+    const Eight x = widen(w[i]);
+    float mn = x.v[0].x, mx = mn;
+    float2 fin = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      mn = fminf(mn, x[j]);
-      mx = fmaxf(mx, x[j]);
-      fin = fmaf(x[j], 0.f, fin);              // 0 unless something is not finite
+    for (int j = 0; j < 4; ++j) {
+      mn = fminf(mn, fminf(x.v[j].x, x.v[j].y));
+      mx = fmaxf(mx, fmaxf(x.v[j].x, x.v[j].y));
+      fin = __ffma2_rn(x.v[j], make_float2(0.f, 0.f), fin);    // 0 unless something is not finite
     }
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
@@ -171,22 +217,15 @@ __global__ void __launch_bounds__(kWarps * 32)
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
     }
     const float range = mx - mn;
-    const bool bad = !(range < INFINITY) || fin != 0.f;      // NaN != 0
+    const bool bad = !(range < INFINITY) || fin.x + fin.y != 0.f;   // NaN != 0
     const bool row_bad = ((__ballot_sync(kFull, bad) >> (lane & 24)) & 0xffu) != 0;
     if (r >= rows) continue;
     uint32_t code = 0;
     uint32_t sz = 0x7fc07fc0u;          // a row that is not finite stands for NaN
     if (!row_bad) {
       const uint32_t sb = (__float_as_uint(__fdiv_rn(range, 15.0f)) + 0xffffu) & 0xffff0000u;
-      const float s = __uint_as_float(sb);
       sz = (sb >> 16) | (__float_as_uint(mn) & 0xffff0000u);
-      if (s > 0.f) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int v = __float2int_rn(__fdiv_rn(x[j] - mn, s));
-          code |= static_cast<uint32_t>(min(v, 15)) << (4 * j);
-        }
-      }
+      code = row_codes(x, mn, __uint_as_float(sb));
     } else if (c == 0) {
       report(p.status, TVL_DEV_NONFINITE);
     }

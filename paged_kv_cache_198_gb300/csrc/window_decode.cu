@@ -63,10 +63,20 @@ constexpr int kD = 64;
 constexpr int kChunk = 16;
 constexpr uint32_t kBf16Tile = kChunk * kD * 2;   // one head's K (or V) of a chunk
 constexpr float kMaxSum = 256.0f;             // a lane's weights under the reference maximum
-constexpr float kMaxVScale = 128.0f;
+constexpr float kMaxProduct = 32768.0f;        // 4-bit: a lane's weights times its V scales
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr uint32_t kSmemLimit = 227 * 1024;
+// Cost of a sequence start, in chunks: a partly filled stage, the warps' meeting
+// and the store.  Measured on batches of 64 (4-bit, 0.5k-4k tokens: 28.4 us at
+// 4, 27.3 at 16, 27.7 at 32) and 256 (bf16, window 1024: 51.2 us at 1, 50.9 at
+// 4, 51.6 at 6).
+constexpr int kSegWeight4 = 14, kSegWeight16 = 3;
+// Longest sequence (chunks) that one CTA a KV head does alone, without the split
+// and its merge.  One sequence, 8 heads, alone / split: 4-bit 512 tokens 6.5 /
+// 10.2 us, 1024 7.8 / 9.8, 2048 11.4 / 9.8; bf16 128 tokens 7.5 / 10.3, 512 9.7
+// / 11.8, 1024 12.8 / 12.3.
+constexpr int kDirectChunks4 = 80, kDirectChunks16 = 40;
 constexpr int kCombPitch = 72;                // floats a head of a warp hands over: 64 + m, l
 
 enum Format : int { kBf16 = 0, k4Bit = 1 };
@@ -94,11 +104,12 @@ struct Params {
   int num_seqs, hq, hkv, group, num_blocks, max_blocks;
   int cpb_log2;          // log2 of the 16-token chunks in a block
   int window, sinks;     // window 0: none
-  int hpc, wph, cps, first_cps, batch, stages;   // first_cps: chunks of a CTA's first stage
+  int hpc, wph, cps, batch, stages;
   uint32_t stage_bytes, kv_bytes;
   float scale_log2;
   int ctas, seg_weight;
   int small;             // schedule_small serves
+  int direct;            // CTA (x, z) does sequence x, KV head z alone; no merge
   float* ws_m;           // records [2 * ctas][hq]
   float* ws_l;
   float* ws_acc;
@@ -309,7 +320,7 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
     prefetch_tensormap(tm_v);
   }
 
-  int st = 0, filled = 0, it = 0;   // next stage; stages filled so far, capped; fills
+  int st = 0, filled = 0;        // next stage; stages filled so far, capped
   uint32_t ph = 0;               // parity of the fill before the next one of stage st
   bool ok = true;
   auto acquire = [&]() {
@@ -358,7 +369,7 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
     return p.block_tables[static_cast<long long>(g.s) * p.max_blocks + (c >> p.cpb_log2)];
   };
 
-  const bool by_seq = p.num_seqs <= p.ctas && blockIdx.z == 0;
+  const bool by_seq = p.num_seqs <= p.ctas && blockIdx.z == 0 && !p.direct;
   int4 split = make_int4(-1, 0, 0, 0);
   Segment g;
   bool have = find(sc.seq0, sc.v0, true, g);
@@ -378,8 +389,8 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
       // the next batch's entries (of this segment or the next) are fetched while
       // this batch's copies are issued
       const int ntbl = vb + p.batch < g.e ? entry(g, vb + p.batch) : (have_next ? entry(nx, nx.v) : 0);
-      for (int v = vb; v < g.e && v < vb + p.batch;) {
-        const int n = min(min(it == 0 ? p.first_cps : p.cps, vb + p.batch - v), g.e - v);
+      for (int v = vb; v < g.e && v < vb + p.batch; v += p.cps) {
+        const int n = min(p.cps, g.e - v);
         if (!acquire()) break;
         uint8_t* base = smem + static_cast<size_t>(st) * p.stage_bytes;
         const bool first = v == g.v;
@@ -425,8 +436,6 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
           bulk_load(base + p.kv_bytes,
                     p.q + (static_cast<size_t>(g.s) * p.hq + static_cast<size_t>(h0) * p.group) * kD,
                     q_bytes, &full[st], keep_policy);
-        v += n;
-        ++it;
         advance_stage();
       }
       tbl = ntbl;
@@ -434,7 +443,7 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
     g = nx;
     have = have_next;
   }
-  if (blockIdx.z == 0 && lane == 0) {
+  if (blockIdx.z == 0 && lane == 0 && !p.direct) {
     if (!by_seq) p.ws_split[cta] = split;
     if (cta == 0) *p.ws_total = sc.total;
   }
@@ -551,9 +560,8 @@ struct State {
   uint32_t qg[4][2];   // 4-bit, up to four heads: qf has columns 0..3, qg columns 4..7
   float acc[4][4];     // output rows, see out_dim
   float2 m, l, zs;     // reference maximum (log2), sum of p, sum of p (z + 8 s)
-  float2 qsum;         // 4-bit: sum(q) * scale_log2
-  float kf;            // 4-bit: factor of q . c
-  float vs;            // 4-bit: power of two on the V scales
+  float2 qsum;         // 4-bit: sum(q), in the units of q . c
+  float kf;            // 4-bit: from those units to log2
 };
 
 // acc[i][0..1] is output dimension out_dim(i, 0), acc[i][2..3] out_dim(i, 1)
@@ -590,15 +598,20 @@ __device__ __forceinline__ void load_q(State& st, const Params& p, const uint8_t
     for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
     sum += __shfl_xor_sync(kFull, sum, 1);
     sum += __shfl_xor_sync(kFull, sum, 2);
-    st.qsum.x = __shfl_sync(kFull, sum, 8 * t) * p.scale_log2;
-    st.qsum.y = __shfl_sync(kFull, sum, 8 * t + 4) * p.scale_log2;
+    // the sign of the scale goes into q (and a zero scale makes q zero), so that
+    // kf is positive and a masked -inf stays one
+    const float sign = p.scale_log2 > 0.f ? 1.f : p.scale_log2 < 0.f ? -1.f : 0.f;
     // the largest |q| of the group to [2^14, 2^15): exact in fp16 for every
     // element down to 2^-28 of it (a bf16 has 8 significant bits)
     int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
     e = max(-100, min(100, e));
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+    const float up = sign * __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
     const float up16 = up * 0.0625f;
-    st.kf = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 10 + e) << 23);
+    st.kf = fmaxf(fabsf(p.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + 10 + e) << 23),
+                  1.17549435e-38f);
+    const float unit = up * 5.9604644775390625e-08f;                 // 2^-24: a code's
+    st.qsum.x = __shfl_sync(kFull, sum, 8 * t) * unit;
+    st.qsum.y = __shfl_sync(kFull, sum, 8 * t + 4) * unit;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int d = (i >> 1) * 8 + (i & 1) * 2;
@@ -615,38 +628,35 @@ __device__ __forceinline__ void load_q(State& st, const Params& p, const uint8_t
   }
 }
 
-// Moves the reference maximum to cover the scores x (two columns a lane), and,
-// on the 4-bit cache, the power of two on the V scales to cover sv; everything
-// summed so far is rescaled.  One reference scales numerator and denominator,
-// so the result does not depend on when this happens.
+// Moves the reference maximum to cover mx (this lane's largest scores, log2), and
+// rescales what is summed so far.  4-bit: the weights meet the V scales, at
+// most sv in this lane, before they are rounded to fp16; the reference is put
+// where the largest product is 2^6 and moved when one could pass 2^15, so the
+// fp16 operand keeps 22 bits of every weight down to 2^-28 of the largest,
+// whatever the magnitude of V.  One reference scales numerator and denominator:
+// the result does not depend on it.
 template <int F, bool kPair>
 __device__ __forceinline__ void move_reference(State& st, float2 mx, float sv) {
-  float f_v = 1.f;
   constexpr int kFirst = kPair ? 2 : 4;      // a pair's two chunks share the columns' reference
-  if (F == k4Bit) {
-#pragma unroll
-    for (int o = kFirst; o < 32; o <<= 1) sv = fmaxf(sv, __shfl_xor_sync(kFull, sv, o));
-    if (st.vs == 0.f || sv * st.vs > kMaxVScale) {
-      int e = static_cast<int>(__float_as_uint(sv) >> 23) - 127;   // the largest to [32, 64)
-      e = max(-100, min(100, e));
-      const float vs = __uint_as_float(static_cast<uint32_t>(127 + 5 - e) << 23);
-      f_v = st.vs == 0.f ? 0.f : vs / st.vs;
-      st.vs = vs;
-    }
-  }
 #pragma unroll
   for (int o = kFirst; o < 32; o <<= 1) {
     mx.x = fmaxf(mx.x, __shfl_xor_sync(kFull, mx.x, o));
     mx.y = fmaxf(mx.y, __shfl_xor_sync(kFull, mx.y, o));
+    if (F == k4Bit) sv = fmaxf(sv, __shfl_xor_sync(kFull, sv, o));
   }
+  if (F == k4Bit) {
+    const int e = static_cast<int>(__float_as_uint(sv) >> 23) - 127;   // sv < 2^(e + 1)
+    const float up = static_cast<float>(max(-60, min(60, e)) - 5);
+    mx.x += up;
+    mx.y += up;
+  }
+  // never down: what was summed stays covered
   mx.x = fmaxf(mx.x, st.m.x);
   mx.y = fmaxf(mx.y, st.m.y);
-  float2 f = make_float2(ex2(st.m.x - mx.x), ex2(st.m.y - mx.y));
+  const float2 f = make_float2(ex2(st.m.x - mx.x), ex2(st.m.y - mx.y));
   st.m = mx;
   st.l = __fmul2_rn(st.l, f);
   st.zs = __fmul2_rn(st.zs, f);
-  f.x *= f_v;
-  f.y *= f_v;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     st.acc[i][0] *= f.x;
@@ -671,7 +681,7 @@ __device__ __forceinline__ uint32_t lds32(const uint8_t* p) {
 }
 
 constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
-constexpr uint32_t k15 = 0x800f800fu, k240 = 0x80f080f0u;     // -15 and -240 times 2^-24
+constexpr uint32_t k15 = 0x800f800fu, k255 = 0x80ff80ffu;     // -15 and -255 times 2^-24
 
 // Scores of a 4-bit chunk's 16 rows: c = q . codes
 __device__ __forceinline__ void codes_dot(float (&c)[4], const uint8_t* rec, const uint32_t (&qf)[4][2],
@@ -699,14 +709,18 @@ __device__ __forceinline__ void load_v(uint32_t (&w)[4], const uint8_t* rec, int
   w[2] = __byte_perm(y2, y3, 0x5410);
   w[3] = __byte_perm(y2, y3, 0x7632);
 }
-// rows 2 i, 2 i + 1 of the lane's dimensions as the row operand, codes centred
+// Rows 2 i, 2 i + 1 of the lane's dimensions as the row operand, centred: the
+// even dimension's codes, 2 c - 15, and the whole bytes, 2 b - 255.  As b = c +
+// 16 c', the odd dimension's 16 (2 c' - 15) is the difference, taken once at the
+// segment's end; a byte costs one operation to isolate, its high half two.
 __device__ __forceinline__ void v_operand(uint32_t (&a)[4], const uint32_t (&w)[4], int i) {
-  const uint32_t u0 = (i & 1) ? w[i >> 1] >> 8 : w[i >> 1];
-  const uint32_t u1 = (i & 1) ? w[2 + (i >> 1)] >> 8 : w[2 + (i >> 1)];
+  constexpr uint32_t kByte = 0x00ff00ffu;
+  const uint32_t u0 = (i & 1) ? __byte_perm(w[i >> 1], 0, 0x4341) : w[i >> 1] & kByte;
+  const uint32_t u1 = (i & 1) ? __byte_perm(w[2 + (i >> 1)], 0, 0x4341) : w[2 + (i >> 1)] & kByte;
   a[0] = half2_twice_plus(u0 & kLo, k15);
-  a[1] = half2_twice_plus(u0 & kHi, k240);
+  a[1] = half2_twice_plus(u0, k255);
   a[2] = half2_twice_plus(u1 & kLo, k15);
-  a[3] = half2_twice_plus(u1 & kHi, k240);
+  a[3] = half2_twice_plus(u1, k255);
 }
 
 // NP pairs of chunks, A and B, of a 4-bit head with at most four query heads.
@@ -734,9 +748,8 @@ __device__ __forceinline__ void process_pairs(State& st, const Params& p, const 
     codes_dot(a, ra[i], st.qf, r0, t);
     codes_dot(b, rb[i], st.qg, r0, t);
     add_to(a, b);            // each is zero in the other's columns
-    const float s0 = k0.x * st.kf, s1 = k1.x * st.kf;
-    x0[i] = make_float2(fmaf(a[0], s0, st.qsum.x * k0.y), fmaf(a[1], s0, st.qsum.y * k0.y));
-    x1[i] = make_float2(fmaf(a[2], s1, st.qsum.x * k1.y), fmaf(a[3], s1, st.qsum.y * k1.y));
+    x0[i] = make_float2(fmaf(a[0], k0.x, st.qsum.x * k0.y), fmaf(a[1], k0.x, st.qsum.y * k0.y));
+    x1[i] = make_float2(fmaf(a[2], k1.x, st.qsum.x * k1.y), fmaf(a[3], k1.x, st.qsum.y * k1.y));
     if (kMasked) {
       const int first = p.window > 0 && ctx > p.window ? ctx - p.window : 0;
       const int k = tok[i] + r0;
@@ -752,10 +765,10 @@ __device__ __forceinline__ void process_pairs(State& st, const Params& p, const 
   }
   float2 sum;
   auto weights = [&]() {
-    const float2 nm = make_float2(-st.m.x, -st.m.y);
+    const float2 nm = make_float2(-st.m.x, -st.m.y), kf = make_float2(st.kf, st.kf);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const float2 d0 = __fadd2_rn(x0[i], nm), d1 = __fadd2_rn(x1[i], nm);
+      const float2 d0 = __ffma2_rn(x0[i], kf, nm), d1 = __ffma2_rn(x1[i], kf, nm);
       w0[i] = make_float2(ex2(d0.x), ex2(d0.y));
       w1[i] = make_float2(ex2(d1.x), ex2(d1.y));
       sum = i == 0 ? __fadd2_rn(w0[0], w1[0]) : __fadd2_rn(sum, __fadd2_rn(w0[i], w1[i]));
@@ -765,12 +778,12 @@ __device__ __forceinline__ void process_pairs(State& st, const Params& p, const 
   float sv = fmaxf(v0[0].x, v1[0].x);
 #pragma unroll
   for (int i = 1; i < NP; ++i) sv = fmaxf(sv, fmaxf(v0[i].x, v1[i].x));
-  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) <= kMaxSum) || sv * st.vs > kMaxVScale)) {
+  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) * sv <= kMaxProduct))) {
     float2 mx = x0[0];
 #pragma unroll
     for (int i = 0; i < NP; ++i)
       mx = make_float2(fmaxf(mx.x, fmaxf(x0[i].x, x1[i].x)), fmaxf(mx.y, fmaxf(x0[i].y, x1[i].y)));
-    move_reference<k4Bit, true>(st, mx, sv);
+    move_reference<k4Bit, true>(st, make_float2(mx.x * st.kf, mx.y * st.kf), sv);
     weights();
   }
   st.l = __fadd2_rn(st.l, sum);
@@ -780,9 +793,8 @@ __device__ __forceinline__ void process_pairs(State& st, const Params& p, const 
     const float z0 = fmaf(7.5f, v0[i].x, v0[i].y), z1 = fmaf(7.5f, v1[i].x, v1[i].y);
     st.zs.x = fmaf(w1[i].x, z1, fmaf(w0[i].x, z0, st.zs.x));
     st.zs.y = fmaf(w1[i].y, z1, fmaf(w0[i].y, z0, st.zs.y));
-    const float e0 = v0[i].x * st.vs, e1 = v1[i].x * st.vs;
-    w0[i] = make_float2(w0[i].x * e0, w0[i].y * e0);
-    w1[i] = make_float2(w1[i].x * e1, w1[i].y * e1);
+    w0[i] = make_float2(w0[i].x * v0[i].x, w0[i].y * v0[i].x);
+    w1[i] = make_float2(w1[i].x * v1[i].x, w1[i].y * v1[i].x);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const float2 w = r == 0 ? w0[i] : w1[i];
@@ -833,8 +845,8 @@ __device__ __forceinline__ void process_wide(State& st, const Params& p, const u
     for (int r = 0; r < 2; ++r) {
       const float2 m = meta_sz(lds32(rec[i] + kRecKMeta + (r0 + 8 * r) * 4));
       mv[i][r] = meta_sz(lds32(rec[i] + kRecVMeta + (r0 + 8 * r) * 4));
-      const float s = m.x * st.kf;
-      x[i][r] = make_float2(fmaf(c[2 * r], s, st.qsum.x * m.y), fmaf(c[2 * r + 1], s, st.qsum.y * m.y));
+      x[i][r] = make_float2(fmaf(c[2 * r], m.x, st.qsum.x * m.y),
+                            fmaf(c[2 * r + 1], m.x, st.qsum.y * m.y));
       if (kMasked) {
         const int first = p.window > 0 && ctx > p.window ? ctx - p.window : 0;
         const int k = tok[i] + r0 + 8 * r;
@@ -847,12 +859,12 @@ __device__ __forceinline__ void process_wide(State& st, const Params& p, const u
   }
   float2 sum;
   auto weights = [&]() {
-    const float2 nm = make_float2(-st.m.x, -st.m.y);
+    const float2 nm = make_float2(-st.m.x, -st.m.y), kf = make_float2(st.kf, st.kf);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float2 d = __fadd2_rn(x[i][r], nm);
+        const float2 d = __ffma2_rn(x[i][r], kf, nm);
         w[i][r] = make_float2(ex2(d.x), ex2(d.y));
         sum = i + r == 0 ? w[0][0] : __fadd2_rn(sum, w[i][r]);
       }
@@ -862,12 +874,12 @@ __device__ __forceinline__ void process_wide(State& st, const Params& p, const u
   float sv = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) sv = fmaxf(sv, fmaxf(mv[i][0].x, mv[i][1].x));
-  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) <= kMaxSum) || sv * st.vs > kMaxVScale)) {
+  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) * sv <= kMaxProduct))) {
     float2 mx = x[0][0];
 #pragma unroll
     for (int i = 0; i < N; ++i)
       mx = make_float2(fmaxf(mx.x, fmaxf(x[i][0].x, x[i][1].x)), fmaxf(mx.y, fmaxf(x[i][0].y, x[i][1].y)));
-    move_reference<k4Bit, false>(st, mx, sv);
+    move_reference<k4Bit, false>(st, make_float2(mx.x * st.kf, mx.y * st.kf), sv);
     weights();
   }
   st.l = __fadd2_rn(st.l, sum);
@@ -876,7 +888,7 @@ __device__ __forceinline__ void process_wide(State& st, const Params& p, const u
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const float zc = fmaf(7.5f, mv[i][r].x, mv[i][r].y), sc = mv[i][r].x * st.vs;
+      const float zc = fmaf(7.5f, mv[i][r].x, mv[i][r].y), sc = mv[i][r].x;
       st.zs.x = fmaf(w[i][r].x, zc, st.zs.x);
       st.zs.y = fmaf(w[i][r].y, zc, st.zs.y);
       const float2 v = make_float2(w[i][r].x * sc, w[i][r].y * sc);
@@ -1023,13 +1035,17 @@ __device__ bool finish(State& st, const Params& p, uint8_t* smem, const Layout& 
     }
   }
   float o[2][8];       // [column][2 i + half]: dimension out_dim(g, i, half)
-  const float f0 = F == k4Bit ? 8388608.f / st.vs : 1.f;
+  const float f0 = F == k4Bit ? 8388608.f : 1.f;      // 2^24 / 2 of the codes
   const float f1 = F == k4Bit ? f0 * 0.0625f : 1.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (kLoCols) st.acc[i][k] += __shfl_xor_sync(kFull, st.acc[i][k], 2);
+    if (F == k4Bit) {           // bytes less their low halves (see v_operand)
+      st.acc[i][2] -= st.acc[i][0];
+      st.acc[i][3] -= st.acc[i][1];
+    }
     o[0][2 * i] = fmaf(st.acc[i][0], f0, F == k4Bit ? st.zs.x : 0.f);
     o[1][2 * i] = fmaf(st.acc[i][1], f0, F == k4Bit ? st.zs.y : 0.f);
     o[0][2 * i + 1] = fmaf(st.acc[i][2], f1, F == k4Bit ? st.zs.x : 0.f);
@@ -1095,7 +1111,7 @@ __device__ bool finish(State& st, const Params& p, uint8_t* smem, const Layout& 
   return true;
 }
 
-template <int F, bool kLoCols>
+template <int F, bool kLoCols, int W>
 __device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = warp % p.hpc, w = warp / p.hpc;
@@ -1106,7 +1122,8 @@ __device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
   constexpr int NC = chunks_per_warp<F, kLoCols>();
   constexpr uint32_t kTile = F == k4Bit ? kRecBytes : kBf16Tile;
   const uint32_t mine = (w * p.hpc + h) * kTile;           // the warp's first chunk in a stage
-  const uint32_t step = p.wph * p.hpc * kTile;             // to its next
+  // to its next: the CTA's consumer warps in turn (4-bit: their number is W)
+  const uint32_t step = (F == k4Bit ? W : p.wph * p.hpc) * kTile;
   const uint32_t v_off = p.kv_bytes / 2;
 
   State st;
@@ -1129,7 +1146,6 @@ __device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
         for (int k = 0; k < 4; ++k) st.acc[i][k] = 0.f;
       st.m = make_float2(-INFINITY, -INFINITY);
       st.l = st.zs = make_float2(0.f, 0.f);
-      st.vs = 0.f;
     }
     const uint8_t* at = base + mine;
     if (!(flags & kPartial)) {
@@ -1212,7 +1228,7 @@ __device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
   }
 }
 
-template <int F, bool kLoCols>
+template <int F, bool kLoCols, int W>
 __global__ void __launch_bounds__((max_warps<F, kLoCols>() + 1) * 32, 1)
     window_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const Params p) {
@@ -1239,7 +1255,9 @@ __global__ void __launch_bounds__((max_warps<F, kLoCols>() + 1) * 32, 1)
   }
   grid_dependency_wait();        // inputs may come from the preceding kernel
   grid_dependents_launch();
-  if (p.small)
+  if (p.direct) {
+    if (tid == 0) *sched = Schedule{static_cast<int>(blockIdx.x), 0, static_cast<int>(blockIdx.x) + 1, 0, 1, 0};
+  } else if (p.small)
     schedule_small(p, sched, reinterpret_cast<int*>(tmp));
   else
     make_schedule(p, sched, tmp);
@@ -1252,11 +1270,11 @@ __global__ void __launch_bounds__((max_warps<F, kLoCols>() + 1) * 32, 1)
     const int n = p.hpc * p.group * kD;
     for (int s = blockIdx.x; s < p.num_seqs; s += p.ctas) {
       if (p.context_lens[s] > 0) continue;
-      if (tid == 0 && blockIdx.z == 0 && p.num_seqs <= p.ctas) p.ws_split[s] = make_int4(-1, 0, 0, 0);
+      if (tid == 0 && blockIdx.z == 0 && p.num_seqs <= p.ctas && !p.direct) p.ws_split[s] = make_int4(-1, 0, 0, 0);
       float* dst = p.out + (static_cast<long long>(s) * p.hq + blockIdx.z * p.hpc * p.group) * kD;
       for (int i = tid; i < n; i += consumers * 32) dst[i] = 0.f;
     }
-    consumer<F, kLoCols>(p, smem, L);
+    consumer<F, kLoCols, W>(p, smem, L);
   }
 }
 
@@ -1379,10 +1397,10 @@ bool cache_map(CUtensorMap* m, const void* base, int hkv, long long tokens, int 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int F, bool kLoCols>
+template <int F, bool kLoCols, int W>
 cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, dim3 grid,
                      uint32_t smem, cudaStream_t stream) {
-  auto kern = window_decode_kernel<F, kLoCols>;
+  auto kern = window_decode_kernel<F, kLoCols, W>;
   static PerDeviceOnce once;
   cudaError_t e = once.run([&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
@@ -1401,12 +1419,11 @@ int heads_per_cta(int num_kv_heads, int most) {
 // The CTA's shape for a format and group size.
 template <int F, bool kLoCols>
 void shape(Params& p) {
-  p.hpc = heads_per_cta(p.hkv, max_heads<F, kLoCols>());
+  p.hpc = p.direct ? 1 : heads_per_cta(p.hkv, max_heads<F, kLoCols>());
   constexpr int nc = chunks_per_warp<F, kLoCols>();
   p.wph = max_warps<F, kLoCols>() / p.hpc;
-  if (p.wph * nc > 32) p.wph = 32 / nc;       // a lane of the producer per chunk of a stage
+  if (p.wph * nc > 32 || (F == k4Bit && p.hpc == 1)) p.wph = 8;   // a producer lane per chunk of a stage
   p.cps = p.wph * nc;
-  p.first_cps = nc == 4 ? 2 * p.wph : p.wph;
   p.batch = 32 / p.cps * p.cps;
 }
 
@@ -1445,12 +1462,18 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
   p.window = a.window;
   p.sinks = a.window > 0 ? a.sinks : 0;
   const bool lo_cols = p.group <= 4;
+  // Small batches of bounded length: one CTA a sequence and KV head, one
+  // launch.  The bound is the block table's capacity or the window.
+  const long long capacity = static_cast<long long>(a.max_blocks_per_seq) << p.cpb_log2;
+  const long long seen = p.window > 0 ? p.window / kChunk + p.sinks / kChunk + 4LL : capacity;
+  p.direct = static_cast<long long>(a.num_seqs) * p.hkv <= a.sms &&
+             (seen < capacity ? seen : capacity) <= (four ? kDirectChunks4 : kDirectChunks16);
   if (!four)
     lo_cols ? shape<kBf16, true>(p) : shape<kBf16, false>(p);
   else
     lo_cols ? shape<k4Bit, true>(p) : shape<k4Bit, false>(p);
   const int groups = p.hkv / p.hpc;
-  p.ctas = a.sms / groups < 1 ? 1 : a.sms / groups;
+  p.ctas = p.direct ? a.num_seqs : a.sms / groups < 1 ? 1 : a.sms / groups;
   p.kv_bytes = p.cps * p.hpc * (four ? kRecBytes : 2 * kBf16Tile);
   p.stage_bytes = align_up(p.kv_bytes + p.hpc * p.group * kD * 2, 1024);
   const uint32_t fixed = make_layout(0, p.stage_bytes, p.hpc, p.wph, p.group).total + 1024 + 16;
@@ -1458,8 +1481,8 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
   p.stages = stages > 8 ? 8 : stages;
   if (p.stages < 2) return cudaErrorInvalidConfiguration;
   p.scale_log2 = a.scale * kLog2e;
-  p.seg_weight = four ? 10 : 2;
-  const long long longest = (static_cast<long long>(a.max_blocks_per_seq) << p.cpb_log2) + p.seg_weight;
+  p.seg_weight = four ? kSegWeight4 : kSegWeight16;
+  const long long longest = capacity + p.seg_weight;
   p.small = a.num_seqs <= (p.hpc * p.wph + 1) * 32 && longest * a.num_seqs * (p.ctas + 1) < (1LL << 31);
   p.status = a.status;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -1481,13 +1504,17 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
   const uint32_t smem = make_layout(p.stages, p.stage_bytes, p.hpc, p.wph, p.group).total + 1024;
   const dim3 grid(p.ctas, 1, groups);
   cudaError_t e;
-  if (four)
-    e = lo_cols ? launch_t<k4Bit, true>(tk, tv, p, grid, smem, stream)
-                     : launch_t<k4Bit, false>(tk, tv, p, grid, smem, stream);
+  const bool one = p.hpc == 1;          // 8 consumer warps instead of 12
+  if (!four)
+    e = lo_cols ? launch_t<kBf16, true, 0>(tk, tv, p, grid, smem, stream)
+                : launch_t<kBf16, false, 0>(tk, tv, p, grid, smem, stream);
+  else if (lo_cols)
+    e = one ? launch_t<k4Bit, true, 8>(tk, tv, p, grid, smem, stream)
+            : launch_t<k4Bit, true, 12>(tk, tv, p, grid, smem, stream);
   else
-    e = lo_cols ? launch_t<kBf16, true>(tk, tv, p, grid, smem, stream)
-                     : launch_t<kBf16, false>(tk, tv, p, grid, smem, stream);
-  if (e != cudaSuccess) return e;
+    e = one ? launch_t<k4Bit, false, 8>(tk, tv, p, grid, smem, stream)
+            : launch_t<k4Bit, false, 12>(tk, tv, p, grid, smem, stream);
+  if (e != cudaSuccess || p.direct) return e;
   // a sequence has about 1 + ctas / num_seqs records: one warp a head and
   // batch of 8, up to 16
   int parts = 1;

@@ -172,7 +172,7 @@ def test_copy_is_bit_exact(bs, hkv):
 # -------------------------------------------------------------------- decode
 
 
-def _decode(seed, ctx, hq, hkv, bs, window=0, sinks=0, spread=1.0, qscale=1.5, cache=None):
+def _decode(seed, ctx, hq, hkv, bs, window=0, sinks=0, spread=1.0, qscale=1.5, cache=None, scale=0.125):
     rng = np.random.default_rng(seed)
     tables, nb = C.deal(rng, ctx, bs)
     if cache is None:
@@ -180,8 +180,8 @@ def _decode(seed, ctx, hq, hkv, bs, window=0, sinks=0, spread=1.0, qscale=1.5, c
     q = C.bf16_to_f64(C.f64_to_bf16_bits(rng.standard_normal((len(ctx), hq, 64)) * qscale))
     out = torch.full((len(ctx), hq, 64), float("nan"), device=DEV)
     tvl.kv4_attention_decode(out, C.bf16(q, DEV), _cuda(cache), _cuda(tables),
-                             _cuda(np.asarray(ctx, np.int32)), 0.125, window=window, sinks=sinks)
-    want, tol = C.decode_ref(q, tables, ctx, 0.125, window, sinks, cache=cache)
+                             _cuda(np.asarray(ctx, np.int32)), scale, window=window, sinks=sinks)
+    want, tol = C.decode_ref(q, tables, ctx, scale, window, sinks, cache=cache)
     return C.f64(out), want, tol
 
 
@@ -215,6 +215,26 @@ def test_decode_window(window, sinks, bs):
 def test_decode_magnitudes(spread, qscale):
     """Rows and queries far from 1: the powers of two folded into q and V."""
     got, want, tol = _decode(60, [500, 77], 16, 4, 16, spread=spread, qscale=qscale)
+    assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()
+
+
+@pytest.mark.parametrize("scale", [-0.125, 0.0, 3.0])
+@pytest.mark.parametrize("hq", [8, 16])
+def test_decode_scales(scale, hq):
+    got, want, tol = _decode(59, [100, 333], hq, 2, 16, 70, 3, scale=scale, qscale=0.3)
+    assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()
+
+
+def test_decode_of_constant_rows():
+    """V rows of one value each (s = 0), so every weight meets a zero scale."""
+    rng = np.random.default_rng(58)
+    ctx = [50, 400]
+    tables, nb = C.deal(np.random.default_rng(57), ctx, 16)
+    cache = C.random_cache(rng, nb, 16, 2)
+    cache[..., 512:1024] = 0
+    meta = cache[..., 1088:1152].view(np.uint16).reshape(nb, 1, 2, 16, 2)
+    meta[..., 0] = 0
+    got, want, tol = _decode(57, ctx, 8, 2, 16, cache=cache)
     assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()
 
 

@@ -87,8 +87,8 @@ def attend(q, k, v, scale, absq=None, absv=None):
     p = np.exp(s - s.max())
     p /= p.sum()
     av = np.abs(v) if absv is None else absv
-    b = (np.abs(k) @ np.abs(q) if absq is None else absq * np.abs(q).sum()).max() * scale
-    return p @ v, p @ av, b
+    b = (np.abs(k) @ np.abs(q) if absq is None else absq * np.abs(q).sum()).max() * abs(scale)
+    return p @ v, p @ av, abs(b)
 
 
 def decode_bound(a, b, n, split_bits):
