@@ -1051,47 +1051,50 @@ __device__ bool finish(State& st, const Params& p, uint8_t* smem, const Layout& 
     o[0][2 * i + 1] = fmaf(st.acc[i][2], f1, F == k4Bit ? st.zs.x : 0.f);
     o[1][2 * i + 1] = fmaf(st.acc[i][3], f1, F == k4Bit ? st.zs.y : 0.f);
   }
-  const float m[2] = {st.m.x, st.m.y}, l[2] = {st.l.x, st.l.y};
+  float m[2] = {st.m.x, st.m.y}, l[2] = {st.l.x, st.l.y};
+  // columns 2 t and 2 t + 1 are heads of the group (not the lo halves' copies)
+  const bool live[2] = {2 * t < G && !(kLoCols && t >= 2), 2 * t + 1 < G && !(kLoCols && t >= 2)};
+  // a warp's hand-over of a head: eight floats a lane in lane order, then m, l
   if (w > 0) {
     if (seg > 0 && !mbar_wait(&cempty[h], (seg - 1) & 1)) return false;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int hg = 2 * t + j;
-      if (hg >= G || (kLoCols && t >= 2)) continue;
-      float* dst = comb + (((w - 1) * p.hpc + h) * G + hg) * kCombPitch;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) dst[out_dim<F>(g, i >> 1, i & 1)] = o[j][i];
-      if (g == 0) {
-        dst[64] = m[j];
-        dst[65] = l[j];
-      }
+      if (!live[j]) continue;
+      float* dst = comb + (((w - 1) * p.hpc + h) * G + 2 * t + j) * kCombPitch;
+      reinterpret_cast<float4*>(dst)[2 * g] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+      reinterpret_cast<float4*>(dst)[2 * g + 1] = make_float4(o[j][4], o[j][5], o[j][6], o[j][7]);
+      if (g == 0) *reinterpret_cast<float2*>(dst + 64) = make_float2(m[j], l[j]);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&cfull[h]);
     return true;
   }
   if (p.wph > 1 && !mbar_wait(&cfull[h], seg & 1)) return false;
+#pragma unroll 2
+  for (int i = 1; i < p.wph; ++i) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (!live[j]) continue;
+      const float* src = comb + (((i - 1) * p.hpc + h) * G + 2 * t + j) * kCombPitch;
+      const float4 a = reinterpret_cast<const float4*>(src)[2 * g];
+      const float4 b = reinterpret_cast<const float4*>(src)[2 * g + 1];
+      const float2 ml = *reinterpret_cast<const float2*>(src + 64);
+      // a warp that had no chunk of the segment: m = -inf, the rest 0
+      const float mn = fmaxf(m[j], ml.x);
+      const float fa = weight_of(m[j], mn), fb = weight_of(ml.x, mn);
+      m[j] = mn;
+      l[j] = l[j] * fa + ml.y * fb;
+      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[j][k] = o[j][k] * fa + v[k] * fb;
+    }
+  }
+  const int kvh = blockIdx.z * p.hpc + h;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int hg = 2 * t + j;
-    if (hg >= G || (kLoCols && t >= 2)) continue;
-    float mm = m[j], ll = l[j];
-    for (int i = 1; i < p.wph; ++i) {
-      const float* src = comb + (((i - 1) * p.hpc + h) * G + hg) * kCombPitch;
-      const float mi = src[64];
-      const float li = src[65];
-      if (mi == -INFINITY && li == 0.f) continue;   // it had no chunk of the segment
-      const float mn = fmaxf(mm, mi);
-      const float fa = weight_of(mm, mn), fb = weight_of(mi, mn);
-      mm = mn;
-      ll = ll * fa + li * fb;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        o[j][k] = o[j][k] * fa + src[out_dim<F>(g, k >> 1, k & 1)] * fb;
-    }
-    const float sc = record < 0 ? 1.0f / ll : 1.0f;
-    const long long row =
-        static_cast<long long>(record < 0 ? seq : record) * p.hq + (blockIdx.z * p.hpc + h) * G + hg;
+    if (!live[j]) continue;
+    const float sc = record < 0 ? 1.0f / l[j] : 1.0f;
+    const long long row = static_cast<long long>(record < 0 ? seq : record) * p.hq + kvh * G + 2 * t + j;
     float* dst = (record < 0 ? p.out : p.ws_acc) + row * kD;
     if constexpr (F == k4Bit) {
       float4* d4 = reinterpret_cast<float4*>(dst + 8 * g);
@@ -1102,8 +1105,8 @@ __device__ bool finish(State& st, const Params& p, uint8_t* smem, const Layout& 
       for (int k = 0; k < 8; ++k) dst[out_dim<F>(g, k >> 1, k & 1)] = o[j][k] * sc;
     }
     if (record >= 0 && g == 0) {
-      p.ws_m[row] = mm;
-      p.ws_l[row] = ll;
+      p.ws_m[row] = m[j];
+      p.ws_l[row] = l[j];
     }
   }
   __syncwarp();
