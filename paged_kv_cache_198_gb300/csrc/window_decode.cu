@@ -61,6 +61,7 @@ namespace {
 
 constexpr int kD = 64;
 constexpr int kChunk = 16;
+constexpr int kMaxThreads = 17 * 32;
 constexpr uint32_t kBf16Tile = kChunk * kD * 2;   // one head's K (or V) of a chunk
 constexpr float kMaxSum = 256.0f;             // a lane's weights under the reference maximum
 constexpr float kMaxProduct = 32768.0f;        // 4-bit: a lane's weights times its V scales
@@ -136,8 +137,8 @@ __host__ __device__ inline Layout make_layout(int stages, uint32_t stage_bytes, 
   off += (2 * stages + 2 * hpc) * 8;
   l.comb = align_up(off, 16);
   off = l.comb + (wph - 1) * hpc * group * kCombPitch * 4;
-  l.sched = align_up(off, 16);
-  off = l.sched + 64 + 32 * 8;
+  l.sched = align_up(off, 16);                         // the schedule, scan totals, lengths
+  off = l.sched + 64 + 32 * 8 + kMaxThreads * 4;
   l.total = off;
   return l;
 }
@@ -219,11 +220,15 @@ __device__ void block_scan(long long v, long long& incl, long long& total, long 
 // before it, and the threads whose sequences hold the CTA's two ends record
 // them.  Every thread whose sequence has chunks in the range prefetches their
 // block table entries for the producer.
-__device__ __forceinline__ void schedule_small(const Params& p, Schedule* sc, int* tmp) {
+__device__ __forceinline__ void schedule_small(const Params& p, Schedule* sc, int* tmp, int* lens) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   const int w = p.seg_weight;
   Visible vis = {0, 0, 0};
-  if (tid < p.num_seqs) vis = visible_of(p, load_ctx(p, tid));
+  if (tid < p.num_seqs) {
+    const int ctx = load_ctx(p, tid);
+    lens[tid] = ctx;                       // for the producer
+    vis = visible_of(p, ctx);
+  }
   const int mine = vis.n > 0 ? vis.n + w : 0;
   int x = mine;
 #pragma unroll
@@ -337,17 +342,22 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
     }
   };
 
-  // lane i: the context length of sequence win + i
+  // lens: the lengths, of a small batch; else lane i's win_ctx: sequence win + i's
+  const int* lens = reinterpret_cast<const int*>(smem + L.sched + 64 + 32 * 8);
   int win = -64, win_ctx = 0;
   // The segment that starts at chunk v of sequence s or after it; false: none left.
   auto find = [&](int s, int v, bool first, Segment& g) {
     for (;; ++s, v = 0) {
       if (s >= p.num_seqs || s > sc.seq_end || (s == sc.seq_end && v >= sc.v_end)) return false;
-      if (s < win || s >= win + 32) {
-        win = s;
-        win_ctx = s + lane < p.num_seqs ? load_ctx(p, s + lane) : 0;
+      if (p.small) {
+        g.ctx = lens[s];
+      } else {
+        if (s < win || s >= win + 32) {
+          win = s;
+          win_ctx = s + lane < p.num_seqs ? load_ctx(p, s + lane) : 0;
+        }
+        g.ctx = __shfl_sync(kFull, win_ctx, s - win);
       }
-      g.ctx = __shfl_sync(kFull, win_ctx, s - win);
       const Visible vis = visible_of(p, g.ctx);
       if (v >= vis.n) continue;
       g.s = s;
@@ -1242,6 +1252,7 @@ __global__ void __launch_bounds__((max_warps<F, kLoCols>() + 1) * 32, 1)
   const Layout L = make_layout(p.stages, p.stage_bytes, p.hpc, p.wph, p.group);
   Schedule* sched = reinterpret_cast<Schedule*>(smem + L.sched);
   long long* tmp = reinterpret_cast<long long*>(smem + L.sched + 64);
+  int* lens = reinterpret_cast<int*>(smem + L.sched + 64 + 32 * 8);
   const int tid = threadIdx.x, warp = tid >> 5;
   const int consumers = p.hpc * p.wph;
   if (tid == 0) {
@@ -1261,7 +1272,7 @@ __global__ void __launch_bounds__((max_warps<F, kLoCols>() + 1) * 32, 1)
   if (p.direct) {
     if (tid == 0) *sched = Schedule{static_cast<int>(blockIdx.x), 0, static_cast<int>(blockIdx.x) + 1, 0, 1, 0};
   } else if (p.small)
-    schedule_small(p, sched, reinterpret_cast<int*>(tmp));
+    schedule_small(p, sched, reinterpret_cast<int*>(tmp), lens);
   else
     make_schedule(p, sched, tmp);
   __syncthreads();
@@ -1486,7 +1497,7 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
   p.scale_log2 = a.scale * kLog2e;
   p.seg_weight = four ? kSegWeight4 : kSegWeight16;
   const long long longest = capacity + p.seg_weight;
-  p.small = a.num_seqs <= (p.hpc * p.wph + 1) * 32 && longest * a.num_seqs * (p.ctas + 1) < (1LL << 31);
+  p.small = !p.direct && a.num_seqs <= (p.hpc * p.wph + 1) * 32 && longest * a.num_seqs * (p.ctas + 1) < (1LL << 31);
   p.status = a.status;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const size_t rows = 2 * static_cast<size_t>(p.ctas) * a.num_q_heads;
