@@ -970,9 +970,14 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   const int cap = a.max_blocks_per_seq * a.block_size;
   p.window = a.window < cap ? a.window : cap;
   p.sinks = a.window == 0 ? 0 : a.sinks < cap ? a.sinks : cap;
-  if (a.windowed)
-    return p.group >= 2 ? launch_nh<2, true>(tq, tk, tv, to, p, a.num_seqs, a.num_sms, stream)
-                        : launch_nh<1, true>(tq, tk, tv, to, p, a.num_seqs, a.num_sms, stream);
+  if (a.windowed) {
+    // With so few units that single heads would still leave no SM two of them,
+    // the tile's latency counts, not the shared K/V tile: one head a unit.
+    const long long pairs = static_cast<long long>(a.num_seqs) * p.n_qtiles * (p.hq / 2);
+    return p.group >= 2 && 2 * pairs > a.num_sms
+               ? launch_nh<2, true>(tq, tk, tv, to, p, a.num_seqs, a.num_sms, stream)
+               : launch_nh<1, true>(tq, tk, tv, to, p, a.num_seqs, a.num_sms, stream);
+  }
   if (p.group >= 2) return launch_nh<2, false>(tq, tk, tv, to, p, a.num_seqs, a.num_sms, stream);
   return launch_nh<1, false>(tq, tk, tv, to, p, a.num_seqs, a.num_sms, stream);
 }
