@@ -61,7 +61,8 @@ namespace {
 
 constexpr int kD = 64;
 constexpr int kChunk = 16;
-constexpr int kMaxThreads = 17 * 32;
+constexpr int kMaxProducers = 4;
+constexpr int kMaxThreads = (12 + kMaxProducers) * 32;
 constexpr uint32_t kBf16Tile = kChunk * kD * 2;   // one head's K (or V) of a chunk
 constexpr float kMaxSum = 256.0f;             // a lane's weights under the reference maximum
 constexpr float kMaxProduct = 32768.0f;        // 4-bit: a lane's weights times its V scales
@@ -73,21 +74,20 @@ constexpr uint32_t kSmemLimit = 227 * 1024;
 // 4, 27.3 at 16, 27.7 at 32) and 256 (bf16, window 1024: 51.2 us at 1, 50.9 at
 // 4, 51.6 at 6).
 constexpr int kSegWeight4 = 14, kSegWeight16 = 3;
-// Longest sequence (chunks) that one CTA a KV head does alone, without the split
-// and its merge.  One sequence, 8 heads, alone / split: 4-bit 512 tokens 6.5 /
-// 10.2 us, 1024 7.8 / 9.8, 2048 11.4 / 9.8; bf16 128 tokens 7.5 / 10.3, 512 9.7
-// / 11.8, 1024 12.8 / 12.3.
-constexpr int kDirectChunks4 = 80, kDirectChunks16 = 40;
+
 constexpr int kCombPitch = 72;                // floats a head of a warp hands over: 64 + m, l
 
 enum Format : int { kBf16 = 0, k4Bit = 1 };
-enum : int { kSegFirst = 1, kSegLast = 2, kTerminate = 4, kPartial = 8 };
+// Bits of a stage's flags: the warp's first and last stage of the segment; no
+// more stages; not all chunks present and visible.  From bit 8: how many of a
+// head's warps have stages of the segment.
+enum : int { kSegFirst = 1, kSegLast = 2, kTerminate = 4, kPartial = 8, kPartsShift = 8 };
 
-// chunks a warp takes from a stage at once (independent work in flight)
+// chunks of a stage: what a warp works on at once (independent work in flight)
 template <int F, bool kLoCols>
-__host__ __device__ constexpr int chunks_per_warp() { return F == k4Bit ? (kLoCols ? 4 : 2) : 1; }
+__host__ __device__ constexpr int chunks_per_stage() { return F == k4Bit ? (kLoCols ? 4 : 2) : 1; }
 template <int F, bool kLoCols>
-__host__ __device__ constexpr int max_warps() { return F == k4Bit ? 12 : 16; }
+__host__ __device__ constexpr int max_warps() { return F == k4Bit ? 12 : 8; }
 template <int F, bool kLoCols>
 __host__ __device__ constexpr int max_heads() { return F == k4Bit ? 4 : 8; }
 
@@ -105,12 +105,13 @@ struct Params {
   int num_seqs, hq, hkv, group, num_blocks, max_blocks;
   int cpb_log2;          // log2 of the 16-token chunks in a block
   int window, sinks;     // window 0: none
-  int hpc, wph, cps, batch, stages;
+  int hpc, wph, cps_log2;
+  int stages, ring;      // wph rings of `ring` stages
+  int producers;         // warps that fill them: warp j the rings j, j + producers, ...
   uint32_t stage_bytes, kv_bytes;
   float scale_log2;
   int ctas, seg_weight;
   int small;             // schedule_small serves
-  int direct;            // CTA (x, z) does sequence x, KV head z alone; no merge
   float* ws_m;           // records [2 * ctas][hq]
   float* ws_l;
   float* ws_acc;
@@ -133,10 +134,10 @@ __host__ __device__ inline Layout make_layout(int stages, uint32_t stage_bytes, 
   uint32_t off = stages * stage_bytes;
   l.meta = off;
   off += stages * sizeof(StageMeta);
-  l.bars = off;                                        // full, empty; comb full, empty per head
-  off += (2 * stages + 2 * hpc) * 8;
+  l.bars = off;                                        // full, empty; hand-over full, empty a warp
+  off += (2 * stages + 2 * hpc * wph) * 8;
   l.comb = align_up(off, 16);
-  off = l.comb + (wph - 1) * hpc * group * kCombPitch * 4;
+  off = l.comb + wph * hpc * group * kCombPitch * 4;
   l.sched = align_up(off, 16);                         // the schedule, scan totals, lengths
   off = l.sched + 64 + 32 * 8 + kMaxThreads * 4;
   l.total = off;
@@ -309,7 +310,7 @@ struct Segment {
 };
 
 template <int F>
-__device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, const Layout& L,
+__device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, const Layout& L, int pj,
                          const CUtensorMap* tm_k, const CUtensorMap* tm_v) {
   const int lane = threadIdx.x & 31;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars);
@@ -325,22 +326,13 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
     prefetch_tensormap(tm_v);
   }
 
-  int st = 0, filled = 0;        // next stage; stages filled so far, capped
-  uint32_t ph = 0;               // parity of the fill before the next one of stage st
-  bool ok = true;
-  auto acquire = [&]() {
-    bool good = true;
-    if (filled >= p.stages && lane == 0) good = mbar_wait(&empty[st], ph ^ 1);
-    ok = __shfl_sync(kFull, good ? 1 : 0, 0) != 0;
-    return ok;
-  };
-  auto advance_stage = [&]() {
-    if (filled < p.stages) ++filled;
-    if (++st == p.stages) {
-      st = 0;
-      ph ^= 1;
-    }
-  };
+  const int cps = 1 << p.cps_log2, wph = p.wph, ring = p.ring;
+  // Stage k of a segment goes to the head's warps k % wph, each with a ring of
+  // its own.  Lane w < wph: warps w's next stage, its fill's parity, and whether
+  // every stage of the ring has been filled.
+  int pos = 0;
+  uint32_t ph = 0;
+  bool used = false, ok = true;
 
   // lens: the lengths, of a small batch; else lane i's win_ctx: sequence win + i's
   const int* lens = reinterpret_cast<const int*>(smem + L.sched + 64 + 32 * 8);
@@ -379,7 +371,7 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
     return p.block_tables[static_cast<long long>(g.s) * p.max_blocks + (c >> p.cpb_log2)];
   };
 
-  const bool by_seq = p.num_seqs <= p.ctas && blockIdx.z == 0 && !p.direct;
+  const bool by_seq = p.num_seqs <= p.ctas && blockIdx.z == 0;
   int4 split = make_int4(-1, 0, 0, 0);
   Segment g;
   bool have = find(sc.seq0, sc.v0, true, g);
@@ -391,38 +383,53 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
       const long long x = sc.hi + (g.n - g.e) - 1;
       split = make_int4(g.s, g.record, cta, static_cast<int>(((x + 1) * p.ctas - 1) / sc.total));
     }
-    if (by_seq && g.v == 0 && lane == 0)
+    if (by_seq && pj == 0 && g.v == 0 && lane == 0)
       p.ws_split[g.s] = g.e < g.n ? split : make_int4(-1, 0, 0, 0);
     Segment nx;
     const bool have_next = find(g.s, g.e, false, nx);
-    for (int vb = g.v; vb < g.e && ok; vb += p.batch) {
-      // the next batch's entries (of this segment or the next) are fetched while
+    const int n_stages = (g.e - g.v + cps - 1) >> p.cps_log2;
+    const int parts = min(wph, n_stages);
+    int k = 0, w = 0, mine = 0;  // the segment's stage, its warps, and their place mod producers
+    for (int vb = g.v; vb < g.e && ok; vb += 32) {
+      // the next 32 entries (of this segment or the next) are fetched while
       // this batch's copies are issued
-      const int ntbl = vb + p.batch < g.e ? entry(g, vb + p.batch) : (have_next ? entry(nx, nx.v) : 0);
-      for (int v = vb; v < g.e && v < vb + p.batch; v += p.cps) {
-        const int n = min(p.cps, g.e - v);
-        if (!acquire()) break;
-        uint8_t* base = smem + static_cast<size_t>(st) * p.stage_bytes;
-        const bool first = v == g.v;
+      const int ntbl = vb + 32 < g.e ? entry(g, vb + 32) : (have_next ? entry(nx, nx.v) : 0);
+      const int ve = min(g.e, vb + 32);
+      for (int v = vb; v < ve; v += cps, ++k) {
+        const int at = w;
+        const bool own = mine == pj;
+        if (++mine == p.producers) mine = 0;
+        if (++w == wph) w = mine = 0;
+        if (!own) continue;
+        const int n = min(cps, ve - v);                   // lane i < n: chunk v + i
+        const int slot = at * ring + __shfl_sync(kFull, pos, at);
+        const uint32_t sp = __shfl_sync(kFull, ph, at);
+        const bool again = __shfl_sync(kFull, used ? 1 : 0, at) != 0;
+        bool good = true;
+        if (lane == 0 && again) good = mbar_wait(&empty[slot], sp ^ 1);
+        ok = __shfl_sync(kFull, good ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        uint8_t* base = smem + static_cast<size_t>(slot) * p.stage_bytes;
         const int vv = v + lane;
         const int c = vv < g.ns ? vv : vv + g.delta;
         const bool whole = c * kChunk + kChunk <= g.ctx &&
                            (c * kChunk >= g.ctx - g.window || c * kChunk + kChunk <= p.sinks);
         const bool all = __all_sync(kFull, lane >= n || whole);
         int page = __shfl_sync(kFull, tbl, (v - vb + lane) & 31);
+        const bool first = k < wph;
         if (lane == 0) {
           StageMeta m;
           m.seq = g.s;
           m.record = g.record;
-          m.flags = (first ? kSegFirst : 0) | (v + n == g.e ? kSegLast : 0) |
-                    (all && n == p.cps ? 0 : kPartial);
+          m.flags = parts << kPartsShift | (first ? kSegFirst : 0) |
+                    (k + wph >= n_stages ? kSegLast : 0) | (all && n == cps ? 0 : kPartial);
           m.n = n;
           m.v0 = v;
           m.ns = g.ns;
           m.delta = g.delta;
           m.ctx = g.ctx;
-          meta[st] = m;
-          mbar_arrive_expect_tx(&full[st], n * chunk_bytes + (first ? q_bytes : 0));
+          meta[slot] = m;
+          mbar_arrive_expect_tx(&full[slot], n * chunk_bytes + (first ? q_bytes : 0));
         }
         __syncwarp();
         if (lane < n) {
@@ -434,46 +441,53 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
           const long long chunk = (static_cast<long long>(page) << p.cpb_log2) + sub;
           if (F == k4Bit) {
             bulk_load(base + lane * chunk_bytes, p.kv4 + (chunk * p.hkv + h0) * kRecBytes,
-                      chunk_bytes, &full[st], stream_policy);
+                      chunk_bytes, &full[slot], stream_policy);
           } else {
             const int tok = static_cast<int>(chunk * kChunk);
             const uint32_t half = hpc * kBf16Tile;
-            tma_load_3d(base + lane * half, tm_k, 0, tok, h0, &full[st]);
-            tma_load_3d(base + p.kv_bytes / 2 + lane * half, tm_v, 0, tok, h0, &full[st]);
+            tma_load_3d(base + lane * half, tm_k, 0, tok, h0, &full[slot]);
+            tma_load_3d(base + p.kv_bytes / 2 + lane * half, tm_v, 0, tok, h0, &full[slot]);
           }
         }
         if (first && lane == 31)
           bulk_load(base + p.kv_bytes,
                     p.q + (static_cast<size_t>(g.s) * p.hq + static_cast<size_t>(h0) * p.group) * kD,
-                    q_bytes, &full[st], keep_policy);
-        advance_stage();
+                    q_bytes, &full[slot], keep_policy);
+        if (lane == at && ++pos == ring) {
+          pos = 0;
+          ph ^= 1;
+          used = true;
+        }
       }
       tbl = ntbl;
     }
     g = nx;
     have = have_next;
   }
-  if (blockIdx.z == 0 && lane == 0 && !p.direct) {
+  if (blockIdx.z == 0 && lane == 0 && pj == 0) {
     if (!by_seq) p.ws_split[cta] = split;
     if (cta == 0) *p.ws_total = sc.total;
   }
-  if (ok && acquire()) {
-    if (lane == 0) {
-      meta[st].flags = kTerminate;
-      mbar_arrive(&full[st]);
+  if (lane < wph && lane % p.producers == pj) {   // each ring's last stage; then its copies land
+    if (ok && used) ok = mbar_wait(&empty[lane * ring + pos], ph ^ 1);
+    if (ok) {
+      meta[lane * ring + pos].flags = kTerminate;
+      mbar_arrive(&full[lane * ring + pos]);
+      if (++pos == ring) {
+        pos = 0;
+        ph ^= 1;
+        used = true;
+      }
+    } else {
+      report(p.status, kDevTimeout);
     }
-    advance_stage();
-  } else if (lane == 0) {
-    report(p.status, kDevTimeout);
-  }
-  // copies in flight land before the CTA may exit: the last fill of each stage
-  if (lane == 0) {
-    for (int i = 0; i < filled; ++i) {
-      if (--st < 0) {
-        st = p.stages - 1;
+    const int fills = used ? ring : pos;
+    for (int i = 0; i < fills; ++i) {
+      if (--pos < 0) {
+        pos = ring - 1;
         ph ^= 1;
       }
-      if (!mbar_wait(&full[st], ph)) report(p.status, kDevTimeout);
+      if (!mbar_wait(&full[lane * ring + pos], ph)) report(p.status, kDevTimeout);
     }
   }
 }
@@ -1023,28 +1037,20 @@ __device__ __forceinline__ void process_bf16(State& st, const Params& p, const u
   }
 }
 
-// Ends a segment.  Sums the lanes' shares; with several warps a head, the
-// others hand (m, l, o) to warp 0 of the head, which stores the output or the
-// record.  False: a bounded wait ran out.
+// Sums the lanes' shares of a warp's state; o[column][2 i + half] is dimension
+// out_dim(g, i, half) of the lane's columns.
 template <int F, bool kLoCols>
-__device__ bool finish(State& st, const Params& p, uint8_t* smem, const Layout& L, int h, int w,
-                       int seg, int seq, int record) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  uint64_t* cfull = reinterpret_cast<uint64_t*>(smem + L.bars) + 2 * p.stages;
-  uint64_t* cempty = cfull + p.hpc;
-  float* comb = reinterpret_cast<float*>(smem + L.comb);
-  const int G = p.group;
+__device__ __forceinline__ void lane_sums(State& st, float (&o)[2][8]) {
   constexpr bool kPair = F == k4Bit && kLoCols;
 #pragma unroll
-  for (int o = kPair ? 2 : 4; o < 32; o <<= 1) {
-    st.l.x += __shfl_xor_sync(kFull, st.l.x, o);
-    st.l.y += __shfl_xor_sync(kFull, st.l.y, o);
+  for (int x = kPair ? 2 : 4; x < 32; x <<= 1) {
+    st.l.x += __shfl_xor_sync(kFull, st.l.x, x);
+    st.l.y += __shfl_xor_sync(kFull, st.l.y, x);
     if (F == k4Bit) {
-      st.zs.x += __shfl_xor_sync(kFull, st.zs.x, o);
-      st.zs.y += __shfl_xor_sync(kFull, st.zs.y, o);
+      st.zs.x += __shfl_xor_sync(kFull, st.zs.x, x);
+      st.zs.y += __shfl_xor_sync(kFull, st.zs.y, x);
     }
   }
-  float o[2][8];       // [column][2 i + half]: dimension out_dim(g, i, half)
   const float f0 = F == k4Bit ? 8388608.f : 1.f;      // 2^24 / 2 of the codes
   const float f1 = F == k4Bit ? f0 * 0.0625f : 1.f;
 #pragma unroll
@@ -1061,35 +1067,54 @@ __device__ bool finish(State& st, const Params& p, uint8_t* smem, const Layout& 
     o[0][2 * i + 1] = fmaf(st.acc[i][2], f1, F == k4Bit ? st.zs.x : 0.f);
     o[1][2 * i + 1] = fmaf(st.acc[i][3], f1, F == k4Bit ? st.zs.y : 0.f);
   }
+}
+
+// Ends a warp's part of a segment.  A head's warp 0, which has the segment's first stage, combines: the others with stages of it
+// hand (m, l, o) over to it through shared memory, and it stores the output or
+// the record.  handed: warp 0: bit i, the phase of warp i's next hand-over;
+// else the hand-overs so far.  False: a bounded wait ran out.
+template <int F, bool kLoCols>
+__device__ bool finish(State& st, const Params& p, uint8_t* smem, const Layout& L, int h, int w,
+                       int& handed, int flags, int seq, int record) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint64_t* cfull = reinterpret_cast<uint64_t*>(smem + L.bars) + 2 * p.stages;
+  uint64_t* cempty = cfull + p.hpc * p.wph;
+  float* comb = reinterpret_cast<float*>(smem + L.comb);
+  const int G = p.group;
+  float o[2][8];
+  lane_sums<F, kLoCols>(st, o);
   float m[2] = {st.m.x, st.m.y}, l[2] = {st.l.x, st.l.y};
   // columns 2 t and 2 t + 1 are heads of the group (not the lo halves' copies)
   const bool live[2] = {2 * t < G && !(kLoCols && t >= 2), 2 * t + 1 < G && !(kLoCols && t >= 2)};
   // a warp's hand-over of a head: eight floats a lane in lane order, then m, l
   if (w > 0) {
-    if (seg > 0 && !mbar_wait(&cempty[h], (seg - 1) & 1)) return false;
+    const int me = w * p.hpc + h;
+    if (handed > 0 && !mbar_wait(&cempty[me], (handed - 1) & 1)) return false;
+    ++handed;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (!live[j]) continue;
-      float* dst = comb + (((w - 1) * p.hpc + h) * G + 2 * t + j) * kCombPitch;
+      float* dst = comb + (me * G + 2 * t + j) * kCombPitch;
       reinterpret_cast<float4*>(dst)[2 * g] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
       reinterpret_cast<float4*>(dst)[2 * g + 1] = make_float4(o[j][4], o[j][5], o[j][6], o[j][7]);
       if (g == 0) *reinterpret_cast<float2*>(dst + 64) = make_float2(m[j], l[j]);
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&cfull[h]);
+    if (lane == 0) mbar_arrive(&cfull[me]);
     return true;
   }
-  if (p.wph > 1 && !mbar_wait(&cfull[h], seg & 1)) return false;
-#pragma unroll 2
-  for (int i = 1; i < p.wph; ++i) {
+  const int parts = flags >> kPartsShift;
+  for (int i = 1; i < parts; ++i) {
+    const int from = i * p.hpc + h;
+    if (!mbar_wait(&cfull[from], handed >> i & 1)) return false;
+    handed ^= 1 << i;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (!live[j]) continue;
-      const float* src = comb + (((i - 1) * p.hpc + h) * G + 2 * t + j) * kCombPitch;
+      const float* src = comb + (from * G + 2 * t + j) * kCombPitch;
       const float4 a = reinterpret_cast<const float4*>(src)[2 * g];
       const float4 b = reinterpret_cast<const float4*>(src)[2 * g + 1];
       const float2 ml = *reinterpret_cast<const float2*>(src + 64);
-      // a warp that had no chunk of the segment: m = -inf, the rest 0
       const float mn = fmaxf(m[j], ml.x);
       const float fa = weight_of(m[j], mn), fb = weight_of(ml.x, mn);
       m[j] = mn;
@@ -1098,6 +1123,8 @@ __device__ bool finish(State& st, const Params& p, uint8_t* smem, const Layout& 
 #pragma unroll
       for (int k = 0; k < 8; ++k) o[j][k] = o[j][k] * fa + v[k] * fb;
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&cempty[from]);
   }
   const int kvh = blockIdx.z * p.hpc + h;
 #pragma unroll
@@ -1119,8 +1146,6 @@ __device__ bool finish(State& st, const Params& p, uint8_t* smem, const Layout& 
       p.ws_l[row] = l[j];
     }
   }
-  __syncwarp();
-  if (p.wph > 1 && lane == 0) mbar_arrive(&cempty[h]);
   return true;
 }
 
@@ -1132,36 +1157,40 @@ __device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
   uint64_t* empty = full + p.stages;
   const StageMeta* meta = reinterpret_cast<const StageMeta*>(smem + L.meta);
   constexpr bool kPair = F == k4Bit && kLoCols;
-  constexpr int NC = chunks_per_warp<F, kLoCols>();
+  constexpr int NC = chunks_per_stage<F, kLoCols>();
   constexpr uint32_t kTile = F == k4Bit ? kRecBytes : kBf16Tile;
-  const uint32_t mine = (w * p.hpc + h) * kTile;           // the warp's first chunk in a stage
-  // to its next: the CTA's consumer warps in turn (4-bit: their number is W)
-  const uint32_t step = (F == k4Bit ? W : p.wph * p.hpc) * kTile;
+  const uint32_t mine = h * kTile;                          // the head's first chunk in a stage
+  const uint32_t step = (W > 0 ? W : p.hpc) * kTile;       // to its next
   const uint32_t v_off = p.kv_bytes / 2;
 
   State st;
-  int seg = 0, stage = 0;
+  int handed = 0;
+  const int ring0 = w * p.ring;  // the warp's ring
+  int stage = ring0;
   uint32_t ph = 0;
-  const uint8_t* base = smem;
+  auto release = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[stage]);
+  };
+  auto advance = [&]() {
+    if (++stage == ring0 + p.ring) {
+      stage = ring0;
+      ph ^= 1;
+    }
+  };
   for (;;) {
-    if (!mbar_wait(&full[stage], ph)) {
-      if (lane == 0) report(p.status, kDevTimeout);
-      return;
-    }
-    const StageMeta& md = meta[stage];
-    const int flags = md.flags;
-    if (flags & kTerminate) return;
-    if (flags & kSegFirst) {
-      load_q<F, kLoCols>(st, p, base + p.kv_bytes + h * p.group * (kD * 2));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) st.acc[i][k] = 0.f;
-      st.m = make_float2(-INFINITY, -INFINITY);
-      st.l = st.zs = make_float2(0.f, 0.f);
-    }
-    const uint8_t* at = base + mine;
-    if (!(flags & kPartial)) {
+    // whole stages inside a segment: a loop of their own, so that the compiler
+    // keeps its registers for them
+    int flags;
+    const uint8_t* at;
+    for (;;) {
+      if (!mbar_wait(&full[stage], ph)) {
+        if (lane == 0) report(p.status, kDevTimeout);
+        return;
+      }
+      flags = meta[stage].flags;
+      at = smem + static_cast<size_t>(stage) * p.stage_bytes + mine;
+      if (flags & (kSegFirst | kSegLast | kTerminate | kPartial)) break;
       if constexpr (kPair) {
         constexpr int NP = NC / 2;
         const uint8_t *ra[NP], *rb[NP];
@@ -1183,66 +1212,74 @@ __device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
         }
         process_wide<NC, false>(st, p, rec, tok, 0);
       } else {
-#pragma unroll
-        for (int i = 0; i < NC; ++i) process_bf16<kLoCols, false>(st, p, at + i * step, v_off, 0, 0);
+#pragma unroll 1
+        for (int i = 0; i < 1 << p.cps_log2; ++i)
+          process_bf16<kLoCols, false>(st, p, at + i * step, v_off, 0, 0);
       }
-    } else {
-      // a short stage, or one with slots that are not visible
+      release();
+      advance();
+    }
+    if (flags & kTerminate) return;
+    const StageMeta& md = meta[stage];
+    if (flags & kSegFirst) {
+      load_q<F, kLoCols>(st, p, at - mine + p.kv_bytes + h * p.group * (kD * 2));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) st.acc[i][k] = 0.f;
+      st.m = make_float2(-INFINITY, -INFINITY);
+      st.l = st.zs = make_float2(0.f, 0.f);
+    }
+    {
+      // a segment's ends, a short stage, or one with slots that are not visible
       const int n = md.n, ctx = md.ctx, v0 = md.v0, ns = md.ns, delta = md.delta;
       auto token_of = [&](int j) { return (v0 + j < ns ? v0 + j : v0 + j + delta) * kChunk; };
-      const int cnt = n > w ? (n - w + p.wph - 1) / p.wph : 0;      // the warp's chunks
       // a missing chunk of a group is stood in for by the first, all unseen
-      auto rec_of = [&](int i) { return at + (i < cnt ? i : 0) * step; };
-      auto tok_of = [&](int i) { return i < cnt ? token_of(w + i * p.wph) : 0x7fffff00; };
+      auto rec_of = [&](int i) { return at + (i < n ? i : 0) * step; };
+      auto tok_of = [&](int i) { return i < n ? token_of(i) : 0x7fffff00; };
       if constexpr (kPair) {
-        if (cnt > 2) {
+        if (n > 2) {
           const uint8_t* ra[2] = {rec_of(0), rec_of(2)};
           const uint8_t* rb[2] = {rec_of(1), rec_of(3)};
           const int o = (lane & 2) >> 1;
           const int tok[2] = {tok_of(o), tok_of(2 + o)};
           process_pairs<2, true>(st, p, ra, rb, tok, ctx);
-        } else if (cnt > 0) {
+        } else {
           const uint8_t* ra[1] = {rec_of(0)};
           const uint8_t* rb[1] = {rec_of(1)};
           const int tok[1] = {tok_of((lane & 2) >> 1)};
           process_pairs<1, true>(st, p, ra, rb, tok, ctx);
         }
       } else if constexpr (F == k4Bit) {
-        if (cnt > 1) {
+        if (n > 1) {
           const uint8_t* rec[2] = {rec_of(0), rec_of(1)};
           const int tok[2] = {tok_of(0), tok_of(1)};
           process_wide<2, true>(st, p, rec, tok, ctx);
-        } else if (cnt > 0) {
+        } else {
           const uint8_t* rec[1] = {rec_of(0)};
           const int tok[1] = {tok_of(0)};
           process_wide<1, true>(st, p, rec, tok, ctx);
         }
       } else {
-        for (int i = 0; i < cnt; ++i)
+#pragma unroll 1
+        for (int i = 0; i < n; ++i)
           process_bf16<kLoCols, true>(st, p, rec_of(i), v_off, tok_of(i), ctx);
       }
     }
     const int seq = md.seq, record = md.record;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[stage]);
+    release();
     if (flags & kSegLast) {
-      if (!finish<F, kLoCols>(st, p, smem, L, h, w, seg, seq, record)) {
+      if (!finish<F, kLoCols>(st, p, smem, L, h, w, handed, flags, seq, record)) {
         if (lane == 0) report(p.status, kDevTimeout);
         return;
       }
-      ++seg;
     }
-    base += p.stage_bytes;
-    if (++stage == p.stages) {
-      stage = 0;
-      ph ^= 1;
-      base = smem;
-    }
+    advance();
   }
 }
 
 template <int F, bool kLoCols, int W>
-__global__ void __launch_bounds__((max_warps<F, kLoCols>() + 1) * 32, 1)
+__global__ void __launch_bounds__((max_warps<F, kLoCols>() + kMaxProducers) * 32, 1)
     window_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -1259,37 +1296,163 @@ __global__ void __launch_bounds__((max_warps<F, kLoCols>() + 1) * 32, 1)
     uint64_t* b = reinterpret_cast<uint64_t*>(smem + L.bars);
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&b[i], 1);
-      mbar_init(&b[p.stages + i], consumers);
+      mbar_init(&b[p.stages + i], p.hpc);
     }
-    for (int i = 0; i < p.hpc; ++i) {
-      mbar_init(&b[2 * p.stages + i], p.wph > 1 ? p.wph - 1 : 1);
-      mbar_init(&b[2 * p.stages + p.hpc + i], 1);
-    }
+    for (int i = 0; i < 2 * consumers; ++i) mbar_init(&b[2 * p.stages + i], 1);
     fence_barrier_init();
   }
   grid_dependency_wait();        // inputs may come from the preceding kernel
   grid_dependents_launch();
-  if (p.direct) {
-    if (tid == 0) *sched = Schedule{static_cast<int>(blockIdx.x), 0, static_cast<int>(blockIdx.x) + 1, 0, 1, 0};
-  } else if (p.small)
+  if (p.small)
     schedule_small(p, sched, reinterpret_cast<int*>(tmp), lens);
   else
     make_schedule(p, sched, tmp);
   __syncthreads();
   const Schedule sc = *sched;
-  if (warp == consumers) {
-    producer<F>(p, sc, smem, L, &tm_k, &tm_v);
+  if (warp >= consumers) {
+    producer<F>(p, sc, smem, L, warp - consumers, &tm_k, &tm_v);
   } else {
     // empty contexts have no chunk and so no segment: zero rows, dealt out
     const int n = p.hpc * p.group * kD;
     for (int s = blockIdx.x; s < p.num_seqs; s += p.ctas) {
       if (p.context_lens[s] > 0) continue;
-      if (tid == 0 && blockIdx.z == 0 && p.num_seqs <= p.ctas && !p.direct) p.ws_split[s] = make_int4(-1, 0, 0, 0);
+      if (tid == 0 && blockIdx.z == 0 && p.num_seqs <= p.ctas) p.ws_split[s] = make_int4(-1, 0, 0, 0);
       float* dst = p.out + (static_cast<long long>(s) * p.hq + blockIdx.z * p.hpc * p.group) * kD;
       for (int i = tid; i < n; i += consumers * 32) dst[i] = 0.f;
     }
     consumer<F, kLoCols, W>(p, smem, L);
   }
+}
+
+// -------------------------------------------------------------------- direct
+
+// Small batches of bounded length: CTA (x, z) does KV head z of sequence x alone,
+// in one launch.  Warp w takes chunks w, w + 16, ... : it fetches their block
+// ids, issues their copies (all of them fit) and q's loads, waits once, and the
+// warps meet at the end.  Bound by latency: four dependent memory round trips.
+constexpr int kDirectWarps = 16;
+constexpr int kDirectChunks4 = 128, kDirectChunks16 = 48;    // longest sequence (chunks)
+
+template <int F, bool kLoCols>
+__global__ void __launch_bounds__(kDirectWarps * 32, 1)
+    window_direct_kernel(const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const Params p, int per_warp) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bars[kDirectWarps];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  constexpr uint32_t kBytes = F == k4Bit ? kRecBytes : 2 * kBf16Tile;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int seq = blockIdx.x, kvh = blockIdx.z, G = p.group;
+  uint8_t* mine = smem + static_cast<size_t>(w) * per_warp * kBytes;
+  float* comb = reinterpret_cast<float*>(smem + static_cast<size_t>(kDirectWarps) * per_warp * kBytes);
+  if (lane == 0) {
+    if (F == kBf16) {
+      prefetch_tensormap(&tm_k);
+      prefetch_tensormap(&tm_v);
+    }
+    mbar_init(&bars[w], 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int ctx = load_ctx(p, seq);
+  const Visible vis = visible_of(p, ctx);
+  auto chunk_of = [&](int i) {               // the warp's i-th chunk as a token chunk
+    const int v = w + kDirectWarps * i;
+    return v < vis.ns ? v : v + vis.delta;
+  };
+  const int n = w < vis.n ? (vis.n - w + kDirectWarps - 1) / kDirectWarps : 0;   // <= per_warp <= 8
+  if (n > 0) {
+    int page = 0;
+    if (lane < n) page = p.block_tables[static_cast<long long>(seq) * p.max_blocks + (chunk_of(lane) >> p.cpb_log2)];
+    if (lane == 0) mbar_arrive_expect_tx(&bars[w], n * kBytes);
+    __syncwarp();
+    if (lane < n) {
+      if (page < 0 || page >= p.num_blocks) {
+        report(p.status, TVL_DEV_BAD_BLOCK_ID);
+        page = 0;
+      }
+      const long long chunk = (static_cast<long long>(page) << p.cpb_log2) +
+                              (chunk_of(lane) & ((1 << p.cpb_log2) - 1));
+      if (F == k4Bit) {
+        bulk_load(mine + lane * kBytes, p.kv4 + (chunk * p.hkv + kvh) * kRecBytes, kBytes, &bars[w],
+                  policy_evict_first());
+      } else {
+        const int tok = static_cast<int>(chunk * kChunk);
+        tma_load_3d(mine + lane * kBytes, &tm_k, 0, tok, kvh, &bars[w]);
+        tma_load_3d(mine + lane * kBytes + kBf16Tile, &tm_v, 0, tok, kvh, &bars[w]);
+      }
+    }
+  }
+  State st;
+  load_q<F, kLoCols>(st, p, reinterpret_cast<const uint8_t*>(
+                                p.q + (static_cast<size_t>(seq) * p.hq + static_cast<size_t>(kvh) * G) * kD));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) st.acc[i][k] = 0.f;
+  st.m = make_float2(-INFINITY, -INFINITY);
+  st.l = st.zs = make_float2(0.f, 0.f);
+  if (n > 0 && !mbar_wait(&bars[w], 0) && lane == 0) report(p.status, kDevTimeout);
+  // a missing second chunk is stood in for by the first, all unseen
+  auto rec_of = [&](int i) -> const uint8_t* { return mine + (i < n ? i : 0) * kBytes; };
+  auto tok_of = [&](int i) { return i < n ? chunk_of(i) * kChunk : 0x7fffff00; };
+#pragma unroll 1
+  for (int i = 0; i < n; i += 2) {
+    if constexpr (F == k4Bit && kLoCols) {
+      const uint8_t* ra[1] = {rec_of(i)};
+      const uint8_t* rb[1] = {i + 1 < n ? rec_of(i + 1) : rec_of(i)};
+      const int tok[1] = {tok_of(i + ((lane & 2) >> 1))};
+      process_pairs<1, true>(st, p, ra, rb, tok, ctx);
+    } else if constexpr (F == k4Bit) {
+      const uint8_t* rec[2] = {rec_of(i), rec_of(i + 1)};
+      const int tok[2] = {tok_of(i), tok_of(i + 1)};
+      process_wide<2, true>(st, p, rec, tok, ctx);
+    } else {
+      process_bf16<kLoCols, true>(st, p, rec_of(i), kBf16Tile, tok_of(i), ctx);
+      if (i + 1 < n) process_bf16<kLoCols, true>(st, p, rec_of(i + 1), kBf16Tile, tok_of(i + 1), ctx);
+    }
+  }
+  float o[2][8];
+  lane_sums<F, kLoCols>(st, o);
+  const float m[2] = {st.m.x, st.m.y}, l[2] = {st.l.x, st.l.y};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (2 * t + j >= G || (kLoCols && t >= 2)) continue;
+    float* dst = comb + (w * G + 2 * t + j) * kCombPitch;
+    reinterpret_cast<float4*>(dst)[2 * g] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+    reinterpret_cast<float4*>(dst)[2 * g + 1] = make_float4(o[j][4], o[j][5], o[j][6], o[j][7]);
+    if (g == 0) *reinterpret_cast<float2*>(dst + 64) = make_float2(m[j], l[j]);
+  }
+  __syncthreads();
+  if (w >= G) return;
+  // warp w: query head w of the group, two dimensions a lane; lane i knows warp i's weight
+  const float2 ml = lane < kDirectWarps
+                        ? *reinterpret_cast<const float2*>(comb + (lane * G + w) * kCombPitch + 64)
+                        : make_float2(-INFINITY, 0.f);
+  float top = ml.x;
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+  // (a warp without chunks: l and o are 0; all scores NaN: kept)
+  const float mine_w = weight_of(ml.x, top);
+  float den = ml.y * mine_w;
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) den += __shfl_xor_sync(kFull, den, x);
+  float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kDirectWarps; ++i) {
+    const float wi = __shfl_sync(kFull, mine_w, i);
+    const float2 v = reinterpret_cast<const float2*>(comb + (i * G + w) * kCombPitch)[lane];
+    sum.x = fmaf(wi, v.x, sum.x);
+    sum.y = fmaf(wi, v.y, sum.y);
+  }
+  const float inv = ctx > 0 ? 1.0f / den : 0.f;           // an empty context: zero rows
+  float* dst = p.out + (static_cast<long long>(seq) * p.hq + static_cast<long long>(kvh) * G + w) * kD;
+  const int e = 2 * lane;                                  // place 8 g + k in the hand-over
+  dst[out_dim<F>(e >> 3, (e & 7) >> 1, 0)] = sum.x * inv;
+  dst[out_dim<F>(e >> 3, (e & 7) >> 1, 1)] = sum.y * inv;
 }
 
 // --------------------------------------------------------------------- merge
@@ -1411,6 +1574,22 @@ bool cache_map(CUtensorMap* m, const void* base, int hkv, long long tokens, int 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int F, bool kLoCols>
+cudaError_t launch_direct(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int chunks,
+                          cudaStream_t stream) {
+  auto kern = window_direct_kernel<F, kLoCols>;
+  static PerDeviceOnce once;
+  cudaError_t e = once.run([&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit - 1024);
+  });
+  if (e != cudaSuccess) return e;
+  const int per_warp = (chunks + kDirectWarps - 1) / kDirectWarps;
+  const uint32_t smem = 1024 + kDirectWarps * (per_warp * (F == k4Bit ? kRecBytes : 2 * kBf16Tile) +
+                                               p.group * kCombPitch * 4);
+  return launch_pdl(kern, dim3(p.num_seqs, 1, p.hkv), dim3(kDirectWarps * 32), smem, stream, tk, tv,
+                    p, per_warp);
+}
+
 template <int F, bool kLoCols, int W>
 cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, dim3 grid,
                      uint32_t smem, cudaStream_t stream) {
@@ -1420,7 +1599,7 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const Params&
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, grid, dim3((p.hpc * p.wph + 1) * 32), smem, stream, tk, tv, p);
+  return launch_pdl(kern, grid, dim3((p.hpc * p.wph + p.producers) * 32), smem, stream, tk, tv, p);
 }
 
 // KV heads one CTA owns: the largest divisor up to `most`.
@@ -1433,12 +1612,12 @@ int heads_per_cta(int num_kv_heads, int most) {
 // The CTA's shape for a format and group size.
 template <int F, bool kLoCols>
 void shape(Params& p) {
-  p.hpc = p.direct ? 1 : heads_per_cta(p.hkv, max_heads<F, kLoCols>());
-  constexpr int nc = chunks_per_warp<F, kLoCols>();
+  p.hpc = heads_per_cta(p.hkv, max_heads<F, kLoCols>());
   p.wph = max_warps<F, kLoCols>() / p.hpc;
-  if (p.wph * nc > 32 || (F == k4Bit && p.hpc == 1)) p.wph = 8;   // a producer lane per chunk of a stage
-  p.cps = p.wph * nc;
-  p.batch = 32 / p.cps * p.cps;
+  p.producers = p.wph < kMaxProducers ? p.wph : kMaxProducers;
+  // bf16 takes a stage's chunks one by one: as many as make 32 KB of it
+  const int nc = F == k4Bit ? chunks_per_stage<F, kLoCols>() : p.hpc > 4 ? 1 : p.hpc > 2 ? 2 : 4;
+  p.cps_log2 = nc == 4 ? 2 : nc == 2 ? 1 : 0;
 }
 
 }  // namespace
@@ -1475,30 +1654,49 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
   while ((kChunk << p.cpb_log2) < a.block_size) ++p.cpb_log2;
   p.window = a.window;
   p.sinks = a.window > 0 ? a.sinks : 0;
+  p.scale_log2 = a.scale * kLog2e;
+  p.status = a.status;
   const bool lo_cols = p.group <= 4;
-  // Small batches of bounded length: one CTA a sequence and KV head, one
-  // launch.  The bound is the block table's capacity or the window.
+  const long long tokens = static_cast<long long>(a.num_blocks) * a.block_size;
+  CUtensorMap tk = {}, tv = {};
+  auto maps = [&](int heads) {
+    return four || (cache_map(&tk, a.k_cache, a.num_kv_heads, tokens, heads) &&
+                    cache_map(&tv, a.v_cache, a.num_kv_heads, tokens, heads));
+  };
+  // The chunks a sequence can have: the block table's capacity, or the window's
+  // and the sinks' with their edges.
   const long long capacity = static_cast<long long>(a.max_blocks_per_seq) << p.cpb_log2;
-  const long long seen = p.window > 0 ? p.window / kChunk + p.sinks / kChunk + 4LL : capacity;
-  p.direct = static_cast<long long>(a.num_seqs) * p.hkv <= a.sms &&
-             (seen < capacity ? seen : capacity) <= (four ? kDirectChunks4 : kDirectChunks16);
+  const long long seen = p.window > 0 ? p.window / kChunk + 2LL + (p.sinks + kChunk - 1LL) / kChunk : capacity;
+  const long long chunks = seen < capacity ? seen : capacity;
+  if (static_cast<long long>(a.num_seqs) * p.hkv <= a.sms &&
+      chunks <= (four ? kDirectChunks4 : kDirectChunks16)) {
+    if (!maps(1)) return cudaErrorInvalidValue;
+    const int n = static_cast<int>(chunks);
+    if (!four)
+      return lo_cols ? launch_direct<kBf16, true>(tk, tv, p, n, stream)
+                     : launch_direct<kBf16, false>(tk, tv, p, n, stream);
+    return lo_cols ? launch_direct<k4Bit, true>(tk, tv, p, n, stream)
+                   : launch_direct<k4Bit, false>(tk, tv, p, n, stream);
+  }
   if (!four)
     lo_cols ? shape<kBf16, true>(p) : shape<kBf16, false>(p);
   else
     lo_cols ? shape<k4Bit, true>(p) : shape<k4Bit, false>(p);
   const int groups = p.hkv / p.hpc;
-  p.ctas = p.direct ? a.num_seqs : a.sms / groups < 1 ? 1 : a.sms / groups;
-  p.kv_bytes = p.cps * p.hpc * (four ? kRecBytes : 2 * kBf16Tile);
-  p.stage_bytes = align_up(p.kv_bytes + p.hpc * p.group * kD * 2, 1024);
-  const uint32_t fixed = make_layout(0, p.stage_bytes, p.hpc, p.wph, p.group).total + 1024 + 16;
-  int stages = static_cast<int>((kSmemLimit - fixed) / (p.stage_bytes + sizeof(StageMeta) + 16));
-  p.stages = stages > 8 ? 8 : stages;
-  if (p.stages < 2) return cudaErrorInvalidConfiguration;
-  p.scale_log2 = a.scale * kLog2e;
+  p.ctas = a.sms / groups < 1 ? 1 : a.sms / groups;
+  for (;; --p.cps_log2) {              // two stages a ring at least (bf16: by smaller stages)
+    p.kv_bytes = (p.hpc << p.cps_log2) * (four ? kRecBytes : 2 * kBf16Tile);
+    p.stage_bytes = align_up(p.kv_bytes + p.hpc * p.group * kD * 2, 1024);
+    const uint32_t fixed = make_layout(0, p.stage_bytes, p.hpc, p.wph, p.group).total + 1024 + 16;
+    const int most = static_cast<int>((kSmemLimit - fixed) / (p.stage_bytes + sizeof(StageMeta) + 16));
+    p.ring = (most > 48 ? 48 : most) / p.wph;
+    if (p.ring >= 2 || four || p.cps_log2 == 0) break;
+  }
+  p.stages = p.ring * p.wph;
+  if (p.ring < 1) return cudaErrorInvalidConfiguration;
   p.seg_weight = four ? kSegWeight4 : kSegWeight16;
   const long long longest = capacity + p.seg_weight;
-  p.small = !p.direct && a.num_seqs <= (p.hpc * p.wph + 1) * 32 && longest * a.num_seqs * (p.ctas + 1) < (1LL << 31);
-  p.status = a.status;
+  p.small = a.num_seqs <= (p.hpc * p.wph + p.producers) * 32 && longest * a.num_seqs * (p.ctas + 1) < (1LL << 31);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const size_t rows = 2 * static_cast<size_t>(p.ctas) * a.num_q_heads;
   const size_t ab = (rows * 4 + 255) / 256 * 256;
@@ -1508,27 +1706,21 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
   p.ws_split = reinterpret_cast<int4*>(ws + 2 * ab + rows * kD * 4);
   p.ws_total = reinterpret_cast<long long*>(ws + 2 * ab + rows * kD * 4 +
                                             (static_cast<size_t>(p.ctas) * 16 + 255) / 256 * 256);
-  CUtensorMap tk = {}, tv = {};
-  if (!four) {
-    const long long tokens = static_cast<long long>(a.num_blocks) * a.block_size;
-    if (!cache_map(&tk, a.k_cache, a.num_kv_heads, tokens, p.hpc) ||
-        !cache_map(&tv, a.v_cache, a.num_kv_heads, tokens, p.hpc))
-      return cudaErrorInvalidValue;
-  }
+  if (!maps(p.hpc)) return cudaErrorInvalidValue;
   const uint32_t smem = make_layout(p.stages, p.stage_bytes, p.hpc, p.wph, p.group).total + 1024;
   const dim3 grid(p.ctas, 1, groups);
   cudaError_t e;
-  const bool one = p.hpc == 1;          // 8 consumer warps instead of 12
+  const bool wide = p.hpc == 4;         // a constant stride between a head's chunks
   if (!four)
     e = lo_cols ? launch_t<kBf16, true, 0>(tk, tv, p, grid, smem, stream)
                 : launch_t<kBf16, false, 0>(tk, tv, p, grid, smem, stream);
   else if (lo_cols)
-    e = one ? launch_t<k4Bit, true, 8>(tk, tv, p, grid, smem, stream)
-            : launch_t<k4Bit, true, 12>(tk, tv, p, grid, smem, stream);
+    e = wide ? launch_t<k4Bit, true, 4>(tk, tv, p, grid, smem, stream)
+             : launch_t<k4Bit, true, 0>(tk, tv, p, grid, smem, stream);
   else
-    e = one ? launch_t<k4Bit, false, 8>(tk, tv, p, grid, smem, stream)
-            : launch_t<k4Bit, false, 12>(tk, tv, p, grid, smem, stream);
-  if (e != cudaSuccess || p.direct) return e;
+    e = wide ? launch_t<k4Bit, false, 4>(tk, tv, p, grid, smem, stream)
+             : launch_t<k4Bit, false, 0>(tk, tv, p, grid, smem, stream);
+  if (e != cudaSuccess) return e;
   // a sequence has about 1 + ctas / num_seqs records: one warp a head and
   // batch of 8, up to 16
   int parts = 1;
