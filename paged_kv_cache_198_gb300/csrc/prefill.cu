@@ -609,18 +609,32 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         auto hidden = [&](int cc) -> uint32_t {
           return ~below(limit + 1 - 32 * cc) | (below(low - 32 * cc) & ~below(sink - 32 * cc));
         };
+        if constexpr (kWin) {
+          // masked scores are set to infinity (against the scale's sign), so
+          // that one path serves every tile
+          if (masked) {
+            const uint32_t none = __float_as_uint(p.scale_log2 < 0.f ? INFINITY : -INFINITY);
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+              const uint32_t hid = hidden(cc);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (hid >> e & 1u) sr[cc][e] = none;
+            }
+            masked = false;
+          }
+        }
         // row maximum of the scaled scores of this tile
         auto tile_max = [&]() -> float {
           float mt;
-          if (masked) {
+          if (!kWin && masked) {
             mt = -INFINITY;
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) {
-              const uint32_t hid = kWin ? hidden(cc) : 0u;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 float v = __uint_as_float(sr[cc][e]) * p.scale_log2;
-                if (kWin ? (hid >> e & 1u) != 0 : cc * 32 + e > limit) v = -INFINITY;
+                if (cc * 32 + e > limit) v = -INFINITY;
                 mt = fmaxf(mt, v);
               }
             }
@@ -648,16 +662,15 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         auto make_p = [&](float mref) -> float2 {
           const float2 nm2 = make_float2(-mref, -mref);
           float2 tsum = make_float2(0.f, 0.f);
-          if (masked) {
+          if (!kWin && masked) {
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) {
-              const uint32_t hid = kWin ? hidden(cc) : 0u;
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 float2 v = make_float2(__uint_as_float(sr[cc][e]), __uint_as_float(sr[cc][e + 1]));
                 v = __ffma2_rn(v, sl2, nm2);
-                if (kWin ? (hid >> e & 1u) != 0 : cc * 32 + e > limit) v.x = -INFINITY;
-                if (kWin ? (hid >> e & 2u) != 0 : cc * 32 + e + 1 > limit) v.y = -INFINITY;
+                if (cc * 32 + e > limit) v.x = -INFINITY;
+                if (cc * 32 + e + 1 > limit) v.y = -INFINITY;
                 const float2 pv = make_float2(ex2(v.x), ex2(v.y));
                 tsum = __fadd2_rn(tsum, pv);
                 pk[cc >> 1][(cc & 1) * 16 + e / 2] = pack_half2(pv.x, pv.y);
@@ -680,8 +693,8 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         float f = 1.f;
         bool move = false;
         float2 tsum;
-        if (j == 0) {
-          m_used = tile_max();
+        if (j == 0) m_used = tile_max();
+        if (!kWin && j == 0) {
           tsum = make_p(m_used == -INFINITY ? 0.f : m_used);
         } else {
           // P straight from the reference maximum; only a row sum that shows
@@ -691,7 +704,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
           move = !(ts <= 60000.f);
           // a window may leave a row without a key in its first tiles: it has
           // no reference yet (and O and l are 0)
-          if constexpr (kWin) move |= m_used == -INFINITY;
+          if constexpr (kWin) move = j > 0 && (move || m_used == -INFINITY);
           if (__any_sync(kFull, move)) {
             if (move) {
               const float m_new = fmaxf(m_used, tile_max());
@@ -971,6 +984,9 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   p.window = a.window < cap ? a.window : cap;
   p.sinks = a.window == 0 ? 0 : a.sinks < cap ? a.sinks : cap;
   if (a.windowed) {
+    // masked scores become infinities, which a zero scale would turn into NaN;
+    // 1e-37 times any finite score that leaves P other than 1 is out of range
+    if (fabsf(p.scale_log2) < 1e-37f) p.scale_log2 = copysignf(1e-37f, p.scale_log2);
     // With so few units that single heads would still leave no SM two of them,
     // the tile's latency counts, not the shared K/V tile: one head a unit.
     const long long pairs = static_cast<long long>(a.num_seqs) * p.n_qtiles * (p.hq / 2);
