@@ -42,7 +42,7 @@
 //             2^-14 <= |v| <= 65504; smaller values keep an absolute error
 //             below 2^-25; a larger one becomes infinite, which leaves rows
 //             that are not finite, reported as TVL_DEV_NONFINITE; keys past
-//             the context become 0);
+//             the context become 0); kWin: the softmax warps convert instead;
 //   4NH+3     P.V issuer (below).
 // P and V go through fp16 rather than bf16 so that rounding P costs at most
 // 2^-11 relative (bf16 would cost 2^-8) -- the fp32-accumulated result stays
@@ -58,6 +58,24 @@
 // four sinks is nine or ten tiles of 128 keys, where whole tiles would be ten
 // or eleven.  The output is bf16 (P's fp16 rounding, 2^-11, is below the
 // output's, 2^-8), staged as one swizzled 128-byte row.
+// What bounds it: the softmax warps' tile, not the tensor pipe (32% active, 2
+// sequences x 4096 new rows, window 2048: 208 us, 667 TFLOP/s).  Per tile of
+// two heads, ~3200 cycles: ~1700 of both heads' exponentials (1024 at the exp
+// unit's rate), the rest waits of 200-250 cycles each for S, V and the last
+// P.V.  Three things this form does differently, with what they gave there:
+//   - masked scores become infinite in place, so one copy of the exponential
+//     loop serves every tile (the loop streams through the instruction cache):
+//     230 -> 216 us;
+//   - V is converted by the softmax warps, four pieces a thread, between the
+//     wait for S and the exponentials: one converting warp took 2800 cycles a
+//     tile, beside two busy softmax warps on its scheduler, and set the pace;
+//     four of its own left the softmax 208 registers and spills (212 us);
+//   - the issuing warps stay whole and elect one thread: 660 + 740 cycles a
+//     tile for 24 MMAs, where a divergent thread took 2030 + 1040.  With the
+//     conversion: 216 -> 208 us.
+// Measured and left: two warps a row (16 softmax warps, 64 keys each): 230 us;
+// the scores 32 at a time in rolled loops: 242; a fourth stage: no gain; the
+// heads started half a tile apart: 213.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -76,6 +94,8 @@ constexpr int kD = 64;
 constexpr int kBM = 128;
 constexpr int kBN = 128;
 constexpr int kStages = 3;
+constexpr int kConvBatch = 8;           // 16-byte pieces of V a lane converts at once
+                                        // (one converting warp: 2800 -> 2170 cycles a tile)
 constexpr int kOPitch = kD * 4 + 16;    // bytes per staged output row: 16-byte rows
                                         // land on distinct banks (no conflicts)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -179,6 +199,17 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, co
   return false;
 }
 
+// True in one thread of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(pred));
+  return pred != 0;
+}
+
 // One work unit: a 128-row query tile of NH query heads of one sequence.
 // Every role of the CTA derives the same units in the same order.
 struct Unit {
@@ -196,6 +227,38 @@ __device__ __forceinline__ void window_blocks(const Params& p, int pos_first, in
   const int w0 = first / p.bs;
   sb = min(p.sinks / p.bs + (p.sinks % p.bs != 0 ? 1 : 0), w0);
   delta = (w0 - sb) * p.bs;
+}
+
+// N 16-byte pieces of a V tile, `step` apart from piece e on: bf16 to fp16 in
+// place.  Keys that no row of the unit sees become 0.
+template <int N, int kStep>
+__device__ __forceinline__ void load_pieces(const uint8_t* vt, int e, uint4 (&w)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint4*>(vt + (e + kStep * i) * 16);
+}
+template <int N, int kStep, bool kWin>
+__device__ __forceinline__ void convert_pieces(const Params& p, const Unit& x, int j, uint8_t* vt, int e,
+                                               uint4 (&w)[N]) {
+  // of the tile's keys i < end, those with i < sink or i >= low
+  const int end = x.ctx - (kWin ? x.delta : 0) - j * kBN;
+  const int low = kWin && p.window > 0 ? x.pos_first - p.window - x.delta + 1 - j * kBN : 0;
+  const int sink = kWin ? p.sinks - j * kBN : 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    w[i].x = bf16x2_to_half2(w[i].x);
+    w[i].y = bf16x2_to_half2(w[i].y);
+    w[i].z = bf16x2_to_half2(w[i].z);
+    w[i].w = bf16x2_to_half2(w[i].w);
+  }
+  if (end < kBN || (low > 0 && sink < kBN)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = (e + kStep * i) >> 3;
+      if (!(u < end && (u < sink || u >= low))) w[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) *reinterpret_cast<uint4*>(vt + (e + kStep * i) * 16) = w[i];
 }
 
 // Index of the k-th unit of CTA c among G: the units in longest-first order
@@ -356,7 +419,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&B->kv_full[i], 1);
       mbar_init(&B->kv_empty[i], 1);
-      mbar_init(&B->v_ready[i], 1);
+      mbar_init(&B->v_ready[i], kWin ? C::kSoftmaxWarps : 1);
     }
     for (int i = 0; i < NH; ++i) {
       mbar_init(&B->s_full[i], 1);
@@ -457,63 +520,81 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
     //   P.V: O_h += P_h(t) V(t) once P_h(t) is in TMEM (p_full) and V(t) is
     //   fp16 (v_ready); then the stage goes back to the producer (kv_empty:
     //   Q K^T(t) is complete too, the softmax having read S_h(t)).
-    if (lane == 0) {
-      const bool is_qk = warp == C::kMmaWarp;
-      const uint32_t q_addr = smem_addr(smem + C::kQOff);
-      int gt = 0;                                       // key tile of the stream
-      int st = 0, ph = 0;                               // its stage and phase
-      int nq = 0;                                       // units begun
-      bool ok = true;
-      for (int k = 0; ok; ++k) {
-        Unit x;
-        if (!next_valid_unit<NH, K, false, kWin>(p, tab, k, x)) break;
-        for (int j = 0; ok && j < x.n_kv; ++j, ++gt) {
-          if (is_qk) {
-            ok = wait_or_abort(&B->kv_full[st], ph, p);
-            if (ok && j == 0) ok = wait_or_abort(&B->q_full, nq & 1, p);
-            const uint32_t k_addr = smem_addr(smem + C::kKOff + st * kTileBytes);
-            for (int hh = 0; ok && hh < NH; ++hh) {
-              if (gt > 0) ok = wait_or_abort(&B->s_free[hh], (gt - 1) & 1, p);
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t qa = q_addr + hh * kTileBytes;
+    // The whole warp walks the loop and one elected thread issues: addresses
+    // and descriptors are then uniform values, which tcgen05.mma takes as they
+    // are (under a divergent branch each costs a transfer of its own).
+    const bool is_qk = __shfl_sync(kFull, warp, 0) == C::kMmaWarp;
+    const uint32_t q_addr = __shfl_sync(kFull, smem_addr(smem + C::kQOff), 0);
+    const uint32_t k_base = __shfl_sync(kFull, smem_addr(smem + C::kKOff), 0);
+    const uint32_t v_base = __shfl_sync(kFull, smem_addr(smem + C::kVOff), 0);
+    const uint32_t td = __shfl_sync(kFull, tmem, 0);
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(kFull, wait_or_abort(bar, parity, p));
+    };
+    int gt = 0;                                         // key tile of the stream
+    int st = 0, ph = 0;                                 // its stage and phase
+    int nq = 0;                                         // units begun
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      Unit x;
+      if (!next_unit(k, x)) break;
+      const int n_kv = __shfl_sync(kFull, x.n_kv, 0);
+      for (int j = 0; ok && j < n_kv; ++j, ++gt) {
+        if (is_qk) {
+          ok = wait_all(&B->kv_full[st], ph);
+          if (ok && j == 0) ok = wait_all(&B->q_full, nq & 1);
+          const uint32_t k_addr = k_base + st * kTileBytes;
+#pragma unroll
+          for (int hh = 0; hh < NH; ++hh) {
+            if (ok && gt > 0) ok = wait_all(&B->s_free[hh], (gt - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t da = desc_sw128(q_addr + hh * kTileBytes, 16, 1024);
+            const uint64_t db = desc_sw128(k_addr, 16, 1024);
+            if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kD / 16; ++kk)
-                mma_f16_ss(tmem + C::s_col(hh), desc_sw128(qa + kk * 32, 16, 1024),
-                           desc_sw128(k_addr + kk * 32, 16, 1024), kIdescQK, kk > 0);
+                mma_f16_ss(td + C::s_col(hh), da + kk * 2, db + kk * 2, kIdescQK, kk > 0);
               mma_commit(&B->s_full[hh]);
+              if (hh == NH - 1 && j + 1 == n_kv) mma_commit(&B->q_empty);
             }
-            if (ok && j + 1 == x.n_kv) mma_commit(&B->q_empty);
-          } else {
-            ok = wait_or_abort(&B->v_ready[st], ph, p);
-            const uint32_t v_addr = smem_addr(smem + C::kVOff + st * kTileBytes);
-            for (int hh = 0; ok && hh < NH; ++hh) {
-              ok = wait_or_abort(&B->p_full[hh], gt & 1, p);
-              if (!ok) break;
-              tc_fence_after();
+            __syncwarp();
+          }
+        } else {
+          ok = wait_all(&B->v_ready[st], ph);
+          const uint32_t v_addr = v_base + st * kTileBytes;
+#pragma unroll
+          for (int hh = 0; hh < NH; ++hh) {
+            if (ok) ok = wait_all(&B->p_full[hh], gt & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t db = desc_sw128(v_addr, 16, 1024);
+            if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kBN / 16; ++kk)
-                mma_f16_ts(tmem + C::o_col(hh), tmem + C::p_col(hh) + kk * 8,
-                           desc_sw128(v_addr + kk * 2048, 16, 1024), kIdescPV,
+                mma_f16_ts(td + C::o_col(hh), td + C::p_col(hh) + kk * 8, db + kk * 128, kIdescPV,
                            (j > 0 || kk > 0));
               mma_commit(&B->pv_done[hh]);
+              if (hh == NH - 1) mma_commit(&B->kv_empty[st]);
             }
-            if (ok) mma_commit(&B->kv_empty[st]);
+            __syncwarp();
           }
-          if (++st == kStages) { st = 0; ph ^= 1; }
         }
-        ++nq;
+        if (++st == kStages) { st = 0; ph ^= 1; }
       }
-      // every MMA issued must be complete before TMEM is released
+      ++nq;
+    }
+    // every MMA issued must be complete before TMEM is released
+    if (elect_one()) {
       mma_commit(&B->mma_done);
       if (!mbar_wait(&B->mma_done, 0)) report(p.status, kDevTimeout);
     }
-  } else {
+    __syncwarp();
+  } else if (!kWin) {
     // ------------------------------------------------------- V conversion
     // V tile bf16 -> fp16 in place, 16 bytes at a time (the swizzle only
     // permutes 16-byte chunks within a 128-byte row, so a chunk's row is its
     // offset / 128); keys past the context become 0.
-    const int t = lane;
     int gt = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -524,25 +605,11 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         ok = wait_or_abort(&B->kv_full[st], (gt / kStages) & 1, p);
         if (__any_sync(kFull, !ok)) { ok = false; break; }
         uint8_t* vt = smem + C::kVOff + st * kTileBytes;
-#pragma unroll 4
-        for (int e = t; e < static_cast<int>(kTileBytes / 16); e += 32) {
-          uint4 w = *reinterpret_cast<const uint4*>(vt + e * 16);
-          bool live = j * kBN + (e >> 3) < x.ctx;
-          if constexpr (kWin) {
-            // keys that no row of the unit sees become 0 as well
-            const int u = j * kBN + (e >> 3);
-            live = u < x.ctx - x.delta &&
-                   (u < p.sinks || p.window == 0 || u > x.pos_first - p.window - x.delta);
-          }
-          if (live) {
-            w.x = bf16x2_to_half2(w.x);
-            w.y = bf16x2_to_half2(w.y);
-            w.z = bf16x2_to_half2(w.z);
-            w.w = bf16x2_to_half2(w.w);
-          } else {
-            w = make_uint4(0, 0, 0, 0);
-          }
-          *reinterpret_cast<uint4*>(vt + e * 16) = w;
+#pragma unroll 1
+        for (int e = lane; e < static_cast<int>(kTileBytes / 16); e += 32 * kConvBatch) {
+          uint4 w[kConvBatch];                          // loads first: one latency a batch
+          load_pieces<kConvBatch, 32>(vt, e, w);
+          convert_pieces<kConvBatch, 32, kWin>(p, x, j, vt, e, w);
         }
         fence_async_smem();
         __syncwarp();
@@ -585,6 +652,17 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         ok = wait_or_abort(&B->s_full[hh], gt & 1, p);
         if (__any_sync(kFull, !ok)) { ok = false; break; }
         tc_fence_after();
+        // kWin: the softmax warps also convert V, a few pieces each between two
+        // waits
+        constexpr int kPieces = static_cast<int>(kTileBytes / 16) / (C::kSoftmaxWarps * 32);
+        const int st = gt % kStages;
+        uint8_t* vt = smem + C::kVOff + st * kTileBytes;
+        uint4 w[kPieces];
+        if constexpr (kWin) {
+          ok = wait_or_abort(&B->kv_full[st], (gt / kStages) & 1, p);
+          if (__any_sync(kFull, !ok)) { ok = false; break; }
+          load_pieces<kPieces, C::kSoftmaxWarps * 32>(vt, threadIdx.x, w);
+        }
         uint32_t sr[4][32];                             // this row's 128 scores
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) tmem_ld32(s_addr + cc * 32, sr[cc]);
@@ -593,6 +671,12 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&B->s_free[hh]);
+        if constexpr (kWin) {
+          convert_pieces<kPieces, C::kSoftmaxWarps * 32, kWin>(p, x, j, vt, threadIdx.x, w);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B->v_ready[st]);
+        }
 
         // Tiles on the causal diagonal or past the context need the mask.
         bool masked = (key0 + kBN - 1 > pos_first) || (key0 + kBN > ctx);
