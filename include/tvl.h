@@ -6,7 +6,7 @@
  * prefix; around them the rotary embedding fused into the write, block
  * copies for copy-on-write, and a host block allocator.  Two ways to hold
  * more context: a cache in 4 bits (write, expand, copy, decode) and attention
- * with a sliding window and sinks (decode, prefill, release of old blocks).
+ * with a sliding window and sinks (decode, prefill).
  *
  * Sources of the method (web pages on tiny-vLLM and nano-vLLM):
  *   [tiny-vllm README]  "tiny-vllm" README, Korean translation: feature list
@@ -343,8 +343,8 @@ tvl_status tvl_kv4_copy_blocks(void* cache, const int32_t* src, const int32_t* d
  * tokens j <= p with j > p - window or j < sinks: the last `window` tokens,
  * itself included, and the first `sinks`.  window == 0: no window, every j <=
  * p is seen (sinks then has no effect).  Blocks that hold no visible token
- * are not read, and their block table entries may hold anything (see
- * tvl_allocator_trim).
+ * are not read, and their block table entries may hold anything: a caller may
+ * hand such blocks back and reuse them.
  */
 
 /* Workspace of the two decode calls below, for the current device (its SM
@@ -359,7 +359,7 @@ tvl_status tvl_window_decode_workspace_size(int num_q_heads, int num_kv_heads, i
  * 16-token groups are balanced over one CTA per SM and merged by log-sum-exp;
  * results do not vary from call to call.
  *   out : float32 [S, Hq, D]; q : bf16 [S, Hq, D]; cache : see above
- * context_lens[s] == 0 gives a zero row.  Two launches; no allocation.
+ * context_lens[s] == 0 gives a zero row.  One or two launches; no allocation.
  * Supported: D == 64, G from 1 to 8, bs in {16, 32, 64, 128}, any Hkv,
  * |q| < 2^100, cached V below 2^60 in magnitude, NB * bs < 2^31.
  */
@@ -372,8 +372,8 @@ tvl_status tvl_kv4_attention_decode(float* out, const void* q, const void* cache
 
 /*
  * Decode attention with a window over the bf16 caches: the same call on the
- * layout of tvl_paged_attention_decode.  P is carried in two bf16 halves (16
- * bits).  Slots of a read block that are not visible may hold anything, NaN
+ * layout of tvl_paged_attention_decode.  P is carried in three bf16 parts
+ * (24 bits).  Slots of a read block that are not visible may hold anything, NaN
  * included.
  */
 tvl_status tvl_paged_attention_window_decode(

@@ -9,12 +9,14 @@
 //
 // Bound: every visible K/V byte is read once, so HBM bandwidth -- provided
 // that the arithmetic keeps up.  At 4 bits an SM is handed a 16-token record
-// of one head (1152 bytes) every 26 cycles (6.8 TB/s, 152 SMs, 1.9 GHz), 104
-// issue slots of each of its four schedulers; one fp32 FMA per (value, query
+// of one head (1152 bytes) every 49 cycles (6.8 TB/s, 152 SMs, 1.9 GHz), 196
+// issue slots of its four schedulers together; one fp32 FMA per (value, query
 // head) would need 256 for four heads.  So both products run on mma.sync
 // m16n8k16 with the tokens (Q K^T) or the dimensions (P V) as the 16 rows and
-// the query heads of the GQA group as the 8 columns; the operands come straight
-// from shared memory into registers, with no dequantised copy.
+// the query heads of the GQA group as the 8 columns (a single token's few
+// heads leave a tcgen05 tile of 128 rows nearly empty); the operands come
+// straight from shared memory into registers, with no dequantised copy: 38
+// cycles a record and head with all warps busy.
 //
 // 4-bit codes as operands.  A code in the low bits of a 16-bit word is the
 // fp16 subnormal c * 2^-24, in bits 4..7 it is 16 c * 2^-24: one AND turns two
@@ -22,28 +24,42 @@
 // final scale.  The k order of a product is free, so lane t of a row takes
 // the row's dimensions 16 t .. 16 t + 15 as one 8-byte load.  Per row
 //   scale q . K_j = s_j (q . c_j) F + z_j sum(q),
-// and for V the weight p_j s_j multiplies c_j - 8 (one packed subtract) while
-// p_j (z_j + 8 s_j) is summed in fp32 beside it: centred codes keep the long
-// sum as small as the output, so fp32 accumulation loses nothing to
+// and for V the weight p_j s_j multiplies 2 c_j - 15 (one packed operation)
+// while p_j (z_j + 7.5 s_j) is summed in fp32 beside it: centred codes keep the
+// long sum as small as the output, so fp32 accumulation loses nothing to
 // cancellation.  q (bf16) is exact in fp16 after a power-of-two scale.
 //
-// P in two halves.  The weights p are fp32; hi + lo, two 16-bit numbers, keep
-// 22 (fp16) or 16 (bf16) bits of them, so the fp32 output carries no rounding
-// of P.  With four query heads or fewer the lo halves ride in columns 4..7 of
-// the same product at no cost; with five to eight they take a second one.
+// P in parts.  The weights p are fp32; two fp16 parts keep 22 bits of them,
+// three bf16 parts all 24, so the fp32 output carries no rounding of P.  With
+// four query heads or fewer the products' spare columns 4..7 take another
+// chunk (4-bit) or the lo parts (bf16) at no cost; with five to eight each part
+// takes a product of its own.  The tensor cores truncate what they add, so no
+// accumulator runs through them: each stage starts a fresh one, added in fp32.
 //
 // Work split.  The visible 16-token chunks of all sequences form one line, cut
 // into equal ranges, one CTA per SM and KV-head group, each sequence start
 // counted as `seg_weight` chunks more.  A range's piece of a sequence is a
 // segment; one that covers its whole sequence writes the output, any other a
 // partial (m, l, acc) record; the CTA that holds a split sequence's first
-// chunk lists it for merge_kernel.
+// chunk lists it for the merge kernel.  (Merged by the last CTA to finish, found
+// through counters, the launch was slower: 29.2 against 27.6 us, batch of 64.)
 //
-// CTA.  One producer warp fills a ring of shared-memory stages (bulk copies
-// of whole 16-token runs of the 4-bit cache, swizzled tensor copies of the
-// bf16 one), one mbarrier each; up to 16 consumer warps, `wph` per KV head,
-// take the chunks of a stage in turn.  The warps of a head combine at a segment's
-// end through shared memory.  All waits are bounded.
+// CTA.  Consumer warps, `wph` per KV head, each with its own ring of
+// shared-memory stages of up to four chunks, one mbarrier each, so no warp waits
+// for another's stage; stage k of a segment goes to the head's warp k mod wph.
+// min(wph, 4) producer warps fill the rings (bulk copies of whole 16-token runs
+// of the 4-bit cache, swizzled tensor copies of the bf16 one): a stage costs a
+// producer some 1300 cycles of look-ups, waits and issue, one after the other
+// (8 sequences of 32k-128k tokens, 4 bits: 91 us with one, 75 with two, 68 with
+// four).  The warps of a head combine at a segment's end through shared memory.
+// All waits are bounded.
+//
+// Measured, us per call: 4 bits, G = 4: 64 sequences of 0.5-4k tokens 26.2 (the
+// copies alone: 21.7), 8 of 32k-128k 67.6 (0.80 of HBM; copies
+// alone 61.3), 256 of G = 8 with a window of 2048 41.6 (copies alone 29.4).  bf16: 256
+// sequences, window 1024, 50.3, which is the copies alone; 8 long ones 86.5
+// (0.92 of HBM).  A call's fixed part is about 9 us: the schedule 1.4, the first
+// data 3 to 4.6, the merge 4.4.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -1069,8 +1085,8 @@ __device__ __forceinline__ void lane_sums(State& st, float (&o)[2][8]) {
   }
 }
 
-// Ends a warp's part of a segment.  A head's warp 0, which has the segment's first stage, combines: the others with stages of it
-// hand (m, l, o) over to it through shared memory, and it stores the output or
+// Ends a warp's part of a segment.  A head's warp 0, which has the segment's
+// first stage, combines: the others with stages of it hand (m, l, o) over to it through shared memory, and it stores the output or
 // the record.  handed: warp 0: bit i, the phase of warp i's next hand-over;
 // else the hand-overs so far.  False: a bounded wait ran out.
 template <int F, bool kLoCols>
@@ -1330,6 +1346,9 @@ __global__ void __launch_bounds__((max_warps<F, kLoCols>() + kMaxProducers) * 32
 // in one launch.  Warp w takes chunks w, w + 16, ... : it fetches their block
 // ids, issues their copies (all of them fit) and q's loads, waits once, and the
 // warps meet at the end.  Bound by latency: four dependent memory round trips.
+// One sequence with a window of 512 (bf16) takes 4.7 us, against 9.6 through the
+// schedule and the merge; one of 777 tokens (4 bits) 5.2 against 7.8.  A CTA must hold
+// the whole sequence at once, and past one CTA an SM the balanced split wins.
 constexpr int kDirectWarps = 16;
 constexpr int kDirectChunks4 = 128, kDirectChunks16 = 48;    // longest sequence (chunks)
 
