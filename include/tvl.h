@@ -307,7 +307,8 @@ tvl_status tvl_copy_blocks(void* k_cache, void* v_cache, const int32_t* src,
  * are given: as tvl_rope_paged_kv_write (q rotated in place, K rotated and
  * rounded to bf16), then every K and V row of a token with slot_mapping[t] >=
  * 0 is quantised into that slot.  positions == NULL: no rotation, and q must
- * be NULL.  Each output row depends on its input row alone.
+ * be NULL.  Each output row depends on its input row alone.  Slots must be
+ * distinct (a row written twice in one call is unspecified).
  *   q : bf16 [T, Hq, D] or NULL; k_new, v_new : bf16 [T, Hkv, D]
  *   cache : uint8, written in place; slot_mapping : int32 [T]
  *   positions : int32 [T] >= 0, or NULL
@@ -348,7 +349,9 @@ tvl_status tvl_kv4_copy_blocks(void* cache, const int32_t* src, const int32_t* d
  */
 
 /* Workspace of the two decode calls below, for the current device (its SM
- * count), whatever the batch; written to *bytes. */
+ * count), whatever the batch; written to *bytes.  Calls that may run at the
+ * same time (other streams, graphs replayed side by side) need one each; calls
+ * in order on a stream may share one. */
 tvl_status tvl_window_decode_workspace_size(int num_q_heads, int num_kv_heads, int head_dim,
                                             size_t* bytes);
 

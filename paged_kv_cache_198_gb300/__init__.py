@@ -24,6 +24,7 @@ device that was current at bind time must be current when the call is made.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -154,6 +155,14 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _stream_context(stream):
+    """torch's allocator on `stream` (None: the current one; a torch stream or a handle)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream")
+                             else torch.cuda.ExternalStream(int(stream)))
 
 
 def _ptr(t) -> ctypes.c_void_p:
@@ -563,8 +572,10 @@ def _prep_window_decode(out, q, caches, nb, bs, hkv, block_tables, context_lens,
         raise ValueError("block_tables / context_lens must have num_seqs rows")
     with _on_device(dev):
         if workspace is None:
-            workspace = torch.empty(window_decode_workspace_size(hq, hkv, d), dtype=torch.uint8,
-                                    device=dev)
+            # allocated on the call's stream: handed out again only behind it
+            with _stream_context(stream):
+                workspace = torch.empty(window_decode_workspace_size(hq, hkv, d),
+                                        dtype=torch.uint8, device=dev)
         _need(workspace, "workspace", torch.uint8, 1, dev)
         args = (_ptr(out), _ptr(q), *(_ptr(c) for c in caches), _ptr(block_tables),
                 _ptr(context_lens), s, hq, hkv, d, bs, nb, block_tables.shape[1], float(scale),

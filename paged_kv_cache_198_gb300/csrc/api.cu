@@ -493,6 +493,7 @@ bool kv4_block_size(int bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 1
 tvl_status kv4_sizes(int num_kv_heads, int head_dim, int block_size, int num_blocks) {
   if (num_kv_heads <= 0 || num_blocks <= 0)
     return fail(TVL_ERR_INVALID_ARG, "num_kv_heads and num_blocks must be positive");
+  if (num_kv_heads > 65535) return fail(TVL_ERR_UNSUPPORTED, "num_kv_heads %d > 65535", num_kv_heads);
   if (head_dim != 64) return fail(TVL_ERR_UNSUPPORTED, "head_dim %d (supported: 64)", head_dim);
   if (!kv4_block_size(block_size))
     return fail(TVL_ERR_UNSUPPORTED, "block_size %d (4-bit cache: 16, 32, 64, 128)", block_size);
@@ -507,6 +508,7 @@ tvl_status tvl_kv4_write(void* q, const void* k_new, const void* v_new, void* ca
                          int num_blocks, float rope_theta, void* stream) {
   if (num_tokens < 0) return fail(TVL_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
   if (num_q_heads < 0) return fail(TVL_ERR_INVALID_ARG, "num_q_heads %d < 0", num_q_heads);
+  if (num_q_heads > 524280) return fail(TVL_ERR_UNSUPPORTED, "num_q_heads %d > 524280", num_q_heads);
   tvl_status st = kv4_sizes(num_kv_heads, head_dim, block_size, num_blocks);
   if (st != TVL_OK) return st;
   if (positions && (!(rope_theta > 1.0f) || !std::isfinite(rope_theta)))
@@ -549,6 +551,8 @@ tvl_status tvl_kv4_expand_blocks(void* k_cache, void* v_cache, const void* cache
   tvl_status st = kv4_sizes(num_kv_heads, head_dim, block_size, num_blocks);
   if (st != TVL_OK) return st;
   if (out_blocks <= 0) return fail(TVL_ERR_INVALID_ARG, "out_blocks %d <= 0", out_blocks);
+  if (static_cast<long long>(n) * (block_size / 16) * num_kv_heads > INT_MAX)
+    return fail(TVL_ERR_UNSUPPORTED, "more than 2^31 - 1 records to expand");
   if (n == 0) return TVL_OK;
   if (!k_cache || !v_cache || !cache || !src || !dst)
     return fail(TVL_ERR_INVALID_ARG, "null pointer");

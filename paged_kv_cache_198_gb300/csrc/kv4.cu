@@ -312,7 +312,7 @@ cudaError_t launch_kv4_write(const Kv4WriteArgs& a, cudaStream_t stream) {
   p.num_slots = a.num_slots;
   p.status = a.status;
   static const RopeTurns none = {};
-  return launch_pdl(kv4_write_kernel, dim3((a.num_tokens + kWarps - 1) / kWarps, p.parts_q + parts_kv),
+  return launch_pdl(kv4_write_kernel, dim3((a.num_tokens - 1) / kWarps + 1, p.parts_q + parts_kv),
                     dim3(kWarps * 32), 0, stream, p,
                     a.positions ? rope_turns(a.rope_theta) : none);
 }

@@ -117,3 +117,36 @@ def test_drawn_shapes(seed):
     ctx = [int(x) for x in np.exp(rng.uniform(0, np.log(1500), n))]
     _run(1000 + seed, ctx, hkv * g, hkv, int(rng.choice([16, 32, 64, 128])), int(rng.integers(1, 800)),
          int(rng.integers(0, 70)), poison=bool(seed & 1))
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_a_workspace_of_its_own_on_another_stream(as_handle):
+    """Without a workspace the call allocates one; on a stream other than the
+    current one its memory must not be handed to the current stream while the
+    call's kernels may still run."""
+    rng = np.random.default_rng(77)
+    ctx = rng.integers(200, 900, 40).astype(np.int32)
+    bs, hkv, hq = 16, 8, 32
+    need = -(-ctx // bs)
+    nb = int(need.sum())
+    tables = np.full((len(ctx), int(need.max())), -1, np.int32)
+    ids, at = rng.permutation(nb).astype(np.int32), 0
+    for i, n in enumerate(need):
+        tables[i, :n] = ids[at:at + n]
+        at += n
+    k, v = (torch.randn(nb, bs, hkv, 64, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    q = torch.randn(len(ctx), hq, 64, device=DEV, dtype=torch.bfloat16)
+    args = (q, k, v, _cuda(tables), _cuda(ctx), 0.125, 0)
+    want = torch.empty(len(ctx), hq, 64, device=DEV)
+    tvl.paged_attention_window_decode(want, *args)
+    size = tvl.window_decode_workspace_size(hq, hkv)
+    side = torch.cuda.Stream(DEV)
+    outs = [torch.empty_like(want) for _ in range(30)]
+    torch.cuda.synchronize()
+    for o in outs:
+        tvl.paged_attention_window_decode(o, *args, stream=side.cuda_stream if as_handle else side)
+        torch.full((size,), 255, dtype=torch.uint8, device=DEV)      # the current stream's memory
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, want)
+    assert_clean_status()

@@ -150,3 +150,11 @@ def test_window_prefill_refusals(tvl, bad, want):
         a["out"], a["q"], a["qsl"], a["kc"], a["vc"], a["tab"], a["ctx"], a["s"], a["tq"], a["maxq"], a["hq"],
         a["hkv"], a["d"], a["bs"], a["nb"], a["mb"], a["scale"], a["window"], a["sinks"], None)
     assert rc == getattr(tvl, "ERR_" + want)
+
+
+def test_sizes_past_the_launch_grid_are_refused(tvl):
+    assert _write(tvl, hkv=65536) == tvl.ERR_UNSUPPORTED
+    assert _write(tvl, q=D16, pos=D16, hq=524281) == tvl.ERR_UNSUPPORTED
+    lib = tvl._load()
+    assert lib.tvl_kv4_expand_blocks(D16, D16, D16, D16, D16, 1 << 28, 8, 64, 128, 8, 8,
+                                     None) == tvl.ERR_UNSUPPORTED
