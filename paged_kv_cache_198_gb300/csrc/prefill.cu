@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&B->kv_full[i], 1);
       mbar_init(&B->kv_empty[i], 1);
-      mbar_init(&B->v_ready[i], kWin ? C::kSoftmaxWarps : 1);
+      mbar_init(&B->v_ready[i], 1);
     }
     for (int i = 0; i < NH; ++i) {
       mbar_init(&B->s_full[i], 1);
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
       if (!mbar_wait(&B->mma_done, 0)) report(p.status, kDevTimeout);
     }
     __syncwarp();
-  } else if (!kWin) {
+  } else {
     // ------------------------------------------------------- V conversion
     // V tile bf16 -> fp16 in place, 16 bytes at a time (the swizzle only
     // permutes 16-byte chunks within a 128-byte row, so a chunk's row is its
@@ -652,17 +652,6 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         ok = wait_or_abort(&B->s_full[hh], gt & 1, p);
         if (__any_sync(kFull, !ok)) { ok = false; break; }
         tc_fence_after();
-        // kWin: the softmax warps also convert V, a few pieces each between two
-        // waits
-        constexpr int kPieces = static_cast<int>(kTileBytes / 16) / (C::kSoftmaxWarps * 32);
-        const int st = gt % kStages;
-        uint8_t* vt = smem + C::kVOff + st * kTileBytes;
-        uint4 w[kPieces];
-        if constexpr (kWin) {
-          ok = wait_or_abort(&B->kv_full[st], (gt / kStages) & 1, p);
-          if (__any_sync(kFull, !ok)) { ok = false; break; }
-          load_pieces<kPieces, C::kSoftmaxWarps * 32>(vt, threadIdx.x, w);
-        }
         uint32_t sr[4][32];                             // this row's 128 scores
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) tmem_ld32(s_addr + cc * 32, sr[cc]);
@@ -671,13 +660,6 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&B->s_free[hh]);
-        if constexpr (kWin) {
-          convert_pieces<kPieces, C::kSoftmaxWarps * 32, kWin>(p, x, j, vt, threadIdx.x, w);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&B->v_ready[st]);
-        }
-
         // Tiles on the causal diagonal or past the context need the mask.
         bool masked = (key0 + kBN - 1 > pos_first) || (key0 + kBN > ctx);
         if constexpr (kWin)
