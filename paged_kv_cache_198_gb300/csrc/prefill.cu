@@ -42,7 +42,7 @@
 //             2^-14 <= |v| <= 65504; smaller values keep an absolute error
 //             below 2^-25; a larger one becomes infinite, which leaves rows
 //             that are not finite, reported as TVL_DEV_NONFINITE; keys past
-//             the context become 0); kWin: the softmax warps convert instead;
+//             the context become 0);
 //   4NH+3     P.V issuer (below).
 // P and V go through fp16 rather than bf16 so that rounding P costs at most
 // 2^-11 relative (bf16 would cost 2^-8) -- the fp32-accumulated result stays
@@ -58,24 +58,28 @@
 // four sinks is nine or ten tiles of 128 keys, where whole tiles would be ten
 // or eleven.  The output is bf16 (P's fp16 rounding, 2^-11, is below the
 // output's, 2^-8), staged as one swizzled 128-byte row.
-// What bounds it: the softmax warps' tile, not the tensor pipe (32% active, 2
-// sequences x 4096 new rows, window 2048: 208 us, 667 TFLOP/s).  Per tile of
-// two heads, ~3200 cycles: ~1700 of both heads' exponentials (1024 at the exp
-// unit's rate), the rest waits of 200-250 cycles each for S, V and the last
-// P.V.  Three things this form does differently, with what they gave there:
+//
+// What bounds it: the softmax warps' tile, not the tensor pipe (a third active).
+// Windowed, 2 sequences x 4096 new rows, window 2048: 200 us, 693 TFLOP/s; 16
+// chunks of 512 rows, window 1024: 113.5 us, 524 TFLOP/s (units of ten tiles,
+// three of them masked, and a unit's start and end).  Per tile of two heads,
+// ~3000 cycles: ~1700 of both heads' exponentials (1024 at the exp unit's
+// rate), the rest waits and hand-overs of 200-250 cycles each.  What brought
+// it there, in us of the first case:
 //   - masked scores become infinite in place, so one copy of the exponential
 //     loop serves every tile (the loop streams through the instruction cache):
-//     230 -> 216 us;
-//   - V is converted by the softmax warps, four pieces a thread, between the
-//     wait for S and the exponentials: one converting warp took 2800 cycles a
-//     tile, beside two busy softmax warps on its scheduler, and set the pace;
-//     four of its own left the softmax 208 registers and spills (212 us);
+//     230 -> 216;
 //   - the issuing warps stay whole and elect one thread: 660 + 740 cycles a
-//     tile for 24 MMAs, where a divergent thread took 2030 + 1040.  With the
-//     conversion: 216 -> 208 us.
-// Measured and left: two warps a row (16 softmax warps, 64 keys each): 230 us;
-// the scores 32 at a time in rolled loops: 242; a fourth stage: no gain; the
-// heads started half a tile apart: 213.
+//     tile for its 24 MMAs, where a divergent thread took 2030 + 1040; and V is
+//     converted in batches of loads: 2170 cycles a tile, where 2800 set the
+//     kernel's pace: 216 -> 200.  (The plain form, 16 chunks of 512 rows on
+//     0-2k prefixes: 142 -> 130.)
+// Measured and left: V converted by the softmax warps, 208 us (plain: 136
+// against 130), or by four warps of its own, 212 (the softmax keeps 208
+// registers and spills); two warps a row (16 softmax warps, 64 keys each), 230;
+// the scores 32 at a time in rolled loops, 242; a fourth stage, 203; the heads
+// started half a tile apart, no gain; the masks set in place in the plain form
+// too, 132-134 against 130.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -229,7 +233,7 @@ __device__ __forceinline__ void window_blocks(const Params& p, int pos_first, in
   delta = (w0 - sb) * p.bs;
 }
 
-// N 16-byte pieces of a V tile, `step` apart from piece e on: bf16 to fp16 in
+// N 16-byte pieces of a V tile, kStep apart from piece e on: bf16 to fp16 in
 // place.  Keys that no row of the unit sees become 0.
 template <int N, int kStep>
 __device__ __forceinline__ void load_pieces(const uint8_t* vt, int e, uint4 (&w)[N]) {
