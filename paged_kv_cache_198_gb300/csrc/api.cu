@@ -614,7 +614,8 @@ tvl_status window_heads(int hq, int hkv, int d) {
     return fail(TVL_ERR_INVALID_ARG, "num_q_heads %d not a multiple of num_kv_heads %d", hq, hkv);
   if (d != 64) return fail(TVL_ERR_UNSUPPORTED, "head_dim %d (supported: 64)", d);
   if (hq / hkv > 8) return fail(TVL_ERR_UNSUPPORTED, "GQA group %d (supported: 1 to 8)", hq / hkv);
-  if (hkv > 65535) return fail(TVL_ERR_UNSUPPORTED, "num_kv_heads %d > 65535", hkv);
+  if (hkv > 65535 || hq > 4 * 65535)
+    return fail(TVL_ERR_UNSUPPORTED, "num_kv_heads %d > 65535 or num_q_heads %d > 262140", hkv, hq);
   return TVL_OK;
 }
 

@@ -1086,9 +1086,10 @@ __device__ __forceinline__ void lane_sums(State& st, float (&o)[2][8]) {
 }
 
 // Ends a warp's part of a segment.  A head's warp 0, which has the segment's
-// first stage, combines: the others with stages of it hand (m, l, o) over to it through shared memory, and it stores the output or
-// the record.  handed: warp 0: bit i, the phase of warp i's next hand-over;
-// else the hand-overs so far.  False: a bounded wait ran out.
+// first stage, combines: the others with stages of it hand (m, l, o) over to it
+// through shared memory, and it stores the output or the record.  handed: warp
+// 0: bit i, the phase of warp i's next hand-over; else the hand-overs so far.
+// False: a bounded wait ran out.
 template <int F, bool kLoCols>
 __device__ bool finish(State& st, const Params& p, uint8_t* smem, const Layout& L, int h, int w,
                        int& handed, int flags, int seq, int record) {
@@ -1350,7 +1351,8 @@ __global__ void __launch_bounds__((max_warps<F, kLoCols>() + kMaxProducers) * 32
 // schedule and the merge; one of 777 tokens (4 bits) 5.2 against 7.8.  A CTA must hold
 // the whole sequence at once, and past one CTA an SM the balanced split wins.
 constexpr int kDirectWarps = 16;
-constexpr int kDirectChunks4 = 128, kDirectChunks16 = 48;    // longest sequence (chunks)
+constexpr int kDirectChunks4 = 128, kDirectChunks16 = 48;    // longest sequence (chunks),
+constexpr uint32_t kDirectSmem = kSmemLimit - 1024;          // if it fits (bf16, G = 8: 32)
 
 template <int F, bool kLoCols>
 __global__ void __launch_bounds__(kDirectWarps * 32, 1)
@@ -1593,18 +1595,23 @@ bool cache_map(CUtensorMap* m, const void* base, int hkv, long long tokens, int 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Shared memory of a CTA of window_direct_kernel: its chunks and the hand-overs.
+long long direct_smem(bool four, long long chunks, int group) {
+  const long long per_warp = (chunks + kDirectWarps - 1) / kDirectWarps;
+  return 1024 + kDirectWarps * (per_warp * (four ? kRecBytes : 2 * kBf16Tile) + group * kCombPitch * 4);
+}
+
 template <int F, bool kLoCols>
 cudaError_t launch_direct(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int chunks,
                           cudaStream_t stream) {
   auto kern = window_direct_kernel<F, kLoCols>;
   static PerDeviceOnce once;
   cudaError_t e = once.run([&] {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit - 1024);
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDirectSmem);
   });
   if (e != cudaSuccess) return e;
   const int per_warp = (chunks + kDirectWarps - 1) / kDirectWarps;
-  const uint32_t smem = 1024 + kDirectWarps * (per_warp * (F == k4Bit ? kRecBytes : 2 * kBf16Tile) +
-                                               p.group * kCombPitch * 4);
+  const uint32_t smem = static_cast<uint32_t>(direct_smem(F == k4Bit, chunks, p.group));
   return launch_pdl(kern, dim3(p.num_seqs, 1, p.hkv), dim3(kDirectWarps * 32), smem, stream, tk, tv,
                     p, per_warp);
 }
@@ -1688,7 +1695,8 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
   const long long seen = p.window > 0 ? p.window / kChunk + 2LL + (p.sinks + kChunk - 1LL) / kChunk : capacity;
   const long long chunks = seen < capacity ? seen : capacity;
   if (static_cast<long long>(a.num_seqs) * p.hkv <= a.sms &&
-      chunks <= (four ? kDirectChunks4 : kDirectChunks16)) {
+      chunks <= (four ? kDirectChunks4 : kDirectChunks16) &&
+      direct_smem(four, chunks, p.group) <= kDirectSmem) {
     if (!maps(1)) return cudaErrorInvalidValue;
     const int n = static_cast<int>(chunks);
     if (!four)
@@ -1743,7 +1751,7 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
   // a sequence has about 1 + ctas / num_seqs records: one warp a head and
   // batch of 8, up to 16
   int parts = 1;
-  while (parts < kMergeWarps && parts * kMergeBatch * a.num_seqs < p.ctas) parts *= 2;
+  while (parts < kMergeWarps && static_cast<long long>(parts) * kMergeBatch * a.num_seqs < p.ctas) parts *= 2;
   const int heads = parts < 4 ? 4 : kMergeWarps / parts;
   return launch_pdl(window_merge_kernel,
                     dim3(a.num_seqs < p.ctas ? a.num_seqs : p.ctas,

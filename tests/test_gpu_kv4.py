@@ -388,3 +388,12 @@ def test_serving_run_on_a_4bit_cache():
         assert (np.abs(C.f64(out) - want) <= tol).all(), step
     assert alloc.stats()["shared_blocks"] == 2
     assert_clean_status()
+
+
+@pytest.mark.parametrize("group", range(1, 9))
+@pytest.mark.parametrize("ctx,window,sinks", [(2048, 0, 0), (2047, 0, 0), (4000, 1900, 90), (4000, 2016, 0)])
+def test_decode_the_longest_sequences_of_few(group, ctx, window, sinks):
+    """Few short bounded sequences: around the most chunks that one CTA holds."""
+    got, want, tol = _decode(90 + group, [ctx, 40], group, 1, 16, window, sinks)
+    assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / np.maximum(tol, 1e-30)).max()
+    assert_clean_status()

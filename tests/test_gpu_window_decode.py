@@ -19,12 +19,12 @@ def _bf(rng, shape, spread=1.0):
     return C.bf16_to_f64(C.f64_to_bf16_bits(rng.standard_normal(shape) * spread))
 
 
-def _run(seed, ctx, hq, hkv, bs, window, sinks, spread=1.0, poison=False):
+def _run(seed, ctx, hq, hkv, bs, window, sinks, spread=1.0, poison=False, scale=0.125):
     rng = np.random.default_rng(seed)
     tables, nb = C.deal(rng, ctx, bs)
     k, v = _bf(rng, (nb, bs, hkv, 64), spread), _bf(rng, (nb, bs, hkv, 64), spread)
     q = _bf(rng, (len(ctx), hq, 64), 1.5)
-    want, tol = C.decode_ref(q, tables, ctx, 0.125, window, sinks, kv=(k, v))
+    want, tol = C.decode_ref(q, tables, ctx, scale, window, sinks, kv=(k, v))
     if poison:                      # every slot that is not visible, and the unread table entries
         seen = np.zeros((nb, bs), bool)
         for s, n in enumerate(ctx):
@@ -37,7 +37,7 @@ def _run(seed, ctx, hq, hkv, bs, window, sinks, spread=1.0, poison=False):
         k[~seen], v[~seen] = np.nan, np.inf
     out = torch.full(q.shape, float("nan"), device=DEV)
     tvl.paged_attention_window_decode(out, C.bf16(q, DEV), C.bf16(k, DEV), C.bf16(v, DEV), _cuda(tables),
-                                      _cuda(np.asarray(ctx, np.int32)), 0.125, window, sinks=sinks)
+                                      _cuda(np.asarray(ctx, np.int32)), scale, window, sinks=sinks)
     got = C.f64(out)
     assert np.isfinite(got).all()
     assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / np.maximum(tol, 1e-30)).max()
@@ -150,3 +150,16 @@ def test_a_workspace_of_its_own_on_another_stream(as_handle):
     for o in outs:
         assert torch.equal(o, want)
     assert_clean_status()
+
+
+@pytest.mark.parametrize("scale", [-0.125, 0.0, 3.0])
+@pytest.mark.parametrize("hq", [8, 16])
+def test_scales(scale, hq):
+    _run(80, [300, 700] * 60, hq, 2, 16, 200, 4, scale=scale)
+
+
+@pytest.mark.parametrize("group", range(1, 9))
+@pytest.mark.parametrize("ctx,window,sinks", [(2100, 700, 4), (2100, 736, 0), (768, 0, 0), (2100, 512, 200)])
+def test_the_longest_sequences_of_few(group, ctx, window, sinks):
+    """Few short bounded sequences: around the most chunks that one CTA holds."""
+    _run(90 + group, [ctx, 40], group, 1, 16, window, sinks)

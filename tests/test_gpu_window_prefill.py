@@ -41,7 +41,7 @@ def _ref(q, k, v, tables, ctx, new, scale, window, sinks):
         cnt = ok.sum(1)[:, None]
         for h in range(q.shape[1]):
             x = q[at:at + m, h] @ kk[:, h // g].T * scale
-            b = np.where(ok, np.abs(q[at:at + m, h]) @ np.abs(kk[:, h // g]).T * scale, 0).max(1)[:, None]
+            b = np.where(ok, np.abs(q[at:at + m, h]) @ np.abs(kk[:, h // g]).T * abs(scale), 0).max(1)[:, None]
             x = np.where(ok, x, -np.inf)
             w = np.exp(x - x.max(1, keepdims=True))
             w /= w.sum(1, keepdims=True)
@@ -65,9 +65,9 @@ def _setup(seed, ctx, new, hq, hkv, bs, spread=1.0):
     return rng, tables, nb, k, v, q, starts
 
 
-def _run(seed, ctx, new, hq, hkv, bs, window, sinks, spread=1.0, poison=False, extra_rows=0):
+def _run(seed, ctx, new, hq, hkv, bs, window, sinks, spread=1.0, poison=False, extra_rows=0, scale=0.125):
     rng, tables, nb, k, v, q, starts = _setup(seed, ctx, new, hq, hkv, bs, spread)
-    want, tol = _ref(q, k, v, tables, ctx, new, 0.125, window, sinks)
+    want, tol = _ref(q, k, v, tables, ctx, new, scale, window, sinks)
     if poison:
         seen = np.zeros((nb, bs), bool)
         for s, (n, m) in enumerate(zip(ctx, new)):
@@ -85,7 +85,7 @@ def _run(seed, ctx, new, hq, hkv, bs, window, sinks, spread=1.0, poison=False, e
     out = torch.full((q.shape[0] + extra_rows, hq, 64), 9.0, dtype=torch.bfloat16, device=DEV)
     qq = np.concatenate([q, np.zeros((extra_rows, hq, 64))]) if extra_rows else q
     tvl.paged_attention_window_prefill(out, C.bf16(qq, DEV), _cuda(starts), C.bf16(k, DEV), C.bf16(v, DEV),
-                                       _cuda(tables), _cuda(np.asarray(ctx, np.int32)), 0.125, max(new + [1]),
+                                       _cuda(tables), _cuda(np.asarray(ctx, np.int32)), scale, max(new + [1]),
                                        window, sinks=sinks)
     got = C.f64(out)
     t = q.shape[0]
@@ -227,3 +227,11 @@ def test_drawn_shapes(seed):
     ctx = [m + int(rng.integers(0, 500)) for m in new]
     _run(800 + seed, ctx, new, hkv * g, hkv, int(rng.choice([16, 32, 64, 128])), int(rng.integers(1, 500)),
          int(rng.integers(0, 200)), poison=bool(seed & 1))
+
+
+@pytest.mark.parametrize("scale", [-0.125, 0.0, 1e-42, -1e-42, 1.0])
+@pytest.mark.parametrize("hkv", [2, 8])
+def test_scales(scale, hkv):
+    """Masked scores are infinities against the scale's sign; a scale of nothing
+    must not turn them into NaN."""
+    _run(70, [300, 140], [200, 140], 8, hkv, 16, 100, 4, scale=scale)

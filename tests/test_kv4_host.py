@@ -158,3 +158,4 @@ def test_sizes_past_the_launch_grid_are_refused(tvl):
     lib = tvl._load()
     assert lib.tvl_kv4_expand_blocks(D16, D16, D16, D16, D16, 1 << 28, 8, 64, 128, 8, 8,
                                      None) == tvl.ERR_UNSUPPORTED
+    assert _decode(tvl, True, hq=262144, hkv=32768) == tvl.ERR_UNSUPPORTED
