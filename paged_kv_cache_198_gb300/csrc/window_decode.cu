@@ -344,11 +344,10 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
 
   const int cps = 1 << p.cps_log2, wph = p.wph, ring = p.ring;
   // Stage k of a segment goes to the head's warps k % wph, each with a ring of
-  // its own.  Lane w < wph: warps w's next stage, its fill's parity, and whether
-  // every stage of the ring has been filled.
-  int pos = 0;
-  uint32_t ph = 0;
-  bool used = false, ok = true;
+  // its own.  Lane w < wph: warps w's next stage, in bit 8 its fill's parity and
+  // in bit 9 whether every stage of the ring has been filled.
+  int state = 0;
+  bool ok = true;
 
   // lens: the lengths, of a small batch; else lane i's win_ctx: sequence win + i's
   const int* lens = reinterpret_cast<const int*>(smem + L.sched + 64 + 32 * 8);
@@ -405,78 +404,79 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
     const bool have_next = find(g.s, g.e, false, nx);
     const int n_stages = (g.e - g.v + cps - 1) >> p.cps_log2;
     const int parts = min(wph, n_stages);
-    int k = 0, w = 0, mine = 0;  // the segment's stage, its warps, and their place mod producers
-    for (int vb = g.v; vb < g.e && ok; vb += 32) {
-      // the next 32 entries (of this segment or the next) are fetched while
-      // this batch's copies are issued
-      const int ntbl = vb + 32 < g.e ? entry(g, vb + 32) : (have_next ? entry(nx, nx.v) : 0);
-      const int ve = min(g.e, vb + 32);
-      for (int v = vb; v < ve; v += cps, ++k) {
-        const int at = w;
-        const bool own = mine == pj;
-        if (++mine == p.producers) mine = 0;
-        if (++w == wph) w = mine = 0;
-        if (!own) continue;
-        const int n = min(cps, ve - v);                   // lane i < n: chunk v + i
-        const int slot = at * ring + __shfl_sync(kFull, pos, at);
-        const uint32_t sp = __shfl_sync(kFull, ph, at);
-        const bool again = __shfl_sync(kFull, used ? 1 : 0, at) != 0;
-        bool good = true;
-        if (lane == 0 && again) good = mbar_wait(&empty[slot], sp ^ 1);
-        ok = __shfl_sync(kFull, good ? 1 : 0, 0) != 0;
-        if (!ok) break;
-        uint8_t* base = smem + static_cast<size_t>(slot) * p.stage_bytes;
-        const int vv = v + lane;
-        const int c = vv < g.ns ? vv : vv + g.delta;
-        const bool whole = c * kChunk + kChunk <= g.ctx &&
-                           (c * kChunk >= g.ctx - g.window || c * kChunk + kChunk <= p.sinks);
-        const bool all = __all_sync(kFull, lane >= n || whole);
-        int page = __shfl_sync(kFull, tbl, (v - vb + lane) & 31);
-        const bool first = k < wph;
-        if (lane == 0) {
-          StageMeta m;
-          m.seq = g.s;
-          m.record = g.record;
-          m.flags = parts << kPartsShift | (first ? kSegFirst : 0) |
-                    (k + wph >= n_stages ? kSegLast : 0) | (all && n == cps ? 0 : kPartial);
-          m.n = n;
-          m.v0 = v;
-          m.ns = g.ns;
-          m.delta = g.delta;
-          m.ctx = g.ctx;
-          meta[slot] = m;
-          mbar_arrive_expect_tx(&full[slot], n * chunk_bytes + (first ? q_bytes : 0));
-        }
-        __syncwarp();
-        if (lane < n) {
-          if (page < 0 || page >= p.num_blocks) {
-            report(p.status, TVL_DEV_BAD_BLOCK_ID);
-            page = 0;
-          }
-          const int sub = c & ((1 << p.cpb_log2) - 1);
-          const long long chunk = (static_cast<long long>(page) << p.cpb_log2) + sub;
-          if (F == k4Bit) {
-            bulk_load(base + lane * chunk_bytes, p.kv4 + (chunk * p.hkv + h0) * kRecBytes,
-                      chunk_bytes, &full[slot], stream_policy);
-          } else {
-            const int tok = static_cast<int>(chunk * kChunk);
-            const uint32_t half = hpc * kBf16Tile;
-            tma_load_3d(base + lane * half, tm_k, 0, tok, h0, &full[slot]);
-            tma_load_3d(base + p.kv_bytes / 2 + lane * half, tm_v, 0, tok, h0, &full[slot]);
-          }
-        }
-        if (first && lane == 31)
-          bulk_load(base + p.kv_bytes,
-                    p.q + (static_cast<size_t>(g.s) * p.hq + static_cast<size_t>(h0) * p.group) * kD,
-                    q_bytes, &full[slot], keep_policy);
-        if (lane == at && ++pos == ring) {
-          pos = 0;
-          ph ^= 1;
-          used = true;
+    // the producer's own stages: k (of warp w) with w = k % wph, w % producers == pj
+    int k = pj, w = pj, vb = g.v;
+    int ntbl = vb + 32 < g.e ? entry(g, vb + 32) : (have_next ? entry(nx, nx.v) : 0);
+    for (;;) {
+      const int v = g.v + (k << p.cps_log2);
+      if (v >= g.e) break;
+      while (v >= vb + 32) {          // the next 32 entries (of this segment or the next)
+        vb += 32;                     // are fetched while this batch's copies are issued
+        tbl = ntbl;
+        ntbl = vb + 32 < g.e ? entry(g, vb + 32) : (have_next ? entry(nx, nx.v) : 0);
+      }
+      const int n = min(cps, g.e - v);                  // lane i < n: chunk v + i
+      const int rs = __shfl_sync(kFull, state, w);
+      const int at = rs & 0xff, slot = w * ring + at;
+      const uint32_t sp = rs >> 8 & 1;
+      uint8_t* base = smem + static_cast<size_t>(slot) * p.stage_bytes;
+      const int vv = v + lane;
+      const int c = vv < g.ns ? vv : vv + g.delta;
+      const bool whole = c * kChunk + kChunk <= g.ctx &&
+                         (c * kChunk >= g.ctx - g.window || c * kChunk + kChunk <= p.sinks);
+      const bool all = __all_sync(kFull, lane >= n || whole);
+      int page = __shfl_sync(kFull, tbl, (v - vb + lane) & 31);
+      if (lane < n && (page < 0 || page >= p.num_blocks)) {
+        report(p.status, TVL_DEV_BAD_BLOCK_ID);
+        page = 0;
+      }
+      const long long chunk = (static_cast<long long>(page) << p.cpb_log2) + (c & ((1 << p.cpb_log2) - 1));
+      const bool first = k < wph;
+      if (rs >> 9 && !__all_sync(kFull, mbar_wait(&empty[slot], sp ^ 1))) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        StageMeta m;
+        m.seq = g.s;
+        m.record = g.record;
+        m.flags = parts << kPartsShift | (first ? kSegFirst : 0) |
+                  (k + wph >= n_stages ? kSegLast : 0) | (all && n == cps ? 0 : kPartial);
+        m.n = n;
+        m.v0 = v;
+        m.ns = g.ns;
+        m.delta = g.delta;
+        m.ctx = g.ctx;
+        meta[slot] = m;
+        mbar_arrive_expect_tx(&full[slot], n * chunk_bytes + (first ? q_bytes : 0));
+      }
+      __syncwarp();
+      if (lane < n) {
+        if (F == k4Bit) {
+          bulk_load(base + lane * chunk_bytes, p.kv4 + (chunk * p.hkv + h0) * kRecBytes, chunk_bytes,
+                    &full[slot], stream_policy);
+        } else {
+          const int tok = static_cast<int>(chunk * kChunk);
+          const uint32_t half = hpc * kBf16Tile;
+          tma_load_3d(base + lane * half, tm_k, 0, tok, h0, &full[slot]);
+          tma_load_3d(base + p.kv_bytes / 2 + lane * half, tm_v, 0, tok, h0, &full[slot]);
         }
       }
-      tbl = ntbl;
+      if (first && lane == 31)
+        bulk_load(base + p.kv_bytes,
+                  p.q + (static_cast<size_t>(g.s) * p.hq + static_cast<size_t>(h0) * p.group) * kD,
+                  q_bytes, &full[slot], keep_policy);
+      if (lane == w) state = at + 1 == ring ? (rs ^ 0x100) - at | 0x200 : rs + 1;
+      if (w + p.producers < wph) {
+        w += p.producers;
+        k += p.producers;
+      } else {
+        k += wph - w + pj;
+        w = pj;
+      }
     }
+    // the next segment's first entries: already at hand in the last batch
+    if (have_next) tbl = vb + 32 < g.e ? entry(nx, nx.v) : ntbl;
     g = nx;
     have = have_next;
   }
@@ -484,6 +484,9 @@ __device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, con
     if (!by_seq) p.ws_split[cta] = split;
     if (cta == 0) *p.ws_total = sc.total;
   }
+  int pos = state & 0xff;
+  uint32_t ph = state >> 8 & 1;
+  bool used = state >> 9 != 0;
   if (lane < wph && lane % p.producers == pj) {   // each ring's last stage; then its copies land
     if (ok && used) ok = mbar_wait(&empty[lane * ring + pos], ph ^ 1);
     if (ok) {
