@@ -1644,8 +1644,10 @@ void shape(Params& p) {
   p.hpc = heads_per_cta(p.hkv, max_heads<F, kLoCols>());
   p.wph = max_warps<F, kLoCols>() / p.hpc;
   p.producers = p.wph < kMaxProducers ? p.wph : kMaxProducers;
-  // bf16 takes a stage's chunks one by one: as many as make 32 KB of it
-  const int nc = F == k4Bit ? chunks_per_stage<F, kLoCols>() : p.hpc > 4 ? 1 : p.hpc > 2 ? 2 : 4;
+  // bf16 takes a stage's chunks one by one: as many as make 64 KB of it, fewer
+  // where a ring would hold but one such stage (8 sequences, window 16384: 84.9
+  // us, 87.3 with 32 KB)
+  const int nc = F == k4Bit ? chunks_per_stage<F, kLoCols>() : p.hpc > 4 ? 2 : 4;
   p.cps_log2 = nc == 4 ? 2 : nc == 2 ? 1 : 0;
 }
 
