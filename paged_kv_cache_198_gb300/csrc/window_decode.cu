@@ -50,16 +50,18 @@
 // min(wph, 4) producer warps fill the rings (bulk copies of whole 16-token runs
 // of the 4-bit cache, swizzled tensor copies of the bf16 one): a stage costs a
 // producer some 1300 cycles of look-ups, waits and issue, one after the other
-// (8 sequences of 32k-128k tokens, 4 bits: 91 us with one, 75 with two, 68 with
-// four).  The warps of a head combine at a segment's end through shared memory.
-// All waits are bounded.
+// (8 sequences of 32k-128k tokens, 4 bits: 103 us with one, 80 with two, 67 with
+// three, one a ring).  More would have to share rings, whose parities cannot
+// tell fills two laps apart.  The warps of a head combine at a segment's end
+// through shared memory.  All waits are bounded.
 //
-// Measured, us per call: 4 bits, G = 4: 64 sequences of 0.5-4k tokens 26.2 (the
-// copies alone: 21.7), 8 of 32k-128k 67.6 (0.80 of HBM; copies
-// alone 61.3), 256 of G = 8 with a window of 2048 41.6 (copies alone 29.4).  bf16: 256
-// sequences, window 1024, 50.3, which is the copies alone; 8 long ones 86.5
-// (0.92 of HBM).  A call's fixed part is about 9 us: the schedule 1.4, the first
-// data 3 to 4.6, the merge 4.4.
+// Measured, us per call: 4 bits, G = 4: 64 sequences of 0.5-4k tokens 26.5 (the
+// copies alone: 21.7), 8 of 32k-128k 67.3 (0.80 of HBM; copies alone 61.3); G =
+// 8: 256 with a window of 2048 41.3 (copies alone 29.4; 16 consumer warps of 96
+// registers, a chunk at a time, 45.9; four chunks a stage, 44.2).  bf16: 256
+// sequences, window 1024, 50.3, which is the copies alone; 8 long ones 84 (0.95
+// of HBM).  A call's fixed part is about 9 us: the schedule 1.4, the first data
+// 3 to 4.6, the merge 4.4.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
