@@ -233,45 +233,12 @@ __device__ __forceinline__ void window_blocks(const Params& p, int pos_first, in
   delta = (w0 - sb) * p.bs;
 }
 
-// N 16-byte pieces of a V tile, kStep apart from piece e on: bf16 to fp16 in
-// place.  Keys that no row of the unit sees become 0.
-template <int N, int kStep>
-__device__ __forceinline__ void load_pieces(const uint8_t* vt, int e, uint4 (&w)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint4*>(vt + (e + kStep * i) * 16);
-}
-template <int N, int kStep, bool kWin>
-__device__ __forceinline__ void convert_pieces(const Params& p, const Unit& x, int j, uint8_t* vt, int e,
-                                               uint4 (&w)[N]) {
-  // of the tile's keys i < end, those with i < sink or i >= low
-  const int end = x.ctx - (kWin ? x.delta : 0) - j * kBN;
-  const int low = kWin && p.window > 0 ? x.pos_first - p.window - x.delta + 1 - j * kBN : 0;
-  const int sink = kWin ? p.sinks - j * kBN : 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    w[i].x = bf16x2_to_half2(w[i].x);
-    w[i].y = bf16x2_to_half2(w[i].y);
-    w[i].z = bf16x2_to_half2(w[i].z);
-    w[i].w = bf16x2_to_half2(w[i].w);
-  }
-  if (end < kBN || (low > 0 && sink < kBN)) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int u = (e + kStep * i) >> 3;
-      if (!(u < end && (u < sink || u >= low))) w[i] = make_uint4(0, 0, 0, 0);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) *reinterpret_cast<uint4*>(vt + (e + kStep * i) * 16) = w[i];
-}
-
 // Index of the k-th unit of CTA c among G: the units in longest-first order
 // are dealt to the CTAs row by row, every other row reversed (c, 2G-1-c,
 // 2G+c, ...), which evens out the CTAs' totals.  Increases with k.
 __device__ __forceinline__ long long unit_index(int k, int c, int G) {
   return static_cast<long long>(k) * G + ((k & 1) ? G - 1 - c : c);
 }
-
 
 // Unit u: rank u / pairs in the item order, head group u % pairs.  With
 // `tab`, the order and the items' lengths come from shared memory (tab[0..K)
@@ -320,19 +287,15 @@ __device__ __forceinline__ void unit_info(const Params& p, const int* tab, int u
 }
 
 // The first unit of this CTA at or after index k that has work; k moves to
-// it.  With kWarp it is called by whole warps and the fields go through
-// lane 0, so that the compiler sees them warp-uniform (fewer registers).
-template <int NH, int K, bool kWarp, bool kWin>
+// it.  Called by whole warps; the fields go through lane 0, so that the
+// compiler sees them warp-uniform (fewer registers).
+template <int NH, int K, bool kWin>
 __device__ __forceinline__ bool next_valid_unit(const Params& p, const int* tab, int& k, Unit& x) {
   const int n_units = p.num_seqs * p.n_qtiles * (p.hq / NH);
   for (;; ++k) {
     const long long u = unit_index(k, blockIdx.x, gridDim.x);
     if (u >= n_units) return false;
     unit_info<NH, K, kWin>(p, tab, static_cast<int>(u), x);
-    if (!kWarp) {
-      if (x.valid) return true;
-      continue;
-    }
     if (__shfl_sync(kFull, x.valid ? 1 : 0, 0)) break;
   }
   x.s = __shfl_sync(kFull, x.s, 0);
@@ -414,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
     tab = t;
   }
   auto next_unit = [&](int& k, Unit& x) -> bool {
-    return next_valid_unit<NH, K, true, kWin>(p, tab, k, x);
+    return next_valid_unit<NH, K, kWin>(p, tab, k, x);
   };
 
   if (threadIdx.x == 0) {
@@ -542,7 +505,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
     for (int k = 0; ok; ++k) {
       Unit x;
       if (!next_unit(k, x)) break;
-      const int n_kv = __shfl_sync(kFull, x.n_kv, 0);
+      const int n_kv = x.n_kv;
       for (int j = 0; ok && j < n_kv; ++j, ++gt) {
         if (is_qk) {
           ok = wait_all(&B->kv_full[st], ph);
@@ -609,11 +572,33 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         ok = wait_or_abort(&B->kv_full[st], (gt / kStages) & 1, p);
         if (__any_sync(kFull, !ok)) { ok = false; break; }
         uint8_t* vt = smem + C::kVOff + st * kTileBytes;
+        // of the tile's keys i < end, some row of the unit sees those with i <
+        // sink or i >= low; the others become 0
+        const int end = x.ctx - (kWin ? x.delta : 0) - j * kBN;
+        const int low = kWin && p.window > 0 ? x.pos_first - p.window - x.delta + 1 - j * kBN : 0;
+        const int sink = kWin ? p.sinks - j * kBN : 0;
+        const bool all = end >= kBN && (low <= 0 || sink >= kBN);
 #pragma unroll 1
         for (int e = lane; e < static_cast<int>(kTileBytes / 16); e += 32 * kConvBatch) {
           uint4 w[kConvBatch];                          // loads first: one latency a batch
-          load_pieces<kConvBatch, 32>(vt, e, w);
-          convert_pieces<kConvBatch, 32, kWin>(p, x, j, vt, e, w);
+#pragma unroll
+          for (int i = 0; i < kConvBatch; ++i) w[i] = *reinterpret_cast<const uint4*>(vt + (e + 32 * i) * 16);
+#pragma unroll
+          for (int i = 0; i < kConvBatch; ++i) {
+            w[i].x = bf16x2_to_half2(w[i].x);
+            w[i].y = bf16x2_to_half2(w[i].y);
+            w[i].z = bf16x2_to_half2(w[i].z);
+            w[i].w = bf16x2_to_half2(w[i].w);
+          }
+          if (!all) {
+#pragma unroll
+            for (int i = 0; i < kConvBatch; ++i) {
+              const int u = (e + 32 * i) >> 3;
+              if (!(u < end && (u < sink || u >= low))) w[i] = make_uint4(0, 0, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kConvBatch; ++i) *reinterpret_cast<uint4*>(vt + (e + 32 * i) * 16) = w[i];
         }
         fence_async_smem();
         __syncwarp();
