@@ -6,13 +6,13 @@ Bounds of the decode (fp32 output), per output element.  With A = sum_j p_j
   * a score is an fp32 sum of 64 exact products: its error is below
     (64 + 16) * 2^-24 * B; exp2 adds 2^-21 relative; a relative error e of
     every weight moves the output by at most 2 e A (numerator, denominator);
-  * the weights keep 22 bits (two fp16 halves) or 16 bits (two bf16 halves,
-    2^-9 * 2^-9 after two roundings): e_p A, e_p = 2^-21 or 2^-17;
+  * the weights keep 22 bits (two fp16 halves) or 24 bits (three bf16 parts,
+    2^-8 each time): e_p A, e_p = 2^-21 or 2^-23;
   * fp32 accumulation of n / 16 products, merges included: (n / 16 + 64) *
     2^-23 * A.
-On the 4-bit cache a row enters as s (c - 8) + (z + 8 s) and its score as
-s (q . c) + z sum(q), so |v| is 8 s + |z + 8 s| and sum |q k| is
-(15 s + |z|) sum |q|.
+On the 4-bit cache a row enters as s (c - 7.5) + (z + 7.5 s) and its score as
+s (q . c) + z sum(q), so |v| is at most 8 s + |z + 8 s| (7.5 s + |z + 7.5 s| is
+no larger) and sum |q k| is (15 s + |z|) sum |q|.
 """
 import numpy as np
 import torch
@@ -121,7 +121,7 @@ def decode_ref(q, tables, ctx, scale, window, sinks, kv=None, cache=None):
                 absv = np.repeat((8 * sv + np.abs(zz[1][page, off, g] + 8 * sv))[:, None], D, 1)
             o, a, b = attend(q[s, h], k, v, scale, absq, absv)
             out[s, h] = o
-            tol[s, h] = decode_bound(a, b, len(pos), 21 if cache is not None else 17)
+            tol[s, h] = decode_bound(a, b, len(pos), 21 if cache is not None else 23)
     return out, tol
 
 
