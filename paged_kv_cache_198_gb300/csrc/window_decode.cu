@@ -83,7 +83,13 @@ constexpr int kMaxProducers = 4;
 constexpr int kMaxThreads = (12 + kMaxProducers) * 32;
 constexpr uint32_t kBf16Tile = kChunk * kD * 2;   // one head's K (or V) of a chunk
 constexpr float kMaxSum = 256.0f;             // a lane's weights under the reference maximum
-constexpr float kMaxProduct = 32768.0f;        // 4-bit: a lane's weights times its V scales
+constexpr float kMaxProduct = 32768.0f;        // 4-bit: a lane's weights times its V sizes
+// 4-bit: the size of a V row (s, offset) is max(s, kOffsetSize |offset|,
+// kLeastSize).  The weights are held against it, so that a row of one value (s = 0)
+// counts too: with V below 2^60 a lane's weights stay below 2^75, its weighted
+// offsets below 2^55, a stage, which leaves 2^50 for the sums.
+constexpr float kOffsetSize = 9.094947017729282e-13f;      // 2^-40
+constexpr float kLeastSize = 8.673617379884035e-19f;       // 2^-60
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr uint32_t kSmemLimit = 227 * 1024;
@@ -572,6 +578,11 @@ __device__ __forceinline__ uint32_t half2_twice_plus(uint32_t a, uint32_t b) {
   return d;
 }
 __device__ __forceinline__ float2 meta_sz(uint32_t w) { return bf16x2_to_float2(w); }
+// a V row's scale s and the offset z + 7.5 s of its centred codes
+__device__ __forceinline__ float2 v_scale_offset(uint32_t w) {
+  const float2 m = meta_sz(w);
+  return make_float2(m.x, fmaf(7.5f, m.x, m.y));
+}
 
 template <int F>
 __device__ __forceinline__ uint32_t pack16(float2 v) {
@@ -604,7 +615,7 @@ struct State {
   uint32_t qf[4][2];   // q as the column operand
   uint32_t qg[4][2];   // 4-bit, up to four heads: qf has columns 0..3, qg columns 4..7
   float acc[4][4];     // output rows, see out_dim
-  float2 m, l, zs;     // reference maximum (log2), sum of p, sum of p (z + 8 s)
+  float2 m, l, zs;     // reference maximum (log2), sum of p, sum of p (z + 7.5 s)
   float2 qsum;         // 4-bit: sum(q), in the units of q . c
   float kf;            // 4-bit: from those units to log2
 };
@@ -674,26 +685,27 @@ __device__ __forceinline__ void load_q(State& st, const Params& p, const uint8_t
 }
 
 // Moves the reference maximum to cover mx (this lane's largest scores, log2), and
-// rescales what is summed so far.  4-bit: the weights meet the V scales, at
-// most sv in this lane, before they are rounded to fp16; the reference is put
+// rescales what is summed so far.  4-bit: the weights meet the V scales before
+// they are rounded to fp16; with V sizes of at most `size` in this lane the
+// reference (a whole number, see normalise) is put
 // where the largest product is 2^6 and moved when one could pass 2^15, so the
 // fp16 operand keeps 22 bits of every weight down to 2^-28 of the largest,
 // whatever the magnitude of V.  One reference scales numerator and denominator:
 // the result does not depend on it.
 template <int F, bool kPair>
-__device__ __forceinline__ void move_reference(State& st, float2 mx, float sv) {
+__device__ __forceinline__ void move_reference(State& st, float2 mx, float size) {
   constexpr int kFirst = kPair ? 2 : 4;      // a pair's two chunks share the columns' reference
 #pragma unroll
   for (int o = kFirst; o < 32; o <<= 1) {
     mx.x = fmaxf(mx.x, __shfl_xor_sync(kFull, mx.x, o));
     mx.y = fmaxf(mx.y, __shfl_xor_sync(kFull, mx.y, o));
-    if (F == k4Bit) sv = fmaxf(sv, __shfl_xor_sync(kFull, sv, o));
+    if (F == k4Bit) size = fmaxf(size, __shfl_xor_sync(kFull, size, o));
   }
   if (F == k4Bit) {
-    const int e = static_cast<int>(__float_as_uint(sv) >> 23) - 127;   // sv < 2^(e + 1)
-    const float up = static_cast<float>(max(-60, min(60, e)) - 5);
-    mx.x += up;
-    mx.y += up;
+    const int e = static_cast<int>(__float_as_uint(size) >> 23) - 127;   // size < 2^(e + 1)
+    const float up = static_cast<float>(e - 5);
+    mx.x = ceilf(mx.x) + up;
+    mx.y = ceilf(mx.y) + up;
   }
   // never down: what was summed stays covered
   mx.x = fmaxf(mx.x, st.m.x);
@@ -709,6 +721,23 @@ __device__ __forceinline__ void move_reference(State& st, float2 mx, float sv) {
     st.acc[i][2] *= f.x;
     st.acc[i][3] *= f.y;
   }
+}
+
+// The size of a lane's largest V rows, from their largest scale and offset.
+__device__ __forceinline__ float v_size(float s, float offset) {
+  return fmaxf(fmaxf(s, offset * kOffsetSize), kLeastSize);
+}
+
+// 4-bit: a column's sums, whose reference depends on the sizes of V, in the units
+// of its largest weight's power of two (m is a whole number, so this is exact):
+// what is merged next then differs in m by no more than the scores do.
+__device__ __forceinline__ void normalise(float& m, float& l, float (&o)[8]) {
+  const int e = min(static_cast<int>(__float_as_uint(l) >> 23) - 127, 126);
+  const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  m += static_cast<float>(e);
+  l *= f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] *= f;
 }
 
 __device__ __forceinline__ void add_to(float (&acc)[4], const float (&sum)[4]) {
@@ -787,8 +816,8 @@ __device__ __forceinline__ void process_pairs(State& st, const Params& p, const 
     const uint8_t* mine = second ? rb[i] : ra[i];
     const float2 k0 = meta_sz(lds32(mine + kRecKMeta + r0 * 4));
     const float2 k1 = meta_sz(lds32(mine + kRecKMeta + r0 * 4 + 32));
-    v0[i] = meta_sz(lds32(mine + kRecVMeta + r0 * 4));
-    v1[i] = meta_sz(lds32(mine + kRecVMeta + r0 * 4 + 32));
+    v0[i] = v_scale_offset(lds32(mine + kRecVMeta + r0 * 4));
+    v1[i] = v_scale_offset(lds32(mine + kRecVMeta + r0 * 4 + 32));
     float a[4], b[4];
     codes_dot(a, ra[i], st.qf, r0, t);
     codes_dot(b, rb[i], st.qg, r0, t);
@@ -820,24 +849,27 @@ __device__ __forceinline__ void process_pairs(State& st, const Params& p, const 
     }
   };
   weights();
-  float sv = fmaxf(v0[0].x, v1[0].x);
+  float sv = fmaxf(v0[0].x, v1[0].x), ov = fmaxf(fabsf(v0[0].y), fabsf(v1[0].y));
 #pragma unroll
-  for (int i = 1; i < NP; ++i) sv = fmaxf(sv, fmaxf(v0[i].x, v1[i].x));
-  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) * sv <= kMaxProduct))) {
+  for (int i = 1; i < NP; ++i) {
+    sv = fmaxf(sv, fmaxf(v0[i].x, v1[i].x));
+    ov = fmaxf(ov, fmaxf(fabsf(v0[i].y), fabsf(v1[i].y)));
+  }
+  const float size = v_size(sv, ov);
+  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) * size <= kMaxProduct))) {
     float2 mx = x0[0];
 #pragma unroll
     for (int i = 0; i < NP; ++i)
       mx = make_float2(fmaxf(mx.x, fmaxf(x0[i].x, x1[i].x)), fmaxf(mx.y, fmaxf(x0[i].y, x1[i].y)));
-    move_reference<k4Bit, true>(st, make_float2(mx.x * st.kf, mx.y * st.kf), sv);
+    move_reference<k4Bit, true>(st, make_float2(mx.x * st.kf, mx.y * st.kf), size);
     weights();
   }
   st.l = __fadd2_rn(st.l, sum);
   uint32_t oa[NP][2], ob[NP][2];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    const float z0 = fmaf(7.5f, v0[i].x, v0[i].y), z1 = fmaf(7.5f, v1[i].x, v1[i].y);
-    st.zs.x = fmaf(w1[i].x, z1, fmaf(w0[i].x, z0, st.zs.x));
-    st.zs.y = fmaf(w1[i].y, z1, fmaf(w0[i].y, z0, st.zs.y));
+    st.zs.x = fmaf(w1[i].x, v1[i].y, fmaf(w0[i].x, v0[i].y, st.zs.x));
+    st.zs.y = fmaf(w1[i].y, v1[i].y, fmaf(w0[i].y, v0[i].y, st.zs.y));
     w0[i] = make_float2(w0[i].x * v0[i].x, w0[i].y * v0[i].x);
     w1[i] = make_float2(w1[i].x * v1[i].x, w1[i].y * v1[i].x);
 #pragma unroll
@@ -889,7 +921,7 @@ __device__ __forceinline__ void process_wide(State& st, const Params& p, const u
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const float2 m = meta_sz(lds32(rec[i] + kRecKMeta + (r0 + 8 * r) * 4));
-      mv[i][r] = meta_sz(lds32(rec[i] + kRecVMeta + (r0 + 8 * r) * 4));
+      mv[i][r] = v_scale_offset(lds32(rec[i] + kRecVMeta + (r0 + 8 * r) * 4));
       x[i][r] = make_float2(fmaf(c[2 * r], m.x, st.qsum.x * m.y),
                             fmaf(c[2 * r + 1], m.x, st.qsum.y * m.y));
       if (kMasked) {
@@ -916,15 +948,19 @@ __device__ __forceinline__ void process_wide(State& st, const Params& p, const u
     }
   };
   weights();
-  float sv = 0.f;
+  float sv = 0.f, ov = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) sv = fmaxf(sv, fmaxf(mv[i][0].x, mv[i][1].x));
-  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) * sv <= kMaxProduct))) {
+  for (int i = 0; i < N; ++i) {
+    sv = fmaxf(sv, fmaxf(mv[i][0].x, mv[i][1].x));
+    ov = fmaxf(ov, fmaxf(fabsf(mv[i][0].y), fabsf(mv[i][1].y)));
+  }
+  const float size = v_size(sv, ov);
+  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) * size <= kMaxProduct))) {
     float2 mx = x[0][0];
 #pragma unroll
     for (int i = 0; i < N; ++i)
       mx = make_float2(fmaxf(mx.x, fmaxf(x[i][0].x, x[i][1].x)), fmaxf(mx.y, fmaxf(x[i][0].y, x[i][1].y)));
-    move_reference<k4Bit, false>(st, make_float2(mx.x * st.kf, mx.y * st.kf), sv);
+    move_reference<k4Bit, false>(st, make_float2(mx.x * st.kf, mx.y * st.kf), size);
     weights();
   }
   st.l = __fadd2_rn(st.l, sum);
@@ -933,9 +969,9 @@ __device__ __forceinline__ void process_wide(State& st, const Params& p, const u
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const float zc = fmaf(7.5f, mv[i][r].x, mv[i][r].y), sc = mv[i][r].x;
-      st.zs.x = fmaf(w[i][r].x, zc, st.zs.x);
-      st.zs.y = fmaf(w[i][r].y, zc, st.zs.y);
+      const float sc = mv[i][r].x;
+      st.zs.x = fmaf(w[i][r].x, mv[i][r].y, st.zs.x);
+      st.zs.y = fmaf(w[i][r].y, mv[i][r].y, st.zs.y);
       const float2 v = make_float2(w[i][r].x * sc, w[i][r].y * sc);
       const uint32_t h = pack16<k4Bit>(v);
       const float2 back = unpack16<k4Bit>(h);
@@ -1087,6 +1123,10 @@ __device__ __forceinline__ void lane_sums(State& st, float (&o)[2][8]) {
     o[1][2 * i] = fmaf(st.acc[i][1], f0, F == k4Bit ? st.zs.y : 0.f);
     o[0][2 * i + 1] = fmaf(st.acc[i][2], f1, F == k4Bit ? st.zs.x : 0.f);
     o[1][2 * i + 1] = fmaf(st.acc[i][3], f1, F == k4Bit ? st.zs.y : 0.f);
+  }
+  if (F == k4Bit) {
+    normalise(st.m.x, st.l.x, o[0]);
+    normalise(st.m.y, st.l.y, o[1]);
   }
 }
 

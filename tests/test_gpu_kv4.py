@@ -397,3 +397,76 @@ def test_decode_the_longest_sequences_of_few(group, ctx, window, sinks):
     got, want, tol = _decode(90 + group, [ctx, 40], group, 1, 16, window, sinks)
     assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / np.maximum(tol, 1e-30)).max()
     assert_clean_status()
+
+
+def _put(cache, tables, bs, pos, part, code, s, z):
+    """Sets rows of the 4-bit cache, all heads: at positions pos of sequence 0, K
+    (part 0) or V rows of codes `code` (a number or 64), scales s and minima z."""
+    nib = np.broadcast_to(np.asarray(code, np.uint8), (64,))
+    packed = nib[0::2] | nib[1::2] << 4
+    for i, p in enumerate(pos):
+        block, sub, tok = tables[0][p // bs], p % bs // 16, p % 16
+        cache[block, sub, :, 512 * part + 32 * tok:512 * part + 32 * tok + 32] = packed
+        sz = C.f64_to_bf16_bits(np.array([np.broadcast_to(s, len(pos))[i], np.broadcast_to(z, len(pos))[i]]))
+        cache[block, sub, :, 1024 + 64 * part + 4 * tok:1028 + 64 * part + 4 * tok] = sz.view(np.uint8)
+
+
+def _planned(n, hq, hkv, logits, v, window=0, bs=16):
+    """One sequence of n tokens whose scores are `logits` (natural units; exact: K
+    rows of one value, q of one 8) and whose V rows are v = (codes, s, z), each a
+    number or one a token.  Returns the output, the plain form's and A = sum p
+    (8 s + |z + 8 s|) of the bounds."""
+    rng = np.random.default_rng(n)
+    tables, nb = C.deal(rng, [n], bs)
+    cache = np.zeros(tvl.kv4_cache_shape(nb, hkv, bs), np.uint8)
+    _put(cache, tables, bs, range(n), 0, 0, 0.0, logits)
+    _put(cache, tables, bs, range(n), 1, v[0], v[1], v[2])
+    q = np.zeros((1, hq, 64))
+    q[..., 5] = 8.0
+    out = torch.full((1, hq, 64), float("nan"), device=DEV)
+    tvl.kv4_attention_decode(out, C.bf16(q, DEV), _cuda(cache), _cuda(tables), _cuda(np.array([n], np.int32)),
+                             0.125, window=window)
+    _, _, z = C.unpack(cache)
+    pos = C.visible(n - 1, window, 0)
+    page, off = tables[0][pos // bs], pos % bs
+    x = z[0][page, off, 0]
+    p = np.exp(x - x.max())
+    p /= p.sum()
+    codes, s, z = (y[1][page, off, 0] for y in C.unpack(cache))
+    a = (p * (8 * s + np.abs(z + 8 * s))).sum()
+    spread = float(np.ptp(np.where(p > 0, x, x.max()))) / np.log(2.0)
+    return C.f64(out)[0], p @ (codes * s[:, None] + z[:, None]), a, spread
+
+
+def _planned_bound(n, a, spread):
+    """decode_bound with scores that are exact but for the product with log2 e
+    (and the reference's subtraction in one rounding): 2 * 2^-24 of their range."""
+    return a * (2 * (2 * 2.0 ** -24 * spread + 2.0 ** -21) + 2.0 ** -21 + (n / 16 + 64) * 2.0 ** -23) + 1e-37
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 1), (8, 1), (128, 32), (256, 32)])
+@pytest.mark.parametrize("value", [2.0 ** 59, -100.0, 2.0 ** -80, 0.0])
+@pytest.mark.parametrize("rise", [0.0, 20.0, 41.5, 60.0, 85.0, -50.0])
+def test_decode_of_rows_of_one_value(hq, hkv, value, rise):
+    """V rows of one value (s = 0) of any size, whose scores rise by `rise` at
+    every quarter of the context: weights that meet no scale still must not leave
+    fp32's range."""
+    n = 400 if hkv == 1 else 3100
+    logits = np.repeat([0.0, rise, 2 * rise, 3 * rise], -(-n // 4))[:n]
+    got, want, a, spread = _planned(n, hq, hkv, logits, (0, 0.0, value))
+    assert (np.abs(got - want) <= _planned_bound(n, a, spread)).all(), (got[0, 0], want[0])
+    assert_clean_status()
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 1), (8, 1), (128, 32), (256, 32)])
+@pytest.mark.parametrize("first", [True, False])
+def test_decode_of_rows_of_one_value_among_others(hq, hkv, first):
+    """Rows with s = 0 at 2^59 whose weight is 2^-40, and a row of zeros that has
+    nearly all of it, at the other end of the context."""
+    n = 400 if hkv == 1 else 3100
+    at = 0 if first else n - 1
+    logits, value = np.zeros(n), np.full(n, 2.0 ** 59)
+    logits[at], value[at] = 27.75, 0.0
+    got, want, a, spread = _planned(n, hq, hkv, logits, (0, 0.0, value))
+    assert (np.abs(got - want) <= _planned_bound(n, a, spread)).all(), (got[0, 0], want[0])
+    assert_clean_status()
