@@ -686,26 +686,24 @@ __device__ __forceinline__ void load_q(State& st, const Params& p, const uint8_t
 
 // Moves the reference maximum to cover mx (this lane's largest scores, log2), and
 // rescales what is summed so far.  4-bit: the weights meet the V scales before
-// they are rounded to fp16; with V sizes of at most `size` in this lane the
-// reference (a whole number, see normalise) is put
-// where the largest product is 2^6 and moved when one could pass 2^15, so the
-// fp16 operand keeps 22 bits of every weight down to 2^-28 of the largest,
-// whatever the magnitude of V.  One reference scales numerator and denominator:
-// the result does not depend on it.
+// they are rounded to fp16, so mx is the largest of score + log2 of the V row's
+// size (sized_score) and the reference, a whole number (see normalise), is put
+// where the largest product of a weight and a size is 2^5 to 2^7.  It moves when a
+// lane's bound on them passes 2^15, and only to such a place, so the largest
+// product so far is at least 2^5 and the two fp16 parts keep every product to
+// 2^-22 of itself or 2^-30 of the largest, however the sizes of V are spread.  One
+// reference scales numerator and denominator: the result does not depend on it.
 template <int F, bool kPair>
-__device__ __forceinline__ void move_reference(State& st, float2 mx, float size) {
+__device__ __forceinline__ void move_reference(State& st, float2 mx) {
   constexpr int kFirst = kPair ? 2 : 4;      // a pair's two chunks share the columns' reference
 #pragma unroll
   for (int o = kFirst; o < 32; o <<= 1) {
     mx.x = fmaxf(mx.x, __shfl_xor_sync(kFull, mx.x, o));
     mx.y = fmaxf(mx.y, __shfl_xor_sync(kFull, mx.y, o));
-    if (F == k4Bit) size = fmaxf(size, __shfl_xor_sync(kFull, size, o));
   }
   if (F == k4Bit) {
-    const int e = static_cast<int>(__float_as_uint(size) >> 23) - 127;   // size < 2^(e + 1)
-    const float up = static_cast<float>(e - 5);
-    mx.x = ceilf(mx.x) + up;
-    mx.y = ceilf(mx.y) + up;
+    mx.x = ceilf(mx.x) - 6.f;
+    mx.y = ceilf(mx.y) - 6.f;
   }
   // never down: what was summed stays covered
   mx.x = fmaxf(mx.x, st.m.x);
@@ -726,6 +724,16 @@ __device__ __forceinline__ void move_reference(State& st, float2 mx, float size)
 // The size of a lane's largest V rows, from their largest scale and offset.
 __device__ __forceinline__ float v_size(float s, float offset) {
   return fmaxf(fmaxf(s, offset * kOffsetSize), kLeastSize);
+}
+// scores x (in units of kf) of a row with V's (scale, offset) v, plus floor(log2) of
+// its size
+__device__ __forceinline__ float2 sized_score(float2 x, float kf, float2 v) {
+  const int e = static_cast<int>(__float_as_uint(v_size(v.x, fabsf(v.y))) >> 23) - 127;
+  const float f = static_cast<float>(e);
+  return make_float2(fmaf(x.x, kf, f), fmaf(x.y, kf, f));
+}
+__device__ __forceinline__ float2 max2(float2 a, float2 b) {
+  return make_float2(fmaxf(a.x, b.x), fmaxf(a.y, b.y));
 }
 
 // 4-bit: a column's sums, whose reference depends on the sizes of V, in the units
@@ -857,11 +865,13 @@ __device__ __forceinline__ void process_pairs(State& st, const Params& p, const 
   }
   const float size = v_size(sv, ov);
   if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) * size <= kMaxProduct))) {
-    float2 mx = x0[0];
+    float2 mx = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
-      mx = make_float2(fmaxf(mx.x, fmaxf(x0[i].x, x1[i].x)), fmaxf(mx.y, fmaxf(x0[i].y, x1[i].y)));
-    move_reference<k4Bit, true>(st, make_float2(mx.x * st.kf, mx.y * st.kf), size);
+    for (int i = 0; i < NP; ++i) {
+      mx = max2(mx, sized_score(x0[i], st.kf, v0[i]));
+      mx = max2(mx, sized_score(x1[i], st.kf, v1[i]));
+    }
+    move_reference<k4Bit, true>(st, mx);
     weights();
   }
   st.l = __fadd2_rn(st.l, sum);
@@ -956,11 +966,12 @@ __device__ __forceinline__ void process_wide(State& st, const Params& p, const u
   }
   const float size = v_size(sv, ov);
   if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) * size <= kMaxProduct))) {
-    float2 mx = x[0][0];
+    float2 mx = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      mx = make_float2(fmaxf(mx.x, fmaxf(x[i][0].x, x[i][1].x)), fmaxf(mx.y, fmaxf(x[i][0].y, x[i][1].y)));
-    move_reference<k4Bit, false>(st, make_float2(mx.x * st.kf, mx.y * st.kf), size);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) mx = max2(mx, sized_score(x[i][r], st.kf, mv[i][r]));
+    move_reference<k4Bit, false>(st, mx);
     weights();
   }
   st.l = __fadd2_rn(st.l, sum);
@@ -1045,8 +1056,7 @@ __device__ __forceinline__ void process_bf16(State& st, const Params& p, const u
   };
   weights();
   if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) <= kMaxSum))) {
-    move_reference<kBf16, false>(
-        st, make_float2(fmaxf(x[0].x, x[1].x), fmaxf(x[0].y, x[1].y)), 0.f);
+    move_reference<kBf16, false>(st, max2(x[0], x[1]));
     weights();
   }
   st.l = __fadd2_rn(st.l, sum);

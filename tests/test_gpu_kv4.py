@@ -470,3 +470,17 @@ def test_decode_of_rows_of_one_value_among_others(hq, hkv, first):
     got, want, a, spread = _planned(n, hq, hkv, logits, (0, 0.0, value))
     assert (np.abs(got - want) <= _planned_bound(n, a, spread)).all(), (got[0, 0], want[0])
     assert_clean_status()
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 1), (8, 1), (128, 32), (256, 32)])
+@pytest.mark.parametrize("ratio", [2.0 ** -10, 2.0 ** -16, 2.0 ** -20, 2.0 ** -30])
+@pytest.mark.parametrize("at", [0, 37, 399])
+def test_decode_of_a_heavy_token_with_small_values(hq, hkv, ratio, at):
+    """One token has nearly all the weight and V values far below the others':
+    its weight is kept in 22 bits all the same."""
+    n = 400 if hkv == 1 else 3100
+    logits, s = np.zeros(n), np.full(n, 1.0)
+    logits[at], s[at] = 0.6931 * (8 - np.log2(ratio)) + 20, ratio
+    got, want, a, spread = _planned(n, hq, hkv, logits, (np.arange(64) % 16, s, -8 * s))
+    assert (np.abs(got - want) <= _planned_bound(n, a, spread)).all(), (np.abs(got - want) / a).max()
+    assert_clean_status()
