@@ -24,17 +24,21 @@
 // final scale.  The k order of a product is free, so lane t of a row takes
 // the row's dimensions 16 t .. 16 t + 15 as one 8-byte load.  Per row
 //   scale q . K_j = s_j (q . c_j) F + z_j sum(q),
-// and for V the weight p_j s_j multiplies 2 c_j - 15 (one packed operation)
+// and for V the weight p_j s_j multiplies c_j - 7.5 (one packed operation)
 // while p_j (z_j + 7.5 s_j) is summed in fp32 beside it: centred codes keep the
 // long sum as small as the output, so fp32 accumulation loses nothing to
-// cancellation.  q (bf16) is exact in fp16 after a power-of-two scale.
+// cancellation.  That operation also makes them normal numbers: the tensor core
+// aligns a sum's terms by their exponent fields, so subnormal ones leave its upper
+// bits empty (error 4 10^-6 of the output's norm, 4 10^-7 with normal ones: 64
+// sequences of 0.5-4k tokens).  q (bf16) is exact in fp16 after a power-of-two scale.
 //
 // P in parts.  The weights p are fp32; two fp16 parts keep 22 bits of them,
 // three bf16 parts all 24, so the fp32 output carries no rounding of P.  With
 // four query heads or fewer the products' spare columns 4..7 take another
 // chunk (4-bit) or the lo parts (bf16) at no cost; with five to eight each part
-// takes a product of its own.  The tensor cores truncate what they add, so no
-// accumulator runs through them: each stage starts a fresh one, added in fp32.
+// takes a product of its own.  The tensor cores truncate what they add, so a sum
+// runs through four products at most (4-bit: a head's q . c, a stage's P V; bf16: the
+// parts of P): each stage starts a fresh one, added in fp32.
 //
 // Work split.  The visible 16-token chunks of all sequences form one line, cut
 // into equal ranges, one CTA per SM and KV-head group, each sequence start
@@ -571,10 +575,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-// 2 a + b on fp16 pairs
-__device__ __forceinline__ uint32_t half2_twice_plus(uint32_t a, uint32_t b) {
+// 2^15 a + b on fp16 pairs
+__device__ __forceinline__ uint32_t half2_raise(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(0x40004000u), "r"(b));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(0x78007800u), "r"(b));
   return d;
 }
 __device__ __forceinline__ float2 meta_sz(uint32_t w) { return bf16x2_to_float2(w); }
@@ -763,7 +767,8 @@ __device__ __forceinline__ uint32_t lds32(const uint8_t* p) {
 }
 
 constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
-constexpr uint32_t k15 = 0x800f800fu, k255 = 0x80ff80ffu;     // -15 and -255 times 2^-24
+// fp16 pairs: -7.5 and -127.5 times 2^-9
+constexpr uint32_t kMinus7 = 0xa380a380u, kMinus127 = 0xb3f8b3f8u;
 
 // Scores of a 4-bit chunk's 16 rows: c = q . codes
 __device__ __forceinline__ void codes_dot(float (&c)[4], const uint8_t* rec, const uint32_t (&qf)[4][2],
@@ -792,17 +797,17 @@ __device__ __forceinline__ void load_v(uint32_t (&w)[4], const uint8_t* rec, int
   w[3] = __byte_perm(y2, y3, 0x7632);
 }
 // Rows 2 i, 2 i + 1 of the lane's dimensions as the row operand, centred: the
-// even dimension's codes, 2 c - 15, and the whole bytes, 2 b - 255.  As b = c +
-// 16 c', the odd dimension's 16 (2 c' - 15) is the difference, taken once at the
+// even dimension's codes, 2^-9 (c - 7.5), and the whole bytes, 2^-9 (b - 127.5).  As b =
+// c + 16 c', the odd dimension's 2^-5 (c' - 7.5) is the difference, taken once at the
 // segment's end; a byte costs one operation to isolate, its high half two.
 __device__ __forceinline__ void v_operand(uint32_t (&a)[4], const uint32_t (&w)[4], int i) {
   constexpr uint32_t kByte = 0x00ff00ffu;
   const uint32_t u0 = (i & 1) ? __byte_perm(w[i >> 1], 0, 0x4341) : w[i >> 1] & kByte;
   const uint32_t u1 = (i & 1) ? __byte_perm(w[2 + (i >> 1)], 0, 0x4341) : w[2 + (i >> 1)] & kByte;
-  a[0] = half2_twice_plus(u0 & kLo, k15);
-  a[1] = half2_twice_plus(u0, k255);
-  a[2] = half2_twice_plus(u1 & kLo, k15);
-  a[3] = half2_twice_plus(u1, k255);
+  a[0] = half2_raise(u0 & kLo, kMinus7);
+  a[1] = half2_raise(u0, kMinus127);
+  a[2] = half2_raise(u1 & kLo, kMinus7);
+  a[3] = half2_raise(u1, kMinus127);
 }
 
 // NP pairs of chunks, A and B, of a 4-bit head with at most four query heads.
@@ -1118,7 +1123,7 @@ __device__ __forceinline__ void lane_sums(State& st, float (&o)[2][8]) {
       st.zs.y += __shfl_xor_sync(kFull, st.zs.y, x);
     }
   }
-  const float f0 = F == k4Bit ? 8388608.f : 1.f;      // 2^24 / 2 of the codes
+  const float f0 = F == k4Bit ? 512.f : 1.f;          // the codes' 2^-9
   const float f1 = F == k4Bit ? f0 * 0.0625f : 1.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -484,3 +484,20 @@ def test_decode_of_a_heavy_token_with_small_values(hq, hkv, ratio, at):
     got, want, a, spread = _planned(n, hq, hkv, logits, (np.arange(64) % 16, s, -8 * s))
     assert (np.abs(got - want) <= _planned_bound(n, a, spread)).all(), (np.abs(got - want) / a).max()
     assert_clean_status()
+
+
+@pytest.mark.parametrize("ctx,hq,hkv", [([777], 8, 2), ([3000] * 3, 32, 8), ([2000], 16, 2), ([900] * 40, 64, 8)])
+def test_decode_error_in_the_output_norm(ctx, hq, hkv):
+    """Random rows: the output is the size of the root of the sum of squares of its
+    products, well below the sum that the other bounds are relative to.  In its norm:
+    weights in two fp16 parts, 2^-22; exp2, 2^-22; the weights' exponents of up to 6
+    (log2), rounded once, 2^-22 ln 2; P V's products of a step cut at 2^-24 of the
+    largest, 16 of one sign against a root sum of squares of 4 (the largest 2.5), 10 *
+    2^-25; fp32 sums across steps, 2^-23; scores s (q c) + z sum q, four roundings of
+    terms of about 5, 2^-24 * 5 * 2 / sqrt(3) as a root mean square; q c's products of
+    up to 2.5, cut at 2^-24 in four sums of 16, 2^-24 * 2.5 * sqrt(64) / 2.  In all 2.0
+    * 10^-6."""
+    got, want, _ = _decode(120 + hq, ctx, hq, hkv, 16)
+    rel = np.linalg.norm(got - want) / np.linalg.norm(want)
+    assert rel <= 2.0 ** -22 * (2 + np.log(2.0)) + 10 * 2.0 ** -25 + 2.0 ** -23 + 2.0 ** -24 * (10 / 3 ** 0.5 + 10), rel
+    assert_clean_status()
