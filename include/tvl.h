@@ -364,8 +364,9 @@ tvl_status tvl_window_decode_workspace_size(int num_q_heads, int num_kv_heads, i
  *   out : float32 [S, Hq, D]; q : bf16 [S, Hq, D]; cache : see above
  * context_lens[s] == 0 gives a zero row.  One or two launches; no allocation.
  * Supported: D == 64, G from 1 to 8, bs in {16, 32, 64, 128}, any Hkv,
- * |q| < 2^100, cached V below 2^60 in magnitude, NB * bs < 2^31, Hkv <= 65535,
- * Hq <= 262140.
+ * |q| < 2^100, cached V below 2^60 in magnitude (rows whose scale s is below 2^-42
+ * keep an absolute error below 2^-60 a token), NB * bs < 2^31, Hkv <= 65535, Hq <=
+ * 262140.
  */
 tvl_status tvl_kv4_attention_decode(float* out, const void* q, const void* cache,
                                     const int32_t* block_tables, const int32_t* context_lens,

@@ -88,12 +88,11 @@ constexpr int kMaxThreads = (12 + kMaxProducers) * 32;
 constexpr uint32_t kBf16Tile = kChunk * kD * 2;   // one head's K (or V) of a chunk
 constexpr float kMaxSum = 256.0f;             // a lane's weights under the reference maximum
 constexpr float kMaxProduct = 32768.0f;        // 4-bit: a lane's weights times its V sizes
-// 4-bit: the size of a V row (s, offset) is max(s, kOffsetSize |offset|,
-// kLeastSize).  The weights are held against it, so that a row of one value (s = 0)
-// counts too: with V below 2^60 a lane's weights stay below 2^75, its weighted
-// offsets below 2^55, a stage, which leaves 2^50 for the sums.
-constexpr float kOffsetSize = 9.094947017729282e-13f;      // 2^-40
-constexpr float kLeastSize = 8.673617379884035e-19f;       // 2^-60
+// 4-bit: the weights are held against max(V scale, kLeastScale), so that rows of one
+// value (scale 0) count too: with V below 2^60 a lane's weights stay below 2^49 and
+// their sums with the offsets below 2^109 a stage: room for 2^14 stages of a column's
+// eight lanes (10^6 tokens of a warp).
+constexpr float kLeastScale = 5.820766091346741e-11f;      // 2^-34
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr uint32_t kSmemLimit = 227 * 1024;
@@ -691,12 +690,13 @@ __device__ __forceinline__ void load_q(State& st, const Params& p, const uint8_t
 // Moves the reference maximum to cover mx (this lane's largest scores, log2), and
 // rescales what is summed so far.  4-bit: the weights meet the V scales before
 // they are rounded to fp16, so mx is the largest of score + log2 of the V row's
-// size (sized_score) and the reference, a whole number (see normalise), is put
-// where the largest product of a weight and a size is 2^5 to 2^7.  It moves when a
+// scale (scaled_score) and the reference, a whole number (see normalise), is put
+// where the largest product of a weight and a scale is 2^5 to 2^7.  It moves when a
 // lane's bound on them passes 2^15, and only to such a place, so the largest
 // product so far is at least 2^5 and the two fp16 parts keep every product to
-// 2^-22 of itself or 2^-30 of the largest, however the sizes of V are spread.  One
-// reference scales numerator and denominator: the result does not depend on it.
+// 2^-22 of itself or 2^-30 of the largest, however the scales are spread (below
+// kLeastScale: of that scale's).  One reference scales numerator and denominator:
+// the result does not depend on it.
 template <int F, bool kPair>
 __device__ __forceinline__ void move_reference(State& st, float2 mx) {
   constexpr int kFirst = kPair ? 2 : 4;      // a pair's two chunks share the columns' reference
@@ -725,14 +725,9 @@ __device__ __forceinline__ void move_reference(State& st, float2 mx) {
   }
 }
 
-// The size of a lane's largest V rows, from their largest scale and offset.
-__device__ __forceinline__ float v_size(float s, float offset) {
-  return fmaxf(fmaxf(s, offset * kOffsetSize), kLeastSize);
-}
-// scores x (in units of kf) of a row with V's (scale, offset) v, plus floor(log2) of
-// its size
-__device__ __forceinline__ float2 sized_score(float2 x, float kf, float2 v) {
-  const int e = static_cast<int>(__float_as_uint(v_size(v.x, fabsf(v.y))) >> 23) - 127;
+// scores x (in units of kf) of a row with V scale s, plus floor(log2 s)
+__device__ __forceinline__ float2 scaled_score(float2 x, float kf, float s) {
+  const int e = static_cast<int>(__float_as_uint(fmaxf(s, kLeastScale)) >> 23) - 127;
   const float f = static_cast<float>(e);
   return make_float2(fmaf(x.x, kf, f), fmaf(x.y, kf, f));
 }
@@ -740,7 +735,7 @@ __device__ __forceinline__ float2 max2(float2 a, float2 b) {
   return make_float2(fmaxf(a.x, b.x), fmaxf(a.y, b.y));
 }
 
-// 4-bit: a column's sums, whose reference depends on the sizes of V, in the units
+// 4-bit: a column's sums, whose reference depends on the scales of V, in the units
 // of its largest weight's power of two (m is a whole number, so this is exact):
 // what is merged next then differs in m by no more than the scores do.
 __device__ __forceinline__ void normalise(float& m, float& l, float (&o)[8]) {
@@ -862,19 +857,15 @@ __device__ __forceinline__ void process_pairs(State& st, const Params& p, const 
     }
   };
   weights();
-  float sv = fmaxf(v0[0].x, v1[0].x), ov = fmaxf(fabsf(v0[0].y), fabsf(v1[0].y));
+  float sv = kLeastScale;
 #pragma unroll
-  for (int i = 1; i < NP; ++i) {
-    sv = fmaxf(sv, fmaxf(v0[i].x, v1[i].x));
-    ov = fmaxf(ov, fmaxf(fabsf(v0[i].y), fabsf(v1[i].y)));
-  }
-  const float size = v_size(sv, ov);
-  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) * size <= kMaxProduct))) {
+  for (int i = 0; i < NP; ++i) sv = fmaxf(sv, fmaxf(v0[i].x, v1[i].x));
+  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) * sv <= kMaxProduct))) {
     float2 mx = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      mx = max2(mx, sized_score(x0[i], st.kf, v0[i]));
-      mx = max2(mx, sized_score(x1[i], st.kf, v1[i]));
+      mx = max2(mx, scaled_score(x0[i], st.kf, v0[i].x));
+      mx = max2(mx, scaled_score(x1[i], st.kf, v1[i].x));
     }
     move_reference<k4Bit, true>(st, mx);
     weights();
@@ -963,19 +954,15 @@ __device__ __forceinline__ void process_wide(State& st, const Params& p, const u
     }
   };
   weights();
-  float sv = 0.f, ov = 0.f;
+  float sv = kLeastScale;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    sv = fmaxf(sv, fmaxf(mv[i][0].x, mv[i][1].x));
-    ov = fmaxf(ov, fmaxf(fabsf(mv[i][0].y), fabsf(mv[i][1].y)));
-  }
-  const float size = v_size(sv, ov);
-  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) * size <= kMaxProduct))) {
+  for (int i = 0; i < N; ++i) sv = fmaxf(sv, fmaxf(mv[i][0].x, mv[i][1].x));
+  if (__any_sync(kFull, !(fmaxf(sum.x, sum.y) * sv <= kMaxProduct))) {
     float2 mx = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) mx = max2(mx, sized_score(x[i][r], st.kf, mv[i][r]));
+      for (int r = 0; r < 2; ++r) mx = max2(mx, scaled_score(x[i][r], st.kf, mv[i][r].x));
     move_reference<k4Bit, false>(st, mx);
     weights();
   }
