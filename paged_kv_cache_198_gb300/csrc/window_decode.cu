@@ -87,7 +87,7 @@ constexpr int kMaxProducers = 4;
 constexpr int kMaxThreads = (12 + kMaxProducers) * 32;
 constexpr uint32_t kBf16Tile = kChunk * kD * 2;   // one head's K (or V) of a chunk
 constexpr float kMaxSum = 256.0f;             // a lane's weights under the reference maximum
-constexpr float kMaxProduct = 32768.0f;        // 4-bit: a lane's weights times its V sizes
+constexpr float kMaxProduct = 32768.0f;        // 4-bit: a lane's weights times its V scales
 // 4-bit: the weights are held against max(V scale, kLeastScale), so that rows of one
 // value (scale 0) count too: with V below 2^60 a lane's weights stay below 2^49 and
 // their sums with the offsets below 2^109 a stage: room for 2^14 stages of a column's
@@ -101,6 +101,10 @@ constexpr uint32_t kSmemLimit = 227 * 1024;
 // 4, 27.3 at 16, 27.7 at 32) and 256 (bf16, window 1024: 51.2 us at 1, 50.9 at
 // 4, 51.6 at 6).
 constexpr int kSegWeight4 = 14, kSegWeight16 = 3;
+
+// First token of a chunk that stands in for a missing one: past every context (at
+// most 2^31 - 128 tokens), and its 16 tokens still fit 32 bits.
+constexpr int kUnseenToken = 0x7fffffe0;
 
 constexpr int kCombPitch = 72;                // floats a head of a warp hands over: 64 + m, l
 
@@ -1300,7 +1304,7 @@ __device__ void consumer(const Params& p, uint8_t* smem, const Layout& L) {
       auto token_of = [&](int j) { return (v0 + j < ns ? v0 + j : v0 + j + delta) * kChunk; };
       // a missing chunk of a group is stood in for by the first, all unseen
       auto rec_of = [&](int i) { return at + (i < n ? i : 0) * step; };
-      auto tok_of = [&](int i) { return i < n ? token_of(i) : 0x7fffff00; };
+      auto tok_of = [&](int i) { return i < n ? token_of(i) : kUnseenToken; };
       if constexpr (kPair) {
         if (n > 2) {
           const uint8_t* ra[2] = {rec_of(0), rec_of(2)};
@@ -1466,7 +1470,7 @@ __global__ void __launch_bounds__(kDirectWarps * 32, 1)
   if (n > 0 && !mbar_wait(&bars[w], 0) && lane == 0) report(p.status, kDevTimeout);
   // a missing second chunk is stood in for by the first, all unseen
   auto rec_of = [&](int i) -> const uint8_t* { return mine + (i < n ? i : 0) * kBytes; };
-  auto tok_of = [&](int i) { return i < n ? chunk_of(i) * kChunk : 0x7fffff00; };
+  auto tok_of = [&](int i) { return i < n ? chunk_of(i) * kChunk : kUnseenToken; };
 #pragma unroll 1
   for (int i = 0; i < n; i += 2) {
     if constexpr (F == k4Bit && kLoCols) {

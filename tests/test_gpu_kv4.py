@@ -501,3 +501,24 @@ def test_decode_error_in_the_output_norm(ctx, hq, hkv):
     rel = np.linalg.norm(got - want) / np.linalg.norm(want)
     assert rel <= 2.0 ** -22 * (2 + np.log(2.0)) + 10 * 2.0 ** -25 + 2.0 ** -23 + 2.0 ** -24 * (10 / 3 ** 0.5 + 10), rel
     assert_clean_status()
+
+
+@pytest.mark.parametrize("hq,hkv,window", [(2, 2, 300), (8, 1, 300), (2, 2, 3000), (8, 1, 3000), (160, 160, 300)])
+def test_decode_at_the_longest_context(hq, hkv, window):
+    """A context of 2^31 - 128 tokens, nearly all of them behind the window: the
+    result of the same last rows at the end of a short context."""
+    bs, short = 128, 128 * 24
+    tables, nb = C.deal(np.random.default_rng(3), [short], bs)
+    rng = np.random.default_rng(4)
+    cache = C.random_cache(rng, nb, bs, hkv)
+    q = C.bf16_to_f64(C.f64_to_bf16_bits(rng.standard_normal((1, hq, 64)) * 1.5))
+    mb = (2 ** 31 - 128) // bs
+    far = torch.full((1, mb), -1, dtype=torch.int32, device=DEV)
+    far[0, mb - short // bs:] = _cuda(tables[0])
+    out = torch.full((1, hq, 64), float("nan"), device=DEV)
+    for cut in (0, 5):
+        tvl.kv4_attention_decode(out, C.bf16(q, DEV), _cuda(cache), far,
+                                 torch.tensor([2 ** 31 - 128 - cut], dtype=torch.int32, device=DEV), 0.125, window=window)
+        want, tol = C.decode_ref(q, tables, [short - cut], 0.125, window, 0, cache=cache)
+        assert (np.abs(C.f64(out) - want) <= tol).all(), (np.abs(C.f64(out) - want) / tol).max()
+    assert_clean_status()
