@@ -234,9 +234,10 @@ tvl_status tvl_paged_decode_step(
  * Precision: P and V enter the P.V product as fp16 (P rounded to 2^-11
  * relative, exact where the sum is taken in fp32).  V values must lie within
  * the fp16 range, |v| <= 65504 (bf16 can hold more): a larger one makes
- * the output rows of the query tiles whose key range holds it inf or NaN,
- * and any output row that is not finite sets TVL_DEV_NONFINITE.  V values
- * below 2^-14 in magnitude keep an absolute error under 2^-25.
+ * the output rows of the 128-row query tiles that see it (in whose last row's
+ * keys it is) inf or NaN, and any output row that is not finite sets
+ * TVL_DEV_NONFINITE.  V values below 2^-14 in magnitude keep an absolute error
+ * under 2^-25.
  * Supported: D == 64, G in {1, 2, 4, 8}, bs in {16, 32, 64, 128}, Hkv <= 255,
  * num_seqs <= 65535 and num_seqs * ceil(max_q_len / 128) * Hq < 2^31
  * (else TVL_ERR_UNSUPPORTED).  The call launches one kernel (at most one

@@ -31,7 +31,7 @@
 //   4NH       producer: TMA loads of the Q tiles and, per 128-key tile, one
 //             box of bs tokens x 64 dims per physical block (K and V) found
 //             through the block table -- the paged gather; blocks past the
-//             context are requested out of range, so TMA fills them with 0;
+//             unit's last row are requested out of range, so TMA fills them with 0;
 //   4NH+1     MMA issuer: S_h = Q_h K^T (M 128, N 128, bf16, both operands in
 //             shared memory) and O_h += P_h V (M 128, N 64, fp16, P read from
 //             TMEM, V an MN-major shared operand), fp32 accumulation.  The
@@ -42,7 +42,7 @@
 //             2^-14 <= |v| <= 65504; smaller values keep an absolute error
 //             below 2^-25; a larger one becomes infinite, which leaves rows
 //             that are not finite, reported as TVL_DEV_NONFINITE; keys past
-//             the context become 0);
+//             the unit's last row become 0);
 //   4NH+3     P.V issuer (below).
 // P and V go through fp16 rather than bf16 so that rounding P costs at most
 // 2^-11 relative (bf16 would cost 2^-8) -- the fp32-accumulated result stays
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
       if (!ok) break;
       ++nq;
       const int g = x.h0 / p.group;                     // shared KV head
-      const int nblk = (x.ctx + p.bs - 1) / p.bs;
+      const int nblk = (x.pos_first + x.rows + p.bs - 1) / p.bs;   // up to the last row's block
       const int32_t* table = p.block_tables + static_cast<long long>(x.s) * p.max_blocks;
       for (int j = 0; j < x.n_kv; ++j, ++gt) {
         const int st = gt % kStages;
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
     // ------------------------------------------------------- V conversion
     // V tile bf16 -> fp16 in place, 16 bytes at a time (the swizzle only
     // permutes 16-byte chunks within a 128-byte row, so a chunk's row is its
-    // offset / 128); keys past the context become 0.
+    // offset / 128); keys past the unit's last row become 0.
     int gt = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -572,9 +572,10 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         ok = wait_or_abort(&B->kv_full[st], (gt / kStages) & 1, p);
         if (__any_sync(kFull, !ok)) { ok = false; break; }
         uint8_t* vt = smem + C::kVOff + st * kTileBytes;
-        // of the tile's keys i < end, some row of the unit sees those with i <
-        // sink or i >= low; the others become 0
-        const int end = x.ctx - (kWin ? x.delta : 0) - j * kBN;
+        // of the tile's keys i < end (the unit's last row), some row of the unit sees
+        // those with i < sink or i >= low; the others become 0: a later key's
+        // weight is 0, but 0 times a V that is not finite in fp16 is not
+        const int end = x.pos_first + x.rows - (kWin ? x.delta : 0) - j * kBN;
         const int low = kWin && p.window > 0 ? x.pos_first - p.window - x.delta + 1 - j * kBN : 0;
         const int sink = kWin ? p.sinks - j * kBN : 0;
         const bool all = end >= kBN && (low <= 0 || sink >= kBN);

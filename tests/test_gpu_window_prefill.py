@@ -235,3 +235,46 @@ def test_scales(scale, hkv):
     """Masked scores are infinities against the scale's sign; a scale of nothing
     must not turn them into NaN."""
     _run(70, [300, 140], [200, 140], 8, hkv, 16, 100, 4, scale=scale)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1000, 0), (100, 4)])
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (32, 8)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 1e5])
+def test_v_of_a_later_token_leaves_the_earlier_tiles(window, sinks, hq, hkv, value):
+    """Rows 400 .. 699 in tiles of 128 rows: a V at position 530 that fp16 does not
+    hold is seen by no row of the first tile (400 .. 527), whose last key tile
+    reaches past it; its rows equal those without it bit for bit."""
+    rng, tables, nb, k, v, q, starts = _setup(72, [700], [300], hq, hkv, 16)
+    k, q = C.bf16(k, DEV), C.bf16(q, DEV)
+    outs = []
+    for x in (None, value):
+        if x is not None:
+            v[tables[0][530 // 16], 530 % 16] = x
+        outs.append(torch.empty(300, hq, 64, dtype=torch.bfloat16, device=DEV))
+        tvl.paged_attention_window_prefill(outs[-1], q, _cuda(starts), k, C.bf16(v, DEV), _cuda(tables),
+                                           _cuda(np.array([700], np.int32)), 0.125, 300, window, sinks=sinks)
+    assert tvl.get_device_status() == tvl.DEV_NONFINITE
+    assert torch.equal(outs[0][:128], outs[1][:128])
+    assert not torch.isfinite(outs[1][130:131]).all()
+    if window == 0:              # and so in the plain form
+        plain = torch.empty(300, hq, 64, device=DEV)
+        tvl.paged_attention_prefill(plain, q, _cuda(starts), k, C.bf16(v, DEV), _cuda(tables),
+                                    _cuda(np.array([700], np.int32)), 0.125, 300)
+        assert tvl.get_device_status() == tvl.DEV_NONFINITE
+        assert torch.equal(plain[:128].to(torch.bfloat16), outs[0][:128])
+
+
+def test_repeats_bit_for_bit():
+    """More units than SMs, of different lengths: the same call again, and again
+    among other work."""
+    ctx, new = [900, 300, 77, 1500] * 4, [400, 300, 1, 513] * 4
+    rng, tables, nb, k, v, q, starts = _setup(73, ctx, new, 32, 8, 16)
+    args = [C.bf16(q, DEV), _cuda(starts), C.bf16(k, DEV), C.bf16(v, DEV), _cuda(tables),
+            _cuda(np.array(ctx, np.int32)), 0.125, 513, 200]
+    outs = [torch.empty(sum(new), 32, 64, dtype=torch.bfloat16, device=DEV) for _ in range(6)]
+    for o in outs:
+        tvl.paged_attention_window_prefill(o, *args, sinks=4)
+    torch.cuda.synchronize()
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+    assert_clean_status()
