@@ -161,8 +161,10 @@ def _stream_context(stream):
     """torch's allocator on `stream` (None: the current one; a torch stream or a handle)."""
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream")
-                             else torch.cuda.ExternalStream(int(stream)))
+    if not hasattr(stream, "cuda_stream"):
+        # torch takes an external handle of 0 for "no handle" and gives a stream of its own
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t) -> ctypes.c_void_p:

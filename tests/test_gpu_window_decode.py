@@ -163,3 +163,22 @@ def test_scales(scale, hq):
 def test_the_longest_sequences_of_few(group, ctx, window, sinks):
     """Few short bounded sequences: around the most chunks that one CTA holds."""
     _run(90 + group, [ctx, 40], group, 1, 16, window, sinks)
+
+
+def test_a_workspace_for_the_default_stream_given_as_a_handle():
+    """The handle of the default stream is 0: the workspace of a call on it belongs to
+    that stream, not to one of torch's own."""
+    with tvl._stream_context(torch.cuda.default_stream().cuda_stream):
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    rng = np.random.default_rng(78)
+    tables, nb = C.deal(rng, [300, 90], 16)
+    k, v, q = (_bf(rng, s) for s in ((nb, 16, 2, 64), (nb, 16, 2, 64), (2, 8, 64)))
+    want, tol = C.decode_ref(q, tables, [300, 90], 0.125, 0, 0, kv=(k, v))
+    out = torch.empty(2, 8, 64, device=DEV)
+    args = [C.bf16(q, DEV), C.bf16(k, DEV), C.bf16(v, DEV), _cuda(tables), _cuda(np.array([300, 90], np.int32)), 0.125]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream(DEV)):
+        tvl.paged_attention_window_decode(out, *args, 0, stream=0)
+    torch.cuda.synchronize()
+    assert (np.abs(C.f64(out) - want) <= tol).all()
+    assert_clean_status()
