@@ -387,9 +387,18 @@ def bind_paged_decode_step(out, q, k_new, v_new, k_cache, v_cache, block_tables,
                                    context_lens, scale, partition_size, workspace, stream))
 
 
+def _visibility(window, sinks):
+    """(window, sinks) as 32-bit integers; ctypes would drop the upper bits of larger ones."""
+    window, sinks = int(window), int(sinks)
+    if not -2 ** 31 <= min(window, sinks) <= max(window, sinks) < 2 ** 31:
+        raise ValueError(f"window {window} and sinks {sinks} must fit 32 bits")
+    return window, sinks
+
+
 def _prep_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables, context_lens, scale,
                   max_q_len, stream, window=None, sinks=0):
     """`window` None: the plain prefill (fp32 out); else the windowed one (bf16 out)."""
+    visible = () if window is None else _visibility(window, sinks)
     _need(k_cache, "k_cache", torch.bfloat16, 4)
     dev = k_cache.get_device()
     _need(v_cache, "v_cache", torch.bfloat16, 4, dev)
@@ -410,7 +419,7 @@ def _prep_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables, conte
         args = (_ptr(out), _ptr(q), _ptr(query_start_loc), _ptr(k_cache), _ptr(v_cache),
                 _ptr(block_tables), _ptr(context_lens), s, tq, int(max_q_len), hq, hkv, d, bs,
                 nb, mb, float(scale))
-        args += (() if window is None else (int(window), int(sinks))) + (_stream(stream),)
+        args += visible + (_stream(stream),)
     keep = (out, q, query_start_loc, k_cache, v_cache, block_tables, context_lens)
     if window is not None:
         return dev, _load().tvl_paged_attention_window_prefill, args, keep
@@ -561,7 +570,7 @@ def window_decode_workspace_size(num_q_heads, num_kv_heads, head_dim=64) -> int:
 def _prep_window_decode(out, q, caches, nb, bs, hkv, block_tables, context_lens, scale, window,
                         sinks, workspace, stream):
     """Checks shared by the 4-bit and the windowed decode; `caches` is the
-    4-bit cache alone or the two bf16 caches."""
+    4-bit cache alone or the two bf16 caches; (window, sinks) are _visibility's."""
     dev = caches[0].get_device()
     _need(q, "q", torch.bfloat16, 3, dev)
     _need(out, "out", torch.float32, 3, dev)
@@ -581,7 +590,7 @@ def _prep_window_decode(out, q, caches, nb, bs, hkv, block_tables, context_lens,
         _need(workspace, "workspace", torch.uint8, 1, dev)
         args = (_ptr(out), _ptr(q), *(_ptr(c) for c in caches), _ptr(block_tables),
                 _ptr(context_lens), s, hq, hkv, d, bs, nb, block_tables.shape[1], float(scale),
-                int(window), int(sinks), _ptr(workspace), workspace.numel(), _stream(stream))
+                window, sinks, _ptr(workspace), workspace.numel(), _stream(stream))
     lib = _load()
     fn = (lib.tvl_kv4_attention_decode if len(caches) == 1
           else lib.tvl_paged_attention_window_decode)
@@ -590,6 +599,7 @@ def _prep_window_decode(out, q, caches, nb, bs, hkv, block_tables, context_lens,
 
 def _prep_kv4_decode(out, q, cache, block_tables, context_lens, scale, window, sinks, workspace,
                      stream):
+    window, sinks = _visibility(window, sinks)
     nb, bs, hkv = _need_kv4(cache)
     return _prep_window_decode(out, q, (cache,), nb, bs, hkv, block_tables, context_lens, scale,
                                window, sinks, workspace, stream)
@@ -597,6 +607,7 @@ def _prep_kv4_decode(out, q, cache, block_tables, context_lens, scale, window, s
 
 def _prep_bf16_window_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, window,
                              sinks, workspace, stream):
+    window, sinks = _visibility(window, sinks)
     _need(k_cache, "k_cache", torch.bfloat16, 4)
     _need(v_cache, "v_cache", torch.bfloat16, 4, k_cache.get_device())
     nb, bs, hkv, d = k_cache.shape

@@ -159,3 +159,19 @@ def test_sizes_past_the_launch_grid_are_refused(tvl):
     assert lib.tvl_kv4_expand_blocks(D16, D16, D16, D16, D16, 1 << 28, 8, 64, 128, 8, 8,
                                      None) == tvl.ERR_UNSUPPORTED
     assert _decode(tvl, True, hq=262144, hkv=32768) == tvl.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 31, 0), (2 ** 32 + 5, 0), (5, 2 ** 32), (-2 ** 32, 0), (5, -2 ** 31 - 1)])
+def test_windows_past_32_bits_are_refused(tvl, window, sinks):
+    """ctypes keeps the lower 32 bits of an argument: 2^32 + 5 would be a window of 5."""
+    x = torch.zeros(1)                 # no tensor is looked at before the window
+    for call in (tvl.kv4_attention_decode, tvl.bind_kv4_attention_decode):
+        with pytest.raises(ValueError, match="32 bits"):
+            call(x, x, x, x, x, 0.125, window=window, sinks=sinks)
+    for call in (tvl.paged_attention_window_decode, tvl.bind_paged_attention_window_decode):
+        with pytest.raises(ValueError, match="32 bits"):
+            call(x, x, x, x, x, x, 0.125, window, sinks=sinks)
+    for call in (tvl.paged_attention_window_prefill, tvl.bind_paged_attention_window_prefill):
+        with pytest.raises(ValueError, match="32 bits"):
+            call(x, x, x, x, x, x, x, 0.125, 8, window, sinks=sinks)
+    assert tvl._visibility(2 ** 31 - 1, 0) == (2 ** 31 - 1, 0) and tvl._visibility(-1, -1) == (-1, -1)
