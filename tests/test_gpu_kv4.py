@@ -522,3 +522,14 @@ def test_decode_at_the_longest_context(hq, hkv, window):
         want, tol = C.decode_ref(q, tables, [short - cut], 0.125, window, 0, cache=cache)
         assert (np.abs(C.f64(out) - want) <= tol).all(), (np.abs(C.f64(out) - want) / tol).max()
     assert_clean_status()
+
+
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (64, 8), (16, 16)])
+@pytest.mark.parametrize("n,top,window", [(200, 900, 0), (200, 900, 300), (600, 120, 0)])
+def test_decode_of_more_sequences_than_ctas(hq, hkv, n, top, window):
+    """More sequences than CTAs (and than threads of one), whose lengths make most
+    CTAs end inside a sequence: one split sequence a CTA in the list to merge."""
+    ctx = [int(x) for x in np.random.default_rng(n).integers(0, top, n)]
+    got, want, tol = _decode(110 + n, ctx, hq, hkv, 16, window, 3 if window else 0)
+    assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / np.maximum(tol, 1e-30)).max()
+    assert_clean_status()

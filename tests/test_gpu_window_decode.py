@@ -182,3 +182,32 @@ def test_a_workspace_for_the_default_stream_given_as_a_handle():
     torch.cuda.synchronize()
     assert (np.abs(C.f64(out) - want) <= tol).all()
     assert_clean_status()
+
+
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (64, 8), (16, 16)])
+@pytest.mark.parametrize("n,top,window", [(200, 900, 0), (200, 900, 300), (600, 120, 0)])
+def test_more_sequences_than_ctas(hq, hkv, n, top, window):
+    """More sequences than CTAs (and than threads of one), whose lengths make most
+    CTAs end inside a sequence: one split sequence a CTA in the list to merge."""
+    _run(110 + n, [int(x) for x in np.random.default_rng(n).integers(0, top, n)], hq, hkv, 16, window, 3)
+
+
+@pytest.mark.parametrize("hq,hkv,window", [(2, 2, 300), (8, 1, 3000), (160, 160, 300)])
+def test_the_longest_context(hq, hkv, window):
+    """A context of 2^31 - 128 tokens, nearly all of them behind the window: the
+    result of the same last rows at the end of a short context."""
+    bs, short = 128, 128 * 24
+    tables, nb = C.deal(np.random.default_rng(3), [short], bs)
+    rng = np.random.default_rng(4)
+    k, v, q = (_bf(rng, s) for s in ((nb, bs, hkv, 64), (nb, bs, hkv, 64), (1, hq, 64)))
+    mb = (2 ** 31 - 128) // bs
+    far = torch.full((1, mb), -1, dtype=torch.int32, device=DEV)
+    far[0, mb - short // bs:] = _cuda(tables[0])
+    out = torch.full((1, hq, 64), float("nan"), device=DEV)
+    for cut in (0, 5):
+        tvl.paged_attention_window_decode(out, C.bf16(q, DEV), C.bf16(k, DEV), C.bf16(v, DEV), far,
+                                          torch.tensor([2 ** 31 - 128 - cut], dtype=torch.int32, device=DEV), 0.125,
+                                          window)
+        want, tol = C.decode_ref(q, tables, [short - cut], 0.125, window, 0, kv=(k, v))
+        assert (np.abs(C.f64(out) - want) <= tol).all(), (np.abs(C.f64(out) - want) / tol).max()
+    assert_clean_status()
