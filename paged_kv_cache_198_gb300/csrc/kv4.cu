@@ -5,9 +5,10 @@
 // place) and of its new K heads, then each K and V row x (64 values) becomes
 //   z = min x,  s = bf16 rounded up of (max x - z) / 15,
 //   c_d = min(15, rint((x_d - z) / s))   (ties to even; s = 0: all 0),
-// so |s c_d + z - x_d| <= s / 2.  s is rounded up, so the largest value needs
-// no code above 15.  bf16 inputs make exact ties common, so the quotient's
-// rounding is the exact one (row_codes).
+// with max x - z and x_d - z in fp32 (exact unless the magnitudes are some 2^16
+// apart), so |s c_d + z - x_d| <= s / 2 + 2^-19 s.  s is rounded up, so the largest
+// value needs no code above 15.  bf16 inputs make exact ties common, so the
+// quotients' roundings are the exact ones (row_codes).
 //
 // Bound: HBM bandwidth for a prefill chunk (per token 256 Hkv bytes in, 72 Hkv
 // out, and q both ways), latency for a decode step.  Eight lanes hold a row, 16
@@ -86,7 +87,7 @@ __device__ __forceinline__ uint4 rotate(uint4 w, const Turn& t) {
 
 // A row's (s, z) from its extremes, and the codes of this lane's eight values.
 //
-// c = rint((x - z) / s), ties to even, without a division a value: t = d * inv
+// c = rint(d / s), d = x - z in fp32, ties to even, without a division a value: t = d * inv
 // rounded to an integer is off by at most one, and only next to a tie (inv is
 // within 2^-24 of 1 / s and d / s <= 15).  The residual e = d - t s is exact, so
 // |e| > s / 2, or = with t odd, says that the other neighbour is the nearer or

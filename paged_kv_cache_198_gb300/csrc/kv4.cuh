@@ -3,7 +3,8 @@
 // A row (one token, one head, K or V; 64 values) is held as 64 unsigned 4-bit
 // codes c and two bf16 numbers s, z; code c stands for s * c + z.  z is the
 // row's minimum (a bf16 input, so exact) and s = (max - min) / 15 rounded up
-// to bf16, so all 64 values lie within s / 2 of what their code stands for.
+// to bf16, so all 64 values lie within s / 2 (and 2^-19 s for the differences,
+// which are taken in fp32) of what their code stands for.
 //
 // Rows are grouped into records of 16 tokens of one KV head, the unit every
 // kernel moves and computes on:

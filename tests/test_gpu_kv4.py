@@ -533,3 +533,34 @@ def test_decode_of_more_sequences_than_ctas(hq, hkv, n, top, window):
     got, want, tol = _decode(110 + n, ctx, hq, hkv, 16, window, 3 if window else 0)
     assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / np.maximum(tol, 1e-30)).max()
     assert_clean_status()
+
+
+def test_write_of_rows_of_unlike_magnitude():
+    """Where max - z or x - z has more than 24 bits the definition takes it rounded to
+    fp32: codes and s are exact from there on, and a value is kept within s / 2 and
+    2^-24 of the row's range, 15 s (1 + 2^-7) at most, so 2^-19.9 s."""
+    rng = np.random.default_rng(12)
+    t, hkv, bs, nb = 64, 4, 16, 6
+    x = C.bf16_to_f64(C.f64_to_bf16_bits(rng.standard_normal((t, hkv, 64)) * 2.0 ** rng.integers(-40, 5, (t, hkv, 64))))
+    x[0, 0], x[0, 0, 1], x[0, 0, 2] = 7.5, 15.0, -2.0 ** -30       # range 15 + 2^-30: s = 1
+    x[0, 1], x[0, 1, 1], x[0, 1, 2] = 2.0 ** -30, 8.0, -7.0        # x - z = 7 + 2^-30: as 7
+    x[0, 2], x[0, 2, 1], x[0, 2, 2] = -0.5, 7.0, 2.0 ** -40
+    x[0, 3], x[0, 3, 5] = 2.0 ** -126, -2.0 ** -20
+    slots = rng.permutation(nb * bs)[:t].astype(np.int32)
+    cache = torch.zeros(tvl.kv4_cache_shape(nb, hkv, bs), dtype=torch.uint8, device=DEV)
+    v = x[::-1].copy()
+    tvl.kv4_write(C.bf16(x, DEV), C.bf16(v, DEV), cache, _cuda(slots))
+    codes, s, z = C.unpack(cache.cpu().numpy())
+    page, off = slots // bs, slots % bs
+    for part, rows in ((0, x), (1, v)):
+        z0 = rows.min(-1)
+        f = lambda y: y.astype(np.float32).astype(np.float64)
+        m, e = np.frexp(f(rows.max(-1) - z0) / 15.0)
+        s0 = np.ldexp(np.ceil(m * 256.0), e - 8)
+        c0 = np.clip(np.where(s0[..., None] > 0, np.rint(f(rows - z0[..., None]) / s0[..., None]), 0), 0, 15)
+        assert np.array_equal(z[part][page, off], z0) and np.array_equal(s[part][page, off], s0)
+        assert np.array_equal(codes[part][page, off], c0)
+        got = s0[..., None] * c0 + z0[..., None]
+        assert (np.abs(got - rows) <= s0[..., None] * (0.5 + 2.0 ** -19.9)).all()
+    assert s[0][page[0], off[0], 0] == 1.0 and codes[0][page[0], off[0], 0, 0] == 8
+    assert_clean_status()
