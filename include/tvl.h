@@ -347,7 +347,8 @@ tvl_status tvl_kv4_copy_blocks(void* cache, const int32_t* src, const int32_t* d
  * itself included, and the first `sinks`.  window == 0: no window, every j <=
  * p is seen (sinks then has no effect).  Blocks that hold no visible token
  * are not read, and their block table entries may hold anything: a caller may
- * hand such blocks back and reuse them.
+ * reuse such blocks for other sequences.  (A caller that deals out blocks itself:
+ * tvl_allocator_* gives back whole sequences only.)
  */
 
 /* Workspace of the two decode calls below, for the current device (its SM

@@ -55,14 +55,14 @@
 // end in key tiles; key u of that list is key u of the sequence, or u + delta
 // behind the sink blocks, so the mask of a row is again a pair of ranges of u.
 // Gaps are cut out per block, not per 128-key tile: a window of 1024 behind
-// four sinks is nine or ten tiles of 128 keys, where whole tiles would be ten
-// or eleven.  The output is bf16 (P's fp16 rounding, 2^-11, is below the
+// four sinks is ten tiles of 128 keys at most, where whole tiles would be eleven.  The output is bf16 (P's fp16 rounding, 2^-11, is below the
 // output's, 2^-8), staged as one swizzled 128-byte row.
 //
 // What bounds it: the softmax warps' tile, not the tensor pipe (a third active).
-// Windowed, 2 sequences x 4096 new rows, window 2048: 200 us, 693 TFLOP/s; 16
-// chunks of 512 rows, window 1024: 113.5 us, 524 TFLOP/s (units of ten tiles,
-// three of them masked, and a unit's start and end).  Per tile of two heads,
+// Windowed, 2 sequences x 4096 new rows, window 2048: 200.5 us, 691 TFLOP/s (units
+// of 18 tiles, four of them masked); 16 chunks of 512 rows on prefixes of 0-2k, window
+// 1024: 114 us, 522 TFLOP/s (units of 2 to 10 tiles, 8.5 on average, 3.3 of them
+// masked, and a unit's start and end).  Per tile of two heads,
 // ~3000 cycles: ~1700 of both heads' exponentials (1024 at the exp unit's
 // rate), the rest waits and hand-overs of 200-250 cycles each.  What brought
 // it there, in us of the first case:
@@ -73,13 +73,14 @@
 //     tile for its 24 MMAs, where a divergent thread took 2030 + 1040; and V is
 //     converted in batches of loads: 2170 cycles a tile, where 2800 set the
 //     kernel's pace: 216 -> 200.  (The plain form, 16 chunks of 512 rows on
-//     0-2k prefixes: 142 -> 130.)
-// Measured and left: V converted by the softmax warps, 208 us (plain: 136
-// against 130), or by four warps of its own, 212 (the softmax keeps 208
+//     0-2k prefixes, kernel alone: 142 -> 131 from a flushed L2, 131-133 -> 121
+//     over rotating inputs.)
+// Measured and left: V converted by the softmax warps, 208 us (plain, from a
+// flushed L2: 136 against 130), or by four warps of its own, 212 (the softmax keeps 208
 // registers and spills); two warps a row (16 softmax warps, 64 keys each), 230;
 // the scores 32 at a time in rolled loops, 242; a fourth stage, 203; the heads
 // started half a tile apart, no gain; the masks set in place in the plain form
-// too, 132-134 against 130.
+// too, 132-134 against 130 (flushed L2).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>

@@ -27,10 +27,10 @@
 // and for V the weight p_j s_j multiplies c_j - 7.5 (one packed operation)
 // while p_j (z_j + 7.5 s_j) is summed in fp32 beside it: centred codes keep the
 // long sum as small as the output, so fp32 accumulation loses nothing to
-// cancellation.  That operation also makes them normal numbers: the tensor core
-// aligns a sum's terms by their exponent fields, so subnormal ones leave its upper
-// bits empty (error 4 10^-6 of the output's norm, 4 10^-7 with normal ones: 64
-// sequences of 0.5-4k tokens).  q (bf16) is exact in fp16 after a power-of-two scale.
+// cancellation.  That operation also makes them normal numbers: subnormal ones
+// cost ten times the error (4 10^-6 of the output's norm against 3 10^-7, 64
+// sequences of 0.5-4k tokens), as if the tensor core aligned a sum's terms by
+// their exponent fields and left its upper bits empty.  q (bf16) is exact in fp16 after a power-of-two scale.
 //
 // P in parts.  The weights p are fp32; two fp16 parts keep 22 bits of them,
 // three bf16 parts all 24, so the fp32 output carries no rounding of P.  With
@@ -59,12 +59,12 @@
 // tell fills two laps apart.  The warps of a head combine at a segment's end
 // through shared memory.  All waits are bounded.
 //
-// Measured, us per call: 4 bits, G = 4: 64 sequences of 0.5-4k tokens 26.5 (the
-// copies alone: 21.7), 8 of 32k-128k 67.3 (0.80 of HBM; copies alone 61.3); G =
-// 8: 256 with a window of 2048 41.3 (copies alone 29.4; 16 consumer warps of 96
+// Measured, us per call: 4 bits, G = 4: 64 sequences of 0.5-4k tokens 26.3 (the
+// copies alone: 21.7), 8 of 32k-128k 67.0 (0.80 of HBM; copies alone 61.3); G =
+// 8: 256 with a window of 2048 41.4 (copies alone 29.4; 16 consumer warps of 96
 // registers, a chunk at a time, 45.9; four chunks a stage, 44.2).  bf16: 256
-// sequences, window 1024, 50.3, which is the copies alone; 8 long ones 84 (0.95
-// of HBM).  A call's fixed part is about 9 us: the schedule 1.4, the first data
+// sequences, window 1024, 50.6, which is the copies alone; 8 long ones 84 to 85
+// (0.94 of HBM).  A call's fixed part is about 9 us: the schedule 1.4, the first data
 // 3 to 4.6, the merge 4.4.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -1399,7 +1399,7 @@ __global__ void __launch_bounds__((max_warps<F, kLoCols>() + kMaxProducers) * 32
 // ids, issues their copies (all of them fit) and q's loads, waits once, and the
 // warps meet at the end.  Bound by latency: four dependent memory round trips.
 // One sequence with a window of 512 (bf16) takes 4.7 us, against 9.6 through the
-// schedule and the merge; one of 777 tokens (4 bits) 5.2 against 7.8.  A CTA must hold
+// schedule and the merge; one of 777 tokens (4 bits) 5.3 against 7.8.  A CTA must hold
 // the whole sequence at once, and past one CTA an SM the balanced split wins.
 constexpr int kDirectWarps = 16;
 constexpr int kDirectChunks4 = 128, kDirectChunks16 = 48;    // longest sequence (chunks),
