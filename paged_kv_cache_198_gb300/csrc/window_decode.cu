@@ -30,7 +30,8 @@
 // cancellation.  That operation also makes them normal numbers: subnormal ones
 // cost ten times the error (4 10^-6 of the output's norm against 3 10^-7, 64
 // sequences of 0.5-4k tokens), as if the tensor core aligned a sum's terms by
-// their exponent fields and left its upper bits empty.  q (bf16) is exact in fp16 after a power-of-two scale.
+// their exponent fields and left its upper bits empty.  q (bf16) is exact in fp16
+// after a power-of-two scale of its head's.
 //
 // P in parts.  The weights p are fp32; two fp16 parts keep 22 bits of them,
 // three bf16 parts all 24, so the fp32 output carries no rounding of P.  With
@@ -624,7 +625,7 @@ struct State {
   float acc[4][4];     // output rows, see out_dim
   float2 m, l, zs;     // reference maximum (log2), sum of p, sum of p (z + 7.5 s)
   float2 qsum;         // 4-bit: sum(q), in the units of q . c
-  float kf;            // 4-bit: from those units to log2
+  float2 kf;           // 4-bit: from those units to log2
 };
 
 // acc[i][0..1] is output dimension out_dim(i, 0), acc[i][2..3] out_dim(i, 1)
@@ -658,23 +659,26 @@ __device__ __forceinline__ void load_q(State& st, const Params& p, const uint8_t
       if (fabsf(f.y) < INFINITY) mx = fmaxf(mx, fabsf(f.y));
     }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-    sum += __shfl_xor_sync(kFull, sum, 1);
-    sum += __shfl_xor_sync(kFull, sum, 2);
+    for (int o = 1; o < 4; o <<= 1) {       // over the head's four lanes
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+      sum += __shfl_xor_sync(kFull, sum, o);
+    }
     // the sign of the scale goes into q (and a zero scale makes q zero), so that
     // kf is positive and a masked -inf stays one
     const float sign = p.scale_log2 > 0.f ? 1.f : p.scale_log2 < 0.f ? -1.f : 0.f;
-    // the largest |q| of the group to [2^14, 2^15): exact in fp16 for every
-    // element down to 2^-28 of it (a bf16 has 8 significant bits)
+    // the head's largest |q| to [2^14, 2^15): exact in fp16 for every element down
+    // to 2^-27 of it (a bf16 has 8 significant bits)
     int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
     e = max(-100, min(100, e));
     const float up = sign * __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
     const float up16 = up * 0.0625f;
-    st.kf = fmaxf(fabsf(p.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + 10 + e) << 23),
-                  1.17549435e-38f);
-    const float unit = up * 5.9604644775390625e-08f;                 // 2^-24: a code's
-    st.qsum.x = __shfl_sync(kFull, sum, 8 * t) * unit;
-    st.qsum.y = __shfl_sync(kFull, sum, 8 * t + 4) * unit;
+    const float kf =
+        fmaxf(fabsf(p.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + 10 + e) << 23), 1.17549435e-38f);
+    st.kf.x = __shfl_sync(kFull, kf, 8 * t);
+    st.kf.y = __shfl_sync(kFull, kf, 8 * t + 4);
+    sum *= up * 5.9604644775390625e-08f;                             // 2^-24: a code's
+    st.qsum.x = __shfl_sync(kFull, sum, 8 * t);
+    st.qsum.y = __shfl_sync(kFull, sum, 8 * t + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int d = (i >> 1) * 8 + (i & 1) * 2;
@@ -730,10 +734,10 @@ __device__ __forceinline__ void move_reference(State& st, float2 mx) {
 }
 
 // scores x (in units of kf) of a row with V scale s, plus floor(log2 s)
-__device__ __forceinline__ float2 scaled_score(float2 x, float kf, float s) {
+__device__ __forceinline__ float2 scaled_score(float2 x, float2 kf, float s) {
   const int e = static_cast<int>(__float_as_uint(fmaxf(s, kLeastScale)) >> 23) - 127;
   const float f = static_cast<float>(e);
-  return make_float2(fmaf(x.x, kf, f), fmaf(x.y, kf, f));
+  return make_float2(fmaf(x.x, kf.x, f), fmaf(x.y, kf.y, f));
 }
 __device__ __forceinline__ float2 max2(float2 a, float2 b) {
   return make_float2(fmaxf(a.x, b.x), fmaxf(a.y, b.y));
@@ -851,7 +855,7 @@ __device__ __forceinline__ void process_pairs(State& st, const Params& p, const 
   }
   float2 sum;
   auto weights = [&]() {
-    const float2 nm = make_float2(-st.m.x, -st.m.y), kf = make_float2(st.kf, st.kf);
+    const float2 nm = make_float2(-st.m.x, -st.m.y), kf = st.kf;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const float2 d0 = __ffma2_rn(x0[i], kf, nm), d1 = __ffma2_rn(x1[i], kf, nm);
@@ -946,7 +950,7 @@ __device__ __forceinline__ void process_wide(State& st, const Params& p, const u
   }
   float2 sum;
   auto weights = [&]() {
-    const float2 nm = make_float2(-st.m.x, -st.m.y), kf = make_float2(st.kf, st.kf);
+    const float2 nm = make_float2(-st.m.x, -st.m.y), kf = st.kf;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
 #pragma unroll

@@ -564,3 +564,21 @@ def test_write_of_rows_of_unlike_magnitude():
         assert (np.abs(got - rows) <= s0[..., None] * (0.5 + 2.0 ** -19.9)).all()
     assert s[0][page[0], off[0], 0] == 1.0 and codes[0][page[0], off[0], 0, 0] == 8
     assert_clean_status()
+
+
+@pytest.mark.parametrize("hq,hkv,n", [(4, 1, 300), (8, 1, 300), (6, 2, 2500), (128, 32, 2500), (224, 32, 2500)])
+def test_decode_of_heads_of_unlike_magnitude(hq, hkv, n):
+    """Query heads of one group 2^40 apart: each is scaled for itself, so that a small
+    one keeps its scores beside a large one (whose softmax has one token)."""
+    rng = np.random.default_rng(n + hq)
+    tables, nb = C.deal(rng, [n], 16)
+    cache = C.random_cache(rng, nb, 16, hkv)
+    q = C.bf16_to_f64(C.f64_to_bf16_bits(rng.standard_normal((1, hq, 64)) * 1.5))
+    big = np.arange(hq) % (hq // hkv) == 1
+    q[:, big] *= 2.0 ** 40
+    out = torch.full((1, hq, 64), float("nan"), device=DEV)
+    tvl.kv4_attention_decode(out, C.bf16(q, DEV), _cuda(cache), _cuda(tables), _cuda(np.array([n], np.int32)), 0.125)
+    want, tol = C.decode_ref(q, tables, [n], 0.125, 0, 0, cache=cache)
+    got = C.f64(out)
+    assert (np.abs(got - want) <= tol)[:, ~big].all(), (np.abs(got - want) / tol)[:, ~big].max()
+    assert_clean_status()
