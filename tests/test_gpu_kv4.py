@@ -582,3 +582,28 @@ def test_decode_of_heads_of_unlike_magnitude(hq, hkv, n):
     got = C.f64(out)
     assert (np.abs(got - want) <= tol)[:, ~big].all(), (np.abs(got - want) / tol)[:, ~big].max()
     assert_clean_status()
+
+
+@pytest.mark.parametrize("hq,hkv,n", [(2, 1, 300), (8, 1, 300), (128, 32, 2500), (256, 32, 2500)])
+@pytest.mark.parametrize("size", [2.0 ** 26, 2.0 ** 40, 2.0 ** 90])
+def test_decode_of_huge_scores(hq, hkv, n, size):
+    """Scores past 2^24, whose differences are whole numbers: the largest one's V row,
+    to the parts' 2^-22 and a few fp32 roundings, 2^-20 of 8 s + |z + 8 s|."""
+    rng = np.random.default_rng(n + hq)
+    tables, nb = C.deal(rng, [n], 16)
+    cache = C.random_cache(rng, nb, 16, hkv)
+    q = C.bf16_to_f64(C.f64_to_bf16_bits(rng.standard_normal((1, hq, 64)) * size))
+    out = torch.full((1, hq, 64), float("nan"), device=DEV)
+    tvl.kv4_attention_decode(out, C.bf16(q, DEV), _cuda(cache), _cuda(tables), _cuda(np.array([n], np.int32)), 0.125)
+    codes, ss, zz = C.unpack(cache)
+    at = tables[0][np.arange(n) // 16], np.arange(n) % 16
+    got = C.f64(out)[0]
+    for h in range(hq):
+        g = h // (hq // hkv)
+        s, z = (x[:, at[0], at[1], g] for x in (ss, zz))
+        score = (codes[0][at[0], at[1], g] * s[0][:, None] + z[0][:, None]) @ q[0, h] * 0.125
+        j, second = np.argsort(score)[:-3:-1]
+        assert score[j] - score[second] > 1e-5 * np.abs(score).max() + 200      # one token, told apart in fp32
+        v = codes[1][at[0], at[1], g][j] * s[1][j] + z[1][j]
+        assert (np.abs(got[h] - v) <= 2.0 ** -20 * (8 * s[1][j] + abs(z[1][j] + 8 * s[1][j]))).all(), h
+    assert_clean_status()
