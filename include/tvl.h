@@ -237,7 +237,8 @@ tvl_status tvl_paged_decode_step(
  * the output rows of the 128-row query tiles that see it (in whose last row's
  * keys it is) inf or NaN, and any output row that is not finite sets
  * TVL_DEV_NONFINITE.  V values below 2^-14 in magnitude keep an absolute error
- * under 2^-25.
+ * under 2^-25.  Scores must stay below 2^27 in magnitude (their distance from
+ * the running maximum is taken in fp32; past 2^28 rows go wrong).
  * Supported: D == 64, G in {1, 2, 4, 8}, bs in {16, 32, 64, 128}, Hkv <= 255,
  * num_seqs <= 65535 and num_seqs * ceil(max_q_len / 128) * Hq < 2^31
  * (else TVL_ERR_UNSUPPORTED).  The call launches one kernel (at most one
@@ -379,8 +380,8 @@ tvl_status tvl_kv4_attention_decode(float* out, const void* q, const void* cache
                                     size_t workspace_bytes, void* stream);
 
 /*
- * Decode attention with a window over the bf16 caches: the same call on the
- * layout of tvl_paged_attention_decode.  P is carried in three bf16 parts
+ * Decode attention with a window over the bf16 caches: the same call, with the
+ * same limits, on the layout of tvl_paged_attention_decode.  P is carried in three bf16 parts
  * (24 bits).  Slots of a read block that are not visible may hold anything, NaN
  * included.
  */

@@ -61,8 +61,8 @@
 // through shared memory.  All waits are bounded.
 //
 // Measured, us per call: 4 bits, G = 4: 64 sequences of 0.5-4k tokens 26.3 (the
-// copies alone: 21.7), 8 of 32k-128k 67.0 (0.80 of HBM; copies alone 61.3); G =
-// 8: 256 with a window of 2048 41.4 (copies alone 29.4; 16 consumer warps of 96
+// copies alone: 21.7), 8 of 32k-128k 67.2 (0.80 of HBM; copies alone 61.3); G =
+// 8: 256 with a window of 2048 41.6 (copies alone 29.4; 16 consumer warps of 96
 // registers, a chunk at a time, 45.9; four chunks a stage, 44.2).  bf16: 256
 // sequences, window 1024, 50.6, which is the copies alone; 8 long ones 84 to 85
 // (0.94 of HBM).  A call's fixed part is about 9 us: the schedule 1.4, the first data
