@@ -278,3 +278,48 @@ def test_repeats_bit_for_bit():
     for o in outs[1:]:
         assert torch.equal(o, outs[0])
     assert_clean_status()
+
+
+def test_pools_past_32_bit_offsets():
+    """Blocks at both ends of a 4-bit pool of 5 GB and bf16 pools of 9.5 GB each: write,
+    decode, copy, expansion, and decode and prefill over the expanded blocks."""
+    rng = np.random.default_rng(74)
+    hq, hkv, bs, n = 32, 8, 16, 700
+    nb = 5 * 2 ** 30 // (bs * hkv * 72)
+    cache = torch.zeros(tvl.kv4_cache_shape(nb, hkv, bs), dtype=torch.uint8, device=DEV)
+    kc, vc = (torch.empty(nb, bs, hkv, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    ids = np.concatenate([nb - 1 - np.arange(0, 40, 2), [0, 1], nb // 2 + np.arange(22)]).astype(np.int32)
+    pos = np.arange(n)
+    k, v = (C.bf16(_bf(rng, (n, hkv, 64)), DEV) for _ in range(2))
+    q = _bf(rng, (n, hq, 64), 1.5)
+    tables, ln = _cuda(ids[None]), _cuda(np.array([n], np.int32))
+    tvl.kv4_write(k, v, cache, _cuda((ids[pos // bs].astype(np.int64) * bs + pos % bs).astype(np.int32)))
+    small = cache[_cuda(ids).long()].cpu().numpy()
+    here = np.arange(len(ids), dtype=np.int32)[None]
+    codes, s, z = C.unpack(small)
+    c0, s0, z0 = C.quantise(C.f64(v))
+    assert np.array_equal(codes[1][pos // bs, pos % bs], c0) and np.array_equal(z[1][pos // bs, pos % bs], z0)
+
+    def check_decode(window, call, **ref):
+        out = torch.full((1, hq, 64), float("nan"), device=DEV)
+        call(out, C.bf16(q[-1:], DEV))
+        want, tol = C.decode_ref(q[-1:], here, [n], 0.125, window, 0, **ref)
+        assert (np.abs(C.f64(out) - want) <= tol).all()
+
+    check_decode(0, lambda o, x: tvl.kv4_attention_decode(o, x, cache, tables, ln, 0.125), cache=small)
+    tvl.kv4_copy_blocks(cache, _cuda(ids[:2]), _cuda(np.array([nb - 2, 7], np.int32)))
+    assert torch.equal(cache[nb - 2], cache[int(ids[0])]) and torch.equal(cache[7], cache[int(ids[1])])
+    tvl.kv4_expand_blocks(kc, vc, cache, _cuda(ids), _cuda(ids))
+    big = C.f64(kc[_cuda(ids).long()]), C.f64(vc[_cuda(ids).long()])
+    val = C.values(small)
+    seen = (np.arange(len(ids))[:, None] * bs + np.arange(bs))[..., None, None] < n
+    for got, want in zip(big, val):
+        assert (np.where(seen, np.abs(got - want), 0) <= np.abs(want) * 2.0 ** -8 + 2.0 ** -20).all()
+    big = [np.where(seen, x, 0) for x in big]
+    check_decode(100, lambda o, x: tvl.paged_attention_window_decode(o, x, kc, vc, tables, ln, 0.125, 100), kv=big)
+    out = torch.empty(300, hq, 64, dtype=torch.bfloat16, device=DEV)
+    tvl.paged_attention_window_prefill(out, C.bf16(q[-300:], DEV), _cuda(np.array([0, 300], np.int32)), kc, vc, tables,
+                                       ln, 0.125, 300, 200, sinks=4)
+    want, tol = _ref(q[-300:], *big, here, [n], [300], 0.125, 200, 4)
+    assert (np.abs(C.f64(out) - want) <= tol).all()
+    assert_clean_status()
