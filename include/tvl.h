@@ -297,8 +297,9 @@ tvl_status tvl_copy_blocks(void* k_cache, void* v_cache, const int32_t* src,
  * bf16, code = min(15, rint((x - z) / s)) (ties to even; s = 0 gives code 0).
  * The two differences are taken in fp32 (exact unless the magnitudes are some
  * 2^16 apart) and all else exactly, so every value is kept within s / 2 + 2^-19
- * s.  A row that is not finite, or whose range is not, stands for NaN.  Layout: uint8 [NB, bs / 16, Hkv, 1152]; the
- * 1152 bytes of 16 tokens of a head are K codes [16][32], V codes [16][32]
+ * s.  A row that is not finite, or whose range is not, stands for NaN.
+ * Layout: uint8 [NB, bs / 16, Hkv, 1152]; the 1152 bytes of 16 tokens of a
+ * head are K codes [16][32], V codes [16][32]
  * (dimension d in byte d / 2, even d in the low half), K (s, z) [16][2] and V
  * (s, z) [16][2] in bf16.  72 bytes a token and KV head, 3.56 times fewer than
  * in bf16.  Slots, block tables and the allocator are those of the bf16 cache.
@@ -327,8 +328,8 @@ tvl_status tvl_kv4_write(void* q, const void* k_new, const void* v_new, void* ca
 /*
  * Expands blocks of the 4-bit cache to bf16: for i in [0, n), block dst[i] of
  * k_cache and v_cache (bf16 [out_blocks, bs, Hkv, D]) becomes s * code + z of
- * block src[i], rounded to fp32 and then to bf16.  This is how a prefill attends to a prefix held
- * in 4 bits: expand the prefix's blocks, then call a prefill over the bf16
+ * block src[i], rounded to fp32 and then to bf16.  This is how a prefill
+ * attends to a prefix held in 4 bits: expand the prefix's blocks, then call a prefill over the bf16
  * blocks.  Destinations must be distinct; ids out of range are skipped and
  * set TVL_DEV_BAD_BLOCK_ID.
  */
@@ -381,8 +382,8 @@ tvl_status tvl_kv4_attention_decode(float* out, const void* q, const void* cache
 
 /*
  * Decode attention with a window over the bf16 caches: the same call, with the
- * same limits, on the layout of tvl_paged_attention_decode.  P is carried in three bf16 parts
- * (24 bits).  Slots of a read block that are not visible may hold anything, NaN
+ * same limits, on the layout of tvl_paged_attention_decode.  P is carried in
+ * three bf16 parts (24 bits).  Slots of a read block that are not visible may hold anything, NaN
  * included.
  */
 tvl_status tvl_paged_attention_window_decode(
