@@ -88,6 +88,8 @@ typedef enum {
                                         a V value with |v| > 65504 (beyond the
                                         fp16 range its P.V uses) or non-finite
                                         inputs                                  */
+#define TVL_DEV_OUT_OF_BLOCKS   0x40 /* step tables: the free blocks cannot cover
+                                        the step                                */
 
 /*
  * Paged KV write [tiny-vllm README, curriculum "Paged KV cache" and "Why KV
@@ -133,6 +135,72 @@ tvl_status tvl_rope_paged_kv_write(void* q, const void* k_new, const void* v_new
                                    int num_q_heads, int num_kv_heads,
                                    int head_dim, int block_size, int num_blocks,
                                    float rope_theta, void* stream);
+
+/*
+ * Rotary positions with several axes: as tvl_rope_paged_kv_write, with
+ * positions of A axes (time, height and width of image and video tokens; text
+ * tokens have the same position on every axis).  Pair i is turned by the angle
+ *   a = positions[axis(i)][t] * rope_theta^(-2i/D),
+ * where the axes share the D / 2 pairs out by `sections` (host, [A], positive,
+ * sum D / 2): in order (the first sections[0] pairs belong to axis 0, the next
+ * sections[1] to axis 1, ...), or, interleaved != 0, in turn: axis(i) = i % A
+ * where i < A * sections[i % A], else 0 (which must give axis 0 sections[0]
+ * pairs: A * (sections[a] - 1) + a < D / 2 for a > 0).
+ *   q : bf16 [T, Hq, D] or NULL (rotated in place); k_new, v_new : bf16 [T, Hkv, D]
+ *   positions : int32 [A, T], any value (device); A from 1 to 4
+ * Each result is within one bf16 ulp of the double-precision definition plus
+ * 2^-20 * (|x_i| + |x_{i+D/2}|).  Slots as in tvl_paged_kv_write.  Supported:
+ * D == 64, Hkv <= 262140, Hq <= 524280.
+ */
+tvl_status tvl_rope_axes_paged_kv_write(void* q, const void* k_new, const void* v_new,
+                                        void* k_cache, void* v_cache, const int32_t* slot_mapping,
+                                        const int32_t* positions, const int* sections, int num_axes,
+                                        int interleaved, int num_tokens, int num_q_heads,
+                                        int num_kv_heads, int head_dim, int block_size,
+                                        int num_blocks, float rope_theta, void* stream);
+
+/*
+ * The tables of an engine step, made on the GPU from request lengths [nano-vLLM
+ * guide ch. 4 "PagedAttention" (the block allocator), ch. 5 "The Scheduler"]: the
+ * device-side counterpart of tvl_allocator_append / _build_tables /
+ * _free_sequence for caches whose blocks are not shared, so that a step (or a
+ * captured loop of steps) needs no copy from the host.  Row s of the batch keeps
+ * its place in block_tables while it lives.
+ *   cached_lens : int32 [S], tokens in the cache before the step
+ *   new_lens    : int32 [S], tokens the step appends (0: none); < 0: the row is
+ *                 done -- it gives its blocks back and ends with length 0
+ *   free_blocks : int32 [NB], a stack; the first *free_count entries are free
+ * In row order, done rows push their ceil(cached / bs) blocks onto the stack (in
+ * table order).  Then the step's k-th new block (rows in order, each row's in
+ * order of position) is the k-th from the top of the stack; it becomes the next
+ * entry of its row of block_tables.  No other entry is written; entries that are
+ * popped stay in free_blocks above the new count.
+ *   block_tables    : int32 [S, MB], in place;  free_blocks : in place
+ *   free_count_out  : int32 [1], may be free_count
+ *   context_lens    : int32 [S], lengths after the step; may be cached_lens
+ *   query_start_loc : int32 [S + 1], first packed token of each row, and their number
+ *   slot_mapping    : int32 [max_tokens], the tokens' cache slots in packed order
+ *   positions       : int32 [max_tokens], their positions, or NULL
+ * Places behind the last token get slot -1 and position 0 (the writes skip them).
+ * Otherwise the arrays must not overlap.  All-or-nothing: a step with a length
+ * that is negative or past MB * bs (TVL_DEV_BAD_CONTEXT_LEN), more than
+ * max_tokens tokens (TVL_DEV_BAD_QUERY_LEN), a count outside [0, NB] or more
+ * blocks given back than the stack has room for (TVL_DEV_BAD_BLOCK_ID), or too
+ * few free blocks (TVL_DEV_OUT_OF_BLOCKS) leaves tables, stack and count as they
+ * were, gives context_lens = cached_lens, and starts of 0 and slots of -1 as for
+ * a step without tokens.  A block id outside [0, NB), in the stack or in the table
+ * entry of a partly filled block, is reported (TVL_DEV_BAD_BLOCK_ID) and its
+ * tokens get slot -1.
+ * Any block_size > 0; NB * bs and MB * bs < 2^31.  One or two launches; no
+ * workspace; results do not vary.
+ */
+tvl_status tvl_build_step_tables(int32_t* block_tables, int32_t* free_blocks,
+                                 int32_t* free_count_out, int32_t* context_lens,
+                                 int32_t* query_start_loc, int32_t* slot_mapping,
+                                 int32_t* positions, const int32_t* free_count,
+                                 const int32_t* cached_lens, const int32_t* new_lens, int num_seqs,
+                                 int max_tokens, int block_size, int num_blocks,
+                                 int max_blocks_per_seq, void* stream);
 
 /*
  * Workspace needed by tvl_paged_attention_decode for these sizes, written to
@@ -324,6 +392,14 @@ tvl_status tvl_kv4_write(void* q, const void* k_new, const void* v_new, void* ca
                          const int32_t* slot_mapping, const int32_t* positions, int num_tokens,
                          int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                          int num_blocks, float rope_theta, void* stream);
+
+/* tvl_kv4_write with positions of several axes (int32 [A, T], not NULL), which
+ * share the pairs out as in tvl_rope_axes_paged_kv_write. */
+tvl_status tvl_kv4_axes_write(void* q, const void* k_new, const void* v_new, void* cache,
+                              const int32_t* slot_mapping, const int32_t* positions,
+                              const int* sections, int num_axes, int interleaved, int num_tokens,
+                              int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                              int num_blocks, float rope_theta, void* stream);
 
 /*
  * Expands blocks of the 4-bit cache to bf16: for i in [0, n), block dst[i] of

@@ -10,12 +10,13 @@ Functions (same names as the C entry points, without the ``tvl_`` prefix):
   paged_kv_write, paged_attention_decode, paged_attention_decode_workspace_size,
   paged_decode_step, paged_attention_prefill, rope_paged_kv_write,
   copy_blocks, get_device_status, version; on the 4-bit cache kv4_write,
-  kv4_expand_blocks, kv4_copy_blocks, kv4_attention_decode; with a window and
-  sinks paged_attention_window_decode, window_decode_workspace_size,
+  kv4_expand_blocks, kv4_copy_blocks, kv4_attention_decode; rotary positions with
+  several axes rope_axes_paged_kv_write, kv4_axes_write; a step's tables on the
+  GPU build_step_tables; with a window and sinks paged_attention_window_decode, window_decode_workspace_size,
   paged_attention_window_prefill.
 
-Bound calls (``bind_`` before the name of a write, decode, prefill or
-``kv4_expand_blocks`` call) check their
+Bound calls (``bind_`` before the name of a write, decode, prefill,
+``kv4_expand_blocks`` or ``build_step_tables`` call) check their
 tensors once and return a callable that re-issues the same C call -- same
 pointers, sizes and stream -- with one ctypes call and no further checks.
 They are for loops that call the library with the same buffers every step
@@ -43,7 +44,9 @@ __all__ = [
     "kv4_attention_decode", "paged_attention_window_decode", "window_decode_workspace_size",
     "bind_kv4_write", "bind_kv4_expand_blocks", "bind_kv4_attention_decode",
     "bind_paged_attention_window_decode", "paged_attention_window_prefill",
-    "bind_paged_attention_window_prefill",
+    "bind_paged_attention_window_prefill", "DEV_OUT_OF_BLOCKS",
+    "rope_axes_paged_kv_write", "bind_rope_axes_paged_kv_write", "kv4_axes_write",
+    "bind_kv4_axes_write", "build_step_tables", "bind_build_step_tables",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -53,7 +56,7 @@ _LIB_PATH = os.path.join(_PKG, "libtvl.so")
  ERR_OUT_OF_BLOCKS) = range(7)
 DEV_BAD_SLOT, DEV_BAD_BLOCK_ID, DEV_BAD_CONTEXT_LEN, DEV_BAD_QUERY_LEN, DEV_TIMEOUT = (
     0x1, 0x2, 0x4, 0x8, 0x10)
-DEV_NONFINITE = 0x20
+DEV_NONFINITE, DEV_OUT_OF_BLOCKS = 0x20, 0x40
 
 _lock = threading.Lock()
 _lib = None
@@ -118,12 +121,18 @@ def _load():
             lib.tvl_paged_attention_window_prefill.argtypes = [
                 P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, I, P]
             lib.tvl_paged_attention_window_prefill.restype = I
-            for name in ("tvl_kv4_write", "tvl_kv4_expand_blocks", "tvl_kv4_copy_blocks",
+            IP = ctypes.POINTER(ctypes.c_int)
+            lib.tvl_rope_axes_paged_kv_write.argtypes = [
+                P, P, P, P, P, P, P, IP, I, I, I, I, I, I, I, I, F, P]
+            lib.tvl_kv4_axes_write.argtypes = [P, P, P, P, P, P, IP, I, I, I, I, I, I, I, I, F, P]
+            lib.tvl_build_step_tables.argtypes = [P] * 10 + [I] * 5 + [P]
+            for name in ("tvl_rope_axes_paged_kv_write", "tvl_kv4_axes_write",
+                         "tvl_build_step_tables", "tvl_kv4_write", "tvl_kv4_expand_blocks",
+                         "tvl_kv4_copy_blocks",
                          "tvl_window_decode_workspace_size", "tvl_kv4_attention_decode",
                          "tvl_paged_attention_window_decode"):
                 getattr(lib, name).restype = I
             I32P = ctypes.POINTER(ctypes.c_int32)
-            IP = ctypes.POINTER(ctypes.c_int)
             lib.tvl_allocator_create.argtypes = [I, I, ctypes.POINTER(P)]
             lib.tvl_allocator_destroy.argtypes = [P]
             lib.tvl_allocator_destroy.restype = None
@@ -274,6 +283,119 @@ def rope_paged_kv_write(q, k_new, v_new, k_cache, v_cache, slot_mapping, positio
                                                _ptr(v_cache), _ptr(slot_mapping),
                                                _ptr(positions), t, hq, hkv, d, bs, nb,
                                                float(rope_theta), _stream(stream)))
+
+
+def _need_axes(sections, positions, t, dev):
+    """Checks positions [A, T] and returns the C arguments of the axes' sections."""
+    sections = [int(x) for x in sections]
+    if not 1 <= len(sections) <= 4 or any(not 1 <= x <= 32 for x in sections):
+        raise ValueError(f"sections {sections}: one to four positive counts of pairs")
+    _need(positions, "positions", torch.int32, 2, dev)
+    if tuple(positions.shape) != (len(sections), t):
+        raise ValueError(f"positions must be [{len(sections)}, {t}], got {tuple(positions.shape)}")
+    return (ctypes.c_int * len(sections))(*sections), len(sections)
+
+
+def _prep_rope_axes(q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, sections,
+                    interleaved, rope_theta, stream):
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    dev = k_cache.get_device()
+    _need(v_cache, "v_cache", torch.bfloat16, 4, dev)
+    _need(k_new, "k_new", torch.bfloat16, 3, dev)
+    _need(v_new, "v_new", torch.bfloat16, 3, dev)
+    _need(slot_mapping, "slot_mapping", torch.int32, 1, dev)
+    nb, bs, hkv, d = k_cache.shape
+    t, hq = slot_mapping.shape[0], 0
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    if q is not None:
+        _need(q, "q", torch.bfloat16, 3, dev)
+        if q.shape[0] != t or q.shape[2] != d:
+            raise ValueError("q must be [T, Hq, D]")
+        hq = q.shape[1]
+    if k_new.shape != (t, hkv, d) or v_new.shape != (t, hkv, d):
+        raise ValueError(f"k_new/v_new must be [{t}, {hkv}, {d}]")
+    sec, axes = _need_axes(sections, positions, t, dev)
+    with _on_device(dev):
+        args = (_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+                _ptr(slot_mapping), _ptr(positions), sec, axes, int(bool(interleaved)), t, hq, hkv,
+                d, bs, nb, float(rope_theta), _stream(stream))
+    return (dev, _load().tvl_rope_axes_paged_kv_write, args,
+            (q, k_new, v_new, k_cache, v_cache, slot_mapping, positions))
+
+
+def rope_axes_paged_kv_write(q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, sections,
+                             interleaved=False, rope_theta=500000.0, stream=None) -> None:
+    """RoPE of q (in place; may be None) and of k_new by positions of several
+    axes (int32 [A, T]), then the paged write of the rotated K rows and the V
+    rows.  sections: how many of the D / 2 pairs each axis turns, in order or
+    (interleaved) in turn."""
+    dev, fn, args, _ = _prep_rope_axes(q, k_new, v_new, k_cache, v_cache, slot_mapping, positions,
+                                       sections, interleaved, rope_theta, stream)
+    with _on_device(dev):
+        _check(fn(*args))
+
+
+def bind_rope_axes_paged_kv_write(q, k_new, v_new, k_cache, v_cache, slot_mapping, positions,
+                                  sections, interleaved=False, rope_theta=500000.0, stream=None):
+    """rope_axes_paged_kv_write, checked once; returns a BoundCall."""
+    return BoundCall(*_prep_rope_axes(q, k_new, v_new, k_cache, v_cache, slot_mapping, positions,
+                                      sections, interleaved, rope_theta, stream))
+
+
+def _prep_step_tables(block_tables, free_blocks, context_lens, query_start_loc, slot_mapping,
+                      positions, free_count, cached_lens, new_lens, block_size, free_count_out,
+                      stream):
+    free_count_out = free_count if free_count_out is None else free_count_out
+    _need(block_tables, "block_tables", torch.int32, 2)
+    dev = block_tables.get_device()
+    s, mb = block_tables.shape
+    for name, t, n in (("free_blocks", free_blocks, None), ("context_lens", context_lens, s),
+                       ("query_start_loc", query_start_loc, s + 1),
+                       ("slot_mapping", slot_mapping, None), ("free_count", free_count, 1),
+                       ("free_count_out", free_count_out, 1), ("cached_lens", cached_lens, s),
+                       ("new_lens", new_lens, s)):
+        _need(t, name, torch.int32, 1, dev)
+        if n is not None and t.shape[0] != n:
+            raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
+    if positions is not None:
+        _need(positions, "positions", torch.int32, 1, dev)
+        if positions.shape != slot_mapping.shape:
+            raise ValueError("positions must have slot_mapping's shape")
+    with _on_device(dev):
+        args = tuple(_ptr(t) for t in (block_tables, free_blocks, free_count_out, context_lens,
+                                       query_start_loc, slot_mapping, positions, free_count,
+                                       cached_lens, new_lens))
+        args += (s, slot_mapping.shape[0], int(block_size), free_blocks.shape[0], mb,
+                 _stream(stream))
+    return (dev, _load().tvl_build_step_tables, args,
+            (block_tables, free_blocks, free_count_out, context_lens, query_start_loc,
+             slot_mapping, positions, free_count, cached_lens, new_lens))
+
+
+def build_step_tables(block_tables, free_blocks, context_lens, query_start_loc, slot_mapping,
+                      positions, free_count, cached_lens, new_lens, block_size,
+                      free_count_out=None, stream=None) -> None:
+    """One engine step's tables on the GPU (all int32): rows with new_lens < 0
+    give their blocks back to the stack free_blocks[:free_count], the others get
+    blocks for new_lens tokens behind their cached_lens; block_tables [S, MB],
+    free_blocks and the count (free_count_out; None: in place) are updated, and
+    context_lens [S] (may be cached_lens), query_start_loc [S + 1], slot_mapping
+    and positions (may be None), padded with -1 and 0, are written."""
+    dev, fn, args, _ = _prep_step_tables(block_tables, free_blocks, context_lens, query_start_loc,
+                                         slot_mapping, positions, free_count, cached_lens,
+                                         new_lens, block_size, free_count_out, stream)
+    with _on_device(dev):
+        _check(fn(*args))
+
+
+def bind_build_step_tables(block_tables, free_blocks, context_lens, query_start_loc, slot_mapping,
+                           positions, free_count, cached_lens, new_lens, block_size,
+                           free_count_out=None, stream=None):
+    """build_step_tables, checked once; returns a BoundCall."""
+    return BoundCall(*_prep_step_tables(block_tables, free_blocks, context_lens, query_start_loc,
+                                        slot_mapping, positions, free_count, cached_lens,
+                                        new_lens, block_size, free_count_out, stream))
 
 
 def paged_attention_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
@@ -506,6 +628,46 @@ def bind_kv4_write(k_new, v_new, cache, slot_mapping, q=None, positions=None,
     """kv4_write, checked once; returns a BoundCall."""
     return BoundCall(*_prep_kv4_write(k_new, v_new, cache, slot_mapping, q, positions,
                                       rope_theta, stream))
+
+
+def _prep_kv4_axes(k_new, v_new, cache, slot_mapping, q, positions, sections, interleaved,
+                   rope_theta, stream):
+    nb, bs, hkv = _need_kv4(cache)
+    dev = cache.get_device()
+    _need(k_new, "k_new", torch.bfloat16, 3, dev)
+    _need(v_new, "v_new", torch.bfloat16, 3, dev)
+    _need(slot_mapping, "slot_mapping", torch.int32, 1, dev)
+    t, d, hq = slot_mapping.shape[0], k_new.shape[2], 0
+    if k_new.shape != (t, hkv, d) or v_new.shape != k_new.shape:
+        raise ValueError(f"k_new/v_new must be [{t}, {hkv}, D]")
+    if q is not None:
+        _need(q, "q", torch.bfloat16, 3, dev)
+        if q.shape[0] != t or q.shape[2] != d:
+            raise ValueError("q must be [T, Hq, D]")
+        hq = q.shape[1]
+    sec, axes = _need_axes(sections, positions, t, dev)
+    with _on_device(dev):
+        args = (_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(cache), _ptr(slot_mapping),
+                _ptr(positions), sec, axes, int(bool(interleaved)), t, hq, hkv, d, bs, nb,
+                float(rope_theta), _stream(stream))
+    return dev, _load().tvl_kv4_axes_write, args, (q, k_new, v_new, cache, slot_mapping, positions)
+
+
+def kv4_axes_write(k_new, v_new, cache, slot_mapping, q, positions, sections, interleaved=False,
+                   rope_theta=500000.0, stream=None) -> None:
+    """kv4_write with positions of several axes (int32 [A, T]); sections as in
+    rope_axes_paged_kv_write, q may be None."""
+    dev, fn, args, _ = _prep_kv4_axes(k_new, v_new, cache, slot_mapping, q, positions, sections,
+                                      interleaved, rope_theta, stream)
+    with _on_device(dev):
+        _check(fn(*args))
+
+
+def bind_kv4_axes_write(k_new, v_new, cache, slot_mapping, q, positions, sections,
+                        interleaved=False, rope_theta=500000.0, stream=None):
+    """kv4_axes_write, checked once; returns a BoundCall."""
+    return BoundCall(*_prep_kv4_axes(k_new, v_new, cache, slot_mapping, q, positions, sections,
+                                     interleaved, rope_theta, stream))
 
 
 def _prep_kv4_expand(k_cache, v_cache, cache, src, dst, stream):

@@ -484,6 +484,159 @@ tvl_status tvl_paged_attention_window_prefill(
                       stream);
 }
 
+// ---------------------------------------- rotary positions with several axes
+
+namespace {
+
+// The axis of each of the 32 pairs, two bits a pair.
+tvl_status axes_of_pairs(const int* sections, int num_axes, int interleaved,
+                         unsigned long long* axis_of) {
+  constexpr int kPairs = 32;
+  if (!sections) return fail(TVL_ERR_INVALID_ARG, "null sections");
+  if (num_axes < 1 || num_axes > 4)
+    return fail(TVL_ERR_UNSUPPORTED, "%d axes (supported: 1 to 4)", num_axes);
+  int sum = 0;
+  for (int a = 0; a < num_axes; ++a) {
+    if (sections[a] < 1 || sections[a] > kPairs)
+      return fail(TVL_ERR_INVALID_ARG, "sections[%d] = %d (1 to %d)", a, sections[a], kPairs);
+    sum += sections[a];
+    if (interleaved && a > 0 && num_axes * (sections[a] - 1) + a >= kPairs)
+      return fail(TVL_ERR_INVALID_ARG, "sections[%d] = %d: too many pairs to interleave", a,
+                  sections[a]);
+  }
+  if (sum != kPairs) return fail(TVL_ERR_INVALID_ARG, "sections sum to %d, not %d", sum, kPairs);
+  unsigned long long out = 0;
+  int axis = 0, end = sections[0];
+  for (int i = 0; i < kPairs; ++i) {
+    if (interleaved) {
+      axis = i % num_axes;
+      if (i >= num_axes * sections[axis]) axis = 0;
+    } else if (i == end) {
+      end += sections[++axis];
+    }
+    out |= static_cast<unsigned long long>(axis) << (2 * i);
+  }
+  *axis_of = out;
+  return TVL_OK;
+}
+
+}  // namespace
+
+tvl_status tvl_rope_axes_paged_kv_write(void* q, const void* k_new, const void* v_new,
+                                        void* k_cache, void* v_cache, const int32_t* slot_mapping,
+                                        const int32_t* positions, const int* sections, int num_axes,
+                                        int interleaved, int num_tokens, int num_q_heads,
+                                        int num_kv_heads, int head_dim, int block_size,
+                                        int num_blocks, float rope_theta, void* stream) {
+  if (num_tokens < 0) return fail(TVL_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+  if (num_kv_heads <= 0 || block_size <= 0 || num_blocks <= 0)
+    return fail(TVL_ERR_INVALID_ARG, "num_kv_heads, block_size and num_blocks must be positive");
+  if (head_dim != 64) return fail(TVL_ERR_UNSUPPORTED, "head_dim %d (supported: 64)", head_dim);
+  if (q && num_q_heads <= 0) return fail(TVL_ERR_INVALID_ARG, "num_q_heads %d <= 0", num_q_heads);
+  if (num_kv_heads > 262140 || num_q_heads > 524280)   // 16-row parts of both: a grid's 65535
+    return fail(TVL_ERR_UNSUPPORTED, "num_kv_heads %d > 262140 or num_q_heads %d > 524280",
+                num_kv_heads, num_q_heads);
+  if (!(rope_theta > 1.0f) || !std::isfinite(rope_theta))
+    return fail(TVL_ERR_INVALID_ARG, "rope_theta must be finite and > 1");
+  unsigned long long axis_of = 0;
+  tvl_status st = axes_of_pairs(sections, num_axes, interleaved, &axis_of);
+  if (st != TVL_OK) return st;
+  if (!k_cache || !v_cache) return fail(TVL_ERR_INVALID_ARG, "null cache pointer");
+  if (!aligned16(k_cache) || !aligned16(v_cache))
+    return fail(TVL_ERR_INVALID_ARG, "cache pointers must be 16-byte aligned");
+  if (num_tokens == 0) return TVL_OK;
+  if (!k_new || !v_new || !slot_mapping || !positions)
+    return fail(TVL_ERR_INVALID_ARG, "null input pointer");
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(q))
+    return fail(TVL_ERR_INVALID_ARG, "q, k_new and v_new must be 16-byte aligned");
+  uint32_t* word = nullptr;
+  st = status_word(&word);
+  if (st != TVL_OK) return st;
+  tvl::RopeAxesWriteArgs a;
+  a.q = q;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.num_slots = static_cast<long long>(num_blocks) * block_size;
+  a.rope_theta = rope_theta;
+  a.axis_of = axis_of;
+  a.status = word;
+  cudaError_t e = tvl::launch_rope_axes_write(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope_axes_paged_kv_write launch");
+  return TVL_OK;
+}
+
+// ------------------------------------------------- an engine step's tables
+
+tvl_status tvl_build_step_tables(int32_t* block_tables, int32_t* free_blocks,
+                                 int32_t* free_count_out, int32_t* context_lens,
+                                 int32_t* query_start_loc, int32_t* slot_mapping,
+                                 int32_t* positions, const int32_t* free_count,
+                                 const int32_t* cached_lens, const int32_t* new_lens, int num_seqs,
+                                 int max_tokens, int block_size, int num_blocks,
+                                 int max_blocks_per_seq, void* stream) {
+  if (num_seqs < 0 || max_tokens < 0)
+    return fail(TVL_ERR_INVALID_ARG, "num_seqs %d or max_tokens %d < 0", num_seqs, max_tokens);
+  if (block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0)
+    return fail(TVL_ERR_INVALID_ARG,
+                "block_size, num_blocks and max_blocks_per_seq must be positive");
+  if (static_cast<long long>(num_blocks) * block_size > INT_MAX ||
+      static_cast<long long>(max_blocks_per_seq) * block_size > INT_MAX)
+    return fail(TVL_ERR_UNSUPPORTED, "more than 2^31 - 1 token slots");
+  if (!free_blocks || !free_count_out || !query_start_loc || !free_count)
+    return fail(TVL_ERR_INVALID_ARG, "null pointer argument");
+  if (num_seqs > 0 && (!block_tables || !context_lens || !cached_lens || !new_lens))
+    return fail(TVL_ERR_INVALID_ARG, "null pointer argument");
+  if (max_tokens > 0 && !slot_mapping) return fail(TVL_ERR_INVALID_ARG, "null slot_mapping");
+  // arrays [first, last) that must not overlap: what is written against everything
+  const struct { const int32_t* p; long long n; } arr[] = {
+      {block_tables, static_cast<long long>(num_seqs) * max_blocks_per_seq}, {free_blocks, num_blocks},
+      {free_count_out, 1}, {context_lens, num_seqs}, {query_start_loc, num_seqs + 1LL},
+      {slot_mapping, max_tokens}, {positions, positions ? max_tokens : 0},
+      {free_count, 1}, {cached_lens, num_seqs}, {new_lens, num_seqs}};
+  for (int i = 0; i < 7; ++i)
+    for (int j = i + 1; j < 10; ++j) {
+      if ((i == 2 && j == 7) || (i == 3 && j == 8)) {   // in place: the same array or another
+        if (arr[i].p == arr[j].p) continue;
+      }
+      const uintptr_t x = reinterpret_cast<uintptr_t>(arr[i].p), y = reinterpret_cast<uintptr_t>(arr[j].p);
+      if (arr[i].n > 0 && arr[j].n > 0 && x < y + 4 * arr[j].n && y < x + 4 * arr[i].n)
+        return fail(TVL_ERR_INVALID_ARG, "arrays overlap");
+    }
+  for (const auto& r : arr)
+    if ((reinterpret_cast<uintptr_t>(r.p) & 3u) != 0)
+      return fail(TVL_ERR_INVALID_ARG, "pointers must be 4-byte aligned");
+  uint32_t* word = nullptr;
+  tvl_status st = status_word(&word);
+  if (st != TVL_OK) return st;
+  tvl::StepTablesArgs a;
+  a.block_tables = block_tables;
+  a.free_blocks = free_blocks;
+  a.free_count_out = free_count_out;
+  a.context_lens = context_lens;
+  a.query_start_loc = query_start_loc;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.free_count = free_count;
+  a.cached_lens = cached_lens;
+  a.new_lens = new_lens;
+  a.num_seqs = num_seqs;
+  a.max_tokens = max_tokens;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.status = word;
+  cudaError_t e = tvl::launch_step_tables(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "step tables launch");
+  return TVL_OK;
+}
+
 // ------------------------------------------------------------ 4-bit cache
 
 namespace {
@@ -500,12 +653,11 @@ tvl_status kv4_sizes(int num_kv_heads, int head_dim, int block_size, int num_blo
   return TVL_OK;
 }
 
-}  // namespace
-
-tvl_status tvl_kv4_write(void* q, const void* k_new, const void* v_new, void* cache,
-                         const int32_t* slot_mapping, const int32_t* positions, int num_tokens,
-                         int num_q_heads, int num_kv_heads, int head_dim, int block_size,
-                         int num_blocks, float rope_theta, void* stream) {
+tvl_status kv4_write_impl(void* q, const void* k_new, const void* v_new, void* cache,
+                          const int32_t* slot_mapping, const int32_t* positions,
+                          unsigned long long axis_of, int num_tokens, int num_q_heads,
+                          int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                          float rope_theta, void* stream) {
   if (num_tokens < 0) return fail(TVL_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
   if (num_q_heads < 0) return fail(TVL_ERR_INVALID_ARG, "num_q_heads %d < 0", num_q_heads);
   if (num_q_heads > 524280) return fail(TVL_ERR_UNSUPPORTED, "num_q_heads %d > 524280", num_q_heads);
@@ -537,10 +689,36 @@ tvl_status tvl_kv4_write(void* q, const void* k_new, const void* v_new, void* ca
   a.block_size = block_size;
   a.num_slots = static_cast<long long>(num_blocks) * block_size;
   a.rope_theta = rope_theta;
+  a.axis_of = axis_of;
   a.status = word;
   cudaError_t e = tvl::launch_kv4_write(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv4_write launch");
   return TVL_OK;
+}
+
+}  // namespace
+
+tvl_status tvl_kv4_write(void* q, const void* k_new, const void* v_new, void* cache,
+                         const int32_t* slot_mapping, const int32_t* positions, int num_tokens,
+                         int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                         int num_blocks, float rope_theta, void* stream) {
+  return kv4_write_impl(q, k_new, v_new, cache, slot_mapping, positions, 0, num_tokens, num_q_heads,
+                        num_kv_heads, head_dim, block_size, num_blocks, rope_theta, stream);
+}
+
+tvl_status tvl_kv4_axes_write(void* q, const void* k_new, const void* v_new, void* cache,
+                              const int32_t* slot_mapping, const int32_t* positions,
+                              const int* sections, int num_axes, int interleaved, int num_tokens,
+                              int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                              int num_blocks, float rope_theta, void* stream) {
+  unsigned long long axis_of = 0;
+  tvl_status st = axes_of_pairs(sections, num_axes, interleaved, &axis_of);
+  if (st != TVL_OK) return st;
+  if (num_tokens > 0 && !positions) return fail(TVL_ERR_INVALID_ARG, "null positions");
+  if (!positions) q = nullptr;   // no tokens: nothing to rotate
+  return kv4_write_impl(q, k_new, v_new, cache, slot_mapping, positions, axis_of, num_tokens,
+                        num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, rope_theta,
+                        stream);
 }
 
 tvl_status tvl_kv4_expand_blocks(void* k_cache, void* v_cache, const void* cache,

@@ -55,6 +55,23 @@ struct RopeKvWriteArgs {
 };
 cudaError_t launch_rope_kv_write(const RopeKvWriteArgs& a, cudaStream_t stream);
 
+// Rotary positions with several axes.
+struct RopeAxesWriteArgs {
+  void* q;                 // may be null
+  const void* k_new;
+  const void* v_new;
+  void* k_cache;
+  void* v_cache;
+  const int32_t* slot_mapping;
+  const int32_t* positions;     // [axes, T]
+  int num_tokens, num_q_heads, num_kv_heads;
+  long long num_slots;
+  float rope_theta;
+  unsigned long long axis_of;   // two bits a pair
+  uint32_t* status;
+};
+cudaError_t launch_rope_axes_write(const RopeAxesWriteArgs& a, cudaStream_t stream);
+
 struct CopyBlocksArgs {
   void* k_cache;
   void* v_cache;           // null: one cache only (the 4-bit cache)
@@ -140,6 +157,24 @@ struct PrefillArgs {
 };
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 
+// ------------------------------------------------- an engine step's tables
+
+struct StepTablesArgs {
+  int32_t* block_tables;       // [S, MB], in place
+  int32_t* free_blocks;        // [NB]: the stack, in place
+  int32_t* free_count_out;
+  int32_t* context_lens;       // [S], may be cached_lens
+  int32_t* query_start_loc;    // [S + 1]
+  int32_t* slot_mapping;       // [max_tokens]
+  int32_t* positions;          // [max_tokens] or null
+  const int32_t* free_count;   // may be free_count_out
+  const int32_t* cached_lens;
+  const int32_t* new_lens;     // < 0: the row is done
+  int num_seqs, max_tokens, block_size, num_blocks, max_blocks;
+  uint32_t* status;
+};
+cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream);
+
 // ------------------------------------------------------------ 4-bit cache
 
 struct Kv4WriteArgs {
@@ -148,10 +183,11 @@ struct Kv4WriteArgs {
   const void* v_new;
   void* cache;
   const int32_t* slot_mapping;
-  const int32_t* positions;   // null: no rotation
+  const int32_t* positions;   // [axes, T]; null: no rotation
   int num_tokens, num_q_heads, num_kv_heads, block_size;
   long long num_slots;
   float rope_theta;
+  unsigned long long axis_of;   // two bits a pair
   uint32_t* status;
 };
 cudaError_t launch_kv4_write(const Kv4WriteArgs& a, cudaStream_t stream);

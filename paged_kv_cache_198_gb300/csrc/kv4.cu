@@ -21,26 +21,16 @@
 // and a decode step of 64 tokens over 192.
 #include <cuda_bf16.h>
 
-#include <cmath>
-
 #include "device.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
+#include "rope.cuh"
 
 namespace tvl {
 namespace {
 
-constexpr int kD = 64;
 constexpr int kWarps = 4;              // per CTA
 constexpr int kRowsPerWarp = 16;
-constexpr unsigned kFull = 0xffffffffu;
-
-// theta^(-2i/D) / (2 pi) in units of 2^-64 turns, from a double: position times
-// this, modulo 2^64, is the angle reduced without further error, so it is off by
-// position * 2^-53 of a step, 2 10^-7 at most (position 2^31).
-struct RopeTurns {
-  unsigned long long f[kD / 2];
-};
 
 struct WriteParams {
   __nv_bfloat16* q;
@@ -48,47 +38,11 @@ struct WriteParams {
   const __nv_bfloat16* v_new;
   uint8_t* cache;
   const int32_t* slots;
-  const int32_t* positions;     // null: no rotation
+  const int32_t* positions;     // [axes, T]; null: no rotation
   int num_tokens, hq, hkv, parts_q;
   long long num_slots;
   uint32_t* status;
 };
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// A row's eight values of this lane, as four pairs.
-struct Eight {
-  float2 v[4];
-};
-__device__ __forceinline__ Eight widen(uint4 w) {
-  return {{bf16x2_to_float2(w.x), bf16x2_to_float2(w.y), bf16x2_to_float2(w.z),
-           bf16x2_to_float2(w.w)}};
-}
-__device__ __forceinline__ uint4 narrow(const Eight& x) {
-  return make_uint4(pack_bf16(x.v[0].x, x.v[0].y), pack_bf16(x.v[1].x, x.v[1].y),
-                    pack_bf16(x.v[2].x, x.v[2].y), pack_bf16(x.v[3].x, x.v[3].y));
-}
-
-// This lane's share of the rotation: dimensions 8 c .. 8 c + 7 of a row, whose
-// partners (d, d + 32) are lane c ^ 4's; sn carries the sign.
-struct Turn {
-  float2 cs[4], sn[4];
-};
-__device__ __forceinline__ uint4 rotate(uint4 w, const Turn& t) {
-  uint4 o;
-  o.x = __shfl_xor_sync(kFull, w.x, 4);
-  o.y = __shfl_xor_sync(kFull, w.y, 4);
-  o.z = __shfl_xor_sync(kFull, w.z, 4);
-  o.w = __shfl_xor_sync(kFull, w.w, 4);
-  Eight x = widen(w);
-  const Eight y = widen(o);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x.v[j] = __ffma2_rn(x.v[j], t.cs[j], __fmul2_rn(y.v[j], t.sn[j]));
-  return narrow(x);
-}
 
 // A row's (s, z) from its extremes, and the codes of this lane's eight values.
 //
@@ -165,21 +119,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   Turn turn;
   const bool rope = p.positions != nullptr && row0 - (lane >> 3) < (is_q ? p.hq : p.hkv);
   if (rope) {
-    // lane i: pair i's angle in [-1/2, 1/2) turns, then its sine and cosine
-    const unsigned long long a =
-        static_cast<unsigned long long>(static_cast<long long>(p.positions[t])) * turns.f[lane];
-    float sn, cs;
-    sincospif(__ll2float_rn(static_cast<long long>(a)) * 1.0842021724855044e-19f, &sn, &cs);  // 2^-63
-    trig[warp][lane] = make_float2(cs, sn);
-    __syncwarp();
-    const float4* tr = reinterpret_cast<const float4*>(&trig[warp][8 * (c & 3)]);
-    const float sign = c < 4 ? -1.f : 1.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 f = tr[j];
-      turn.cs[j] = make_float2(f.x, f.z);
-      turn.sn[j] = make_float2(f.y * sign, f.w * sign);
-    }
+    turn = token_turn(p.positions, p.num_tokens, t, turns, trig[warp]);
   }
   if (is_q) {
 #pragma unroll
@@ -286,19 +226,6 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-const RopeTurns& rope_turns(float theta) {
-  static thread_local float have = 0.f;
-  static thread_local RopeTurns t = {};
-  if (have != theta) {
-    for (int i = 0; i < kD / 2; ++i)
-      t.f[i] = static_cast<unsigned long long>(
-          std::llrint(std::pow(static_cast<double>(theta), -2.0 * i / kD) / 6.283185307179586476925 *
-                      4611686018427387904.0)) << 2;      // 2^62 steps a turn, then 2^64
-    have = theta;
-  }
-  return t;
-}
-
 }  // namespace
 
 cudaError_t launch_kv4_write(const Kv4WriteArgs& a, cudaStream_t stream) {
@@ -320,7 +247,7 @@ cudaError_t launch_kv4_write(const Kv4WriteArgs& a, cudaStream_t stream) {
   static const RopeTurns none = {};
   return launch_pdl(kv4_write_kernel, dim3((a.num_tokens - 1) / kWarps + 1, p.parts_q + parts_kv),
                     dim3(kWarps * 32), 0, stream, p,
-                    a.positions ? rope_turns(a.rope_theta) : none);
+                    a.positions ? rope_turns(a.rope_theta, a.axis_of) : none);
 }
 
 cudaError_t launch_kv4_expand(const Kv4ExpandArgs& a, cudaStream_t stream) {
