@@ -486,6 +486,44 @@ tvl_status tvl_paged_attention_window_prefill(
     void* stream);
 
 /*
+ * Differential attention over the bf16 caches.  Query heads 2 i and 2 i + 1 are the
+ * two maps of query pair i, KV heads 2 j and 2 j + 1 the two keys of KV pair j, and
+ * its value is the two V heads side by side, 128 wide (the layout of the caches is
+ * that of every other call); pair i reads KV pair i / G.  With
+ *   d = softmax(scale q_{2i} K_{2j}) V - lambda softmax(scale q_{2i+1} K_{2j+1}) V
+ * over the visible tokens (window and sinks as above; window == 0: all),
+ *   out = out_scale * w * d / sqrt(mean d^2 + norm_eps),  or out_scale * d
+ * without w.  (A model's lambda = exp(l1 . l2) - exp(l3 . l4) + lambda_init is
+ * worked out once when it is loaded; its output factor 1 - lambda_init is out_scale.)
+ * Softmax sums, the difference and the norm are fp32; the output is rounded once.
+ */
+
+/* Workspace of the call below, for the current device (its SM count), whatever the
+ * batch; shared as that of tvl_window_decode_workspace_size. */
+tvl_status tvl_diff_decode_workspace_size(int num_q_heads, int num_kv_heads, int head_dim,
+                                          size_t* bytes);
+
+/*
+ * One query token a sequence, as tvl_paged_attention_window_decode.  P is carried in
+ * two bf16 parts (16 bits).
+ *   out : bf16 [S, Hq / 2, 128]; q : bf16 [S, Hq, D]
+ *   lambda : float32 [Hq / 2], or [S, Hq / 2] with lambda_per_token != 0 (device)
+ *   norm_weight : bf16 [128] (device) or NULL;  norm_eps >= 0
+ * context_lens[s] == 0 gives a zero row, and so does d == 0.  One or two launches; no
+ * allocation; results do not vary from call to call.
+ * Supported: D == 64, Hq and Hkv even, G from 1 to 8, bs in {16, 32, 64, 128}, cached V
+ * below 2^60 in magnitude (the norm's squares), NB * bs < 2^31, Hkv <= 65534, Hq <=
+ * 262140.
+ */
+tvl_status tvl_diff_attention_decode(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens, const float* lambda,
+    int lambda_per_token, const void* norm_weight, float norm_eps, float out_scale, int num_seqs,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+    int max_blocks_per_seq, float scale, int window, int sinks, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/*
  * Host block allocator: the CPU control plane that hands out the physical
  * blocks and slots the kernels read [nano-vLLM guide ch. 2 (control plane vs
  * data plane), ch. 4 "PagedAttention" (block allocator, no fragmentation

@@ -12,7 +12,8 @@ Functions (same names as the C entry points, without the ``tvl_`` prefix):
   copy_blocks, get_device_status, version; on the 4-bit cache kv4_write,
   kv4_expand_blocks, kv4_copy_blocks, kv4_attention_decode; rotary positions with
   several axes rope_axes_paged_kv_write, kv4_axes_write; a step's tables on the
-  GPU build_step_tables; with a window and sinks paged_attention_window_decode, window_decode_workspace_size,
+  GPU build_step_tables; differential attention diff_attention_decode,
+  diff_decode_workspace_size; with a window and sinks paged_attention_window_decode, window_decode_workspace_size,
   paged_attention_window_prefill.
 
 Bound calls (``bind_`` before the name of a write, decode, prefill,
@@ -47,6 +48,7 @@ __all__ = [
     "bind_paged_attention_window_prefill", "DEV_OUT_OF_BLOCKS",
     "rope_axes_paged_kv_write", "bind_rope_axes_paged_kv_write", "kv4_axes_write",
     "bind_kv4_axes_write", "build_step_tables", "bind_build_step_tables",
+    "diff_attention_decode", "bind_diff_attention_decode", "diff_decode_workspace_size",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -126,7 +128,11 @@ def _load():
                 P, P, P, P, P, P, P, IP, I, I, I, I, I, I, I, I, F, P]
             lib.tvl_kv4_axes_write.argtypes = [P, P, P, P, P, P, IP, I, I, I, I, I, I, I, I, F, P]
             lib.tvl_build_step_tables.argtypes = [P] * 10 + [I] * 5 + [P]
-            for name in ("tvl_rope_axes_paged_kv_write", "tvl_kv4_axes_write",
+            lib.tvl_diff_decode_workspace_size.argtypes = [I, I, I, ctypes.POINTER(SZ)]
+            lib.tvl_diff_attention_decode.argtypes = [
+                P, P, P, P, P, P, P, I, P, F, F, I, I, I, I, I, I, I, F, I, I, P, SZ, P]
+            for name in ("tvl_diff_decode_workspace_size", "tvl_diff_attention_decode",
+                         "tvl_rope_axes_paged_kv_write", "tvl_kv4_axes_write",
                          "tvl_build_step_tables", "tvl_kv4_write", "tvl_kv4_expand_blocks",
                          "tvl_kv4_copy_blocks",
                          "tvl_window_decode_workspace_size", "tvl_kv4_attention_decode",
@@ -838,6 +844,93 @@ def bind_paged_attention_window_prefill(out, q, query_start_loc, k_cache, v_cach
     """paged_attention_window_prefill, checked once; returns a BoundCall."""
     return BoundCall(*_prep_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables,
                                     context_lens, scale, max_q_len, stream, int(window), sinks))
+
+
+def diff_decode_workspace_size(num_q_heads, num_kv_heads, head_dim=64) -> int:
+    """Bytes of workspace the differential decode needs on the current device
+    (tvl_diff_decode_workspace_size); remembered per device and heads."""
+    key = (torch.cuda.current_device() if torch.cuda.is_available() else -1, "diff",
+           num_q_heads, num_kv_heads, head_dim)
+    hit = _ws_sizes.get(key)
+    if hit is not None:
+        return hit
+    out = ctypes.c_size_t(0)
+    _check(_load().tvl_diff_decode_workspace_size(num_q_heads, num_kv_heads, head_dim,
+                                                  ctypes.byref(out)))
+    _ws_sizes[key] = int(out.value)
+    return int(out.value)
+
+
+def _need_diff(out, q, k_cache, v_cache, block_tables, context_lens, lam, norm_weight):
+    """Checks shared by the differential decode and prefill."""
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    dev = k_cache.get_device()
+    _need(v_cache, "v_cache", torch.bfloat16, 4, dev)
+    _need(q, "q", torch.bfloat16, 3, dev)
+    _need(out, "out", torch.bfloat16, 3, dev)
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    _need(lam, "lam", torch.float32, None, dev)
+    t, hq, d = q.shape
+    if v_cache.shape != k_cache.shape or d != k_cache.shape[3]:
+        raise ValueError("inconsistent q / cache shapes")
+    if hq % 2 or tuple(out.shape) != (t, hq // 2, 2 * d):
+        raise ValueError(f"out must be [{t}, Hq / 2, {2 * d}], got {tuple(out.shape)} for {hq} heads")
+    if tuple(lam.shape) not in ((hq // 2,), (t, hq // 2)):
+        raise ValueError(f"lam must be [{hq // 2}] or [{t}, {hq // 2}], got {tuple(lam.shape)}")
+    if norm_weight is not None:
+        _need(norm_weight, "norm_weight", torch.bfloat16, 1, dev)
+        if norm_weight.shape[0] != 2 * d:
+            raise ValueError(f"norm_weight must be [{2 * d}]")
+    return dev
+
+
+def _prep_diff_decode(out, q, k_cache, v_cache, block_tables, context_lens, lam, scale, window,
+                      sinks, norm_weight, norm_eps, out_scale, workspace, stream):
+    window, sinks = _visibility(window, sinks)
+    dev = _need_diff(out, q, k_cache, v_cache, block_tables, context_lens, lam, norm_weight)
+    nb, bs, hkv, d = k_cache.shape
+    s, hq, _ = q.shape
+    if block_tables.shape[0] != s or context_lens.shape[0] != s:
+        raise ValueError("block_tables / context_lens must have num_seqs rows")
+    with _on_device(dev):
+        if workspace is None:
+            # allocated on the call's stream: handed out again only behind it
+            with _stream_context(stream):
+                workspace = torch.empty(diff_decode_workspace_size(hq, hkv, d), dtype=torch.uint8,
+                                        device=dev)
+        _need(workspace, "workspace", torch.uint8, 1, dev)
+        args = (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                _ptr(context_lens), _ptr(lam), int(lam.dim() == 2), _ptr(norm_weight),
+                float(norm_eps), float(out_scale), s, hq, hkv, d, bs, nb, block_tables.shape[1],
+                float(scale), window, sinks, _ptr(workspace), workspace.numel(), _stream(stream))
+    return (dev, _load().tvl_diff_attention_decode, args,
+            (out, q, k_cache, v_cache, block_tables, context_lens, lam, norm_weight, workspace))
+
+
+def diff_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens, lam, scale,
+                          window=0, sinks=0, norm_weight=None, norm_eps=1e-5, out_scale=1.0,
+                          workspace=None, stream=None):
+    """out bf16 [S, Hq / 2, 128] <- differential attention of q bf16 [S, Hq, 64]
+    (heads 2 i, 2 i + 1: the maps of pair i) over the bf16 cache, with lam fp32
+    [Hq / 2] or [S, Hq / 2] and, with norm_weight bf16 [128], the norm of each
+    pair's row.  workspace: uint8 CUDA tensor (allocated here when None)."""
+    dev, fn, args, _ = _prep_diff_decode(out, q, k_cache, v_cache, block_tables, context_lens, lam,
+                                         scale, window, sinks, norm_weight, norm_eps, out_scale,
+                                         workspace, stream)
+    with _on_device(dev):
+        _check(fn(*args))
+    return out
+
+
+def bind_diff_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens, lam, scale,
+                               window=0, sinks=0, norm_weight=None, norm_eps=1e-5, out_scale=1.0,
+                               workspace=None, stream=None):
+    """diff_attention_decode, checked once (a workspace of None is allocated
+    here once); returns a BoundCall."""
+    return BoundCall(*_prep_diff_decode(out, q, k_cache, v_cache, block_tables, context_lens, lam,
+                                        scale, window, sinks, norm_weight, norm_eps, out_scale,
+                                        workspace, stream))
 
 
 class BoundCall:

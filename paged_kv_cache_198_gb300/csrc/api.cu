@@ -797,13 +797,7 @@ tvl_status window_heads(int hq, int hkv, int d) {
   return TVL_OK;
 }
 
-tvl_status window_decode_impl(float* out, const void* q, const void* k_cache, const void* v_cache,
-                              const void* kv4, const int32_t* block_tables,
-                              const int32_t* context_lens, int num_seqs, int num_q_heads,
-                              int num_kv_heads, int head_dim, int block_size, int num_blocks,
-                              int max_blocks_per_seq, float scale, int window, int sinks,
-                              void* workspace, size_t workspace_bytes, void* stream) {
-  if (num_seqs < 0) return fail(TVL_ERR_INVALID_ARG, "num_seqs %d < 0", num_seqs);
+tvl_status paged_sizes(int block_size, int num_blocks, int max_blocks_per_seq) {
   if (max_blocks_per_seq <= 0 || num_blocks <= 0)
     return fail(TVL_ERR_INVALID_ARG, "num_blocks and max_blocks_per_seq must be positive");
   if (!kv4_block_size(block_size))
@@ -811,10 +805,22 @@ tvl_status window_decode_impl(float* out, const void* q, const void* k_cache, co
   if (static_cast<long long>(num_blocks) * block_size > INT_MAX ||
       static_cast<long long>(max_blocks_per_seq) * block_size > INT_MAX - 127)
     return fail(TVL_ERR_UNSUPPORTED, "more than 2^31 - 1 token slots");
+  return TVL_OK;
+}
+
+tvl_status window_decode_impl(float* out, const void* q, const void* k_cache, const void* v_cache,
+                              const void* kv4, const int32_t* block_tables,
+                              const int32_t* context_lens, int num_seqs, int num_q_heads,
+                              int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                              int max_blocks_per_seq, float scale, int window, int sinks,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  if (num_seqs < 0) return fail(TVL_ERR_INVALID_ARG, "num_seqs %d < 0", num_seqs);
+  tvl_status st = paged_sizes(block_size, num_blocks, max_blocks_per_seq);
+  if (st != TVL_OK) return st;
   if (window < 0 || sinks < 0)
     return fail(TVL_ERR_INVALID_ARG, "window %d and sinks %d must not be negative", window, sinks);
   if (!std::isfinite(scale)) return fail(TVL_ERR_INVALID_ARG, "scale is not finite");
-  tvl_status st = window_heads(num_q_heads, num_kv_heads, head_dim);
+  st = window_heads(num_q_heads, num_kv_heads, head_dim);
   if (st != TVL_OK) return st;
   if (num_seqs == 0) return TVL_OK;
   if (!out || !q || (!kv4 && (!k_cache || !v_cache)) || !block_tables || !context_lens)
@@ -898,6 +904,108 @@ tvl_status tvl_paged_attention_window_decode(float* out, const void* q, const vo
                             num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
                             max_blocks_per_seq, scale, window, sinks, workspace, workspace_bytes,
                             stream);
+}
+
+// -------------------------------------------------- differential attention
+
+namespace {
+
+tvl_status diff_heads(int hq, int hkv, int d) {
+  tvl_status st = window_heads(hq, hkv, d);
+  if (st != TVL_OK) return st;
+  if (hkv % 2 != 0)
+    return fail(TVL_ERR_INVALID_ARG, "num_kv_heads %d is odd: heads come in pairs", hkv);
+  return TVL_OK;
+}
+
+// Checks of both calls' last step.
+tvl_status diff_tail(const float* lambda, const void* norm_weight, float norm_eps, float out_scale) {
+  if (!lambda) return fail(TVL_ERR_INVALID_ARG, "null lambda");
+  if ((reinterpret_cast<uintptr_t>(lambda) & 3u) != 0)
+    return fail(TVL_ERR_INVALID_ARG, "lambda must be 4-byte aligned");
+  if (!aligned16(norm_weight))
+    return fail(TVL_ERR_INVALID_ARG, "norm_weight must be 16-byte aligned");
+  if (!(norm_eps >= 0.0f) || !std::isfinite(norm_eps))
+    return fail(TVL_ERR_INVALID_ARG, "norm_eps must be finite and not negative");
+  if (!std::isfinite(out_scale)) return fail(TVL_ERR_INVALID_ARG, "out_scale is not finite");
+  return TVL_OK;
+}
+
+}  // namespace
+
+tvl_status tvl_diff_decode_workspace_size(int num_q_heads, int num_kv_heads, int head_dim,
+                                          size_t* bytes) {
+  if (!bytes) return fail(TVL_ERR_INVALID_ARG, "null bytes pointer");
+  tvl_status st = diff_heads(num_q_heads, num_kv_heads, head_dim);
+  if (st != TVL_OK) return st;
+  int sms = 0;
+  st = sm_count(&sms);
+  if (st != TVL_OK) return st;
+  *bytes = tvl::diff_workspace_bytes(tvl::diff_max_ctas(num_kv_heads, sms), num_q_heads);
+  return TVL_OK;
+}
+
+tvl_status tvl_diff_attention_decode(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens, const float* lambda,
+    int lambda_per_token, const void* norm_weight, float norm_eps, float out_scale, int num_seqs,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+    int max_blocks_per_seq, float scale, int window, int sinks, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  if (num_seqs < 0) return fail(TVL_ERR_INVALID_ARG, "num_seqs %d < 0", num_seqs);
+  tvl_status st = paged_sizes(block_size, num_blocks, max_blocks_per_seq);
+  if (st != TVL_OK) return st;
+  if (window < 0 || sinks < 0)
+    return fail(TVL_ERR_INVALID_ARG, "window %d and sinks %d must not be negative", window, sinks);
+  if (!std::isfinite(scale)) return fail(TVL_ERR_INVALID_ARG, "scale is not finite");
+  st = diff_heads(num_q_heads, num_kv_heads, head_dim);
+  if (st != TVL_OK) return st;
+  if (num_seqs == 0) return TVL_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens)
+    return fail(TVL_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    return fail(TVL_ERR_INVALID_ARG, "out, q and the caches must be 16-byte aligned");
+  st = diff_tail(lambda, norm_weight, norm_eps, out_scale);
+  if (st != TVL_OK) return st;
+  if (!workspace) return fail(TVL_ERR_WORKSPACE, "null workspace");
+  if (!aligned16(workspace)) return fail(TVL_ERR_INVALID_ARG, "workspace not 16-byte aligned");
+  int sms = 0;
+  st = sm_count(&sms);
+  if (st != TVL_OK) return st;
+  const size_t need =
+      tvl::diff_workspace_bytes(tvl::diff_max_ctas(num_kv_heads, sms), num_q_heads);
+  if (workspace_bytes < need)
+    return fail(TVL_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  uint32_t* word = nullptr;
+  st = status_word(&word);
+  if (st != TVL_OK) return st;
+  tvl::DiffDecodeArgs a;
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.lam = lambda;
+  a.lam_per_token = lambda_per_token != 0;
+  a.norm_weight = norm_weight;
+  a.norm_eps = norm_eps;
+  a.out_scale = out_scale;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.window = window;
+  a.sinks = sinks;
+  a.scale = scale;
+  a.sms = sms;
+  a.workspace = workspace;
+  a.status = word;
+  cudaError_t e = tvl::launch_diff_decode(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "differential decode launch");
+  return TVL_OK;
 }
 
 }  // extern "C"

@@ -225,6 +225,30 @@ int window_max_ctas(int num_kv_heads, int sms);
 size_t window_workspace_bytes(int ctas, int num_q_heads);
 cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream);
 
+// -------------------------------------------------- differential attention
+
+struct DiffDecodeArgs {
+  void* out;               // bf16 [S, Hq / 2, 128]
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const float* lam;        // [Hq / 2], or [S, Hq / 2]
+  bool lam_per_token;
+  const void* norm_weight; // bf16 [128], or null: no norm
+  float norm_eps, out_scale;
+  int num_seqs, num_q_heads, num_kv_heads, block_size, num_blocks, max_blocks_per_seq;
+  int window, sinks;       // window 0: every cached token is visible
+  float scale;
+  int sms;                 // of the device
+  void* workspace;
+  uint32_t* status;
+};
+int diff_max_ctas(int num_kv_heads, int sms);
+size_t diff_workspace_bytes(int ctas, int num_q_heads);
+cudaError_t launch_diff_decode(const DiffDecodeArgs& a, cudaStream_t stream);
+
 // Sets the calling thread's tvl_last_error() text.
 void set_last_error(const char* msg);
 

@@ -67,26 +67,11 @@
 // sequences, window 1024, 50.6, which is the copies alone; 8 long ones 84 to 85
 // (0.94 of HBM).  A call's fixed part is about 9 us: the schedule 1.4, the first data
 // 3 to 4.6, the merge 4.4.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include <mutex>
-
-#include "device.cuh"
-#include "kernels.h"
-#include "kv4.cuh"
-#include "tc.cuh"
+#include "line.cuh"
 
 namespace tvl {
 namespace {
 
-constexpr int kD = 64;
-constexpr int kChunk = 16;
-constexpr int kMaxProducers = 4;
-constexpr int kMaxThreads = (12 + kMaxProducers) * 32;
-constexpr uint32_t kBf16Tile = kChunk * kD * 2;   // one head's K (or V) of a chunk
 constexpr float kMaxSum = 256.0f;             // a lane's weights under the reference maximum
 constexpr float kMaxProduct = 32768.0f;        // 4-bit: a lane's weights times its V scales
 // 4-bit: the weights are held against max(V scale, kLeastScale), so that rows of one
@@ -94,26 +79,17 @@ constexpr float kMaxProduct = 32768.0f;        // 4-bit: a lane's weights times 
 // their sums with the offsets below 2^109 a stage: room for 2^14 stages of a column's
 // eight lanes (10^6 tokens of a warp).
 constexpr float kLeastScale = 5.820766091346741e-11f;      // 2^-34
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr unsigned kFull = 0xffffffffu;
-constexpr uint32_t kSmemLimit = 227 * 1024;
 // Cost of a sequence start, in chunks: a partly filled stage, the warps' meeting
 // and the store.  Measured on batches of 64 (4-bit, 0.5k-4k tokens: 28.4 us at
 // 4, 27.3 at 16, 27.7 at 32) and 256 (bf16, window 1024: 51.2 us at 1, 50.9 at
 // 4, 51.6 at 6).
 constexpr int kSegWeight4 = 14, kSegWeight16 = 3;
 
-// First token of a chunk that stands in for a missing one: past every context (at
-// most 2^31 - 128 tokens), and its 16 tokens still fit 32 bits.
-constexpr int kUnseenToken = 0x7fffffe0;
-
 constexpr int kCombPitch = 72;                // floats a head of a warp hands over: 64 + m, l
 
-enum Format : int { kBf16 = 0, k4Bit = 1 };
-// Bits of a stage's flags: the warp's first and last stage of the segment; no
-// more stages; not all chunks present and visible.  From bit 8: how many of a
-// head's warps have stages of the segment.
-enum : int { kSegFirst = 1, kSegLast = 2, kTerminate = 4, kPartial = 8, kPartsShift = 8 };
+__host__ __device__ inline uint32_t comb_bytes(const Params& p) {
+  return p.wph * p.hpc * p.group * kCombPitch * 4;
+}
 
 // chunks of a stage: what a warp works on at once (independent work in flight)
 template <int F, bool kLoCols>
@@ -122,410 +98,6 @@ template <int F, bool kLoCols>
 __host__ __device__ constexpr int max_warps() { return F == k4Bit ? 12 : 8; }
 template <int F, bool kLoCols>
 __host__ __device__ constexpr int max_heads() { return F == k4Bit ? 4 : 8; }
-
-struct alignas(16) StageMeta {
-  int seq, record, flags, n;   // n: chunks in the stage
-  int v0, ns, delta, ctx;      // first virtual chunk; sink chunks; token chunk = v + (v >= ns) * delta
-};
-
-struct Params {
-  float* out;
-  const __nv_bfloat16* q;
-  const uint8_t* kv4;
-  const int32_t* block_tables;
-  const int32_t* context_lens;
-  int num_seqs, hq, hkv, group, num_blocks, max_blocks;
-  int cpb_log2;          // log2 of the 16-token chunks in a block
-  int window, sinks;     // window 0: none
-  int hpc, wph, cps_log2;
-  int stages, ring;      // wph rings of `ring` stages
-  int producers;         // warps that fill them: warp j the rings j, j + producers, ...
-  uint32_t stage_bytes, kv_bytes;
-  float scale_log2;
-  int ctas, seg_weight;
-  int small;             // schedule_small serves
-  float* ws_m;           // records [2 * ctas][hq]
-  float* ws_l;
-  float* ws_acc;
-  int4* ws_split;        // split sequences: (seq or -1, first record, first CTA, last CTA); entry
-                         // per sequence, or per CTA that holds the first chunk when there are
-                         // more sequences than CTAs
-  long long* ws_total;   // length of the cost line
-  uint32_t* status;
-};
-
-struct Layout {
-  uint32_t meta, bars, comb, sched, total;
-};
-
-__host__ __device__ inline uint32_t align_up(uint32_t x, uint32_t a) { return (x + a - 1) / a * a; }
-
-__host__ __device__ inline Layout make_layout(int stages, uint32_t stage_bytes, int hpc, int wph,
-                                              int group) {
-  Layout l;
-  uint32_t off = stages * stage_bytes;
-  l.meta = off;
-  off += stages * sizeof(StageMeta);
-  l.bars = off;                                        // full, empty; hand-over full, empty a warp
-  off += (2 * stages + 2 * hpc * wph) * 8;
-  l.comb = align_up(off, 16);
-  off = l.comb + wph * hpc * group * kCombPitch * 4;
-  l.sched = align_up(off, 16);                         // the schedule, scan totals, lengths
-  off = l.sched + 64 + 32 * 8 + kMaxThreads * 4;
-  l.total = off;
-  return l;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Weight of a partial result with reference maximum m under the common one.
-// m = -inf with anything in it means scores that were all NaN: kept as NaN.
-__device__ __forceinline__ float weight_of(float m, float common) {
-  return m == -INFINITY ? 1.f : ex2(m - common);
-}
-
-__device__ __forceinline__ int load_ctx(const Params& p, int s) {
-  int c = p.context_lens[s];
-  const long long cap = static_cast<long long>(p.max_blocks) << (p.cpb_log2 + 4);
-  if (c < 0 || c > cap) {
-    report(p.status, TVL_DEV_BAD_CONTEXT_LEN);
-    c = c < 0 ? 0 : static_cast<int>(cap);
-  }
-  return c;
-}
-
-// The visible chunks of a sequence: ns chunks from 0 (sinks), then the window's
-// from w0.  Virtual chunk v is token chunk v for v < ns, else v - ns + w0.
-struct Visible {
-  int ns, delta, n;
-};
-__device__ __forceinline__ Visible visible_of(const Params& p, int ctx) {
-  const int first = p.window > 0 && ctx > p.window ? ctx - p.window : 0;
-  const int w0 = first / kChunk;
-  const int sc = p.sinks / kChunk + (p.sinks % kChunk != 0 ? 1 : 0);
-  Visible v;
-  v.ns = min(sc, w0);
-  v.delta = w0 - v.ns;
-  v.n = (ctx + kChunk - 1) / kChunk - v.delta;
-  return v;
-}
-__device__ __forceinline__ long long seq_cost(int n, int w) { return n > 0 ? n + w : 0; }
-
-// ------------------------------------------------------------------ schedule
-
-struct Schedule {
-  int seq0, v0;          // first sequence and virtual chunk
-  int seq_end, v_end;    // ends before chunk v_end of sequence seq_end
-  long long total, hi;   // the cost line's length, this CTA's end on it
-};
-
-__device__ void block_scan(long long v, long long& incl, long long& total, long long* tmp) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(kFull, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) tmp[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    long long w = lane < nw ? tmp[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(kFull, w, o);
-      if (lane >= o) w += y;
-    }
-    if (lane < nw) tmp[lane] = w;
-  }
-  __syncthreads();
-  incl = x + (warp > 0 ? tmp[warp - 1] : 0);
-  total = tmp[nw - 1];
-  __syncthreads();
-}
-
-// A batch of at most one sequence a thread whose line surely fits 32 bits times
-// the CTAs (the host checks): one scan, each warp adding up the totals of those
-// before it, and the threads whose sequences hold the CTA's two ends record
-// them.  Every thread whose sequence has chunks in the range prefetches their
-// block table entries for the producer.
-__device__ __forceinline__ void schedule_small(const Params& p, Schedule* sc, int* tmp, int* lens) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  const int w = p.seg_weight;
-  Visible vis = {0, 0, 0};
-  if (tid < p.num_seqs) {
-    const int ctx = load_ctx(p, tid);
-    lens[tid] = ctx;                       // for the producer
-    vis = visible_of(p, ctx);
-  }
-  const int mine = vis.n > 0 ? vis.n + w : 0;
-  int x = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kFull, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) tmp[warp] = x;
-  if (tid == 0) {
-    sc->seq0 = sc->seq_end = p.num_seqs;
-    sc->v0 = sc->v_end = 0;
-  }
-  __syncthreads();
-  const int part = lane < nw ? tmp[lane] : 0;
-  const int total = __reduce_add_sync(kFull, part);
-  const int excl = __reduce_add_sync(kFull, lane < warp ? part : 0) + x - mine;
-  const int lo = static_cast<uint32_t>(total) * blockIdx.x / static_cast<uint32_t>(p.ctas);
-  const int hi = static_cast<uint32_t>(total) * (blockIdx.x + 1) / static_cast<uint32_t>(p.ctas);
-  if (mine > 0 && excl <= lo && lo < excl + mine) {
-    sc->seq0 = tid;
-    sc->v0 = max(0, lo - excl - w);
-  }
-  if (mine > 0 && excl <= hi && hi < excl + mine) {
-    sc->seq_end = tid;
-    sc->v_end = max(0, hi - excl - w);
-  }
-  if (tid == 0) {
-    sc->total = total;
-    sc->hi = hi;
-  }
-  const int a = max(0, lo - excl - w), b = min(vis.n, hi - excl - w);
-  const int32_t* row = p.block_tables + static_cast<long long>(tid) * p.max_blocks;
-  for (int v = a; v < b; v += 32 << p.cpb_log2)
-    asm volatile("prefetch.global.L1 [%0];" ::"l"(row + ((v < vis.ns ? v : v + vis.delta) >> p.cpb_log2)));
-}
-
-// Every thread sums the costs of a contiguous slice of the sequences; one
-// scan places the slices on the line, and the threads whose slices hold this
-// CTA's two ends walk them again.
-__device__ __noinline__ void make_schedule(const Params& p, Schedule* sc, long long* tmp) {
-  const int tid = threadIdx.x, cta = blockIdx.x, w = p.seg_weight;
-  const int per = (p.num_seqs + blockDim.x - 1) / blockDim.x;
-  const int s_lo = min(p.num_seqs, tid * per), s_hi = min(p.num_seqs, s_lo + per);
-  long long mine = 0;
-  for (int s = s_lo; s < s_hi; ++s) mine += seq_cost(visible_of(p, load_ctx(p, s)).n, w);
-  if (tid == 0) {
-    sc->seq0 = sc->seq_end = p.num_seqs;
-    sc->v0 = sc->v_end = 0;
-  }
-  long long incl, total;
-  block_scan(mine, incl, total, tmp);      // its barriers order the initial values
-  const long long excl = incl - mine;
-  const long long lo = total * cta / p.ctas, hi = total * (cta + 1) / p.ctas;
-  auto locate = [&](long long x, int& seq, int& v) {
-    long long run = excl;
-    for (int s = s_lo; s < s_hi; ++s) {
-      const long long c = seq_cost(visible_of(p, load_ctx(p, s)).n, w);
-      if (x < run + c) {
-        seq = s;
-        v = static_cast<int>(x - run - w > 0 ? x - run - w : 0);
-        return;
-      }
-      run += c;
-    }
-  };
-  if (mine > 0 && excl <= lo && lo < incl) locate(lo, sc->seq0, sc->v0);
-  if (mine > 0 && excl <= hi && hi < incl) locate(hi, sc->seq_end, sc->v_end);
-  if (tid == 0) {
-    sc->total = total;
-    sc->hi = hi;
-  }
-}
-
-// ------------------------------------------------------------------ producer
-
-struct Segment {
-  int s, v, e, ctx, ns, delta, n, record, window;
-};
-
-template <int F>
-__device__ void producer(const Params& p, const Schedule& sc, uint8_t* smem, const Layout& L, int pj,
-                         const CUtensorMap* tm_k, const CUtensorMap* tm_v) {
-  const int lane = threadIdx.x & 31;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bars);
-  uint64_t* empty = full + p.stages;
-  StageMeta* meta = reinterpret_cast<StageMeta*>(smem + L.meta);
-  const int hpc = p.hpc, h0 = blockIdx.z * hpc, cta = blockIdx.x;
-  const uint32_t chunk_bytes = hpc * (F == k4Bit ? kRecBytes : 2 * kBf16Tile);
-  const uint32_t q_bytes = hpc * p.group * kD * 2;
-  const uint64_t stream_policy = policy_evict_first();
-  const uint64_t keep_policy = policy_evict_last();
-  if (F == kBf16 && lane == 0) {
-    prefetch_tensormap(tm_k);
-    prefetch_tensormap(tm_v);
-  }
-
-  const int cps = 1 << p.cps_log2, wph = p.wph, ring = p.ring;
-  // Stage k of a segment goes to the head's warps k % wph, each with a ring of
-  // its own.  Lane w < wph: warps w's next stage, in bit 8 its fill's parity and
-  // in bit 9 whether every stage of the ring has been filled.
-  int state = 0;
-  bool ok = true;
-
-  // lens: the lengths, of a small batch; else lane i's win_ctx: sequence win + i's
-  const int* lens = reinterpret_cast<const int*>(smem + L.sched + 64 + 32 * 8);
-  int win = -64, win_ctx = 0;
-  // The segment that starts at chunk v of sequence s or after it; false: none left.
-  auto find = [&](int s, int v, bool first, Segment& g) {
-    for (;; ++s, v = 0) {
-      if (s >= p.num_seqs || s > sc.seq_end || (s == sc.seq_end && v >= sc.v_end)) return false;
-      if (p.small) {
-        g.ctx = lens[s];
-      } else {
-        if (s < win || s >= win + 32) {
-          win = s;
-          win_ctx = s + lane < p.num_seqs ? load_ctx(p, s + lane) : 0;
-        }
-        g.ctx = __shfl_sync(kFull, win_ctx, s - win);
-      }
-      const Visible vis = visible_of(p, g.ctx);
-      if (v >= vis.n) continue;
-      g.s = s;
-      g.v = v;
-      g.e = s == sc.seq_end ? min(sc.v_end, vis.n) : vis.n;
-      g.ns = vis.ns;
-      g.delta = vis.delta;
-      g.n = vis.n;
-      g.window = p.window > 0 ? min(p.window, g.ctx) : g.ctx;
-      g.record = v == 0 && g.e == vis.n ? -1 : 2 * cta + (first ? 0 : 1);
-      return true;
-    }
-  };
-  // this lane's block table entry: chunk vb + lane of the segment
-  auto entry = [&](const Segment& g, int vb) {
-    const int v = vb + lane;
-    if (v >= g.e) return 0;
-    const int c = v < g.ns ? v : v + g.delta;
-    return p.block_tables[static_cast<long long>(g.s) * p.max_blocks + (c >> p.cpb_log2)];
-  };
-
-  const bool by_seq = p.num_seqs <= p.ctas && blockIdx.z == 0;
-  int4 split = make_int4(-1, 0, 0, 0);
-  Segment g;
-  bool have = find(sc.seq0, sc.v0, true, g);
-  int tbl = have ? entry(g, g.v) : 0;
-  while (have && ok) {
-    if (g.v == 0 && g.e < g.n) {
-      // a split sequence's first piece: it ends at this CTA's end of the
-      // line, and the sequence's last chunk lies g.n - g.e - 1 places on
-      const long long x = sc.hi + (g.n - g.e) - 1;
-      split = make_int4(g.s, g.record, cta, static_cast<int>(((x + 1) * p.ctas - 1) / sc.total));
-    }
-    if (by_seq && pj == 0 && g.v == 0 && lane == 0)
-      p.ws_split[g.s] = g.e < g.n ? split : make_int4(-1, 0, 0, 0);
-    Segment nx;
-    const bool have_next = find(g.s, g.e, false, nx);
-    const int n_stages = (g.e - g.v + cps - 1) >> p.cps_log2;
-    const int parts = min(wph, n_stages);
-    // the producer's own stages: k (of warp w) with w = k % wph, w % producers == pj
-    int k = pj, w = pj, vb = g.v;
-    int ntbl = vb + 32 < g.e ? entry(g, vb + 32) : (have_next ? entry(nx, nx.v) : 0);
-    for (;;) {
-      const int v = g.v + (k << p.cps_log2);
-      if (v >= g.e) break;
-      while (v >= vb + 32) {          // the next 32 entries (of this segment or the next)
-        vb += 32;                     // are fetched while this batch's copies are issued
-        tbl = ntbl;
-        ntbl = vb + 32 < g.e ? entry(g, vb + 32) : (have_next ? entry(nx, nx.v) : 0);
-      }
-      const int n = min(cps, g.e - v);                  // lane i < n: chunk v + i
-      const int rs = __shfl_sync(kFull, state, w);
-      const int at = rs & 0xff, slot = w * ring + at;
-      const uint32_t sp = rs >> 8 & 1;
-      uint8_t* base = smem + static_cast<size_t>(slot) * p.stage_bytes;
-      const int vv = v + lane;
-      const int c = vv < g.ns ? vv : vv + g.delta;
-      const bool whole = c * kChunk + kChunk <= g.ctx &&
-                         (c * kChunk >= g.ctx - g.window || c * kChunk + kChunk <= p.sinks);
-      const bool all = __all_sync(kFull, lane >= n || whole);
-      int page = __shfl_sync(kFull, tbl, (v - vb + lane) & 31);
-      if (lane < n && (page < 0 || page >= p.num_blocks)) {
-        report(p.status, TVL_DEV_BAD_BLOCK_ID);
-        page = 0;
-      }
-      const long long chunk = (static_cast<long long>(page) << p.cpb_log2) + (c & ((1 << p.cpb_log2) - 1));
-      const bool first = k < wph;
-      if (rs >> 9 && !__all_sync(kFull, mbar_wait(&empty[slot], sp ^ 1))) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        StageMeta m;
-        m.seq = g.s;
-        m.record = g.record;
-        m.flags = parts << kPartsShift | (first ? kSegFirst : 0) |
-                  (k + wph >= n_stages ? kSegLast : 0) | (all && n == cps ? 0 : kPartial);
-        m.n = n;
-        m.v0 = v;
-        m.ns = g.ns;
-        m.delta = g.delta;
-        m.ctx = g.ctx;
-        meta[slot] = m;
-        mbar_arrive_expect_tx(&full[slot], n * chunk_bytes + (first ? q_bytes : 0));
-      }
-      __syncwarp();
-      if (lane < n) {
-        if (F == k4Bit) {
-          bulk_load(base + lane * chunk_bytes, p.kv4 + (chunk * p.hkv + h0) * kRecBytes, chunk_bytes,
-                    &full[slot], stream_policy);
-        } else {
-          const int tok = static_cast<int>(chunk * kChunk);
-          const uint32_t half = hpc * kBf16Tile;
-          tma_load_3d(base + lane * half, tm_k, 0, tok, h0, &full[slot]);
-          tma_load_3d(base + p.kv_bytes / 2 + lane * half, tm_v, 0, tok, h0, &full[slot]);
-        }
-      }
-      if (first && lane == 31)
-        bulk_load(base + p.kv_bytes,
-                  p.q + (static_cast<size_t>(g.s) * p.hq + static_cast<size_t>(h0) * p.group) * kD,
-                  q_bytes, &full[slot], keep_policy);
-      if (lane == w) state = at + 1 == ring ? (rs ^ 0x100) - at | 0x200 : rs + 1;
-      if (w + p.producers < wph) {
-        w += p.producers;
-        k += p.producers;
-      } else {
-        k += wph - w + pj;
-        w = pj;
-      }
-    }
-    // the next segment's first entries: already at hand in the last batch
-    if (have_next) tbl = vb + 32 < g.e ? entry(nx, nx.v) : ntbl;
-    g = nx;
-    have = have_next;
-  }
-  if (blockIdx.z == 0 && lane == 0 && pj == 0) {
-    if (!by_seq) p.ws_split[cta] = split;
-    if (cta == 0) *p.ws_total = sc.total;
-  }
-  int pos = state & 0xff;
-  uint32_t ph = state >> 8 & 1;
-  bool used = state >> 9 != 0;
-  if (lane < wph && lane % p.producers == pj) {   // each ring's last stage; then its copies land
-    if (ok && used) ok = mbar_wait(&empty[lane * ring + pos], ph ^ 1);
-    if (ok) {
-      meta[lane * ring + pos].flags = kTerminate;
-      mbar_arrive(&full[lane * ring + pos]);
-      if (++pos == ring) {
-        pos = 0;
-        ph ^= 1;
-        used = true;
-      }
-    } else {
-      report(p.status, kDevTimeout);
-    }
-    const int fills = used ? ring : pos;
-    for (int i = 0; i < fills; ++i) {
-      if (--pos < 0) {
-        pos = ring - 1;
-        ph ^= 1;
-      }
-      if (!mbar_wait(&full[lane * ring + pos], ph)) report(p.status, kDevTimeout);
-    }
-  }
-}
 
 // ----------------------------------------------------------------- consumers
 
@@ -536,13 +108,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 // the same with a zero accumulator in
 __device__ __forceinline__ void mma_f16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -550,34 +115,6 @@ __device__ __forceinline__ void mma_f16_0(float (&c)[4], uint32_t a0, uint32_t a
       "{%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-__device__ __forceinline__ void mma_bf16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                           uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-__device__ __forceinline__ float2 add2(float a0, float a1, float b0, float b1) {
-  return __fadd2_rn(make_float2(a0, a1), make_float2(b0, b1));
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-// the 8 x 8 matrix of 16-bit elements held one row per lane quad, transposed
-__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
-  uint32_t d;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-  return d;
 }
 // 2^15 a + b on fp16 pairs
 __device__ __forceinline__ uint32_t half2_raise(uint32_t a, uint32_t b) {
@@ -597,22 +134,6 @@ __device__ __forceinline__ float2 k_scaled(const Params& p, uint32_t w) {
 __device__ __forceinline__ float2 v_scale_offset(uint32_t w) {
   const float2 m = meta_sz(w);
   return make_float2(m.x, fmaf(7.5f, m.x, m.y));
-}
-
-template <int F>
-__device__ __forceinline__ uint32_t pack16(float2 v) {
-  if constexpr (F == k4Bit) {
-    const __half2 h = __floats2half2_rn(v.x, v.y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-template <int F>
-__device__ __forceinline__ float2 unpack16(uint32_t w) {
-  if constexpr (F == k4Bit) return __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return bf16x2_to_float2(w);
 }
 
 // Row r of the 16 rows of a product is token row_token(r) of the chunk.  With
@@ -745,10 +266,6 @@ __device__ __forceinline__ float2 scaled_score(float2 x, float2 kf, float s) {
   const float f = static_cast<float>(e);
   return make_float2(fmaf(x.x, kf.x, f), fmaf(x.y, kf.y, f));
 }
-__device__ __forceinline__ float2 max2(float2 a, float2 b) {
-  return make_float2(fmaxf(a.x, b.x), fmaxf(a.y, b.y));
-}
-
 // 4-bit: a column's sums, whose reference depends on the scales of V, in the units
 // of its largest weight's power of two (m is a whole number, so this is exact):
 // what is merged next then differs in m by no more than the scores do.
@@ -759,16 +276,6 @@ __device__ __forceinline__ void normalise(float& m, float& l, float (&o)[8]) {
   l *= f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] *= f;
-}
-
-__device__ __forceinline__ void add_to(float (&acc)[4], const float (&sum)[4]) {
-  // The tensor core truncates what it accumulates, which over a long context
-  // would pull the sums towards zero; across stages they add up here, rounded.
-  const float2 a = add2(acc[0], acc[1], sum[0], sum[1]), b = add2(acc[2], acc[3], sum[2], sum[3]);
-  acc[0] = a.x;
-  acc[1] = a.y;
-  acc[2] = b.x;
-  acc[3] = b.y;
 }
 
 __device__ __forceinline__ uint32_t lds32(const uint8_t* p) {
@@ -1364,7 +871,7 @@ __global__ void __launch_bounds__((max_warps<F, kLoCols>() + kMaxProducers) * 32
   // 128-byte-swizzled tiles repeat every 1024 bytes
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const Layout L = make_layout(p.stages, p.stage_bytes, p.hpc, p.wph, p.group);
+  const Layout L = make_layout(p.stages, p.stage_bytes, p.hpc * p.wph, comb_bytes(p));
   Schedule* sched = reinterpret_cast<Schedule*>(smem + L.sched);
   long long* tmp = reinterpret_cast<long long*>(smem + L.sched + 64);
   int* lens = reinterpret_cast<int*>(smem + L.sched + 64 + 32 * 8);
@@ -1627,35 +1134,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 2)
 
 // --------------------------------------------------------------------- host
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaDriverEntryPointQueryResult q;
-    void* f = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
-// The bf16 cache as [Hkv][NB * bs tokens][64]: one box is a 16-token chunk of
-// the CTA's heads, in shared memory head after head, 16 swizzled rows each.
-bool cache_map(CUtensorMap* m, const void* base, int hkv, long long tokens, int hpc) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(tokens),
-                              static_cast<cuuint64_t>(hkv)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hkv) * kD * 2, kD * 2};
-  const cuuint32_t box[3] = {kD, kChunk, static_cast<cuuint32_t>(hpc)};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Shared memory of a CTA of window_direct_kernel: its chunks and the hand-overs.
 long long direct_smem(bool four, long long chunks, int group) {
   const long long per_warp = (chunks + kDirectWarps - 1) / kDirectWarps;
@@ -1687,13 +1165,6 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const Params&
   });
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, grid, dim3((p.hpc * p.wph + p.producers) * 32), smem, stream, tk, tv, p);
-}
-
-// KV heads one CTA owns: the largest divisor up to `most`.
-int heads_per_cta(int num_kv_heads, int most) {
-  int h = most;
-  while (num_kv_heads % h != 0) --h;
-  return h;
 }
 
 // The CTA's shape for a format and group size.
@@ -1777,7 +1248,7 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
   for (;; --p.cps_log2) {              // two stages a ring at least (bf16: by smaller stages)
     p.kv_bytes = (p.hpc << p.cps_log2) * (four ? kRecBytes : 2 * kBf16Tile);
     p.stage_bytes = align_up(p.kv_bytes + p.hpc * p.group * kD * 2, 1024);
-    const uint32_t fixed = make_layout(0, p.stage_bytes, p.hpc, p.wph, p.group).total + 1024 + 16;
+    const uint32_t fixed = make_layout(0, p.stage_bytes, p.hpc * p.wph, comb_bytes(p)).total + 1024 + 16;
     const int most = static_cast<int>((kSmemLimit - fixed) / (p.stage_bytes + sizeof(StageMeta) + 16));
     p.ring = (most > 48 ? 48 : most) / p.wph;
     if (p.ring >= 2 || four || p.cps_log2 == 0) break;
@@ -1797,7 +1268,7 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t stream)
   p.ws_total = reinterpret_cast<long long*>(ws + 2 * ab + rows * kD * 4 +
                                             (static_cast<size_t>(p.ctas) * 16 + 255) / 256 * 256);
   if (!maps(p.hpc)) return cudaErrorInvalidValue;
-  const uint32_t smem = make_layout(p.stages, p.stage_bytes, p.hpc, p.wph, p.group).total + 1024;
+  const uint32_t smem = make_layout(p.stages, p.stage_bytes, p.hpc * p.wph, comb_bytes(p)).total + 1024;
   const dim3 grid(p.ctas, 1, groups);
   cudaError_t e;
   const bool wide = p.hpc == 4;         // a constant stride between a head's chunks
