@@ -524,6 +524,25 @@ tvl_status tvl_diff_attention_decode(
     size_t workspace_bytes, void* stream);
 
 /*
+ * Chunks of new tokens, causal, as tvl_paged_attention_window_prefill (the same
+ * arguments, device checks and reports): queries are the last Lq tokens of each
+ * sequence.  P and V enter the P.V product as fp16, as there, and a V value beyond the
+ * fp16 range or not finite spoils the rows of the 128-row query tiles that see it; a
+ * row whose difference is not finite sets TVL_DEV_NONFINITE.
+ *   out : bf16 [Tq, Hq / 2, 128]; q : bf16 [Tq, Hq, D]
+ *   lambda : float32 [Hq / 2], or [Tq, Hq / 2] with lambda_per_token != 0
+ * Supported: as tvl_diff_attention_decode, num_seqs <= 65535, num_seqs *
+ * ceil(max_q_len / 128) * Hq < 2^31, MB * bs <= 2^30 - 256.
+ */
+tvl_status tvl_diff_attention_prefill(
+    void* out, const void* q, const int32_t* query_start_loc, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
+    const float* lambda, int lambda_per_token, const void* norm_weight, float norm_eps,
+    float out_scale, int num_seqs, int total_q_tokens, int max_q_len, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, int max_blocks_per_seq,
+    float scale, int window, int sinks, void* stream);
+
+/*
  * Host block allocator: the CPU control plane that hands out the physical
  * blocks and slots the kernels read [nano-vLLM guide ch. 2 (control plane vs
  * data plane), ch. 4 "PagedAttention" (block allocator, no fragmentation

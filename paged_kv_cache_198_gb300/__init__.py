@@ -13,7 +13,7 @@ Functions (same names as the C entry points, without the ``tvl_`` prefix):
   kv4_expand_blocks, kv4_copy_blocks, kv4_attention_decode; rotary positions with
   several axes rope_axes_paged_kv_write, kv4_axes_write; a step's tables on the
   GPU build_step_tables; differential attention diff_attention_decode,
-  diff_decode_workspace_size; with a window and sinks paged_attention_window_decode, window_decode_workspace_size,
+  diff_decode_workspace_size, diff_attention_prefill; with a window and sinks paged_attention_window_decode, window_decode_workspace_size,
   paged_attention_window_prefill.
 
 Bound calls (``bind_`` before the name of a write, decode, prefill,
@@ -49,6 +49,7 @@ __all__ = [
     "rope_axes_paged_kv_write", "bind_rope_axes_paged_kv_write", "kv4_axes_write",
     "bind_kv4_axes_write", "build_step_tables", "bind_build_step_tables",
     "diff_attention_decode", "bind_diff_attention_decode", "diff_decode_workspace_size",
+    "diff_attention_prefill", "bind_diff_attention_prefill",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -131,7 +132,10 @@ def _load():
             lib.tvl_diff_decode_workspace_size.argtypes = [I, I, I, ctypes.POINTER(SZ)]
             lib.tvl_diff_attention_decode.argtypes = [
                 P, P, P, P, P, P, P, I, P, F, F, I, I, I, I, I, I, I, F, I, I, P, SZ, P]
+            lib.tvl_diff_attention_prefill.argtypes = [
+                P, P, P, P, P, P, P, P, I, P, F, F, I, I, I, I, I, I, I, I, I, F, I, I, P]
             for name in ("tvl_diff_decode_workspace_size", "tvl_diff_attention_decode",
+                         "tvl_diff_attention_prefill",
                          "tvl_rope_axes_paged_kv_write", "tvl_kv4_axes_write",
                          "tvl_build_step_tables", "tvl_kv4_write", "tvl_kv4_expand_blocks",
                          "tvl_kv4_copy_blocks",
@@ -931,6 +935,51 @@ def bind_diff_attention_decode(out, q, k_cache, v_cache, block_tables, context_l
     return BoundCall(*_prep_diff_decode(out, q, k_cache, v_cache, block_tables, context_lens, lam,
                                         scale, window, sinks, norm_weight, norm_eps, out_scale,
                                         workspace, stream))
+
+
+def _prep_diff_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables, context_lens, lam,
+                       scale, max_q_len, window, sinks, norm_weight, norm_eps, out_scale, stream):
+    window, sinks = _visibility(window, sinks)
+    dev = _need_diff(out, q, k_cache, v_cache, block_tables, context_lens, lam, norm_weight)
+    _need(query_start_loc, "query_start_loc", torch.int32, 1, dev)
+    nb, bs, hkv, d = k_cache.shape
+    tq, hq, _ = q.shape
+    s = context_lens.shape[0]
+    if query_start_loc.shape[0] != s + 1 or block_tables.shape[0] != s:
+        raise ValueError("query_start_loc must be [S+1] and block_tables [S, MB]")
+    with _on_device(dev):
+        args = (_ptr(out), _ptr(q), _ptr(query_start_loc), _ptr(k_cache), _ptr(v_cache),
+                _ptr(block_tables), _ptr(context_lens), _ptr(lam), int(lam.dim() == 2),
+                _ptr(norm_weight), float(norm_eps), float(out_scale), s, tq, int(max_q_len), hq,
+                hkv, d, bs, nb, block_tables.shape[1], float(scale), window, sinks,
+                _stream(stream))
+    return (dev, _load().tvl_diff_attention_prefill, args,
+            (out, q, query_start_loc, k_cache, v_cache, block_tables, context_lens, lam,
+             norm_weight))
+
+
+def diff_attention_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables, context_lens,
+                           lam, scale, max_q_len, window=0, sinks=0, norm_weight=None,
+                           norm_eps=1e-5, out_scale=1.0, stream=None):
+    """out bf16 [Tq, Hq / 2, 128] <- causal differential attention of the last
+    Lq tokens of each sequence (q bf16 [Tq, Hq, 64], packed by query_start_loc
+    int32 [S+1]); lam fp32 [Hq / 2] or [Tq, Hq / 2], the rest as in
+    diff_attention_decode."""
+    dev, fn, args, _ = _prep_diff_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables,
+                                          context_lens, lam, scale, max_q_len, window, sinks,
+                                          norm_weight, norm_eps, out_scale, stream)
+    with _on_device(dev):
+        _check(fn(*args))
+    return out
+
+
+def bind_diff_attention_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables,
+                                context_lens, lam, scale, max_q_len, window=0, sinks=0,
+                                norm_weight=None, norm_eps=1e-5, out_scale=1.0, stream=None):
+    """diff_attention_prefill, checked once; returns a BoundCall."""
+    return BoundCall(*_prep_diff_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables,
+                                         context_lens, lam, scale, max_q_len, window, sinks,
+                                         norm_weight, norm_eps, out_scale, stream))
 
 
 class BoundCall:

@@ -1008,4 +1008,68 @@ tvl_status tvl_diff_attention_decode(
   return TVL_OK;
 }
 
+tvl_status tvl_diff_attention_prefill(
+    void* out, const void* q, const int32_t* query_start_loc, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
+    const float* lambda, int lambda_per_token, const void* norm_weight, float norm_eps,
+    float out_scale, int num_seqs, int total_q_tokens, int max_q_len, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, int max_blocks_per_seq,
+    float scale, int window, int sinks, void* stream) {
+  if (num_seqs < 0 || total_q_tokens < 0 || max_q_len < 0)
+    return fail(TVL_ERR_INVALID_ARG, "negative size");
+  tvl_status st = paged_sizes(block_size, num_blocks, max_blocks_per_seq);
+  if (st != TVL_OK) return st;
+  if (window < 0 || sinks < 0)
+    return fail(TVL_ERR_INVALID_ARG, "window %d and sinks %d must not be negative", window, sinks);
+  if (static_cast<long long>(max_blocks_per_seq) * block_size > (1 << 30) - 256)
+    return fail(TVL_ERR_UNSUPPORTED, "a block table of more than 2^30 - 256 tokens");
+  if (!std::isfinite(scale)) return fail(TVL_ERR_INVALID_ARG, "scale is not finite");
+  st = diff_heads(num_q_heads, num_kv_heads, head_dim);
+  if (st != TVL_OK) return st;
+  if (num_seqs == 0 || total_q_tokens == 0) return TVL_OK;
+  if (max_q_len == 0) return fail(TVL_ERR_INVALID_ARG, "max_q_len 0 with queries present");
+  if (num_seqs > 65535) return fail(TVL_ERR_UNSUPPORTED, "num_seqs %d > 65535", num_seqs);
+  if (static_cast<long long>(num_seqs) * ((max_q_len + 127LL) / 128) * num_q_heads > INT_MAX)
+    return fail(TVL_ERR_UNSUPPORTED, "num_seqs * ceil(max_q_len / 128) * num_q_heads > 2^31 - 1");
+  if (!out || !q || !query_start_loc || !k_cache || !v_cache || !block_tables || !context_lens)
+    return fail(TVL_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    return fail(TVL_ERR_INVALID_ARG, "out, q and the caches must be 16-byte aligned");
+  st = diff_tail(lambda, norm_weight, norm_eps, out_scale);
+  if (st != TVL_OK) return st;
+  uint32_t* word = nullptr;
+  st = status_word(&word);
+  if (st != TVL_OK) return st;
+  tvl::DiffPrefillArgs a;
+  a.out = out;
+  a.q = q;
+  a.query_start_loc = query_start_loc;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.lam = lambda;
+  a.lam_per_token = lambda_per_token != 0;
+  a.norm_weight = norm_weight;
+  a.norm_eps = norm_eps;
+  a.out_scale = out_scale;
+  a.num_seqs = num_seqs;
+  a.total_q_tokens = total_q_tokens;
+  a.max_q_len = max_q_len;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.scale = scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.status = word;
+  st = sm_count(&a.num_sms);
+  if (st != TVL_OK) return st;
+  cudaError_t e = tvl::launch_diff_prefill(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "differential prefill launch");
+  return TVL_OK;
+}
+
 }  // extern "C"

@@ -1,0 +1,665 @@
+// diff_prefill.cu -- differential attention of chunks of new tokens over the paged
+// KV cache, causal, with an optional sliding window and sinks, on the Blackwell tensor
+// cores (tcgen05 MMA, TMEM accumulators, TMA gathers).
+//
+// What it computes: as diff_decode.cu, for every query row: row i of a sequence's Lq
+// new tokens sits at position ctx - Lq + i and sees the keys j <= that position (of
+// those the last `window` and the first `sinks`); per query pair
+//   d = softmax(scale q_0 K_0) V - lambda softmax(scale q_1 K_1) V, V 128 wide.
+//
+// A unit of work is a 128-row query tile of one query pair; the kernel is persistent
+// and walks units as the plain prefill does (prefill_tiles.cuh).  Keys go in tiles of
+// 64.  Warps:
+//   0..7    softmax, a warpgroup a map: thread r owns query row r (TMEM lane r).  It
+//           takes a tile's 64 scores into registers, writes P = 2^(s - m) as fp16 over
+//           the scores' own TMEM columns, and hands them to P V.  m is the first tile's
+//           maximum and moves only when a tile's row sum nears the fp16 limit.
+//   8       producer: Q tiles, and per key tile the two keys and two V heads of each
+//           physical block, one TMA box each (the paged gather)
+//   9       issues S_h = Q_h K_h^T (M 128, N 64, bf16, both operands in shared memory)
+//   10      issues O_h += P_h V (M 128, N 128, fp16, P read from TMEM)
+//   12..15  V conversion bf16 -> fp16 in place (as in prefill.cu)
+// TMEM: S/P of map h in two buffers of 64 columns each (256), O_0 and O_1 128 each:
+// all 512.  With O 128 wide there is no room for P beside S; two buffers a map let one
+// tile's P V and the Q K^T after next run while the softmax works on the tile between.
+//
+// At a unit's end the two warps of a row quarter, one a map, each take half of the 128
+// dimensions of both O's: they exchange the row sums, then the halves' sums of squares
+// of d = O_0 / l_0 - lambda O_1 / l_1, and store their half through swizzled staging.
+#include "diff.cuh"
+#include "prefill_tiles.cuh"
+
+namespace tvl {
+namespace {
+
+constexpr int kBN = 64;
+constexpr int kStages = 4;
+constexpr int kThreads = 512;
+constexpr int kProducerWarp = 8, kQkWarp = 9, kPvWarp = 10, kConvWarp0 = 12, kConvWarps = 4;
+constexpr uint32_t kKvTile = kBN * kD * 2;            // 8 KB: one head's K (or V) of a tile
+constexpr uint32_t kStageBytes = 4 * kKvTile;         // K_0, K_1, V_0, V_1
+
+constexpr uint32_t kQOff = 0;
+constexpr uint32_t kKvOff = 2 * kTileBytes;
+constexpr uint32_t kOutOff = kKvOff + kStages * kStageBytes;   // two halves of 128 rows x 128 B
+constexpr uint32_t kBarOff = kOutOff + 2 * kBM * 128;
+constexpr uint32_t kExOff = kBarOff + 1024;                    // the maps' exchange, [2][2][128]
+constexpr uint32_t kTabOff = kExOff + 4 * kBM * 4;
+constexpr uint32_t kSmemBytes = kTabOff + 5 * 4 * kThreads + 1024;   // + alignment slack
+static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
+
+// Register split: 16 warps launched with 128 registers each; the two softmax
+// warpgroups rise to 168, the other two drop to 88: 256 x 168 + 256 x 88 = 65536.
+// The host checks the launch allocation before the first launch.
+constexpr int kRegsSoftmax = 168, kRegsAux = 88;
+
+constexpr uint32_t kIdescQK = idesc_f16_f32acc(1, 0, kBM, kBN);    // bf16, K-major B
+constexpr uint32_t kIdescPV = idesc_f16_f32acc(0, 1, kBM, kDV);    // fp16, MN-major B
+
+// TMEM columns; P of a buffer lies over its scores (32 columns of fp16 pairs)
+__device__ __forceinline__ uint32_t s_col(int h, int buf) { return (2 * h + buf) * kBN; }
+__device__ __forceinline__ uint32_t o_col(int h) { return 4 * kBN + h * kDV; }
+constexpr uint32_t kTmemCols = 512;
+
+struct Barriers {
+  uint64_t q_full, q_empty;
+  uint64_t kv_full[kStages], kv_empty[kStages], v_ready[kStages];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // [map][buffer]
+  uint64_t o_free;               // both O's read at a unit's end
+  uint64_t sums[4], squares[4];  // per row quarter: the maps' exchanges
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int4 ustash[8];                // per softmax warp: its unit's rows, first output row, pair
+};
+static_assert(sizeof(Barriers) <= 1024, "barrier area");
+
+struct DiffPrefillParams : Params {
+  DiffTail tail;
+  int box_tokens, box_log2;      // tokens of a TMA box: min(bs, kBN)
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    diff_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
+                        const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_o, const DiffPrefillParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Barriers* B = reinterpret_cast<Barriers*>(smem + kBarOff);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int G = static_cast<int>(gridDim.x);
+  const int c = static_cast<int>(blockIdx.x);
+
+  grid_dependency_wait();          // inputs may come from the preceding kernel
+  grid_dependents_launch();
+
+  const int n_units = p.num_seqs * p.n_qtiles * (p.hq / 2);   // < 2^31 (host check)
+  const int n_items = p.num_seqs * p.n_qtiles;
+  const int* tab = nullptr;
+  if (n_items <= kThreads) {
+    int* t = reinterpret_cast<int*>(smem + kTabOff);
+    rank_items<kThreads, true, kBN>(p, n_items, t);
+    tab = t;
+  }
+  auto next_unit = [&](int& k, Unit& x) -> bool {
+    return next_valid_unit<2, kThreads, true, kBN>(p, tab, k, x);
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(&B->q_full, 1);
+    mbar_init(&B->q_empty, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&B->kv_full[i], 1);
+      mbar_init(&B->kv_empty[i], 1);
+      mbar_init(&B->v_ready[i], kConvWarps);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&B->s_full[i >> 1][i & 1], 1);
+      mbar_init(&B->p_full[i >> 1][i & 1], 4);
+      mbar_init(&B->pv_done[i >> 1][i & 1], 1);
+      mbar_init(&B->sums[i], 2);
+      mbar_init(&B->squares[i], 2);
+    }
+    mbar_init(&B->o_free, 8);
+    mbar_init(&B->mma_done, 2);           // one commit from each MMA issuer
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&B->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem_base;
+
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsAux));
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tensormap(&tm_q);
+      prefetch_tensormap(&tm_k);
+      prefetch_tensormap(&tm_v);
+      prefetch_tensormap(&tm_o);
+    }
+    const int boxes = kBN >> p.box_log2;                // boxes of a head's tile
+    int gt = 0;                                         // key tiles issued
+    int nq = 0;                                         // Q loads issued
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      Unit x;
+      if (!next_unit(k, x)) break;
+      if (lane == 0) {
+        if (nq > 0) ok = wait_or_abort(&B->q_empty, (nq - 1) & 1, p);
+        if (ok) {
+          mbar_arrive_expect_tx(&B->q_full, 2 * kTileBytes);
+          for (int i = 0; i < 2; ++i)
+            tma_load_3d(smem + kQOff + i * kTileBytes, &tm_q, 0, x.h0 + i, x.q0 + x.row0, &B->q_full);
+        }
+      }
+      ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      ++nq;
+      const int head = (x.h0 / 2) / p.group * 2;        // the KV pair's first head
+      const int nblk = (x.pos_first + x.rows + p.bs - 1) / p.bs;   // up to the last row's block
+      const int32_t* table = p.block_tables + static_cast<long long>(x.s) * p.max_blocks;
+      for (int j = 0; j < x.n_kv; ++j, ++gt) {
+        const int st = gt % kStages;
+        if (gt >= kStages && lane == 0)
+          ok = wait_or_abort(&B->kv_empty[st], ((gt / kStages) - 1) & 1, p);
+        ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&B->kv_full[st], kStageBytes);
+        __syncwarp();
+        // lane: box lane / 4 of K_0, K_1, V_0 or V_1
+        if (lane < 4 * boxes) {
+          const int b = lane >> 2, which = lane & 3;
+          const int u = j * kBN + (b << p.box_log2);    // the box's first key in the unit's list
+          int lb = u / p.bs;                            // logical block
+          const int off = u - lb * p.bs;
+          lb += lb < x.sb ? 0 : x.delta / p.bs;
+          int phys = p.num_blocks;                      // out of range: zero fill
+          if (lb < nblk) {
+            phys = table[lb];
+            if (phys < 0 || phys >= p.num_blocks) {
+              report(p.status, TVL_DEV_BAD_BLOCK_ID);
+              phys = p.num_blocks;
+            }
+          }
+          uint8_t* dst = smem + kKvOff + st * kStageBytes + which * kKvTile +
+                         (static_cast<uint32_t>(b) << p.box_log2) * (kD * 2);
+          tma_load_4d(dst, which < 2 ? &tm_k : &tm_v, 0, head + (which & 1), off, phys, &B->kv_full[st]);
+        }
+      }
+    }
+    // the loads in flight must land before exit
+    if (lane == 0) {
+      for (int t = gt > kStages ? gt - kStages : 0; t < gt; ++t)
+        if (!mbar_wait(&B->kv_full[t % kStages], (t / kStages) & 1)) report(p.status, kDevTimeout);
+      if (nq > 0 && !mbar_wait(&B->q_full, (nq - 1) & 1)) report(p.status, kDevTimeout);
+    }
+  } else if (warp == kQkWarp || warp == kPvWarp) {
+    // ------------------------------------------------------- MMA issuers
+    // Whole warps walk the CTA's stream of key tiles, one elected thread issues.
+    //   Q K^T: S_h(t) into buffer t & 1 once K(t) has landed and P_h V(t - 2), which
+    //   reads P from that buffer, is complete (pv_done) -- across unit boundaries too.
+    //   P.V: O_h += P_h(t) V(t) once P_h(t) is in TMEM (p_full) and V(t) is fp16
+    //   (v_ready); a unit's first one waits until the last unit's O's were read.
+    const bool is_qk = __shfl_sync(kFull, warp, 0) == kQkWarp;
+    const uint32_t q_addr = __shfl_sync(kFull, smem_addr(smem + kQOff), 0);
+    const uint32_t kv_base = __shfl_sync(kFull, smem_addr(smem + kKvOff), 0);
+    const uint32_t td = __shfl_sync(kFull, tmem, 0);
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(kFull, wait_or_abort(bar, parity, p));
+    };
+    int gt = 0, st = 0, ph = 0;                         // key tile, its stage and phase
+    int nq = 0;                                         // units begun
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      Unit x;
+      if (!next_unit(k, x)) break;
+      const int n_kv = x.n_kv;
+      if (!is_qk && nq > 0) ok = wait_all(&B->o_free, (nq - 1) & 1);
+      for (int j = 0; ok && j < n_kv; ++j, ++gt) {
+        const int buf = gt & 1;
+        const uint32_t kv_addr = kv_base + st * kStageBytes;
+        if (is_qk) {
+          ok = wait_all(&B->kv_full[st], ph);
+          if (ok && j == 0) ok = wait_all(&B->q_full, nq & 1);
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            if (ok && gt >= 2) ok = wait_all(&B->pv_done[hh][buf], ((gt >> 1) - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t da = desc_sw128(q_addr + hh * kTileBytes, 16, 1024);
+            const uint64_t db = desc_sw128(kv_addr + hh * kKvTile, 16, 1024);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < kD / 16; ++kk)
+                mma_f16_ss(td + s_col(hh, buf), da + kk * 2, db + kk * 2, kIdescQK, kk > 0);
+              mma_commit(&B->s_full[hh][buf]);
+              if (hh == 1 && j + 1 == n_kv) mma_commit(&B->q_empty);
+            }
+            __syncwarp();
+          }
+        } else {
+          ok = wait_all(&B->v_ready[st], ph);
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            if (ok) ok = wait_all(&B->p_full[hh][buf], (gt >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            // V_0 and V_1 are the two 64-column atoms of the 128-wide operand
+            const uint64_t db = desc_sw128(kv_addr + 2 * kKvTile, kKvTile, 1024);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < kBN / 16; ++kk)
+                mma_f16_ts(td + o_col(hh), td + s_col(hh, buf) + kk * 8, db + kk * 128, kIdescPV,
+                           (j > 0 || kk > 0));
+              mma_commit(&B->pv_done[hh][buf]);
+              if (hh == 1) mma_commit(&B->kv_empty[st]);
+            }
+            __syncwarp();
+          }
+        }
+        if (++st == kStages) { st = 0; ph ^= 1; }
+      }
+      ++nq;
+    }
+    // every MMA issued must be complete before TMEM is released
+    if (elect_one()) {
+      mma_commit(&B->mma_done);
+      if (!mbar_wait(&B->mma_done, 0)) report(p.status, kDevTimeout);
+    }
+    __syncwarp();
+  } else if (warp >= kConvWarp0) {
+    // ------------------------------------------------------- V conversion
+    // Both V tiles bf16 -> fp16 in place, 16 bytes at a time (the swizzle only
+    // permutes 16-byte chunks within a 128-byte row); keys that no row of the unit
+    // sees become 0: their weights are 0, but 0 times a V that is not finite in fp16
+    // is not.
+    constexpr int kBatch = 2 * kKvTile / 16 / (32 * kConvWarps);   // pieces a lane
+    const int e0 = (warp - kConvWarp0) * 32 + lane;
+    int gt = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      Unit x;
+      if (!next_unit(k, x)) break;
+      for (int j = 0; j < x.n_kv; ++j, ++gt) {
+        const int st = gt % kStages;
+        ok = wait_or_abort(&B->kv_full[st], (gt / kStages) & 1, p);
+        if (__any_sync(kFull, !ok)) { ok = false; break; }
+        uint8_t* vt = smem + kKvOff + st * kStageBytes + 2 * kKvTile;
+        const int end = x.pos_first + x.rows - x.delta - j * kBN;
+        const int low = p.window > 0 ? x.pos_first - p.window - x.delta + 1 - j * kBN : 0;
+        const int sink = p.sinks - j * kBN;
+        const bool all = end >= kBN && (low <= 0 || sink >= kBN);
+        uint4 w[kBatch];                                // loads first: one latency a batch
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          w[i] = *reinterpret_cast<const uint4*>(vt + (e0 + 32 * kConvWarps * i) * 16);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          w[i].x = bf16x2_to_half2(w[i].x);
+          w[i].y = bf16x2_to_half2(w[i].y);
+          w[i].z = bf16x2_to_half2(w[i].z);
+          w[i].w = bf16x2_to_half2(w[i].w);
+        }
+        if (!all) {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int u = ((e0 + 32 * kConvWarps * i) >> 3) & (kBN - 1);   // the piece's key
+            if (!(u < end && (u < sink || u >= low))) w[i] = make_uint4(0, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          *reinterpret_cast<uint4*>(vt + (e0 + 32 * kConvWarps * i) * 16) = w[i];
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B->v_ready[st]);
+      }
+    }
+  }
+  } else {
+    // ------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int hh = warp >> 2;                           // map of this warpgroup
+    const int wi = warp & 3;                            // TMEM lane quadrant
+    const int r = wi * 32 + lane;                       // row == TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(wi * 32) << 16;
+    float* ex = reinterpret_cast<float*>(smem + kExOff);           // [sums, squares][map][row]
+    const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+    int gt = 0;                                         // global key-tile index
+    int units = 0;
+    bool ok = true;
+
+    for (int k = 0; ok; ++k, ++units) {
+      Unit x;
+      if (!next_unit(k, x)) break;
+      // the unit's place, for the output at its end
+      if (lane == 0) B->ustash[warp] = make_int4(x.rows, x.q0 + x.row0, x.h0 / 2, 0);
+      __syncwarp();
+      // positions in the unit's key list
+      const int pos_first = x.pos_first - x.delta;
+      const int qpos = pos_first + r;
+      const int ctx = x.ctx - x.delta;
+      const int n_kv = x.n_kv;
+      float m_used = -INFINITY;                         // reference maximum (log2 units)
+      float2 l2 = make_float2(0.f, 0.f);
+
+      for (int j = 0; j < n_kv; ++j, ++gt) {
+        const int key0 = j * kBN;
+        const int buf = gt & 1;
+        const uint32_t s_addr = tmem + lane_off + s_col(hh, buf);
+        ok = wait_or_abort(&B->s_full[hh][buf], (gt >> 1) & 1, p);
+        if (__any_sync(kFull, !ok)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t sr[2][32];                             // this row's 64 scores
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) tmem_ld32(s_addr + cc * 32, sr[cc]);
+        tmem_ld_wait();
+        // Tiles on the causal diagonal, past the context or across the window's edge
+        // need the mask: masked scores are set to infinity (against the scale's sign),
+        // so that one path serves every tile.
+        bool masked = (key0 + kBN - 1 > pos_first) || (key0 + kBN > ctx);
+        masked |= p.window > 0 && key0 <= pos_first + kBM - 1 - p.window && key0 + kBN > p.sinks;
+        if (masked) {
+          const int limit = min(qpos, ctx - 1) - key0;  // last visible column
+          // columns below `low` are visible only below `sink`
+          const int low = p.window > 0 ? qpos - p.window + 1 - key0 : -0x40000000;
+          const int sink = p.sinks - key0;
+          auto below = [](int n) -> uint32_t {          // bits 0 .. n - 1
+            return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+          };
+          const uint32_t none = __float_as_uint(p.scale_log2 < 0.f ? INFINITY : -INFINITY);
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            const uint32_t hid = ~below(limit + 1 - 32 * cc) | (below(low - 32 * cc) & ~below(sink - 32 * cc));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (hid >> e & 1u) sr[cc][e] = none;
+          }
+        }
+        // row maximum of the scaled scores of this tile
+        auto tile_max = [&]() -> float {
+          if (p.scale_log2 >= 0.f) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                mx = max3(mx, __uint_as_float(sr[cc][e]), __uint_as_float(sr[cc][e + 1]));
+            return mx * p.scale_log2;
+          }
+          float mn = INFINITY;
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              mn = min3(mn, __uint_as_float(sr[cc][e]), __uint_as_float(sr[cc][e + 1]));
+          return mn * p.scale_log2;
+        };
+        uint32_t pk[32];
+        // P = 2^(s * scale * log2e - m) as fp16 pairs; returns the fp32 row sum
+        auto make_p = [&](float mref) -> float2 {
+          const float2 nm2 = make_float2(-mref, -mref);
+          float2 tsum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float2 v = make_float2(__uint_as_float(sr[cc][e]), __uint_as_float(sr[cc][e + 1]));
+              v = __ffma2_rn(v, sl2, nm2);
+              const float2 pv = make_float2(ex2(v.x), ex2(v.y));
+              tsum = __fadd2_rn(tsum, pv);
+              pk[cc * 16 + e / 2] = pack_half2(pv.x, pv.y);
+            }
+          return tsum;
+        };
+        if (j == 0) m_used = tile_max();
+        // P straight from the reference maximum; only a row sum that shows some P near
+        // the fp16 limit (65504), or a row that had no key yet, calls for the tile's
+        // maximum
+        float2 tsum = make_p(m_used == -INFINITY ? 0.f : m_used);
+        const bool move = j > 0 && (!(tsum.x + tsum.y <= 60000.f) || m_used == -INFINITY);
+        if (__any_sync(kFull, move)) {
+          float f = 1.f;
+          if (move) {
+            const float m_new = fmaxf(m_used, tile_max());
+            f = m_new == -INFINITY ? 1.f : ex2(m_used - m_new);
+            m_used = m_new;
+          }
+          tsum = make_p(m_used == -INFINITY ? 0.f : m_used);
+          l2.x *= f;
+          l2.y *= f;
+          // O_h is rescaled when every P V before this tile's is complete; this
+          // tile's waits for this warp's P
+          ok = wait_or_abort(&B->pv_done[hh][buf ^ 1], ((gt - 1) >> 1) & 1, p);
+          if (__any_sync(kFull, !ok)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int cc = 0; cc < kDV / 32; ++cc) {
+            const uint32_t at = tmem + lane_off + o_col(hh) + cc * 32;
+            uint32_t o[32];
+            tmem_ld32(at, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(at, o);
+          }
+        }
+        l2 = __fadd2_rn(l2, tsum);
+        tmem_st32(s_addr, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B->p_full[hh][buf]);
+      }
+      if (!ok) break;
+      // ---- the unit's end: both O's are complete once their last P V is
+      const int last = gt - 1;
+      ok = wait_or_abort(&B->pv_done[0][last & 1], (last >> 1) & 1, p) &&
+           wait_or_abort(&B->pv_done[1][last & 1], (last >> 1) & 1, p);
+      if (__any_sync(kFull, !ok)) { ok = false; break; }
+      tc_fence_after();
+      const int4 us = B->ustash[warp];                  // rows, first output row, pair
+      const int r0 = wi * 32;                           // the warp's first row
+      const int nrows = min(32, us.x - r0);             // rows of it inside the unit
+      const int pairs = p.hq / 2;
+      ex[hh * kBM + r] = l2.x + l2.y;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&B->sums[wi]);
+        bulk_wait_read();                               // the last unit's stores have read the staging
+      }
+      const float lam = lane < nrows
+                            ? p.tail.lam[(us.y + r) * p.tail.lam_stride + us.z] : 0.f;
+      ok = wait_or_abort(&B->sums[wi], units & 1, p);
+      if (__any_sync(kFull, !ok)) { ok = false; break; }
+      const float f0 = 1.0f / ex[r], f1 = lam / ex[kBM + r];
+      // this warp's half of the dimensions
+      float d[64];
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        uint32_t a[32], b[32];
+        tmem_ld32(tmem + lane_off + o_col(0) + 64 * hh + 32 * cc, a);
+        tmem_ld32(tmem + lane_off + o_col(1) + 64 * hh + 32 * cc, b);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)     // (the products rounded one by one: equal maps cancel exactly)
+          d[32 * cc + e] = __fmul_rn(__uint_as_float(a[e]), f0) - __fmul_rn(__uint_as_float(b[e]), f1);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B->o_free);
+      float2 sq[4] = {};
+#pragma unroll
+      for (int e = 0; e < 64; e += 2) {
+        const float2 v = make_float2(d[e], d[e + 1]);
+        sq[(e >> 1) & 3] = __ffma2_rn(v, v, sq[(e >> 1) & 3]);
+      }
+      const float2 s2 = __fadd2_rn(__fadd2_rn(sq[0], sq[1]), __fadd2_rn(sq[2], sq[3]));
+      const float half = s2.x + s2.y;
+      ex[(2 + hh) * kBM + r] = half;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B->squares[wi]);
+      ok = wait_or_abort(&B->squares[wi], units & 1, p);
+      if (__any_sync(kFull, !ok)) { ok = false; break; }
+      const float ss = ex[2 * kBM + r] + ex[3 * kBM + r];
+      const float fac = diff_factor(p.tail, ss);
+      if (lane < nrows && !isfinite(ss)) report(p.status, TVL_DEV_NONFINITE);
+      auto bf16x8 = [&](int jc) -> uint4 {              // dimensions 64 hh + 8 jc ..
+        float wt[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wt[i] = fac;
+        if (p.tail.weight != nullptr) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.tail.weight) + 8 * hh + jc);
+          const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y), e = bf16x2_to_float2(w.z),
+                       g = bf16x2_to_float2(w.w);
+          wt[0] *= a.x; wt[1] *= a.y; wt[2] *= b.x; wt[3] *= b.y;
+          wt[4] *= e.x; wt[5] *= e.y; wt[6] *= g.x; wt[7] *= g.y;
+        }
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(d[8 * jc + 2 * i] * wt[2 * i],
+                                                         d[8 * jc + 2 * i + 1] * wt[2 * i + 1]);
+          o[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(o[0], o[1], o[2], o[3]);
+      };
+      // Each warp stages its 32 rows x 64 dimensions in the tensor store's layout
+      // (128-byte rows, 16-byte chunks in swizzled order j ^ (r & 7)); whole 16-row
+      // groups leave through the TMA engine, the rows behind them from registers.
+      uint8_t* st_half = smem + kOutOff + hh * (kBM * 128);
+      const int full = nrows >= 32 ? 32 : (nrows >= 16 ? 16 : 0);
+      uint4* row_out = reinterpret_cast<uint4*>(
+          static_cast<__nv_bfloat16*>(p.out) + (static_cast<long long>(us.y + r) * pairs + us.z) * kDV + 64 * hh);
+#pragma unroll
+      for (int jc = 0; jc < 8; ++jc) {
+        const uint4 v = bf16x8(jc);
+        if (lane < full)
+          *reinterpret_cast<uint4*>(st_half + r * 128 + ((jc ^ (r & 7)) << 4)) = v;
+        else if (lane < nrows)
+          row_out[jc] = v;
+      }
+      fence_async_smem();                               // the staging, for the TMA engine
+      __syncwarp();
+      if (lane == 0 && full > 0) {
+        for (int g = 0; g < full; g += 16)
+          tma_store_3d(&tm_o, st_half + (r0 + g) * 128, 64 * hh, us.z, us.y + r0 + g);
+        bulk_commit();
+      }
+    }
+    if (lane == 0) bulk_wait_all();                     // the output stores are complete
+    if (threadIdx.x == 0) {
+      // units of sequences with inconsistent lengths were skipped: say so
+      for (int k = 0;; ++k) {
+        const long long u = unit_index(k, c, G);
+        if (u >= n_units) break;
+        Unit x;
+        unit_info<2, kThreads, true, kBN>(p, tab, static_cast<int>(u), x);
+        if (x.bad) report(p.status, x.bad_ctx ? TVL_DEV_BAD_CONTEXT_LEN : TVL_DEV_BAD_QUERY_LEN);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_diff_prefill(const DiffPrefillArgs& a, cudaStream_t stream) {
+  DiffPrefillParams p = {};
+  p.box_tokens = a.block_size < kBN ? a.block_size : kBN;
+  while ((1 << p.box_log2) < p.box_tokens) ++p.box_log2;
+  const int pairs = a.num_q_heads / 2;
+  CUtensorMap tq, tk, tv, to;
+  {
+    // the output [Tq, pairs, 128]: 16-row x 64-column tiles
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kDV), static_cast<cuuint64_t>(pairs),
+                                static_cast<cuuint64_t>(a.total_q_tokens)};
+    const cuuint64_t strides[2] = {kDV * 2, static_cast<cuuint64_t>(pairs) * kDV * 2};
+    const cuuint32_t box[3] = {64, 1, 16};
+    if (!make_map(&to, a.out, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(a.num_q_heads),
+                                static_cast<cuuint64_t>(a.total_q_tokens)};
+    const cuuint64_t strides[2] = {kD * 2, static_cast<cuuint64_t>(a.num_q_heads) * kD * 2};
+    const cuuint32_t box[3] = {kD, 1, kBM};
+    if (!make_map(&tq, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(a.num_kv_heads),
+                                static_cast<cuuint64_t>(a.block_size),
+                                static_cast<cuuint64_t>(a.num_blocks)};
+    const cuuint64_t strides[3] = {
+        kD * 2, static_cast<cuuint64_t>(a.num_kv_heads) * kD * 2,
+        static_cast<cuuint64_t>(a.block_size) * a.num_kv_heads * kD * 2};
+    const cuuint32_t box[4] = {kD, 1, static_cast<cuuint32_t>(p.box_tokens), 1};
+    if (!make_map(&tk, a.k_cache, 4, dims, strides, box)) return cudaErrorInvalidValue;
+    if (!make_map(&tv, a.v_cache, 4, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  p.out = a.out;
+  p.query_start_loc = a.query_start_loc;
+  p.block_tables = a.block_tables;
+  p.context_lens = a.context_lens;
+  p.num_seqs = a.num_seqs;
+  p.total_q = a.total_q_tokens;
+  p.hq = a.num_q_heads;
+  p.hkv = a.num_kv_heads;
+  p.group = a.num_q_heads / a.num_kv_heads;
+  p.bs = a.block_size;
+  p.num_blocks = a.num_blocks;
+  p.max_blocks = a.max_blocks_per_seq;
+  p.n_qtiles = (a.max_q_len + kBM - 1) / kBM;
+  p.scale_log2 = a.scale * kLog2e;
+  // masked scores become infinities, which a zero scale would turn into NaN; 1e-37
+  // times any finite score that leaves P other than 1 is out of range
+  if (fabsf(p.scale_log2) < 1e-37f) p.scale_log2 = copysignf(1e-37f, p.scale_log2);
+  p.status = a.status;
+  // a window or sinks past the table's capacity act as the capacity (and keep the
+  // mask's arithmetic inside 32 bits)
+  const int cap = a.max_blocks_per_seq * a.block_size;
+  p.window = a.window < cap ? a.window : cap;
+  p.sinks = a.window == 0 ? 0 : a.sinks < cap ? a.sinks : cap;
+  p.tail.lam = a.lam;
+  p.tail.lam_stride = a.lam_per_token ? pairs : 0;
+  p.tail.weight = static_cast<const __nv_bfloat16*>(a.norm_weight);
+  p.tail.eps = a.norm_eps;
+  p.tail.out_scale = a.out_scale;
+  // once per device: the shared-memory limit, and the check that the register split
+  // fits the registers the block is launched with
+  static PerDeviceOnce once;
+  cudaError_t e = once.run([] {
+    cudaError_t r = cudaFuncSetAttribute(diff_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmemBytes);
+    if (r != cudaSuccess) return r;
+    cudaFuncAttributes fa;
+    r = cudaFuncGetAttributes(&fa, diff_prefill_kernel);
+    if (r != cudaSuccess) return r;
+    if (fa.numRegs * kThreads < 256 * kRegsSoftmax + 256 * kRegsAux) {
+      set_last_error("differential prefill register allocation smaller than its register split");
+      return cudaErrorInvalidConfiguration;
+    }
+    return cudaSuccess;
+  });
+  if (e != cudaSuccess) return e;
+  // persistent: one CTA per SM (at most one per unit); a plain launch, as the CTAs
+  // should start together (see prefill.cu)
+  const long long units = static_cast<long long>(a.num_seqs) * p.n_qtiles * pairs;
+  const dim3 grid(static_cast<unsigned>(units < a.num_sms ? units : a.num_sms));
+  diff_prefill_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, to, p);
+  return cudaGetLastError();
+}
+
+}  // namespace tvl

@@ -249,6 +249,27 @@ int diff_max_ctas(int num_kv_heads, int sms);
 size_t diff_workspace_bytes(int ctas, int num_q_heads);
 cudaError_t launch_diff_decode(const DiffDecodeArgs& a, cudaStream_t stream);
 
+struct DiffPrefillArgs {
+  void* out;               // bf16 [Tq, Hq / 2, 128]
+  const void* q;
+  const int32_t* query_start_loc;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const float* lam;        // [Hq / 2], or [Tq, Hq / 2]
+  bool lam_per_token;
+  const void* norm_weight; // bf16 [128], or null: no norm
+  float norm_eps, out_scale;
+  int num_seqs, total_q_tokens, max_q_len, num_q_heads, num_kv_heads;
+  int block_size, num_blocks, max_blocks_per_seq;
+  float scale;
+  int window, sinks;       // window 0: none
+  int num_sms;             // the persistent grid's size bound
+  uint32_t* status;
+};
+cudaError_t launch_diff_prefill(const DiffPrefillArgs& a, cudaStream_t stream);
+
 // Sets the calling thread's tvl_last_error() text.
 void set_last_error(const char* msg);
 

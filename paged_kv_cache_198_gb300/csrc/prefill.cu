@@ -81,31 +81,17 @@
 // the scores 32 at a time in rolled loops, 242; a fourth stage, 203; the heads
 // started half a tile apart, no gain; the masks set in place in the plain form
 // too, 132-134 against 130 (flushed L2).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include <mutex>
-
-#include "device.cuh"
-#include "kernels.h"
-#include "tc.cuh"
+#include "prefill_tiles.cuh"
 
 namespace tvl {
 namespace {
 
-constexpr int kD = 64;
-constexpr int kBM = 128;
 constexpr int kBN = 128;
 constexpr int kStages = 3;
 constexpr int kConvBatch = 8;           // 16-byte pieces of V a lane converts at once
                                         // (one converting warp: 2800 -> 2170 cycles a tile)
 constexpr int kOPitch = kD * 4 + 16;    // bytes per staged output row: 16-byte rows
                                         // land on distinct banks (no conflicts)
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr unsigned kFull = 0xffffffffu;
-constexpr uint32_t kTileBytes = kBM * kD * 2;      // 16 KB: 128 rows x 128 B
 
 constexpr uint32_t kIdescQK = idesc_f16_f32acc(1, 0, kBM, kBN);   // bf16, K-major B
 constexpr uint32_t kIdescPV = idesc_f16_f32acc(0, 1, kBM, kD);    // fp16, MN-major B
@@ -157,163 +143,6 @@ struct Barriers {
 };
 static_assert(sizeof(Barriers) <= 512, "barrier area");
 
-struct Params {
-  void* out;             // fp32, or bf16 (kWin)
-  const int32_t* query_start_loc;
-  const int32_t* block_tables;
-  const int32_t* context_lens;
-  int num_seqs, total_q, hq, hkv, group, bs, num_blocks, max_blocks, n_qtiles;
-  float scale_log2;
-  uint32_t* status;
-  int window, sinks;     // kWin; window 0: none
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-
-__device__ __forceinline__ float min3(float a, float b, float c) {
-  float y;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ uint32_t bf16x2_to_half2(uint32_t w) {
-  const float2 f = bf16x2_to_float2(w);
-  return pack_half2(f.x, f.y);
-}
-
-// Bounded wait that records a timeout in the status word; returns false
-// when the caller must stop (every role then leaves its loop).
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const Params& p) {
-  if (mbar_wait(bar, parity)) return true;
-  report(p.status, kDevTimeout);
-  return false;
-}
-
-// True in one thread of the (converged) warp, always the same one.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t pred;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(pred));
-  return pred != 0;
-}
-
-// One work unit: a 128-row query tile of NH query heads of one sequence.
-// Every role of the CTA derives the same units in the same order.
-struct Unit {
-  int s, h0, q0, row0, rows, pos_first, ctx, n_kv;
-  int sb, delta;   // kWin: sink blocks; tokens left out behind them
-  bool valid;      // rows to compute and consistent lengths
-  bool bad;        // the sequence's lengths are inconsistent (reported, skipped)
-  bool bad_ctx;    // the inconsistency is a context past the table's capacity
-};
-
-// The key list of a query tile whose rows start at position pos_first: sb sink
-// blocks, then the blocks from the first row's window on, delta tokens later.
-__device__ __forceinline__ void window_blocks(const Params& p, int pos_first, int& sb, int& delta) {
-  const int first = p.window > 0 ? max(0, pos_first - p.window + 1) : 0;
-  const int w0 = first / p.bs;
-  sb = min(p.sinks / p.bs + (p.sinks % p.bs != 0 ? 1 : 0), w0);
-  delta = (w0 - sb) * p.bs;
-}
-
-// Index of the k-th unit of CTA c among G: the units in longest-first order
-// are dealt to the CTAs row by row, every other row reversed (c, 2G-1-c,
-// 2G+c, ...), which evens out the CTAs' totals.  Increases with k.
-__device__ __forceinline__ long long unit_index(int k, int c, int G) {
-  return static_cast<long long>(k) * G + ((k & 1) ? G - 1 - c : c);
-}
-
-// Unit u: rank u / pairs in the item order, head group u % pairs.  With
-// `tab`, the order and the items' lengths come from shared memory (tab[0..K)
-// rank -> item, then K-strided q0, Lq and context per item); without it the
-// order is the item order and the lengths are read from global memory.
-template <int NH, int K, bool kWin>
-__device__ __forceinline__ void unit_info(const Params& p, const int* tab, int u, Unit& x) {
-  const int pairs = p.hq / NH;
-  const int rank = u / pairs;
-  x.h0 = (u - rank * pairs) * NH;
-  int item, lq;
-  if (tab != nullptr) {
-    item = tab[rank];
-    x.q0 = tab[K + item];
-    lq = tab[2 * K + item];
-    x.ctx = tab[3 * K + item];
-  } else {
-    item = rank;
-    const int si = item / p.n_qtiles;
-    x.q0 = p.query_start_loc[si];
-    lq = p.query_start_loc[si + 1] - x.q0;
-    x.ctx = p.context_lens[si];
-  }
-  x.s = item / p.n_qtiles;
-  x.row0 = (p.n_qtiles - 1 - item % p.n_qtiles) * kBM;
-  const int cap = p.max_blocks * p.bs;
-  const bool rows_here = x.row0 < lq;
-  // The whole sequence is skipped (and reported) when its query rows would
-  // leave [0, total_q) -- a negative or decreasing query_start_loc entry, or
-  // one past total_q_tokens -- when it has more rows than max_q_len's query
-  // tiles cover, or when its context cannot hold its chunk or exceeds the
-  // block table.  So no unit ever addresses a row outside `out`.
-  const bool bad_rows = x.q0 < 0 || lq < 0 ||
-                        static_cast<long long>(x.q0) + lq > static_cast<long long>(p.total_q) ||
-                        lq > p.n_qtiles * kBM;
-  x.bad_ctx = !bad_rows && x.ctx > cap;
-  x.bad = bad_rows || (lq > 0 && (x.ctx < lq || x.ctx > cap));
-  x.valid = rows_here && !x.bad;
-  x.rows = min(kBM, lq - x.row0);
-  x.pos_first = x.ctx - lq + x.row0;
-  x.n_kv = (x.pos_first + x.rows - 1) / kBN + 1;
-  if constexpr (kWin) {
-    window_blocks(p, x.pos_first, x.sb, x.delta);
-    x.n_kv = (x.pos_first + x.rows - 1 - x.delta) / kBN + 1;
-  }
-}
-
-// The first unit of this CTA at or after index k that has work; k moves to
-// it.  Called by whole warps; the fields go through lane 0, so that the
-// compiler sees them warp-uniform (fewer registers).
-template <int NH, int K, bool kWin>
-__device__ __forceinline__ bool next_valid_unit(const Params& p, const int* tab, int& k, Unit& x) {
-  const int n_units = p.num_seqs * p.n_qtiles * (p.hq / NH);
-  for (;; ++k) {
-    const long long u = unit_index(k, blockIdx.x, gridDim.x);
-    if (u >= n_units) return false;
-    unit_info<NH, K, kWin>(p, tab, static_cast<int>(u), x);
-    if (__shfl_sync(kFull, x.valid ? 1 : 0, 0)) break;
-  }
-  x.s = __shfl_sync(kFull, x.s, 0);
-  x.h0 = __shfl_sync(kFull, x.h0, 0);
-  x.q0 = __shfl_sync(kFull, x.q0, 0);
-  x.row0 = __shfl_sync(kFull, x.row0, 0);
-  x.rows = __shfl_sync(kFull, x.rows, 0);
-  x.pos_first = __shfl_sync(kFull, x.pos_first, 0);
-  x.ctx = __shfl_sync(kFull, x.ctx, 0);
-  x.n_kv = __shfl_sync(kFull, x.n_kv, 0);
-  if constexpr (kWin) {
-    x.sb = __shfl_sync(kFull, x.sb, 0);
-    x.delta = __shfl_sync(kFull, x.delta, 0);
-  }
-  return true;
-}
-
 template <int NH, bool kWin>
 __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -334,51 +163,16 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
   grid_dependency_wait();          // inputs may come from the preceding kernel
   grid_dependents_launch();
 
-  // ---- the item order.  Item i is sequence i / n_qtiles, query tile
-  // n_qtiles - 1 - i % n_qtiles.  Items with the most key tiles go first
-  // (ties in item order), so the long ones are not left for the end.  Every
-  // CTA ranks the items the same way from the lengths, one item per thread
-  // (beyond that, item order is kept); the ranks are a permutation of the
-  // items whatever the lengths hold.
   const int n_units = p.num_seqs * p.n_qtiles * (p.hq / NH);   // < 2^31 (host check)
   const int n_items = p.num_seqs * p.n_qtiles;
   const int* tab = nullptr;
   if (n_items <= K) {
     int* t = reinterpret_cast<int*>(smem + C::kTabOff);
-    int* keys = t + 4 * K;
-    const int i = threadIdx.x;
-    int key = 0;
-    if (i < n_items) {
-      const int si = i / p.n_qtiles;
-      const int qt = p.n_qtiles - 1 - i % p.n_qtiles;
-      const int qa = p.query_start_loc[si];
-      const int lqi = p.query_start_loc[si + 1] - qa;
-      const int ci = p.context_lens[si];
-      const int last = ci - lqi + min((qt + 1) * kBM, lqi);   // keys seen
-      key = qt * kBM >= lqi ? 0 : (last + kBN - 1) / kBN;
-      if constexpr (kWin) {
-        int sb, delta;
-        window_blocks(p, ci - lqi + qt * kBM, sb, delta);
-        if (key > 0) key = (last - delta + kBN - 1) / kBN;
-      }
-      keys[i] = key;
-      t[K + i] = qa;
-      t[2 * K + i] = lqi;
-      t[3 * K + i] = ci;
-    }
-    __syncthreads();
-    if (i < n_items) {
-      int r = 0;
-      for (int j = 0; j < n_items; ++j) {
-        const int kj = keys[j];
-        r += (kj > key || (kj == key && j < i)) ? 1 : 0;
-      }
-      t[r] = i;
-    }
+    rank_items<K, kWin, kBN>(p, n_items, t);
     tab = t;
   }
   auto next_unit = [&](int& k, Unit& x) -> bool {
-    return next_valid_unit<NH, K, kWin>(p, tab, k, x);
+    return next_valid_unit<NH, K, kWin, kBN>(p, tab, k, x);
   };
 
   if (threadIdx.x == 0) {
@@ -906,7 +700,7 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
         const long long u = unit_index(k, c, G);
         if (u >= n_units) break;
         Unit x;
-        unit_info<NH, K, kWin>(p, tab, static_cast<int>(u), x);
+        unit_info<NH, K, kWin, kBN>(p, tab, static_cast<int>(u), x);
         if (x.bad) report(p.status, x.bad_ctx ? TVL_DEV_BAD_CONTEXT_LEN : TVL_DEV_BAD_QUERY_LEN);
       }
     }
@@ -917,34 +711,6 @@ __global__ void __launch_bounds__(Cfg<NH>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
-}
-
-// ------------------------------------------------------------ tensor maps
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaDriverEntryPointQueryResult q;
-    void* f = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
-bool make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
-              const cuuint64_t* strides, const cuuint32_t* box,
-              CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = fn(m, type, rank, const_cast<void*>(base), dims,
-                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
 }
 
 template <int NH, bool kWin>

@@ -6,8 +6,9 @@ A = sum_j p_j |v_j| and B = scale * max_j sum_d |q_d k_jd| (as in window_common)
   e = A * (2 * (80 * 2^-24 * B + 2^-21) + 2^-bits + (n / 16 + 64) * 2^-23)
 with the weights kept in `bits` bits: 2^-15 in the decode (two bf16 parts, 2^-8 each
 time, with one bit to spare), 2^-11 in the prefill (fp16), whose P.V also adds n / 8
-products in the tensor core: (n / 8 + 64) * 2^-23, and V below 2^-14 keeps an absolute
-error of 2^-25 a token.  d = o1 - lambda o2 is then off by E = e1 + |lambda| e2 +
+products in the tensor core: (n / 8 + 64) * 2^-23, V below 2^-14 keeps an absolute
+error of 2^-25, and so does a weight below 2^-14 of the reference's (whose sum is at
+least 1): 2^-25 sum_j |v_j|.  d = o1 - lambda o2 is then off by E = e1 + |lambda| e2 +
 2^-22 (|o1| + |lambda o2|).  The norm divides by r = sqrt(mean d^2 + eps):
   |error of d_i / r| <= E_i / r + |d_i| / r * (rms(E) / r + 2^-21),
 where r is taken as at least r - rms(E) in the denominators.
@@ -24,7 +25,7 @@ def attend(q, k, v, scale, bits, prefill):
     o, a, b = C.attend(q, k, v, scale)
     n = len(k)
     e = a * (2 * (80 * 2.0 ** -24 * b + 2.0 ** -21) + 2.0 ** -bits + (n / (8 if prefill else 16) + 64) * 2.0 ** -23)
-    return o, e + (2.0 ** -25 if prefill else 1e-37)
+    return o, e + (2.0 ** -25 * (1 + np.abs(v).sum(0)) if prefill else 1e-37)
 
 
 def pair_row(q1, q2, k1, k2, v, scale, lam, weight, eps, out_scale, bits, prefill=False):

@@ -44,8 +44,31 @@ def test_decode_refusals(tvl, bad, want):
     assert tvl._load().tvl_last_error()
 
 
+def _prefill(t, **k):
+    a = dict(out=D16, q=D16, qsl=D16, kc=D16, vc=D16, tab=D16, ctx=D16, lam=D16, per=0, w=D16, eps=1e-5,
+             osc=1.0, s=4, tq=20, mq=7, hq=8, hkv=2, d=64, bs=16, nb=64, mb=8, scale=0.125, window=0, sinks=0)
+    a.update(k)
+    return t._load().tvl_diff_attention_prefill(*a.values(), None)
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(s=-1), "INVALID_ARG"), (dict(tq=-1), "INVALID_ARG"), (dict(mq=-1), "INVALID_ARG"),
+    (dict(mq=0), "INVALID_ARG"), (dict(d=128), "UNSUPPORTED"), (dict(bs=24), "UNSUPPORTED"),
+    (dict(hq=9), "INVALID_ARG"), (dict(hq=9, hkv=3), "INVALID_ARG"), (dict(hq=18, hkv=2), "UNSUPPORTED"),
+    (dict(nb=0), "INVALID_ARG"), (dict(nb=1 << 27), "UNSUPPORTED"), (dict(mb=1 << 26), "UNSUPPORTED"),
+    (dict(s=65536), "UNSUPPORTED"), (dict(s=65535, mq=1 << 20), "UNSUPPORTED"),
+    (dict(mq=2 ** 31 - 1, s=20), "UNSUPPORTED"), (dict(window=-1), "INVALID_ARG"), (dict(sinks=-1), "INVALID_ARG"),
+    (dict(scale=float("inf")), "INVALID_ARG"), (dict(out=None), "INVALID_ARG"), (dict(out=D16 + 8), "INVALID_ARG"),
+    (dict(qsl=None), "INVALID_ARG"), (dict(kc=D16 + 8), "INVALID_ARG"), (dict(lam=None), "INVALID_ARG"),
+    (dict(w=D16 + 2), "INVALID_ARG"), (dict(eps=-0.5), "INVALID_ARG"), (dict(osc=float("nan")), "INVALID_ARG")])
+def test_prefill_refusals(tvl, bad, want):
+    assert _prefill(tvl, **bad) == getattr(tvl, "ERR_" + want)
+    assert tvl._load().tvl_last_error()
+
+
 def test_no_sequences_is_ok(tvl):
     assert _decode(tvl, s=0, out=None, q=None, ws=None) == tvl.OK
+    assert _prefill(tvl, s=0, out=None) == tvl.OK and _prefill(tvl, tq=0, mq=0, q=None) == tvl.OK
 
 
 def test_binding_checks(tvl):
