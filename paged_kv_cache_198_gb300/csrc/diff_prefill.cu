@@ -14,8 +14,9 @@
 //           takes a tile's 64 scores into registers, writes P = 2^(s - m) as fp16 over
 //           the scores' own TMEM columns, and hands them to P V.  m is the first tile's
 //           maximum and moves only when a tile's row sum nears the fp16 limit.
-//   8       producer: Q tiles, and per key tile the two keys and two V heads of each
-//           physical block, one TMA box each (the paged gather)
+//   8, 11   producers: Q tiles and the two keys, and the two V heads, of each key tile's
+//           physical blocks, one TMA box each (the paged gather).  K's ring turns when
+//           its scores are done, V's when its P V is
 //   9       issues S_h = Q_h K_h^T (M 128, N 64, bf16, both operands in shared memory)
 //   10      issues O_h += P_h V (M 128, N 128, fp16, P read from TMEM)
 //   12..15  V conversion bf16 -> fp16 in place (as in prefill.cu)
@@ -33,15 +34,16 @@ namespace tvl {
 namespace {
 
 constexpr int kBN = 64;
-constexpr int kStages = 4;
+constexpr int kKStages = 4, kVStages = 5;
 constexpr int kThreads = 512;
-constexpr int kProducerWarp = 8, kQkWarp = 9, kPvWarp = 10, kConvWarp0 = 12, kConvWarps = 4;
+constexpr int kKWarp = 8, kQkWarp = 9, kPvWarp = 10, kVWarp = 11, kConvWarp0 = 12, kConvWarps = 4;
 constexpr uint32_t kKvTile = kBN * kD * 2;            // 8 KB: one head's K (or V) of a tile
-constexpr uint32_t kStageBytes = 4 * kKvTile;         // K_0, K_1, V_0, V_1
+constexpr uint32_t kStageBytes = 2 * kKvTile;         // K_0, K_1 or V_0, V_1
 
 constexpr uint32_t kQOff = 0;
-constexpr uint32_t kKvOff = 2 * kTileBytes;
-constexpr uint32_t kOutOff = kKvOff + kStages * kStageBytes;   // two halves of 128 rows x 128 B
+constexpr uint32_t kKOff = 2 * kTileBytes;
+constexpr uint32_t kVOff = kKOff + kKStages * kStageBytes;
+constexpr uint32_t kOutOff = kVOff + kVStages * kStageBytes;   // two halves of 128 rows x 128 B
 constexpr uint32_t kBarOff = kOutOff + 2 * kBM * 128;
 constexpr uint32_t kExOff = kBarOff + 1024;                    // the maps' exchange, [2][2][128]
 constexpr uint32_t kTabOff = kExOff + 4 * kBM * 4;
@@ -63,7 +65,8 @@ constexpr uint32_t kTmemCols = 512;
 
 struct Barriers {
   uint64_t q_full, q_empty;
-  uint64_t kv_full[kStages], kv_empty[kStages], v_ready[kStages];
+  uint64_t k_full[kKStages], k_empty[kKStages];
+  uint64_t v_full[kVStages], v_ready[kVStages], v_empty[kVStages];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // [map][buffer]
   uint64_t o_free;               // both O's read at a unit's end
   uint64_t sums[4], squares[4];  // per row quarter: the maps' exchanges
@@ -110,10 +113,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(&B->q_full, 1);
     mbar_init(&B->q_empty, 1);
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&B->kv_full[i], 1);
-      mbar_init(&B->kv_empty[i], 1);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&B->k_full[i], 1);
+      mbar_init(&B->k_empty[i], 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&B->v_full[i], 1);
       mbar_init(&B->v_ready[i], kConvWarps);
+      mbar_init(&B->v_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&B->s_full[i >> 1][i & 1], 1);
@@ -137,69 +144,74 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsAux));
-  if (warp == kProducerWarp) {
-    // ------------------------------------------------------------ producer
+  if (warp == kKWarp || warp == kVWarp) {
+    // ---------------------------------------------------------- producers
+    // One warp loads Q and K, one V, each through a ring of its own.
+    const bool is_k = warp == kKWarp;
+    const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+    const int stages = is_k ? kKStages : kVStages;
+    uint64_t* full = is_k ? B->k_full : B->v_full;
+    uint64_t* empty = is_k ? B->k_empty : B->v_empty;
+    uint8_t* ring = smem + (is_k ? kKOff : kVOff);
     if (lane == 0) {
-      prefetch_tensormap(&tm_q);
-      prefetch_tensormap(&tm_k);
-      prefetch_tensormap(&tm_v);
-      prefetch_tensormap(&tm_o);
+      prefetch_tensormap(tm);
+      prefetch_tensormap(is_k ? &tm_q : &tm_o);
     }
     const int boxes = kBN >> p.box_log2;                // boxes of a head's tile
-    int gt = 0;                                         // key tiles issued
-    int nq = 0;                                         // Q loads issued
+    int gt = 0, st = 0, ph = 0;                         // key tiles issued; stage, its phase
+    int nq = 0;                                         // units begun
     bool ok = true;
     for (int k = 0; ok; ++k) {
       Unit x;
       if (!next_unit(k, x)) break;
-      if (lane == 0) {
-        if (nq > 0) ok = wait_or_abort(&B->q_empty, (nq - 1) & 1, p);
-        if (ok) {
-          mbar_arrive_expect_tx(&B->q_full, 2 * kTileBytes);
-          for (int i = 0; i < 2; ++i)
-            tma_load_3d(smem + kQOff + i * kTileBytes, &tm_q, 0, x.h0 + i, x.q0 + x.row0, &B->q_full);
+      if (is_k) {
+        if (lane == 0) {
+          if (nq > 0) ok = wait_or_abort(&B->q_empty, (nq - 1) & 1, p);
+          if (ok) {
+            mbar_arrive_expect_tx(&B->q_full, 2 * kTileBytes);
+            for (int i = 0; i < 2; ++i)
+              tma_load_3d(smem + kQOff + i * kTileBytes, &tm_q, 0, x.h0 + i, x.q0 + x.row0, &B->q_full);
+          }
         }
+        ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
       }
-      ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
-      if (!ok) break;
       ++nq;
       const int head = (x.h0 / 2) / p.group * 2;        // the KV pair's first head
       const int nblk = (x.pos_first + x.rows + p.bs - 1) / p.bs;   // up to the last row's block
       const int32_t* table = p.block_tables + static_cast<long long>(x.s) * p.max_blocks;
       for (int j = 0; j < x.n_kv; ++j, ++gt) {
-        const int st = gt % kStages;
-        if (gt >= kStages && lane == 0)
-          ok = wait_or_abort(&B->kv_empty[st], ((gt / kStages) - 1) & 1, p);
+        // lane: box lane / 2 of the first or the second head
+        const int b = lane >> 1, which = lane & 1;
+        const int u = j * kBN + (b << p.box_log2);      // the box's first key in the unit's list
+        int lb = u / p.bs;                              // logical block
+        const int off = u - lb * p.bs;
+        lb += lb < x.sb ? 0 : x.delta / p.bs;
+        int phys = p.num_blocks;                        // out of range: zero fill
+        if (b < boxes && lb < nblk) {
+          phys = table[lb];
+          if (phys < 0 || phys >= p.num_blocks) {
+            report(p.status, TVL_DEV_BAD_BLOCK_ID);
+            phys = p.num_blocks;
+          }
+        }
+        if (gt >= stages && lane == 0) ok = wait_or_abort(&empty[st], ph ^ 1, p);
         ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&B->kv_full[st], kStageBytes);
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], kStageBytes);
         __syncwarp();
-        // lane: box lane / 4 of K_0, K_1, V_0 or V_1
-        if (lane < 4 * boxes) {
-          const int b = lane >> 2, which = lane & 3;
-          const int u = j * kBN + (b << p.box_log2);    // the box's first key in the unit's list
-          int lb = u / p.bs;                            // logical block
-          const int off = u - lb * p.bs;
-          lb += lb < x.sb ? 0 : x.delta / p.bs;
-          int phys = p.num_blocks;                      // out of range: zero fill
-          if (lb < nblk) {
-            phys = table[lb];
-            if (phys < 0 || phys >= p.num_blocks) {
-              report(p.status, TVL_DEV_BAD_BLOCK_ID);
-              phys = p.num_blocks;
-            }
-          }
-          uint8_t* dst = smem + kKvOff + st * kStageBytes + which * kKvTile +
-                         (static_cast<uint32_t>(b) << p.box_log2) * (kD * 2);
-          tma_load_4d(dst, which < 2 ? &tm_k : &tm_v, 0, head + (which & 1), off, phys, &B->kv_full[st]);
-        }
+        if (b < boxes)
+          tma_load_4d(ring + st * kStageBytes + which * kKvTile +
+                          (static_cast<uint32_t>(b) << p.box_log2) * (kD * 2),
+                      tm, 0, head + which, off, phys, &full[st]);
+        if (++st == stages) { st = 0; ph ^= 1; }
       }
     }
     // the loads in flight must land before exit
     if (lane == 0) {
-      for (int t = gt > kStages ? gt - kStages : 0; t < gt; ++t)
-        if (!mbar_wait(&B->kv_full[t % kStages], (t / kStages) & 1)) report(p.status, kDevTimeout);
-      if (nq > 0 && !mbar_wait(&B->q_full, (nq - 1) & 1)) report(p.status, kDevTimeout);
+      for (int t = gt > stages ? gt - stages : 0; t < gt; ++t)
+        if (!mbar_wait(&full[t % stages], (t / stages) & 1)) report(p.status, kDevTimeout);
+      if (is_k && nq > 0 && !mbar_wait(&B->q_full, (nq - 1) & 1)) report(p.status, kDevTimeout);
     }
   } else if (warp == kQkWarp || warp == kPvWarp) {
     // ------------------------------------------------------- MMA issuers
@@ -210,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     //   (v_ready); a unit's first one waits until the last unit's O's were read.
     const bool is_qk = __shfl_sync(kFull, warp, 0) == kQkWarp;
     const uint32_t q_addr = __shfl_sync(kFull, smem_addr(smem + kQOff), 0);
-    const uint32_t kv_base = __shfl_sync(kFull, smem_addr(smem + kKvOff), 0);
+    const uint32_t kv_base = __shfl_sync(kFull, smem_addr(smem + (is_qk ? kKOff : kVOff)), 0);
     const uint32_t td = __shfl_sync(kFull, tmem, 0);
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(kFull, wait_or_abort(bar, parity, p));
@@ -227,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int buf = gt & 1;
         const uint32_t kv_addr = kv_base + st * kStageBytes;
         if (is_qk) {
-          ok = wait_all(&B->kv_full[st], ph);
+          ok = wait_all(&B->k_full[st], ph);
           if (ok && j == 0) ok = wait_all(&B->q_full, nq & 1);
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
@@ -241,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int kk = 0; kk < kD / 16; ++kk)
                 mma_f16_ss(td + s_col(hh, buf), da + kk * 2, db + kk * 2, kIdescQK, kk > 0);
               mma_commit(&B->s_full[hh][buf]);
+              if (hh == 1) mma_commit(&B->k_empty[st]);
               if (hh == 1 && j + 1 == n_kv) mma_commit(&B->q_empty);
             }
             __syncwarp();
@@ -253,19 +266,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             // V_0 and V_1 are the two 64-column atoms of the 128-wide operand
-            const uint64_t db = desc_sw128(kv_addr + 2 * kKvTile, kKvTile, 1024);
+            const uint64_t db = desc_sw128(kv_addr, kKvTile, 1024);
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kBN / 16; ++kk)
                 mma_f16_ts(td + o_col(hh), td + s_col(hh, buf) + kk * 8, db + kk * 128, kIdescPV,
                            (j > 0 || kk > 0));
               mma_commit(&B->pv_done[hh][buf]);
-              if (hh == 1) mma_commit(&B->kv_empty[st]);
+              if (hh == 1) mma_commit(&B->v_empty[st]);
             }
             __syncwarp();
           }
         }
-        if (++st == kStages) { st = 0; ph ^= 1; }
+        if (++st == (is_qk ? kKStages : kVStages)) { st = 0; ph ^= 1; }
       }
       ++nq;
     }
@@ -283,16 +296,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // is not.
     constexpr int kBatch = 2 * kKvTile / 16 / (32 * kConvWarps);   // pieces a lane
     const int e0 = (warp - kConvWarp0) * 32 + lane;
-    int gt = 0;
+    int st = 0, ph = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       Unit x;
       if (!next_unit(k, x)) break;
-      for (int j = 0; j < x.n_kv; ++j, ++gt) {
-        const int st = gt % kStages;
-        ok = wait_or_abort(&B->kv_full[st], (gt / kStages) & 1, p);
+      for (int j = 0; j < x.n_kv; ++j) {
+        ok = wait_or_abort(&B->v_full[st], ph, p);
         if (__any_sync(kFull, !ok)) { ok = false; break; }
-        uint8_t* vt = smem + kKvOff + st * kStageBytes + 2 * kKvTile;
+        uint8_t* vt = smem + kVOff + st * kStageBytes;
         const int end = x.pos_first + x.rows - x.delta - j * kBN;
         const int low = p.window > 0 ? x.pos_first - p.window - x.delta + 1 - j * kBN : 0;
         const int sink = p.sinks - j * kBN;
@@ -321,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&B->v_ready[st]);
+        if (++st == kVStages) { st = 0; ph ^= 1; }
       }
     }
   }
