@@ -45,8 +45,8 @@ constexpr uint32_t kKOff = 2 * kTileBytes;
 constexpr uint32_t kVOff = kKOff + kKStages * kStageBytes;
 constexpr uint32_t kOutOff = kVOff + kVStages * kStageBytes;   // two halves of 128 rows x 128 B
 constexpr uint32_t kBarOff = kOutOff + 2 * kBM * 128;
-constexpr uint32_t kExOff = kBarOff + 1024;                    // the maps' exchange, [2][2][128]
-constexpr uint32_t kTabOff = kExOff + 4 * kBM * 4;
+constexpr uint32_t kExOff = kBarOff + 1024;
+constexpr uint32_t kTabOff = kExOff + 3072;
 constexpr uint32_t kSmemBytes = kTabOff + 5 * 4 * kThreads + 1024;   // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
 
@@ -76,6 +76,14 @@ struct Barriers {
 };
 static_assert(sizeof(Barriers) <= 1024, "barrier area");
 
+// What the two maps' warps of a row exchange at a unit's end, and what they need there.
+struct Exchange {
+  float l[2][kBM], squares[2][kBM];      // [map]: sum of P; [half]: sum of d^2
+  float lam[kBM];
+  float weight[kDV];
+};
+static_assert(sizeof(Exchange) <= 3072, "exchange area");
+
 struct DiffPrefillParams : Params {
   DiffTail tail;
   int box_tokens, box_log2;      // tokens of a TMA box: min(bs, kBN)
@@ -90,6 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Barriers* B = reinterpret_cast<Barriers*>(smem + kBarOff);
+  Exchange* X = reinterpret_cast<Exchange*>(smem + kExOff);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int G = static_cast<int>(gridDim.x);
@@ -133,6 +142,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&B->mma_done, 2);           // one commit from each MMA issuer
     fence_barrier_init();
   }
+  if (threadIdx.x < kDV)
+    X->weight[threadIdx.x] =
+        p.tail.weight != nullptr ? __bfloat162float(p.tail.weight[threadIdx.x]) : 1.f;
   if (warp == 0) {
     tmem_alloc(&B->tmem_base, kTmemCols);
     tmem_relinquish();
@@ -344,7 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wi = warp & 3;                            // TMEM lane quadrant
     const int r = wi * 32 + lane;                       // row == TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(wi * 32) << 16;
-    float* ex = reinterpret_cast<float*>(smem + kExOff);           // [sums, squares][map][row]
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
     int gt = 0;                                         // global key-tile index
     int units = 0;
@@ -355,6 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!next_unit(k, x)) break;
       // the unit's place, for the output at its end
       if (lane == 0) B->ustash[warp] = make_int4(x.rows, x.q0 + x.row0, x.h0 / 2, 0);
+      if (hh == 0 && r < x.rows)                        // lambda, there by the unit's end
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(&X->lam[r])),
+                     "l"(p.tail.lam + (x.q0 + x.row0 + r) * p.tail.lam_stride + x.h0 / 2)
+                     : "memory");
       __syncwarp();
       // positions in the unit's key list
       const int pos_first = x.pos_first - x.delta;
@@ -483,17 +498,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r0 = wi * 32;                           // the warp's first row
       const int nrows = min(32, us.x - r0);             // rows of it inside the unit
       const int pairs = p.hq / 2;
-      ex[hh * kBM + r] = l2.x + l2.y;
+      X->l[hh][r] = l2.x + l2.y;
+      asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&B->sums[wi]);
         bulk_wait_read();                               // the last unit's stores have read the staging
       }
-      const float lam = lane < nrows
-                            ? p.tail.lam[(us.y + r) * p.tail.lam_stride + us.z] : 0.f;
       ok = wait_or_abort(&B->sums[wi], units & 1, p);
       if (__any_sync(kFull, !ok)) { ok = false; break; }
-      const float f0 = 1.0f / ex[r], f1 = lam / ex[kBM + r];
+      const float f0 = 1.0f / X->l[0][r], f1 = (lane < nrows ? X->lam[r] : 0.f) / X->l[1][r];
       // this warp's half of the dimensions
       float d[64];
 #pragma unroll
@@ -517,25 +531,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float2 s2 = __fadd2_rn(__fadd2_rn(sq[0], sq[1]), __fadd2_rn(sq[2], sq[3]));
       const float half = s2.x + s2.y;
-      ex[(2 + hh) * kBM + r] = half;
+      X->squares[hh][r] = half;
       __syncwarp();
       if (lane == 0) mbar_arrive(&B->squares[wi]);
       ok = wait_or_abort(&B->squares[wi], units & 1, p);
       if (__any_sync(kFull, !ok)) { ok = false; break; }
-      const float ss = ex[2 * kBM + r] + ex[3 * kBM + r];
+      const float ss = X->squares[0][r] + X->squares[1][r];
       const float fac = diff_factor(p.tail, ss);
       if (lane < nrows && !isfinite(ss)) report(p.status, TVL_DEV_NONFINITE);
       auto bf16x8 = [&](int jc) -> uint4 {              // dimensions 64 hh + 8 jc ..
-        float wt[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) wt[i] = fac;
-        if (p.tail.weight != nullptr) {
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.tail.weight) + 8 * hh + jc);
-          const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y), e = bf16x2_to_float2(w.z),
-                       g = bf16x2_to_float2(w.w);
-          wt[0] *= a.x; wt[1] *= a.y; wt[2] *= b.x; wt[3] *= b.y;
-          wt[4] *= e.x; wt[5] *= e.y; wt[6] *= g.x; wt[7] *= g.y;
-        }
+        const float4 wa = reinterpret_cast<const float4*>(X->weight)[16 * hh + 2 * jc];
+        const float4 wb = reinterpret_cast<const float4*>(X->weight)[16 * hh + 2 * jc + 1];
+        const float wt[8] = {fac * wa.x, fac * wa.y, fac * wa.z, fac * wa.w,
+                             fac * wb.x, fac * wb.y, fac * wb.z, fac * wb.w};
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
