@@ -76,6 +76,12 @@ struct Barriers {
 };
 static_assert(sizeof(Barriers) <= 1024, "barrier area");
 
+// A row's reference is its first tile's maximum.  P may pass it, up to kMaxSum a tile,
+// below fp16's 65504; a tile that would pass it moves the reference to its own maximum,
+// and so does one that needs the mask and is 2^kHeadroom above it (64 P's of 2^8 stay
+// below kMaxSum, so a tile over it always has a P that moves the reference).
+constexpr float kMaxSum = 60000.f, kHeadroom = 8.f;
+
 // What the two maps' warps of a row exchange at a unit's end, and what they need there.
 struct Exchange {
   float l[2][kBM], squares[2][kBM];      // [map]: sum of P; [half]: sum of d^2
@@ -378,114 +384,134 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_kv = x.n_kv;
       float m_used = -INFINITY;                         // reference maximum (log2 units)
       float2 l2 = make_float2(0.f, 0.f);
-
-      for (int j = 0; j < n_kv; ++j, ++gt) {
-        const int key0 = j * kBN;
+      // tiles first .. end - 1 need no mask: whole before the first row's diagonal, and
+      // past every row's window's edge
+      const int end = (pos_first + 1) / kBN;
+      const int edge = p.window > 0 ? pos_first + kBM - p.window : 0;   // (keys below may be masked)
+      const int first = edge > 0 ? (edge + kBN - 1) / kBN : 0;
+      uint32_t sr[2][32];                               // this row's 64 scores
+      uint32_t pk[32];
+      // a tile's scores, into registers
+      auto take = [&]() -> bool {
         const int buf = gt & 1;
         const uint32_t s_addr = tmem + lane_off + s_col(hh, buf);
         ok = wait_or_abort(&B->s_full[hh][buf], (gt >> 1) & 1, p);
-        if (__any_sync(kFull, !ok)) { ok = false; break; }
+        if (__any_sync(kFull, !ok)) return ok = false;
         tc_fence_after();
-        uint32_t sr[2][32];                             // this row's 64 scores
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) tmem_ld32(s_addr + cc * 32, sr[cc]);
         tmem_ld_wait();
-        // Tiles on the causal diagonal, past the context or across the window's edge
-        // need the mask: masked scores are set to infinity (against the scale's sign),
-        // so that one path serves every tile.
-        bool masked = (key0 + kBN - 1 > pos_first) || (key0 + kBN > ctx);
-        masked |= p.window > 0 && key0 <= pos_first + kBM - 1 - p.window && key0 + kBN > p.sinks;
-        if (masked) {
-          const int limit = min(qpos, ctx - 1) - key0;  // last visible column
-          // columns below `low` are visible only below `sink`
-          const int low = p.window > 0 ? qpos - p.window + 1 - key0 : -0x40000000;
-          const int sink = p.sinks - key0;
-          auto below = [](int n) -> uint32_t {          // bits 0 .. n - 1
-            return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-          };
-          const uint32_t none = __float_as_uint(p.scale_log2 < 0.f ? INFINITY : -INFINITY);
+        return true;
+      };
+      // P = 2^(s * scale * log2e - m) as fp16 pairs; returns the fp32 row sum
+      auto make_p = [&]() -> float2 {
+        const float mref = m_used == -INFINITY ? 0.f : m_used;
+        const float2 nm2 = make_float2(-mref, -mref);
+        float2 tsum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            const uint32_t hid = ~below(limit + 1 - 32 * cc) | (below(low - 32 * cc) & ~below(sink - 32 * cc));
+        for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (hid >> e & 1u) sr[cc][e] = none;
+          for (int e = 0; e < 32; e += 2) {
+            float2 v = make_float2(__uint_as_float(sr[cc][e]), __uint_as_float(sr[cc][e + 1]));
+            v = __ffma2_rn(v, sl2, nm2);
+            const float2 pv = make_float2(ex2(v.x), ex2(v.y));
+            tsum = __fadd2_rn(tsum, pv);
+            pk[cc * 16 + e / 2] = pack_half2(pv.x, pv.y);
           }
-        }
-        // row maximum of the scaled scores of this tile
-        auto tile_max = [&]() -> float {
+        return tsum;
+      };
+      // the tile's P, over its scores' columns, to P V
+      auto give = [&]() {
+        tmem_st32(tmem + lane_off + s_col(hh, gt & 1), pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B->p_full[hh][gt & 1]);
+      };
+
+      for (int j = 0; j < n_kv;) {
+        // ---- a tile of any kind: the first one, one that needs the mask, or one that
+        // moves the reference
+        {
+          if (!take()) break;
+          const int key0 = j * kBN;
+          if (j < first || j >= end) {
+            // Masked scores are set to infinity (against the scale's sign).
+            const int limit = min(qpos, ctx - 1) - key0;  // last visible column
+            // columns below `low` are visible only below `sink`
+            const int low = p.window > 0 ? qpos - p.window + 1 - key0 : -0x40000000;
+            const int sink = p.sinks - key0;
+            auto below = [](int n) -> uint32_t {          // bits 0 .. n - 1
+              return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+            };
+            const uint32_t none = __float_as_uint(p.scale_log2 < 0.f ? INFINITY : -INFINITY);
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              const uint32_t hid = ~below(limit + 1 - 32 * cc) | (below(low - 32 * cc) & ~below(sink - 32 * cc));
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (hid >> e & 1u) sr[cc][e] = none;
+            }
+          }
+          // the row's maximum of the scaled scores
+          float mt;
           if (p.scale_log2 >= 0.f) {
-            float mx = -INFINITY;
+            mt = -INFINITY;
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
               for (int e = 0; e < 32; e += 2)
-                mx = max3(mx, __uint_as_float(sr[cc][e]), __uint_as_float(sr[cc][e + 1]));
-            return mx * p.scale_log2;
+                mt = max3(mt, __uint_as_float(sr[cc][e]), __uint_as_float(sr[cc][e + 1]));
+          } else {
+            mt = INFINITY;
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                mt = min3(mt, __uint_as_float(sr[cc][e]), __uint_as_float(sr[cc][e + 1]));
           }
-          float mn = INFINITY;
-#pragma unroll
-          for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              mn = min3(mn, __uint_as_float(sr[cc][e]), __uint_as_float(sr[cc][e + 1]));
-          return mn * p.scale_log2;
-        };
-        uint32_t pk[32];
-        // P = 2^(s * scale * log2e - m) as fp16 pairs; returns the fp32 row sum
-        auto make_p = [&](float mref) -> float2 {
-          const float2 nm2 = make_float2(-mref, -mref);
-          float2 tsum = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float2 v = make_float2(__uint_as_float(sr[cc][e]), __uint_as_float(sr[cc][e + 1]));
-              v = __ffma2_rn(v, sl2, nm2);
-              const float2 pv = make_float2(ex2(v.x), ex2(v.y));
-              tsum = __fadd2_rn(tsum, pv);
-              pk[cc * 16 + e / 2] = pack_half2(pv.x, pv.y);
-            }
-          return tsum;
-        };
-        if (j == 0) m_used = tile_max();
-        // P straight from the reference maximum; only a row sum that shows some P near
-        // the fp16 limit (65504), or a row that had no key yet, calls for the tile's
-        // maximum
-        float2 tsum = make_p(m_used == -INFINITY ? 0.f : m_used);
-        const bool move = j > 0 && (!(tsum.x + tsum.y <= 60000.f) || m_used == -INFINITY);
-        if (__any_sync(kFull, move)) {
-          float f = 1.f;
-          if (move) {
-            const float m_new = fmaxf(m_used, tile_max());
-            f = m_new == -INFINITY ? 1.f : ex2(m_used - m_new);
-            m_used = m_new;
-          }
-          tsum = make_p(m_used == -INFINITY ? 0.f : m_used);
-          l2.x *= f;
-          l2.y *= f;
-          // O_h is rescaled when every P V before this tile's is complete; this
-          // tile's waits for this warp's P
-          ok = wait_or_abort(&B->pv_done[hh][buf ^ 1], ((gt - 1) >> 1) & 1, p);
-          if (__any_sync(kFull, !ok)) { ok = false; break; }
-          tc_fence_after();
+          mt *= p.scale_log2;
+          const bool move = mt > m_used + kHeadroom;
+          if (__any_sync(kFull, move)) {
+            const float f = move ? ex2(m_used - mt) : 1.f;
+            if (move) m_used = mt;
+            l2 = __fmul2_rn(l2, make_float2(f, f));
+            if (j > 0) {
+              // O_h is rescaled when every P V before this tile's is complete; this
+              // tile's waits for this warp's P
+              ok = wait_or_abort(&B->pv_done[hh][(gt & 1) ^ 1], ((gt - 1) >> 1) & 1, p);
+              if (__any_sync(kFull, !ok)) { ok = false; break; }
+              tc_fence_after();
 #pragma unroll 1
-          for (int cc = 0; cc < kDV / 32; ++cc) {
-            const uint32_t at = tmem + lane_off + o_col(hh) + cc * 32;
-            uint32_t o[32];
-            tmem_ld32(at, o);
-            tmem_ld_wait();
+              for (int cc = 0; cc < kDV / 32; ++cc) {
+                const uint32_t at = tmem + lane_off + o_col(hh) + cc * 32;
+                uint32_t o[32];
+                tmem_ld32(at, o);
+                tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(at, o);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(at, o);
+              }
+            }
           }
+          l2 = __fadd2_rn(l2, make_p());
+          give();
+          ++j;
+          ++gt;
         }
-        l2 = __fadd2_rn(l2, tsum);
-        tmem_st32(s_addr, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&B->p_full[hh][buf]);
+        // ---- whole tiles, straight from the reference, in a loop of their own (short
+        // code: it runs at the pace of its instruction fetch).  A row sum that shows a P
+        // near the fp16 limit sends the tile back to the part above.
+        while (j >= first && j < end) {
+          if (!take()) break;
+          const float2 tsum = make_p();
+          if (__any_sync(kFull, !(tsum.x + tsum.y <= kMaxSum) || m_used == -INFINITY)) break;
+          l2 = __fadd2_rn(l2, tsum);
+          give();
+          ++j;
+          ++gt;
+        }
+        if (!ok) break;
       }
       if (!ok) break;
       // ---- the unit's end: both O's are complete once their last P V is
