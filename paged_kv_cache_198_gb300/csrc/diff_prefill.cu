@@ -13,20 +13,38 @@
 //   0..7    softmax, a warpgroup a map: thread r owns query row r (TMEM lane r).  It
 //           takes a tile's 64 scores into registers, writes P = 2^(s - m) as fp16 over
 //           the scores' own TMEM columns, and hands them to P V.  m is the first tile's
-//           maximum and moves only when a tile's row sum nears the fp16 limit.
+//           maximum and moves only when a tile's row sum nears the fp16 limit
 //   8, 11   producers: Q tiles and the two keys, and the two V heads, of each key tile's
 //           physical blocks, one TMA box each (the paged gather).  K's ring turns when
 //           its scores are done, V's when its P V is
 //   9       issues S_h = Q_h K_h^T (M 128, N 64, bf16, both operands in shared memory)
 //   10      issues O_h += P_h V (M 128, N 128, fp16, P read from TMEM)
-//   12..15  V conversion bf16 -> fp16 in place (as in prefill.cu)
+//   12..15  V conversion bf16 -> fp16 in place (as in prefill.cu), and the output
 // TMEM: S/P of map h in two buffers of 64 columns each (256), O_0 and O_1 128 each:
 // all 512.  With O 128 wide there is no room for P beside S; two buffers a map let one
 // tile's P V and the Q K^T after next run while the softmax works on the tile between.
 //
-// At a unit's end the two warps of a row quarter, one a map, each take half of the 128
-// dimensions of both O's: they exchange the row sums, then the halves' sums of squares
-// of d = O_0 / l_0 - lambda O_1 / l_1, and store their half through swizzled staging.
+// At a unit's end the softmax leaves the row sums and goes on; the conversion warps,
+// which run ahead of it, read both O's: a thread takes a row's d = O_0 / l_0 - lambda
+// O_1 / l_1 twice, for the norm and for the output.
+//
+// What bounds it: a softmax warp's chain of steps a tile, some 1600 cycles (scores seen,
+// loaded, 620 for 64 exponentials with two warps a scheduler, vote, store, arrival), not
+// the tensor pipe (45% active), the exp unit (31%) or issue slots (55%).  Timing copies
+// that leave work out say the same (2 sequences x 4096 rows, window 4096, 396 us then):
+// a quarter of the MMAs 400, no exponentials 369, no V conversion 373.
+// Measured: 16 chunks of 512 rows on prefixes of 0-2k 156 us, 837 TFLOP/s of visible
+// work; 2 sequences x 4096 rows, window 4096, 363-370 us, 1090 TFLOP/s; 100 rows 18.4 us.
+// What brought it there, us of the first two:
+//   - K and V in rings of their own, a producer each: 193 -> 160 (bs 16: 16 boxes a tile);
+//   - whole tiles in a short loop of their own: 392 -> 375;
+//   - the output by the conversion warps: 375 -> 366; an arrival without a branch: 363.
+// Measured and left (same two): four softmax warpgroups, a map's two taking alternate
+// tiles and sharing the reference, 179 / 462 (a buffer's MMAs and its warpgroup wait for
+// each other); one MMA issuer a map 183 / 464; halves of a tile in turn 173 / 437; the
+// next tile's scores fetched behind the store 159 / 357; P handed over behind the next
+// tile's first exponentials 178 / 477; parked waits 166 / 422 on 158 / 392; units worked
+// out by one warp for all 160 / 369.
 #include "diff.cuh"
 #include "prefill_tiles.cuh"
 
@@ -35,6 +53,7 @@ namespace {
 
 constexpr int kBN = 64;
 constexpr int kKStages = 4, kVStages = 5;
+constexpr int kSlots = 4;
 constexpr int kThreads = 512;
 constexpr int kKWarp = 8, kQkWarp = 9, kPvWarp = 10, kVWarp = 11, kConvWarp0 = 12, kConvWarps = 4;
 constexpr uint32_t kKvTile = kBN * kD * 2;            // 8 KB: one head's K (or V) of a tile
@@ -46,7 +65,7 @@ constexpr uint32_t kVOff = kKOff + kKStages * kStageBytes;
 constexpr uint32_t kOutOff = kVOff + kVStages * kStageBytes;   // two halves of 128 rows x 128 B
 constexpr uint32_t kBarOff = kOutOff + 2 * kBM * 128;
 constexpr uint32_t kExOff = kBarOff + 1024;
-constexpr uint32_t kTabOff = kExOff + 3072;
+constexpr uint32_t kTabOff = kExOff + 5120;
 constexpr uint32_t kSmemBytes = kTabOff + 5 * 4 * kThreads + 1024;   // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
 
@@ -69,10 +88,9 @@ struct Barriers {
   uint64_t v_full[kVStages], v_ready[kVStages], v_empty[kVStages];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // [map][buffer]
   uint64_t o_free;               // both O's read at a unit's end
-  uint64_t sums[4], squares[4];  // per row quarter: the maps' exchanges
+  uint64_t sums[kSlots];         // a unit's row sums are there
   uint64_t mma_done;
   uint32_t tmem_base;
-  int4 ustash[8];                // per softmax warp: its unit's rows, first output row, pair
 };
 static_assert(sizeof(Barriers) <= 1024, "barrier area");
 
@@ -82,13 +100,23 @@ static_assert(sizeof(Barriers) <= 1024, "barrier area");
 // below kMaxSum, so a tile over it always has a P that moves the reference).
 constexpr float kMaxSum = 60000.f, kHeadroom = 8.f;
 
-// What the two maps' warps of a row exchange at a unit's end, and what they need there.
+// What the output needs of the softmax: the row sums of a unit, in one of kSlots places
+// (the softmax can be done with two units more while one waits to be written out).
 struct Exchange {
-  float l[2][kBM], squares[2][kBM];      // [map]: sum of P; [half]: sum of d^2
-  float lam[kBM];
+  float l[kSlots][2][kBM];
   float weight[kDV];
 };
-static_assert(sizeof(Exchange) <= 3072, "exchange area");
+static_assert(sizeof(Exchange) <= 5120, "exchange area");
+
+// Arrival of lane 0, as a predicated instruction.
+__device__ __forceinline__ void arrive_lane0(uint64_t* bar, int lane) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.eq.s32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(lane)
+      : "memory");
+}
 
 struct DiffPrefillParams : Params {
   DiffTail tail;
@@ -141,10 +169,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B->s_full[i >> 1][i & 1], 1);
       mbar_init(&B->p_full[i >> 1][i & 1], 4);
       mbar_init(&B->pv_done[i >> 1][i & 1], 1);
-      mbar_init(&B->sums[i], 2);
-      mbar_init(&B->squares[i], 2);
+      mbar_init(&B->sums[i], 8);
     }
-    mbar_init(&B->o_free, 8);
+    static_assert(kSlots == 4, "initialised with the maps' buffers");
+    mbar_init(&B->o_free, kConvWarps);
     mbar_init(&B->mma_done, 2);           // one commit from each MMA issuer
     fence_barrier_init();
   }
@@ -307,21 +335,126 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp >= kConvWarp0) {
-    // ------------------------------------------------------- V conversion
+    // ----------------------------------------------- V conversion and output
     // Both V tiles bf16 -> fp16 in place, 16 bytes at a time (the swizzle only
     // permutes 16-byte chunks within a 128-byte row); keys that no row of the unit
     // sees become 0: their weights are 0, but 0 times a V that is not finite in fp16
     // is not.
+    //
+    // A unit is written out by these warps, behind the next unit's first two tiles, so
+    // that the softmax goes on with those: its third tile's scores wait for the first
+    // one's P V, which waits until the last unit's O's are read.
     constexpr int kBatch = 2 * kKvTile / 16 / (32 * kConvWarps);   // pieces a lane
     const int e0 = (warp - kConvWarp0) * 32 + lane;
-    int st = 0, ph = 0;
+    const int r = e0;                                   // row == TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(r & ~31) << 16;
+    struct {
+      int rows, row, pair, last;                        // its rows, first output row, last key tile
+      float lam;
+      bool due;
+    } out = {};
+    int st = 0, ph = 0, gt = 0, written = 0;
     bool ok = true;
+    auto wait = [&](uint64_t* bar, int phase) -> bool {
+      ok = wait_or_abort(bar, phase & 1, p);
+      if (__any_sync(kFull, !ok)) ok = false;
+      return ok;
+    };
+    auto write_out = [&]() -> bool {
+      const int slot = written % kSlots;
+      if (!wait(&B->sums[slot], written / kSlots)) return false;
+      if (!wait(&B->pv_done[0][out.last & 1], out.last >> 1)) return false;
+      if (!wait(&B->pv_done[1][out.last & 1], out.last >> 1)) return false;
+      ++written;
+      out.due = false;
+      tc_fence_after();
+      const float f0 = 1.0f / X->l[slot][0][r], f1 = -out.lam / X->l[slot][1][r];
+      // 16 dimensions of d = O_0 / l_0 - lambda O_1 / l_1 (the products rounded one by
+      // one, in scalar operations, as packed ones are fused with the sum: equal maps cancel
+      // exactly)
+      auto difference = [&](int cc, float2 (&d)[8]) {
+        uint32_t a[16], b[16];
+        tmem_ld16(tmem + lane_off + o_col(0) + 16 * cc, a);
+        tmem_ld16(tmem + lane_off + o_col(1) + 16 * cc, b);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          d[e] = __fadd2_rn(make_float2(__fmul_rn(__uint_as_float(a[2 * e]), f0),
+                                        __fmul_rn(__uint_as_float(a[2 * e + 1]), f0)),
+                            make_float2(__fmul_rn(__uint_as_float(b[2 * e]), f1),
+                                        __fmul_rn(__uint_as_float(b[2 * e + 1]), f1)));
+      };
+      float2 sq = make_float2(0.f, 0.f);
+#pragma unroll 2
+      for (int cc = 0; cc < kDV / 16; ++cc) {
+        float2 d[8];
+        difference(cc, d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sq = __ffma2_rn(d[e], d[e], sq);
+      }
+      const float ss = sq.x + sq.y;
+      const float fac = diff_factor(p.tail, ss);
+      const float2 fac2 = make_float2(fac, fac);
+      const int r0 = r & ~31;                           // the warp's first row
+      const int nrows = min(32, out.rows - r0);         // rows of it inside the unit
+      if (lane < nrows && !isfinite(ss)) report(p.status, TVL_DEV_NONFINITE);
+      // Each warp stages its 32 rows in the tensor store's layout (two halves of 128-byte
+      // rows, 16-byte chunks in swizzled order j ^ (r & 7)); whole 16-row groups leave
+      // through the TMA engine, the rows behind them from registers.
+      if (lane == 0) bulk_wait_read();                  // its last stores have read the rows
+      __syncwarp();
+      uint8_t* staged = smem + kOutOff + r * 128;
+      const int full = nrows >= 32 ? 32 : (nrows >= 16 ? 16 : 0);
+      uint4* row_out = reinterpret_cast<uint4*>(
+          static_cast<__nv_bfloat16*>(p.out) +
+          (static_cast<long long>(out.row + r) * (p.hq / 2) + out.pair) * kDV);
+#pragma unroll 2
+      for (int cc = 0; cc < kDV / 16; ++cc) {
+        float2 d[8];
+        difference(cc, d);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float4* w = reinterpret_cast<const float4*>(X->weight) + 4 * cc + 2 * c;
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float4 f = w[i];
+            const float2 u = __fmul2_rn(__fmul2_rn(d[4 * c + 2 * i], fac2), make_float2(f.x, f.y));
+            const float2 v = __fmul2_rn(__fmul2_rn(d[4 * c + 2 * i + 1], fac2), make_float2(f.z, f.w));
+            const __nv_bfloat162 h = __floats2bfloat162_rn(u.x, u.y);
+            const __nv_bfloat162 g = __floats2bfloat162_rn(v.x, v.y);
+            o[2 * i] = *reinterpret_cast<const uint32_t*>(&h);
+            o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&g);
+          }
+          const uint4 v = make_uint4(o[0], o[1], o[2], o[3]);
+          const int jc = 2 * (cc & 3) + c;
+          if (lane < full)
+            *reinterpret_cast<uint4*>(staged + (cc >> 2) * (kBM * 128) + ((jc ^ (r & 7)) << 4)) = v;
+          else if (lane < nrows)
+            row_out[2 * cc + c] = v;
+        }
+      }
+      tc_fence_before();
+      fence_async_smem();                               // the staging, for the TMA engine
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&B->o_free);
+        for (int g = 0; g < full; g += 16)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            tma_store_3d(&tm_o, smem + kOutOff + half * (kBM * 128) + (r0 + g) * 128, 64 * half, out.pair,
+                         out.row + r0 + g);
+        if (full > 0) bulk_commit();
+      }
+      __syncwarp();
+      return true;
+    };
     for (int k = 0; ok; ++k) {
       Unit x;
       if (!next_unit(k, x)) break;
       for (int j = 0; j < x.n_kv; ++j) {
-        ok = wait_or_abort(&B->v_full[st], ph, p);
-        if (__any_sync(kFull, !ok)) { ok = false; break; }
+        if (j == 2 && out.due && !write_out()) break;
+        if (!wait(&B->v_full[st], ph)) break;
         uint8_t* vt = smem + kVOff + st * kStageBytes;
         const int end = x.pos_first + x.rows - x.delta - j * kBN;
         const int low = p.window > 0 ? x.pos_first - p.window - x.delta + 1 - j * kBN : 0;
@@ -353,7 +486,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&B->v_ready[st]);
         if (++st == kVStages) { st = 0; ph ^= 1; }
       }
+      if (ok && out.due) write_out();
+      gt += x.n_kv;
+      out.rows = x.rows;
+      out.row = x.q0 + x.row0;
+      out.pair = x.h0 / 2;
+      out.last = gt - 1;
+      out.lam = r < x.rows ? p.tail.lam[(out.row + r) * p.tail.lam_stride + out.pair] : 0.f;
+      out.due = true;
     }
+    if (ok && out.due) write_out();
+    if (lane == 0) bulk_wait_all();                     // the output stores are complete
   }
   } else {
     // ------------------------------------------------------------- softmax
@@ -370,13 +513,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok; ++k, ++units) {
       Unit x;
       if (!next_unit(k, x)) break;
-      // the unit's place, for the output at its end
-      if (lane == 0) B->ustash[warp] = make_int4(x.rows, x.q0 + x.row0, x.h0 / 2, 0);
-      if (hh == 0 && r < x.rows)                        // lambda, there by the unit's end
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(&X->lam[r])),
-                     "l"(p.tail.lam + (x.q0 + x.row0 + r) * p.tail.lam_stride + x.h0 / 2)
-                     : "memory");
-      __syncwarp();
       // positions in the unit's key list
       const int pos_first = x.pos_first - x.delta;
       const int qpos = pos_first + r;
@@ -426,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B->p_full[hh][gt & 1]);
+        arrive_lane0(&B->p_full[hh][gt & 1], lane);
       };
 
       for (int j = 0; j < n_kv;) {
@@ -514,95 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       if (!ok) break;
-      // ---- the unit's end: both O's are complete once their last P V is
-      const int last = gt - 1;
-      ok = wait_or_abort(&B->pv_done[0][last & 1], (last >> 1) & 1, p) &&
-           wait_or_abort(&B->pv_done[1][last & 1], (last >> 1) & 1, p);
-      if (__any_sync(kFull, !ok)) { ok = false; break; }
-      tc_fence_after();
-      const int4 us = B->ustash[warp];                  // rows, first output row, pair
-      const int r0 = wi * 32;                           // the warp's first row
-      const int nrows = min(32, us.x - r0);             // rows of it inside the unit
-      const int pairs = p.hq / 2;
-      X->l[hh][r] = l2.x + l2.y;
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      X->l[units % kSlots][hh][r] = l2.x + l2.y;
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&B->sums[wi]);
-        bulk_wait_read();                               // the last unit's stores have read the staging
-      }
-      ok = wait_or_abort(&B->sums[wi], units & 1, p);
-      if (__any_sync(kFull, !ok)) { ok = false; break; }
-      const float f0 = 1.0f / X->l[0][r], f1 = (lane < nrows ? X->lam[r] : 0.f) / X->l[1][r];
-      // this warp's half of the dimensions
-      float d[64];
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        uint32_t a[32], b[32];
-        tmem_ld32(tmem + lane_off + o_col(0) + 64 * hh + 32 * cc, a);
-        tmem_ld32(tmem + lane_off + o_col(1) + 64 * hh + 32 * cc, b);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 32; ++e)     // (the products rounded one by one: equal maps cancel exactly)
-          d[32 * cc + e] = __fmul_rn(__uint_as_float(a[e]), f0) - __fmul_rn(__uint_as_float(b[e]), f1);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&B->o_free);
-      float2 sq[4] = {};
-#pragma unroll
-      for (int e = 0; e < 64; e += 2) {
-        const float2 v = make_float2(d[e], d[e + 1]);
-        sq[(e >> 1) & 3] = __ffma2_rn(v, v, sq[(e >> 1) & 3]);
-      }
-      const float2 s2 = __fadd2_rn(__fadd2_rn(sq[0], sq[1]), __fadd2_rn(sq[2], sq[3]));
-      const float half = s2.x + s2.y;
-      X->squares[hh][r] = half;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&B->squares[wi]);
-      ok = wait_or_abort(&B->squares[wi], units & 1, p);
-      if (__any_sync(kFull, !ok)) { ok = false; break; }
-      const float ss = X->squares[0][r] + X->squares[1][r];
-      const float fac = diff_factor(p.tail, ss);
-      if (lane < nrows && !isfinite(ss)) report(p.status, TVL_DEV_NONFINITE);
-      auto bf16x8 = [&](int jc) -> uint4 {              // dimensions 64 hh + 8 jc ..
-        const float4 wa = reinterpret_cast<const float4*>(X->weight)[16 * hh + 2 * jc];
-        const float4 wb = reinterpret_cast<const float4*>(X->weight)[16 * hh + 2 * jc + 1];
-        const float wt[8] = {fac * wa.x, fac * wa.y, fac * wa.z, fac * wa.w,
-                             fac * wb.x, fac * wb.y, fac * wb.z, fac * wb.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(d[8 * jc + 2 * i] * wt[2 * i],
-                                                         d[8 * jc + 2 * i + 1] * wt[2 * i + 1]);
-          o[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        return make_uint4(o[0], o[1], o[2], o[3]);
-      };
-      // Each warp stages its 32 rows x 64 dimensions in the tensor store's layout
-      // (128-byte rows, 16-byte chunks in swizzled order j ^ (r & 7)); whole 16-row
-      // groups leave through the TMA engine, the rows behind them from registers.
-      uint8_t* st_half = smem + kOutOff + hh * (kBM * 128);
-      const int full = nrows >= 32 ? 32 : (nrows >= 16 ? 16 : 0);
-      uint4* row_out = reinterpret_cast<uint4*>(
-          static_cast<__nv_bfloat16*>(p.out) + (static_cast<long long>(us.y + r) * pairs + us.z) * kDV + 64 * hh);
-#pragma unroll
-      for (int jc = 0; jc < 8; ++jc) {
-        const uint4 v = bf16x8(jc);
-        if (lane < full)
-          *reinterpret_cast<uint4*>(st_half + r * 128 + ((jc ^ (r & 7)) << 4)) = v;
-        else if (lane < nrows)
-          row_out[jc] = v;
-      }
-      fence_async_smem();                               // the staging, for the TMA engine
-      __syncwarp();
-      if (lane == 0 && full > 0) {
-        for (int g = 0; g < full; g += 16)
-          tma_store_3d(&tm_o, st_half + (r0 + g) * 128, 64 * hh, us.z, us.y + r0 + g);
-        bulk_commit();
-      }
+      if (lane == 0) mbar_arrive(&B->sums[units % kSlots]);
     }
-    if (lane == 0) bulk_wait_all();                     // the output stores are complete
     if (threadIdx.x == 0) {
       // units of sequences with inconsistent lengths were skipped: say so
       for (int k = 0;; ++k) {
