@@ -398,6 +398,177 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// -------------------------------------------------------------------- direct
+
+// Small batches of bounded length: a cluster of kSpread CTAs does KV pair z of a
+// sequence alone, in one launch.  Chunk i goes to CTA i mod kSpread, and there to warp
+// i / kSpread mod 8: the warp fetches its chunks' block ids, issues their copies (all of
+// them fit) and q's loads, and waits once.  A CTA adds its warps up; then CTA r takes
+// the group's query pairs r, r + kSpread, ...: it reads the CTAs' sums through
+// distributed shared memory.  Bound by latency (five dependent memory round trips and two
+// cluster barriers): 777 tokens, 8 query heads, 6.4 us, 10.7 through the schedule and
+// the merge.
+constexpr int kSpread = 8;
+constexpr int kDirectMost = 2;                // chunks a warp: what shared memory holds
+constexpr int kDirectClusters = 16;           // at most: two a processing cluster of SMs
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The float at `addr` of this CTA's shared memory, in CTA `rank` of the cluster.
+__device__ __forceinline__ float cluster_load(const float* addr, int rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(addr)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+constexpr uint32_t kPairChunk = 4 * kBf16Tile;        // K_0, K_1, V_0, V_1
+
+__host__ __device__ inline uint32_t direct_smem(int per_warp, int cgs) {
+  return 1024 + kWarps * per_warp * kPairChunk + (kWarps + 1) * cgs * kCols * kCombPitch * 4;
+}
+
+__global__ void __launch_bounds__(kWarps * 32, 1) __cluster_dims__(kSpread, 1, 1)
+    diff_direct_kernel(const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const DiffParams p, int per_warp) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bars[kWarps];
+  __shared__ float norm[kWarps];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int rank = blockIdx.x % kSpread, seq = blockIdx.x / kSpread, kvp = blockIdx.z;
+  uint8_t* mine = smem + w * per_warp * kPairChunk;
+  // [warp][column group][column], then the CTA's own sums
+  float* comb = reinterpret_cast<float*>(smem + kWarps * per_warp * kPairChunk);
+  const int cols = p.cgs * kCols;
+  float* sums = comb + kWarps * cols * kCombPitch;
+  if (lane == 0) {
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+    mbar_init(&bars[w], 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int ctx = load_ctx(p, seq);
+  const Visible vis = visible_of(p, ctx);
+  auto chunk_of = [&](int i) {               // the warp's i-th chunk as a token chunk
+    const int v = rank + kSpread * (w + kWarps * i);
+    return v < vis.ns ? v : v + vis.delta;
+  };
+  const int at = rank + kSpread * w, n = at < vis.n ? (vis.n - 1 - at) / (kSpread * kWarps) + 1 : 0;   // <= per_warp
+  if (n > 0) {
+    int page = 0;
+    if (lane < n) page = p.block_tables[static_cast<long long>(seq) * p.max_blocks + (chunk_of(lane) >> p.cpb_log2)];
+    if (lane == 0) mbar_arrive_expect_tx(&bars[w], n * kPairChunk);
+    __syncwarp();
+    if (lane < n) {
+      if (page < 0 || page >= p.num_blocks) {
+        report(p.status, TVL_DEV_BAD_BLOCK_ID);
+        page = 0;
+      }
+      const long long chunk = (static_cast<long long>(page) << p.cpb_log2) +
+                              (chunk_of(lane) & ((1 << p.cpb_log2) - 1));
+      const int tok = static_cast<int>(chunk * kChunk);
+      tma_load_3d(mine + lane * kPairChunk, &tm_k, 0, tok, 2 * kvp, &bars[w]);
+      tma_load_3d(mine + lane * kPairChunk + 2 * kBf16Tile, &tm_v, 0, tok, 2 * kvp, &bars[w]);
+    }
+  }
+  const uint8_t* q = reinterpret_cast<const uint8_t*>(
+      p.q + (static_cast<size_t>(seq) * p.hq + 2 * static_cast<size_t>(kvp) * p.group) * kD);
+  for (int cg = 0; cg < p.cgs; ++cg) {
+    State st;
+    start(st, p, q, cg);
+    if (cg == 0 && n > 0 && !mbar_wait(&bars[w], 0) && lane == 0) report(p.status, kDevTimeout);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i)
+      process<true>(st, p, mine + i * kPairChunk, 2 * kBf16Tile, chunk_of(i) * kChunk, ctx);
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+      st.l.x += __shfl_xor_sync(kFull, st.l.x, x);
+      st.l.y += __shfl_xor_sync(kFull, st.l.y, x);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float* dst = comb + ((w * p.cgs + cg) * kCols + 2 * t + j) * kCombPitch;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dst[16 * i + g] = st.acc[i][j];
+        dst[16 * i + 8 + g] = st.acc[i][2 + j];
+      }
+      if (g == 0) *reinterpret_cast<float2*>(dst + kDV) = j == 0 ? make_float2(st.m.x, st.l.x) : make_float2(st.m.y, st.l.y);
+    }
+  }
+  __syncthreads();
+  // the CTA's sums: a warp a column, four dimensions a lane
+  for (int c = w; c < cols; c += kWarps) {
+    float top = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) top = fmaxf(top, comb[(i * cols + c) * kCombPitch + kDV]);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const float* src = comb + (i * cols + c) * kCombPitch;
+      const float f = weight_of(src[kDV], top);        // (a warp without chunks: l and o are 0)
+      const float4 v = reinterpret_cast<const float4*>(src)[lane];
+      l = fmaf(f, src[kDV + 1], l);
+      o = make_float4(fmaf(f, v.x, o.x), fmaf(f, v.y, o.y), fmaf(f, v.z, o.z), fmaf(f, v.w, o.w));
+    }
+    float* dst = sums + c * kCombPitch;
+    reinterpret_cast<float4*>(dst)[lane] = o;
+    if (lane == 0) *reinterpret_cast<float2*>(dst + kDV) = make_float2(top, l);
+  }
+  cluster_sync();
+  // query pair h: its maps are columns h and h + 4 of its column group; 128 threads, a
+  // dimension each (the other half of the CTA only takes part in the barriers)
+  for (int h = rank; h < p.group; h += kSpread) {
+    float d = 0.f;
+    if (tid < kDV) {
+      float o[2], l[2];
+#pragma unroll
+      for (int map = 0; map < 2; ++map) {
+        const float* src = sums + ((h >> 2) * kCols + 4 * map + (h & 3)) * kCombPitch;
+        float mv[kSpread], lv[kSpread], ov[kSpread], top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < kSpread; ++r) {
+          mv[r] = cluster_load(src + kDV, r);
+          lv[r] = cluster_load(src + kDV + 1, r);
+          ov[r] = cluster_load(src + tid, r);
+        }
+#pragma unroll
+        for (int r = 0; r < kSpread; ++r) top = fmaxf(top, mv[r]);
+        o[map] = l[map] = 0.f;
+#pragma unroll
+        for (int r = 0; r < kSpread; ++r) {
+          const float f = weight_of(mv[r], top);
+          l[map] = fmaf(f, lv[r], l[map]);
+          o[map] = fmaf(f, ov[r], o[map]);
+        }
+      }
+      const long long pair = static_cast<long long>(kvp) * p.group + h;
+      const float lam = p.tail.lam[seq * p.tail.lam_stride + pair];
+      if (ctx > 0) d = __fmul_rn(o[0], 1.0f / l[0]) - __fmul_rn(o[1], lam / l[1]);
+      float ss = d * d;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) ss += __shfl_xor_sync(kFull, ss, x);
+      if (lane == 0) norm[w] = ss;
+    }
+    __syncthreads();
+    if (tid < kDV) {
+      const float sc = ctx > 0 ? diff_factor(p.tail, (norm[0] + norm[1]) + (norm[2] + norm[3])) : 0.f;
+      const float wt = p.tail.weight != nullptr ? __bfloat162float(p.tail.weight[tid]) : 1.f;
+      p.dout[(static_cast<long long>(seq) * p.pairs + static_cast<long long>(kvp) * p.group + h) * kDV + tid] =
+          __float2bfloat16_rn(d * sc * wt);
+    }
+    __syncthreads();
+  }
+  cluster_sync();                // no CTA leaves while others read its sums
+}
+
 // --------------------------------------------------------------------- merge
 
 constexpr int kMergeWarps = 16;
@@ -558,9 +729,34 @@ cudaError_t launch_diff_decode(const DiffDecodeArgs& a, cudaStream_t stream) {
   p.tail.weight = static_cast<const __nv_bfloat16*>(a.norm_weight);
   p.tail.eps = a.norm_eps;
   p.tail.out_scale = a.out_scale;
+  p.cgs = (p.group + 3) / 4;
+  const long long tokens = static_cast<long long>(a.num_blocks) * a.block_size;
+  const long long capacity = static_cast<long long>(a.max_blocks_per_seq) << p.cpb_log2;
+  CUtensorMap tk = {}, tv = {};
+  {
+    // the chunks a sequence can have: the block table's capacity, or the window's and the
+    // sinks' with their edges
+    const long long seen = p.window > 0 ? p.window / kChunk + 2LL + (p.sinks + kChunk - 1LL) / kChunk : capacity;
+    const long long chunks = seen < capacity ? seen : capacity;
+    const long long per_warp = (chunks + kSpread * kWarps - 1) / (kSpread * kWarps);
+    if (static_cast<long long>(a.num_seqs) * (p.hkv / 2) <= kDirectClusters &&
+        per_warp <= kDirectMost) {
+      if (!cache_map(&tk, a.k_cache, a.num_kv_heads, tokens, 2) ||
+          !cache_map(&tv, a.v_cache, a.num_kv_heads, tokens, 2))
+        return cudaErrorInvalidValue;
+      static PerDeviceOnce once;
+      cudaError_t e = once.run([] {
+        return cudaFuncSetAttribute(diff_direct_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kSmemLimit - 1024);
+      });
+      if (e != cudaSuccess) return e;
+      return launch_pdl(diff_direct_kernel, dim3(a.num_seqs * kSpread, 1, p.hkv / 2), dim3(kWarps * 32),
+                        direct_smem(static_cast<int>(per_warp), p.cgs), stream, tk, tv, p,
+                        static_cast<int>(per_warp));
+    }
+  }
   const int ppc = pairs_per_cta(p.hkv);
   p.hpc = 2 * ppc;
-  p.cgs = (p.group + 3) / 4;
   p.units = ppc * p.cgs;
   p.wph = kWarps / p.units;
   p.producers = p.wph < kMaxProducers ? p.wph : kMaxProducers;
@@ -578,7 +774,6 @@ cudaError_t launch_diff_decode(const DiffDecodeArgs& a, cudaStream_t stream) {
   p.stages = p.ring * p.wph;
   if (p.ring < 1) return cudaErrorInvalidConfiguration;
   p.seg_weight = kSegWeight;
-  const long long capacity = static_cast<long long>(a.max_blocks_per_seq) << p.cpb_log2;
   const long long longest = capacity + p.seg_weight;
   p.small = a.num_seqs <= (p.units * p.wph + p.producers) * 32 && longest * a.num_seqs * (p.ctas + 1) < (1LL << 31);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -590,8 +785,6 @@ cudaError_t launch_diff_decode(const DiffDecodeArgs& a, cudaStream_t stream) {
   p.ws_split = reinterpret_cast<int4*>(ws + 2 * ab + rows * kDV * 4);
   p.ws_total = reinterpret_cast<long long*>(ws + 2 * ab + rows * kDV * 4 +
                                             (static_cast<size_t>(p.ctas) * 16 + 255) / 256 * 256);
-  const long long tokens = static_cast<long long>(a.num_blocks) * a.block_size;
-  CUtensorMap tk = {}, tv = {};
   if (!cache_map(&tk, a.k_cache, a.num_kv_heads, tokens, p.hpc) ||
       !cache_map(&tv, a.v_cache, a.num_kv_heads, tokens, p.hpc))
     return cudaErrorInvalidValue;

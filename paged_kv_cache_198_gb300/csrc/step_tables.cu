@@ -14,9 +14,16 @@
 // table[s][p / bs] * bs + p % bs.
 //
 // Split.  Everything that depends on all rows (three sums and their scans) and
-// everything that is updated (stack, tables, lengths) is done by one CTA: it reads
-// all it needs before it writes, so lengths and count may be updated in place,
-// and nothing has to be handed between CTAs.
+// everything that is updated in place (count, lengths, what is given back) is done by
+// one CTA: it reads all it needs before it writes, and nothing has to be handed
+// between CTAs.  A step of up to kPlanFills (padded) tokens is done by it alone, in one
+// launch; of a larger one a second launch of many CTAs takes the new blocks, slots and
+// positions, from the lengths, starts and count that the first one left.
+//
+// Bound: latency -- launches and four dependent memory round trips (lengths, stack,
+// table, slots): 1 row 3.3 us, 256 rows of one token 3.5 (6.2 with 1024 threads whatever
+// the rows, and rows read again for each scan).  64 prompts of 2-8k tokens (301k tokens,
+// 19k blocks) 9.9 us; with the blocks taken by the first launch's CTA 23.3.
 #include "device.cuh"
 #include "kernels.h"
 
@@ -55,35 +62,49 @@ __device__ __forceinline__ Row load_row(const StepTablesArgs& p, int s) {
   return r;
 }
 
-// Sum of v over the block, in every thread.  tmp: 32 values; ends with a barrier.
-__device__ __forceinline__ long long block_sum(long long v, long long* tmp) {
+// Sums over the block, in every thread.  tmp: 3 x 32 values; ends with a barrier.
+__device__ __forceinline__ void block_sums(long long (&v)[3], long long (*tmp)[32]) {
+  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = tmp[threadIdx.x & 31];
+  for (int i = 0; i < 3; ++i) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
+    if (lane == 0) tmp[i][threadIdx.x >> 5] = v[i];
+  }
   __syncthreads();
-  return v;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    v[i] = lane < nw ? tmp[i][lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
+  }
+  __syncthreads();
 }
 
-// Sum of v over the threads before this one; the block's sum goes to total.
-__device__ __forceinline__ int block_scan(int v, int& total, int* tmp) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+// Sums of a and b over the threads before this one, in place; the block's sums go to
+// ta and tb.  tmp: 2 x 32 values; ends with a barrier.
+__device__ __forceinline__ void block_scan(int& a, int& b, int& ta, int& tb, int (*tmp)[32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  int x = a, y = b;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kFull, x, o);
-    if (lane >= o) x += y;
+    const int u = __shfl_up_sync(kFull, x, o), v = __shfl_up_sync(kFull, y, o);
+    if (lane >= o) {
+      x += u;
+      y += v;
+    }
   }
-  if (lane == 31) tmp[warp] = x;
+  if (lane == 31) {
+    tmp[0][warp] = x;
+    tmp[1][warp] = y;
+  }
   __syncthreads();
-  const int part = tmp[lane];
-  total = __reduce_add_sync(kFull, part);
-  const int before = __reduce_add_sync(kFull, lane < warp ? part : 0);
+  const int pa = lane < nw ? tmp[0][lane] : 0, pb = lane < nw ? tmp[1][lane] : 0;
+  ta = __reduce_add_sync(kFull, pa);
+  tb = __reduce_add_sync(kFull, pb);
+  a = __reduce_add_sync(kFull, lane < warp ? pa : 0) + x - a;
+  b = __reduce_add_sync(kFull, lane < warp ? pb : 0) + y - b;
   __syncthreads();
-  return before + x - v;
 }
 
 // The last i in [0, n) with start[i] <= x; start[0] <= x, non-decreasing.
@@ -96,14 +117,11 @@ __device__ __forceinline__ int last_at_most(const int* start, int n, int x) {
   return lo;
 }
 
-// Slot and position of packed token i of row s, whose tokens end before `end`.
-__device__ __forceinline__ void fill_token(const StepTablesArgs& p, int i, int s, int end, int len) {
-  const int pos = len - (end - i);
-  const int b = pos / p.block_size;
-  const int id = p.block_tables[static_cast<long long>(s) * p.max_blocks + b];
+// Slot and position of the packed token i at position pos, whose block is id.
+__device__ __forceinline__ void fill_token(const StepTablesArgs& p, int i, int pos, int id) {
   int slot = -1;
   if (id >= 0 && id < p.num_blocks)
-    slot = id * p.block_size + (pos - b * p.block_size);   // NB * bs < 2^31
+    slot = id * p.block_size + pos % p.block_size;         // NB * bs < 2^31
   else
     report(p.status, TVL_DEV_BAD_BLOCK_ID);
   p.slot_mapping[i] = slot;
@@ -114,33 +132,35 @@ __device__ __forceinline__ void fill_padding(const StepTablesArgs& p, int i) {
   if (p.positions != nullptr) p.positions[i] = 0;
 }
 
-template <bool kFill>
+// kAlone: up to blockDim.x rows, and no second launch: the new blocks are taken and the
+// tokens filled in here.  kTake: the new blocks are taken here, the rest follows.
+template <bool kAlone, bool kTake>
 __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepTablesArgs p) {
-  __shared__ long long sums[32];
-  __shared__ int scan[32];
+  __shared__ long long sums[3][32];
+  __shared__ int scan[2][32];
   __shared__ int off[kPlanThreads], had[kPlanThreads], starts[kPlanThreads], lens[kPlanThreads];
-  const int tid = threadIdx.x, S = p.num_seqs;
+  const int tid = threadIdx.x, S = p.num_seqs, T = blockDim.x;
   grid_dependency_wait();
   grid_dependents_launch();
 
-  long long give = 0, need = 0, add = 0;
-  bool bad = false;
-  for (int s = tid; s < S; s += kPlanThreads) {
-    const Row r = load_row(p, s);
-    give += r.give;
-    need += r.need;
-    add += r.add;
-    bad |= r.bad;
-  }
   const long long count = *p.free_count;
-  give = block_sum(give, sums);
-  need = block_sum(need, sums);
-  add = block_sum(add, sums);
+  long long v[3] = {0, 0, 0};              // blocks given back, blocks needed, tokens
+  bool bad = false;
+  Row r = load_row(p, tid);
+  for (int s = tid;;) {
+    v[0] += r.give;
+    v[1] += r.need;
+    v[2] += r.add;
+    bad |= r.bad;
+    if (kAlone || (s += T) >= S) break;
+    r = load_row(p, s);
+  }
+  block_sums(v, sums);
   uint32_t why = __syncthreads_or(bad) ? TVL_DEV_BAD_CONTEXT_LEN : 0u;
-  if (add > p.max_tokens) why |= TVL_DEV_BAD_QUERY_LEN;
-  if (count < 0 || count + give > p.num_blocks)
+  if (v[2] > p.max_tokens) why |= TVL_DEV_BAD_QUERY_LEN;
+  if (count < 0 || count + v[0] > p.num_blocks)
     why |= TVL_DEV_BAD_BLOCK_ID;
-  else if (need > count + give)
+  else if (v[1] > count + v[0])
     why |= TVL_DEV_OUT_OF_BLOCKS;
   if (why != 0) {                        // the whole step is refused
     if (tid == 0) {
@@ -148,26 +168,27 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepTable
       p.query_start_loc[S] = 0;
       *p.free_count_out = static_cast<int>(count);
     }
-    for (int s = tid; s < S; s += kPlanThreads) {
+    for (int s = tid; s < S; s += T) {
       p.context_lens[s] = p.cached_lens[s];
       p.query_start_loc[s] = 0;
     }
-    if (kFill)
-      for (int i = tid; i < p.max_tokens; i += kPlanThreads) fill_padding(p, i);
+    if (kAlone)
+      for (int i = tid; i < p.max_tokens; i += T) fill_padding(p, i);
     return;
   }
 
   // from here every sum is at most max(NB, max_tokens) < 2^31
-  const int have = static_cast<int>(count), top = have + static_cast<int>(give);
-  if (give > 0) {
+  const int have = static_cast<int>(count), top = have + static_cast<int>(v[0]);
+  if (v[0] > 0) {
     int done = 0;
-    for (int s0 = 0; s0 < S; s0 += kPlanThreads) {
-      const Row r = load_row(p, s0 + tid);
-      int n;
-      off[tid] = block_scan(r.give, n, scan);
+    for (int s0 = 0; s0 < S; s0 += T) {
+      if (!kAlone) r = load_row(p, s0 + tid);
+      int give = r.give, none = 0, n, unused;
+      block_scan(give, none, n, unused, scan);
+      off[tid] = give;
       __syncthreads();
-      for (int i = tid; i < n; i += kPlanThreads) {
-        const int k = last_at_most(off, kPlanThreads, i);
+      for (int i = tid; i < n; i += T) {
+        const int k = last_at_most(off, T, i);
         p.free_blocks[have + done + i] =
             p.block_tables[static_cast<long long>(s0 + k) * p.max_blocks + i - off[k]];
       }
@@ -176,13 +197,16 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepTable
     }
   }
   int taken = 0, tokens = 0;
-  for (int s0 = 0; s0 < S; s0 += kPlanThreads) {
-    const Row r = load_row(p, s0 + tid);
-    int n, t;
-    off[tid] = block_scan(r.need, n, scan);
-    had[tid] = r.had;
-    const int start = tokens + block_scan(r.add, t, scan);
-    if (kFill) {
+  for (int s0 = 0; s0 < S; s0 += T) {
+    if (!kAlone) r = load_row(p, s0 + tid);
+    int need = r.need, start = r.add, n, t;
+    block_scan(need, start, n, t, scan);
+    start += tokens;
+    if (kTake || kAlone) {
+      off[tid] = need;
+      had[tid] = r.had;
+    }
+    if (kAlone) {
       starts[tid] = start;
       lens[tid] = r.len;
     }
@@ -191,46 +215,72 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepTable
       p.query_start_loc[s0 + tid] = start;
     }
     __syncthreads();
-    for (int i = tid; i < n; i += kPlanThreads) {
-      const int k = last_at_most(off, kPlanThreads, i);
-      const int id = p.free_blocks[top - 1 - taken - i];
-      if (id < 0 || id >= p.num_blocks) report(p.status, TVL_DEV_BAD_BLOCK_ID);
-      p.block_tables[static_cast<long long>(s0 + k) * p.max_blocks + had[k] + i - off[k]] = id;
-    }
+    if (kTake || kAlone)
+      for (int i = tid; i < n; i += T) {
+        const int k = last_at_most(off, T, i);
+        const int id = p.free_blocks[top - 1 - taken - i];
+        if (id < 0 || id >= p.num_blocks) report(p.status, TVL_DEV_BAD_BLOCK_ID);
+        p.block_tables[static_cast<long long>(s0 + k) * p.max_blocks + had[k] + i - off[k]] = id;
+      }
     taken += n;
     tokens += t;
-    __syncthreads();
+    if (!kAlone) __syncthreads();
   }
   if (tid == 0) {
     p.query_start_loc[S] = tokens;
     *p.free_count_out = top - taken;
   }
-  if (kFill) {                           // S <= kPlanThreads: starts and lens are complete
-    for (int i = tid; i < p.max_tokens; i += kPlanThreads) {
+  if (kAlone) {
+    // (a token's new block straight from the stack: the tables are being written)
+    for (int i = tid; i < p.max_tokens; i += T) {
       if (i >= tokens) {
         fill_padding(p, i);
         continue;
       }
       const int s = last_at_most(starts, S, i);
-      fill_token(p, i, s, s + 1 < S ? starts[s + 1] : tokens, lens[s]);
+      const int pos = lens[s] - ((s + 1 < S ? starts[s + 1] : tokens) - i);
+      const int b = pos / p.block_size;
+      fill_token(p, i, pos, b < had[s] ? p.block_tables[static_cast<long long>(s) * p.max_blocks + b]
+                                       : p.free_blocks[top - 1 - off[s] - (b - had[s])]);
     }
   }
 }
 
-// Slots and positions of many tokens, from the plan's starts, lengths and tables.
+// Slots and positions of many tokens, from the plan's starts and lengths.  kTake: the
+// new blocks too (up to kFillRows rows): every CTA scans the rows' needs, a token finds
+// its block on the stack, and the one at a new block's start enters it into the table.
+template <bool kTake>
 __global__ void __launch_bounds__(kFillThreads) step_fill_kernel(const StepTablesArgs p) {
-  __shared__ int kept[kFillRows];
+  __shared__ int starts[kTake ? kFillRows : 1], off[kTake ? kFillRows : 1];
+  __shared__ int scan[2][32];
   const int S = p.num_seqs;
   grid_dependency_wait();
   grid_dependents_launch();
   const int tokens = p.query_start_loc[S];
   const long long i0 = static_cast<long long>(blockIdx.x) * kFillThreads * kFillPerThread;
-  const int* starts = p.query_start_loc;
-  if (S <= kFillRows && i0 < tokens) {
-    for (int s = threadIdx.x; s < S; s += kFillThreads) kept[s] = p.query_start_loc[s];
-    starts = kept;
+  const int* first = p.query_start_loc;
+  int top = 0;
+  if (kTake && i0 < tokens) {
+    int before = 0;
+    for (int s0 = 0; s0 < S; s0 += kFillThreads) {
+      const int s = s0 + threadIdx.x;
+      int start = 0, need = 0, none = 0, n, unused;
+      if (s < S) {
+        start = p.query_start_loc[s];
+        const int len = p.context_lens[s], add = p.query_start_loc[s + 1] - start;
+        need = blocks_of(len, p.block_size) - blocks_of(len - add, p.block_size);
+      }
+      block_scan(need, none, n, unused, scan);
+      if (s < S) {
+        starts[s] = start;
+        off[s] = before + need;
+      }
+      before += n;
+    }
+    top = *p.free_count_out + before;
+    first = starts;
+    __syncthreads();
   }
-  __syncthreads();
 #pragma unroll
   for (int j = 0; j < kFillPerThread; ++j) {
     const long long i = i0 + j * kFillThreads + threadIdx.x;
@@ -239,23 +289,46 @@ __global__ void __launch_bounds__(kFillThreads) step_fill_kernel(const StepTable
       fill_padding(p, static_cast<int>(i));
       continue;
     }
-    const int s = last_at_most(starts, S, static_cast<int>(i));
-    fill_token(p, static_cast<int>(i), s, s + 1 < S ? starts[s + 1] : tokens, p.context_lens[s]);
+    const int s = last_at_most(first, S, static_cast<int>(i));
+    const int start = first[s], end = s + 1 < S ? first[s + 1] : tokens, len = p.context_lens[s];
+    const int pos = len - (end - static_cast<int>(i));
+    const int b = pos / p.block_size;
+    int32_t* entry = p.block_tables + static_cast<long long>(s) * p.max_blocks + b;
+    const int had = blocks_of(len - (end - start), p.block_size);
+    int id;
+    if (kTake && b >= had) {
+      id = p.free_blocks[top - 1 - off[s] - (b - had)];
+      if (pos == b * p.block_size) *entry = id;
+    } else {
+      id = *entry;
+    }
+    fill_token(p, static_cast<int>(i), pos, id);
   }
 }
 
-// Up to this many (padded) tokens the plan's CTA fills them in itself.
+// Up to this many (padded) tokens the plan's CTA fills them in itself (4 rows, us: 4096
+// tokens 6.1, 4100 through the second launch 7.3; 16 rows 6.8 and 8.2).
 constexpr int kPlanFills = 4096;
 
 }  // namespace
 
 cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream) {
-  if (a.max_tokens <= kPlanFills && a.num_seqs <= kPlanThreads)
-    return launch_pdl(step_plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, stream, a);
-  cudaError_t e = launch_pdl(step_plan_kernel<false>, dim3(1), dim3(kPlanThreads), 0, stream, a);
+  if (a.max_tokens <= kPlanFills && a.num_seqs <= kPlanThreads) {
+    // a thread a row, and up to four tokens a thread: no more warps than that, as each
+    // barrier costs by them
+    int threads = (a.max_tokens + 3) / 4 > a.num_seqs ? (a.max_tokens + 3) / 4 : a.num_seqs;
+    threads = (threads + 31) / 32 * 32;
+    if (threads < 32) threads = 32;
+    return launch_pdl(step_plan_kernel<true, true>, dim3(1), dim3(threads), 0, stream, a);
+  }
+  const bool few = a.num_seqs <= kFillRows && a.max_tokens > 0;
+  cudaError_t e = few ? launch_pdl(step_plan_kernel<false, false>, dim3(1), dim3(kPlanThreads), 0, stream, a)
+                      : launch_pdl(step_plan_kernel<false, true>, dim3(1), dim3(kPlanThreads), 0, stream, a);
   if (e != cudaSuccess || a.max_tokens == 0) return e;
   constexpr int per = kFillThreads * kFillPerThread;
-  return launch_pdl(step_fill_kernel, dim3((a.max_tokens - 1) / per + 1), dim3(kFillThreads), 0, stream, a);
+  const dim3 grid((a.max_tokens - 1) / per + 1);
+  return few ? launch_pdl(step_fill_kernel<true>, grid, dim3(kFillThreads), 0, stream, a)
+             : launch_pdl(step_fill_kernel<false>, grid, dim3(kFillThreads), 0, stream, a);
 }
 
 }  // namespace tvl
