@@ -406,11 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // them fit) and q's loads, and waits once.  A CTA adds its warps up; then CTA r takes
 // the group's query pairs r, r + kSpread, ...: it reads the CTAs' sums through
 // distributed shared memory.  Bound by latency (five dependent memory round trips and two
-// cluster barriers): 777 tokens, 8 query heads, 6.4 us, 10.7 through the schedule and
-// the merge.
+// cluster barriers): 777 tokens, 8 query heads, 5.4 us, 10.8 through the schedule and the
+// merge; 2040 tokens, 3 sequences of 4 KV pairs, 6.9 and 10.7.  It wins while all clusters
+// run at once (14 of them 5.8 and 10.4, 16, two waves, 10.3 and 10.5).
 constexpr int kSpread = 8;
 constexpr int kDirectMost = 2;                // chunks a warp: what shared memory holds
-constexpr int kDirectClusters = 16;           // at most: two a processing cluster of SMs
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -687,11 +687,40 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 1)
 
 // --------------------------------------------------------------------- host
 
-// The most CTAs that share one KV-head group's work.
+// KV pairs that a CTA owns.
 int pairs_per_cta(int num_kv_heads) { return heads_per_cta(num_kv_heads / 2, kPairsPerCta); }
+
+// Clusters of diff_direct_kernel that the current device runs at once (0 on an error),
+// asked for once per device with the largest shared memory.
+int direct_clusters() {
+  static std::atomic<int> known[64];                   // 1 + the answer
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSpread);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = direct_smem(kDirectMost, 2);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kSpread;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(diff_direct_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmemLimit - 1024) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, diff_direct_kernel, &cfg) != cudaSuccess || n < 0) {
+    cudaGetLastError();
+    return 0;
+  }
+  known[dev].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
 
 }  // namespace
 
+// The most CTAs that share one KV-head group's work.
 int diff_max_ctas(int num_kv_heads, int sms) {
   const int c = sms / (num_kv_heads / 2 / pairs_per_cta(num_kv_heads));
   return c < 1 ? 1 : c;
@@ -739,17 +768,10 @@ cudaError_t launch_diff_decode(const DiffDecodeArgs& a, cudaStream_t stream) {
     const long long seen = p.window > 0 ? p.window / kChunk + 2LL + (p.sinks + kChunk - 1LL) / kChunk : capacity;
     const long long chunks = seen < capacity ? seen : capacity;
     const long long per_warp = (chunks + kSpread * kWarps - 1) / (kSpread * kWarps);
-    if (static_cast<long long>(a.num_seqs) * (p.hkv / 2) <= kDirectClusters &&
-        per_warp <= kDirectMost) {
+    if (per_warp <= kDirectMost && static_cast<long long>(a.num_seqs) * (p.hkv / 2) <= direct_clusters()) {
       if (!cache_map(&tk, a.k_cache, a.num_kv_heads, tokens, 2) ||
           !cache_map(&tv, a.v_cache, a.num_kv_heads, tokens, 2))
         return cudaErrorInvalidValue;
-      static PerDeviceOnce once;
-      cudaError_t e = once.run([] {
-        return cudaFuncSetAttribute(diff_direct_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kSmemLimit - 1024);
-      });
-      if (e != cudaSuccess) return e;
       return launch_pdl(diff_direct_kernel, dim3(a.num_seqs * kSpread, 1, p.hkv / 2), dim3(kWarps * 32),
                         direct_smem(static_cast<int>(per_warp), p.cgs), stream, tk, tv, p,
                         static_cast<int>(per_warp));
