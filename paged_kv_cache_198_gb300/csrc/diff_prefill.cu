@@ -41,10 +41,10 @@
 //   - the output by the conversion warps: 375 -> 366; an arrival without a branch: 363.
 // Measured and left (same two): four softmax warpgroups, a map's two taking alternate
 // tiles and sharing the reference, 179 / 462 (a buffer's MMAs and its warpgroup wait for
-// each other); one MMA issuer a map 183 / 464; halves of a tile in turn 173 / 437; the
-// next tile's scores fetched behind the store 159 / 357; P handed over behind the next
-// tile's first exponentials 178 / 477; parked waits 166 / 422 on 158 / 392; units worked
-// out by one warp for all 160 / 369.
+// each other), or 32 keys of every tile each 163 / 385; one MMA issuer a map 183 / 464;
+// halves of a tile in turn 173 / 437; the next tile's scores fetched behind the store 159
+// / 357; P handed over behind the next tile's first exponentials 178 / 477; parked waits
+// 166 / 422 on 158 / 392; units worked out by one warp for all 160 / 369.
 #include "diff.cuh"
 #include "prefill_tiles.cuh"
 
@@ -138,6 +138,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = static_cast<int>(gridDim.x);
   const int c = static_cast<int>(blockIdx.x);
 
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+    prefetch_tensormap(&tm_o);
+  }
   grid_dependency_wait();          // inputs may come from the preceding kernel
   grid_dependents_launch();
 
@@ -199,10 +205,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* full = is_k ? B->k_full : B->v_full;
     uint64_t* empty = is_k ? B->k_empty : B->v_empty;
     uint8_t* ring = smem + (is_k ? kKOff : kVOff);
-    if (lane == 0) {
-      prefetch_tensormap(tm);
-      prefetch_tensormap(is_k ? &tm_q : &tm_o);
-    }
     const int boxes = kBN >> p.box_log2;                // boxes of a head's tile
     int gt = 0, st = 0, ph = 0;                         // key tiles issued; stage, its phase
     int nq = 0;                                         // units begun
