@@ -150,7 +150,7 @@ tvl_status tvl_rope_paged_kv_write(void* q, const void* k_new, const void* v_new
  *   positions : int32 [A, T], any value (device); A from 1 to 4
  * Each result is within one bf16 ulp of the double-precision definition plus
  * 2^-20 * (|x_i| + |x_{i+D/2}|).  Slots as in tvl_paged_kv_write.  Supported:
- * D == 64, Hkv <= 262140, Hq <= 524280.
+ * D == 64, Hkv <= 262136, Hq <= 524280.
  */
 tvl_status tvl_rope_axes_paged_kv_write(void* q, const void* k_new, const void* v_new,
                                         void* k_cache, void* v_cache, const int32_t* slot_mapping,

@@ -353,6 +353,14 @@ def bind_rope_axes_paged_kv_write(q, k_new, v_new, k_cache, v_cache, slot_mappin
                                       sections, interleaved, rope_theta, stream))
 
 
+def _c_int(value, name):
+    """value as a C int; ctypes would drop the upper bits of a larger one."""
+    value = int(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} {value} must fit 32 bits")
+    return value
+
+
 def _prep_step_tables(block_tables, free_blocks, context_lens, query_start_loc, slot_mapping,
                       positions, free_count, cached_lens, new_lens, block_size, free_count_out,
                       stream):
@@ -376,7 +384,7 @@ def _prep_step_tables(block_tables, free_blocks, context_lens, query_start_loc, 
         args = tuple(_ptr(t) for t in (block_tables, free_blocks, free_count_out, context_lens,
                                        query_start_loc, slot_mapping, positions, free_count,
                                        cached_lens, new_lens))
-        args += (s, slot_mapping.shape[0], int(block_size), free_blocks.shape[0], mb,
+        args += (s, slot_mapping.shape[0], _c_int(block_size, "block_size"), free_blocks.shape[0], mb,
                  _stream(stream))
     return (dev, _load().tvl_build_step_tables, args,
             (block_tables, free_blocks, free_count_out, context_lens, query_start_loc,
@@ -950,7 +958,8 @@ def _prep_diff_prefill(out, q, query_start_loc, k_cache, v_cache, block_tables, 
     with _on_device(dev):
         args = (_ptr(out), _ptr(q), _ptr(query_start_loc), _ptr(k_cache), _ptr(v_cache),
                 _ptr(block_tables), _ptr(context_lens), _ptr(lam), int(lam.dim() == 2),
-                _ptr(norm_weight), float(norm_eps), float(out_scale), s, tq, int(max_q_len), hq,
+                _ptr(norm_weight), float(norm_eps), float(out_scale), s, tq,
+                _c_int(max_q_len, "max_q_len"), hq,
                 hkv, d, bs, nb, block_tables.shape[1], float(scale), window, sinks,
                 _stream(stream))
     return (dev, _load().tvl_diff_attention_prefill, args,

@@ -533,8 +533,8 @@ tvl_status tvl_rope_axes_paged_kv_write(void* q, const void* k_new, const void* 
     return fail(TVL_ERR_INVALID_ARG, "num_kv_heads, block_size and num_blocks must be positive");
   if (head_dim != 64) return fail(TVL_ERR_UNSUPPORTED, "head_dim %d (supported: 64)", head_dim);
   if (q && num_q_heads <= 0) return fail(TVL_ERR_INVALID_ARG, "num_q_heads %d <= 0", num_q_heads);
-  if (num_kv_heads > 262140 || num_q_heads > 524280)   // 16-row parts of both: a grid's 65535
-    return fail(TVL_ERR_UNSUPPORTED, "num_kv_heads %d > 262140 or num_q_heads %d > 524280",
+  if (num_kv_heads > 262136 || num_q_heads > 524280)   // 16-row parts of both: a grid's 65535
+    return fail(TVL_ERR_UNSUPPORTED, "num_kv_heads %d > 262136 or num_q_heads %d > 524280",
                 num_kv_heads, num_q_heads);
   if (!(rope_theta > 1.0f) || !std::isfinite(rope_theta))
     return fail(TVL_ERR_INVALID_ARG, "rope_theta must be finite and > 1");

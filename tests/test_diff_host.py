@@ -81,6 +81,12 @@ def test_binding_checks(tvl):
         tvl.diff_attention_decode(None, None, kv, kv, None, None, None, 0.125, window=2 ** 31)
 
 
+def test_sizes_past_32_bits_are_refused(tvl):
+    with pytest.raises(ValueError, match="32 bits"):
+        tvl._c_int(2 ** 31, "max_q_len")
+    assert tvl._c_int(7, "x") == 7
+
+
 def test_plain_form():
     """One key: both maps are its value; equal keys: the mean of the values."""
     rng = np.random.default_rng(1)

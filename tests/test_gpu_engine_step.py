@@ -3,6 +3,10 @@ write with positions of several axes, differential prefill and decode -- prompts
 in chunks, rows decode, leave and are followed by others.  The tables are checked
 against the plain row-by-row form, the written rows and the attention against the
 formulas in 64 bits on the cache's contents."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -90,6 +94,7 @@ def test_prompts_decode_steps_and_departures():
         tvl.diff_attention_prefill(e.out, e.q, e.qsl, e.kc, e.vc, e.tables, e.lens, e.lam, 0.125, 128,
                                    norm_weight=e.weight, out_scale=0.5)
         e.check(new, True, e.out)
+        assert e.out[int(e.qsl[-1]):].isnan().all()       # rows behind the last sequence are left
     out = torch.zeros(5, HQ // 2, 128, dtype=torch.bfloat16, device=DEV)
     q = torch.zeros(5, HQ, 64, dtype=torch.bfloat16, device=DEV)
     for step in range(6):
@@ -141,3 +146,102 @@ def test_the_4_bit_cache_with_the_same_tables():
                       e.slots[live].contiguous())
         assert torch.equal(f.cache, want) and torch.equal(e.slots, f.slots)
     assert_clean_status()
+
+
+def test_two_engines_on_two_streams_at_once():
+    """Decode steps of two engines, one a stream, with nothing to order them."""
+    engines = [Engine(rows=3, blocks=40, width=8, room=3) for _ in range(2)]
+    outs = [[] for _ in engines]
+    streams = [torch.cuda.Stream() for _ in engines]
+    tokens = [[C.bf16(np.random.default_rng(i).standard_normal((30, 3, h, 64)), DEV) for h in (HQ, HKV, HKV)]
+              for i in range(2)]
+    ones = _i32([1, 1, 1])
+    torch.cuda.synchronize()
+    for step in range(30):
+        for e, out, stream, x in zip(engines, outs, streams, tokens):
+            with torch.cuda.stream(stream):
+                e.new.copy_(ones)
+                for t, y in zip((e.q, e.k, e.v), x):
+                    t.copy_(y[step])
+                e.bookkeeping()
+                e.write()
+                out.append(torch.zeros(3, HQ // 2, 128, dtype=torch.bfloat16, device=DEV))
+                tvl.diff_attention_decode(out[-1], e.q, e.kc, e.vc, e.tables, e.lens, e.lam, 0.125)
+    torch.cuda.synchronize()
+    for e, out in zip(engines, outs):                     # the same again, one after the other
+        f = Engine(rows=3, blocks=40, width=8, room=3)
+        for step in range(30):
+            f.new.copy_(ones)
+            for t, y in zip((f.q, f.k, f.v), tokens[engines.index(e)]):
+                t.copy_(y[step])
+            f.bookkeeping()
+            f.write()
+            want = torch.zeros_like(out[step])
+            tvl.diff_attention_decode(want, f.q, f.kc, f.vc, f.tables, f.lens, f.lam, 0.125)
+            assert torch.equal(want, out[step])
+        assert torch.equal(e.kc, f.kc) and torch.equal(e.tables, f.tables)
+    assert_clean_status()
+
+
+def test_pools_past_4_gb():
+    """A step's outputs do not depend on where in the pool its blocks lie: the last blocks
+    of a pool of 600000 (4.9 GB a cache, past 2^31 elements) against a small one."""
+    got = []
+    for blocks in (40, 600000):
+        e = Engine(rows=3, blocks=40, width=12, room=160)
+        if blocks > 40:
+            e.kc = e.vc = e.cache = None
+            e.kc, e.vc = (torch.zeros(blocks, BS, HKV, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+            e.free, e.count = torch.arange(blocks, dtype=torch.int32, device=DEV), _i32([blocks])
+        outs = []
+        for new in ([70, 40, 1], [20, 90, 5]):
+            e.draw(new)
+            e.bookkeeping()
+            e.write()
+            out = torch.zeros_like(e.out)
+            tvl.diff_attention_prefill(out, e.q, e.qsl, e.kc, e.vc, e.tables, e.lens, e.lam, 0.125, 128, window=50,
+                                       sinks=3, norm_weight=e.weight)
+            outs.append(out)
+        for rows in (3, 1):                               # (one launch, and with a wide table the split)
+            tab = torch.full((rows, 300), -1, dtype=torch.int32, device=DEV)
+            tab[:, :12] = e.tables[:rows]
+            for t in (e.tables[:rows].contiguous(), tab):
+                out = torch.zeros(rows, HQ // 2, 128, dtype=torch.bfloat16, device=DEV)
+                tvl.diff_attention_decode(out, e.q[:rows].contiguous(), e.kc, e.vc, t, e.lens[:rows].contiguous(), e.lam,
+                                          0.125, norm_weight=e.weight)
+                outs.append(out)
+        if blocks > 40:
+            assert int(e.tables.max()) == blocks - 1
+        got.append(outs)
+        assert_clean_status()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+FIRST_CALLS = """
+import torch, paged_kv_cache_198_gb300 as tvl
+b = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+kc, vc, q, k = b(8, 16, 2, 64), b(8, 16, 2, 64), b(4, 8, 64), b(4, 2, 64)
+tab, lens, new, free, count = i(7, 7, 7, 7).view(1, 4), i(0), i(4), torch.arange(8, dtype=torch.int32, device="cuda"), i(8)
+qsl, slots, pos, axes = i(0, 0), i(0, 0, 0, 0), i(0, 0, 0, 0), torch.zeros(3, 4, dtype=torch.int32, device="cuda")
+lam, po, do = torch.rand(4, device="cuda"), b(4, 4, 128), b(1, 4, 128)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    tvl.build_step_tables(tab, free, lens, qsl, slots, pos, count, lens, new, 16)
+    tvl.rope_axes_paged_kv_write(q, k, k, kc, vc, slots, axes, (8, 12, 12))
+    tvl.diff_attention_prefill(po, q, qsl, kc, vc, tab, lens, lam, 0.125, 4)
+    tvl.diff_attention_decode(do, q[3:], kc, vc, tab, lens, lam, 0.125)
+g.replay()
+torch.cuda.synchronize()
+assert lens.tolist() == [4] and tab[0, 0] == 7 and slots.tolist() == [112, 113, 114, 115], (lens, tab, slots)
+assert (po[3].float() - do[0].float()).abs().max() < 0.05 and tvl.get_device_status() == 0
+print("ok")
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=120,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "ok" in r.stdout, r.stdout + r.stderr

@@ -70,7 +70,7 @@ def _axes(t, four, **k):
     (dict(k=None), "INVALID_ARG"), (dict(v=258), "INVALID_ARG"), (dict(q=260), "INVALID_ARG"),
     (dict(hq=0), "INVALID_ARG"), (dict(slots=None), "INVALID_ARG"), (dict(pos=None), "INVALID_ARG"),
     (dict(theta=1.0), "INVALID_ARG"), (dict(theta=float("inf")), "INVALID_ARG"),
-    (dict(hq=524281), "UNSUPPORTED"), (dict(hkv=262141), "UNSUPPORTED"),
+    (dict(hq=524281), "UNSUPPORTED"), (dict(hkv=262137), "UNSUPPORTED"),
     (dict(sec=None, axes=3), "INVALID_ARG"), (dict(axes=0), "UNSUPPORTED"),
     (dict(sec=(7, 7, 6, 6, 6)), "UNSUPPORTED"), (dict(sec=(16, 15)), "INVALID_ARG"),
     (dict(sec=(32, 0)), "INVALID_ARG"), (dict(sec=(40, -8)), "INVALID_ARG"),
