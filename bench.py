@@ -56,7 +56,7 @@ CSRC = os.path.join(ROOT, "paged_kv_cache_198_gb300", "csrc")
 HOLD_CYCLES = 400_000            # ~0.2 ms GPU hold before each timed region
 SUSTAIN_S = 1.0                  # length of the clock-sampled region
 DECODE_SOURCES = ["decode.cu", "device.cuh"]
-PREFILL_SOURCES = ["prefill.cu", "tc.cuh", "device.cuh"]
+PREFILL_SOURCES = ["prefill.cu", "prefill_tiles.cuh", "tc.cuh", "device.cuh"]
 
 
 # ------------------------------------------------------------------ helpers
