@@ -4,9 +4,11 @@
  * decode (single pass or split-K with a log-sum-exp merge), the two fused
  * into one decode-step call, and chunked causal prefill over a cached
  * prefix; around them the rotary embedding fused into the write, block
- * copies for copy-on-write, and a host block allocator.  Two ways to hold
- * more context: a cache in 4 bits (write, expand, copy, decode) and attention
- * with a sliding window and sinks (decode, prefill).
+ * copies for copy-on-write, a host block allocator, and an engine step's block
+ * tables and slots built on the GPU; rotary positions with several axes.  Two ways
+ * to hold more context: a cache in 4 bits (write, expand, copy, decode) and
+ * attention with a sliding window and sinks (decode, prefill).  Differential
+ * attention over the same cache (decode, prefill).
  *
  * Sources of the method (web pages on tiny-vLLM and nano-vLLM):
  *   [tiny-vllm README]  "tiny-vllm" README, Korean translation: feature list
@@ -33,7 +35,7 @@
  *   D = head_dim, bs = block_size, NB = num_blocks (physical blocks in the
  *   pool), MB = max_blocks_per_seq (columns of block_tables).
  * Element types: q, K and V are bfloat16 (passed as void*, 2 bytes each);
- *   attention outputs are float32; all metadata is int32.
+ *   attention outputs are float32 unless stated; all metadata is int32.
  * Cache layout: k_cache and v_cache are each a contiguous bf16 array
  *   [NB, bs, Hkv, D].  Token slot `x = block * bs + offset` is row x of the
  *   flat view [NB * bs, Hkv * D]; one physical block is one contiguous run of
@@ -44,8 +46,9 @@
  *   read.  Two rows may name the same physical block (shared prefixes).
  * GQA: query head h reads KV head h / G.
  * Scores: s_j = scale * sum_d q[d] * k_j[d], accumulated in float32.
- * Pointers: every pointer except `stream` and a zero-size workspace is a
- *   device pointer, owned by the caller, and must be 16-byte aligned.  The
+ * Pointers: every pointer except `stream`, a zero-size workspace and what is
+ *   marked (host) is a device pointer, owned by the caller, and must be 16-byte
+ *   aligned (lambda and the arrays of tvl_build_step_tables: 4-byte).  The
  *   library allocates no device memory and frees nothing.
  * Streams: every call is asynchronous on `stream` (a cudaStream_t; NULL = the
  *   legacy default stream).  A non-OK return means nothing was launched.
