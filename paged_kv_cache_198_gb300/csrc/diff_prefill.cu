@@ -14,12 +14,14 @@
 //           takes a tile's 64 scores into registers, writes P = 2^(s - m) as fp16 over
 //           the scores' own TMEM columns, and hands them to P V.  m is the first tile's
 //           maximum and moves only when a tile's row sum nears the fp16 limit
-//   8, 11   producers: Q tiles and the two keys, and the two V heads, of each key tile's
+//   8, 9    producers: Q tiles and the two keys, and the two V heads, of each key tile's
 //           physical blocks, one TMA box each (the paged gather).  K's ring turns when
 //           its scores are done, V's when its P V is
-//   9       issues S_h = Q_h K_h^T (M 128, N 64, bf16, both operands in shared memory)
-//   10      issues O_h += P_h V (M 128, N 128, fp16, P read from TMEM)
-//   12..15  V conversion bf16 -> fp16 in place (as in prefill.cu), and the output
+//   10, 11  issue S_h = Q_h K_h^T (M 128, N 64, bf16, both operands in shared memory),
+//           a warp a map
+//   12, 13  issue O_h += P_h V (M 128, N 128, fp16, P read from TMEM), a warp a map
+//   14      works the CTA's units out ahead of the others
+//   16..19  V conversion bf16 -> fp16 in place (as in prefill.cu), and the output
 // TMEM: S/P of map h in two buffers of 64 columns each (256), O_0 and O_1 128 each:
 // all 512.  With O 128 wide there is no room for P beside S; two buffers a map let one
 // tile's P V and the Q K^T after next run while the softmax works on the tile between.
@@ -28,23 +30,26 @@
 // which run ahead of it, read both O's: a thread takes a row's d = O_0 / l_0 - lambda
 // O_1 / l_1 twice, for the norm and for the output.
 //
-// What bounds it: a softmax warp's chain of steps a tile, some 1600 cycles (scores seen,
+// What bounds it: a softmax warp's chain of steps a tile, some 1500 cycles (scores seen,
 // loaded, 620 for 64 exponentials with two warps a scheduler, vote, store, arrival), not
-// the tensor pipe (45% active), the exp unit (31%) or issue slots (55%).  Timing copies
+// the tensor pipe (49% active), the exp unit (33%), issue slots (54%) or L2.  Timing copies
 // that leave work out say the same (2 sequences x 4096 rows, window 4096, 396 us then):
 // a quarter of the MMAs 400, no exponentials 369, no V conversion 373.
-// Measured: 16 chunks of 512 rows on prefixes of 0-2k 156 us, 837 TFLOP/s of visible
-// work; 2 sequences x 4096 rows, window 4096, 363-370 us, 1090 TFLOP/s; 100 rows 18.4 us.
+// Measured: 16 chunks of 512 rows on prefixes of 0-2k 155 us, 841 TFLOP/s of visible
+// work; 2 sequences x 4096 rows, window 4096, 350 us, 1140 TFLOP/s; 100 rows 18.4 us.
 // What brought it there, us of the first two:
 //   - K and V in rings of their own, a producer each: 193 -> 160 (bs 16: 16 boxes a tile);
 //   - whole tiles in a short loop of their own: 392 -> 375;
-//   - the output by the conversion warps: 375 -> 366; an arrival without a branch: 363.
+//   - the output by the conversion warps: 375 -> 366; an arrival without a branch: 363;
+//   - issuers of their own for each map and product: 371 -> 354; units worked out ahead by
+//     a warp (each warp for itself: 2500 cycles a unit): 158 / 354 -> 155 / 350.
 // Measured and left (same two): four softmax warpgroups, a map's two taking alternate
 // tiles and sharing the reference, 179 / 462 (a buffer's MMAs and its warpgroup wait for
 // each other), or 32 keys of every tile each 163 / 385; one MMA issuer a map 183 / 464;
 // halves of a tile in turn 173 / 437; the next tile's scores fetched behind the store 159
 // / 357; P handed over behind the next tile's first exponentials 178 / 477; parked waits
-// 166 / 422 on 158 / 392; units worked out by one warp for all 160 / 369.
+// 166 / 422 on 158 / 392; units worked out by the K producer 160 / 369; O read once, d
+// kept in fp16 until the norm is known, 157 / 349 on 155 / 349.
 #include "diff.cuh"
 #include "prefill_tiles.cuh"
 
@@ -54,8 +59,11 @@ namespace {
 constexpr int kBN = 64;
 constexpr int kKStages = 4, kVStages = 5;
 constexpr int kSlots = 4;
-constexpr int kThreads = 512;
-constexpr int kKWarp = 8, kQkWarp = 9, kPvWarp = 10, kVWarp = 11, kConvWarp0 = 12, kConvWarps = 4;
+constexpr int kUnits = 8;              // units on their way from the warp that works them out
+constexpr int kThreads = 640;
+constexpr int kItems = 384;             // query tiles that are ranked, at most
+constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp0 = 10, kUnitWarp = 14, kConvWarp0 = 16, kConvWarps = 4;
+constexpr int kUnitReaders = 8 + 2 + 4 + kConvWarps;   // softmax, producers, issuers, conversion
 constexpr uint32_t kKvTile = kBN * kD * 2;            // 8 KB: one head's K (or V) of a tile
 constexpr uint32_t kStageBytes = 2 * kKvTile;         // K_0, K_1 or V_0, V_1
 
@@ -66,13 +74,13 @@ constexpr uint32_t kOutOff = kVOff + kVStages * kStageBytes;   // two halves of 
 constexpr uint32_t kBarOff = kOutOff + 2 * kBM * 128;
 constexpr uint32_t kExOff = kBarOff + 1024;
 constexpr uint32_t kTabOff = kExOff + 5120;
-constexpr uint32_t kSmemBytes = kTabOff + 5 * 4 * kThreads + 1024;   // + alignment slack
+constexpr uint32_t kSmemBytes = kTabOff + 5 * 4 * kItems + 1024;   // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
 
-// Register split: 16 warps launched with 128 registers each; the two softmax
-// warpgroups rise to 168, the other two drop to 88: 256 x 168 + 256 x 88 = 65536.
-// The host checks the launch allocation before the first launch.
-constexpr int kRegsSoftmax = 168, kRegsAux = 88;
+// Register split: 20 warps launched with 96 registers each (61440); the two softmax
+// warpgroups rise to 128, the other three drop to 72: 256 x 128 + 384 x 72 = 60416.  The
+// host checks the launch allocation before the first launch.
+constexpr int kRegsSoftmax = 128, kRegsAux = 72;
 
 constexpr uint32_t kIdescQK = idesc_f16_f32acc(1, 0, kBM, kBN);    // bf16, K-major B
 constexpr uint32_t kIdescPV = idesc_f16_f32acc(0, 1, kBM, kDV);    // fp16, MN-major B
@@ -90,6 +98,8 @@ struct Barriers {
   uint64_t o_free;               // both O's read at a unit's end
   uint64_t sums[kSlots];         // a unit's row sums are there
   uint64_t mma_done;
+  uint64_t unit_full[kUnits], unit_empty[kUnits];
+  int4 unit[kUnits][3];
   uint32_t tmem_base;
 };
 static_assert(sizeof(Barriers) <= 1024, "barrier area");
@@ -150,26 +160,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_units = p.num_seqs * p.n_qtiles * (p.hq / 2);   // < 2^31 (host check)
   const int n_items = p.num_seqs * p.n_qtiles;
   const int* tab = nullptr;
-  if (n_items <= kThreads) {
+  if (n_items <= kItems) {
     int* t = reinterpret_cast<int*>(smem + kTabOff);
-    rank_items<kThreads, true, kBN>(p, n_items, t);
+    rank_items<kItems, true, kBN>(p, n_items, t);
     tab = t;
   }
-  auto next_unit = [&](int& k, Unit& x) -> bool {
-    return next_valid_unit<2, kThreads, true, kBN>(p, tab, k, x);
+  // The CTA's n-th unit, worked out by warp kUnitWarp; false: there is none left (or the
+  // wait ran out).  Every warp that asks takes each n once.
+  auto unit_at = [&](int n, Unit& x) -> bool {
+    const int slot = n % kUnits;
+    if (!__all_sync(kFull, wait_or_abort(&B->unit_full[slot], (n / kUnits) & 1, p))) return false;
+    const int4 a = B->unit[slot][0], b = B->unit[slot][1], e = B->unit[slot][2];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&B->unit_empty[slot]);
+    x.n_kv = a.x;
+    x.pos_first = a.y;
+    x.ctx = a.z;
+    x.delta = a.w;
+    x.rows = b.x;
+    x.q0 = b.y;
+    x.row0 = b.z;
+    x.h0 = b.w;
+    x.s = e.x;
+    x.sb = e.y;
+    return x.n_kv > 0;
   };
 
   if (threadIdx.x == 0) {
     mbar_init(&B->q_full, 1);
-    mbar_init(&B->q_empty, 1);
+    mbar_init(&B->q_empty, 2);
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(&B->k_full[i], 1);
-      mbar_init(&B->k_empty[i], 1);
+      mbar_init(&B->k_empty[i], 2);
     }
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(&B->v_full[i], 1);
       mbar_init(&B->v_ready[i], kConvWarps);
-      mbar_init(&B->v_empty[i], 1);
+      mbar_init(&B->v_empty[i], 2);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&B->s_full[i >> 1][i & 1], 1);
@@ -178,8 +205,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B->sums[i], 8);
     }
     static_assert(kSlots == 4, "initialised with the maps' buffers");
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&B->unit_full[i], 1);
+      mbar_init(&B->unit_empty[i], kUnitReaders);
+    }
     mbar_init(&B->o_free, kConvWarps);
-    mbar_init(&B->mma_done, 2);           // one commit from each MMA issuer
+    mbar_init(&B->mma_done, 4);           // one commit from each MMA issuer
     fence_barrier_init();
   }
   if (threadIdx.x < kDV)
@@ -209,9 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int gt = 0, st = 0, ph = 0;                         // key tiles issued; stage, its phase
     int nq = 0;                                         // units begun
     bool ok = true;
-    for (int k = 0; ok; ++k) {
+    for (int n = 0; ok; ++n) {
       Unit x;
-      if (!next_unit(k, x)) break;
+      if (!unit_at(n, x)) break;
       if (is_k) {
         if (lane == 0) {
           if (nq > 0) ok = wait_or_abort(&B->q_empty, (nq - 1) & 1, p);
@@ -261,14 +292,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(&full[t % stages], (t / stages) & 1)) report(p.status, kDevTimeout);
       if (is_k && nq > 0 && !mbar_wait(&B->q_full, (nq - 1) & 1)) report(p.status, kDevTimeout);
     }
-  } else if (warp == kQkWarp || warp == kPvWarp) {
+  } else if (warp >= kMmaWarp0 && warp < kMmaWarp0 + 4) {
     // ------------------------------------------------------- MMA issuers
-    // Whole warps walk the CTA's stream of key tiles, one elected thread issues.
+    // Whole warps walk the CTA's stream of key tiles, one elected thread issues; a warp a
+    // map and product, as four MMAs hold their thread for 200-340 cycles.
     //   Q K^T: S_h(t) into buffer t & 1 once K(t) has landed and P_h V(t - 2), which
     //   reads P from that buffer, is complete (pv_done) -- across unit boundaries too.
     //   P.V: O_h += P_h(t) V(t) once P_h(t) is in TMEM (p_full) and V(t) is fp16
     //   (v_ready); a unit's first one waits until the last unit's O's were read.
-    const bool is_qk = __shfl_sync(kFull, warp, 0) == kQkWarp;
+    const int role = __shfl_sync(kFull, warp, 0) - kMmaWarp0;
+    const bool is_qk = role < 2;
+    const int hh = role & 1;
     const uint32_t q_addr = __shfl_sync(kFull, smem_addr(smem + kQOff), 0);
     const uint32_t kv_base = __shfl_sync(kFull, smem_addr(smem + (is_qk ? kKOff : kVOff)), 0);
     const uint32_t td = __shfl_sync(kFull, tmem, 0);
@@ -278,9 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int gt = 0, st = 0, ph = 0;                         // key tile, its stage and phase
     int nq = 0;                                         // units begun
     bool ok = true;
-    for (int k = 0; ok; ++k) {
+    for (int n = 0; ok; ++n) {
       Unit x;
-      if (!next_unit(k, x)) break;
+      if (!unit_at(n, x)) break;
       const int n_kv = x.n_kv;
       if (!is_qk && nq > 0) ok = wait_all(&B->o_free, (nq - 1) & 1);
       for (int j = 0; ok && j < n_kv; ++j, ++gt) {
@@ -289,42 +323,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (is_qk) {
           ok = wait_all(&B->k_full[st], ph);
           if (ok && j == 0) ok = wait_all(&B->q_full, nq & 1);
+          if (ok && gt >= 2) ok = wait_all(&B->pv_done[hh][buf], ((gt >> 1) - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t da = desc_sw128(q_addr + hh * kTileBytes, 16, 1024);
+          const uint64_t db = desc_sw128(kv_addr + hh * kKvTile, 16, 1024);
+          if (elect_one()) {
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            if (ok && gt >= 2) ok = wait_all(&B->pv_done[hh][buf], ((gt >> 1) - 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t da = desc_sw128(q_addr + hh * kTileBytes, 16, 1024);
-            const uint64_t db = desc_sw128(kv_addr + hh * kKvTile, 16, 1024);
-            if (elect_one()) {
-#pragma unroll
-              for (int kk = 0; kk < kD / 16; ++kk)
-                mma_f16_ss(td + s_col(hh, buf), da + kk * 2, db + kk * 2, kIdescQK, kk > 0);
-              mma_commit(&B->s_full[hh][buf]);
-              if (hh == 1) mma_commit(&B->k_empty[st]);
-              if (hh == 1 && j + 1 == n_kv) mma_commit(&B->q_empty);
-            }
-            __syncwarp();
+            for (int kk = 0; kk < kD / 16; ++kk)
+              mma_f16_ss(td + s_col(hh, buf), da + kk * 2, db + kk * 2, kIdescQK, kk > 0);
+            mma_commit(&B->s_full[hh][buf]);
+            mma_commit(&B->k_empty[st]);
+            if (j + 1 == n_kv) mma_commit(&B->q_empty);
           }
+          __syncwarp();
         } else {
           ok = wait_all(&B->v_ready[st], ph);
+          if (ok) ok = wait_all(&B->p_full[hh][buf], (gt >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          // V_0 and V_1 are the two 64-column atoms of the 128-wide operand
+          const uint64_t db = desc_sw128(kv_addr, kKvTile, 1024);
+          if (elect_one()) {
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            if (ok) ok = wait_all(&B->p_full[hh][buf], (gt >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            // V_0 and V_1 are the two 64-column atoms of the 128-wide operand
-            const uint64_t db = desc_sw128(kv_addr, kKvTile, 1024);
-            if (elect_one()) {
-#pragma unroll
-              for (int kk = 0; kk < kBN / 16; ++kk)
-                mma_f16_ts(td + o_col(hh), td + s_col(hh, buf) + kk * 8, db + kk * 128, kIdescPV,
-                           (j > 0 || kk > 0));
-              mma_commit(&B->pv_done[hh][buf]);
-              if (hh == 1) mma_commit(&B->v_empty[st]);
-            }
-            __syncwarp();
+            for (int kk = 0; kk < kBN / 16; ++kk)
+              mma_f16_ts(td + o_col(hh), td + s_col(hh, buf) + kk * 8, db + kk * 128, kIdescPV,
+                         (j > 0 || kk > 0));
+            mma_commit(&B->pv_done[hh][buf]);
+            mma_commit(&B->v_empty[st]);
           }
+          __syncwarp();
         }
         if (++st == (is_qk ? kKStages : kVStages)) { st = 0; ph ^= 1; }
       }
@@ -336,6 +364,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait(&B->mma_done, 0)) report(p.status, kDevTimeout);
     }
     __syncwarp();
+  } else if (warp == kUnitWarp) {
+    // -------------------------------------------------------------- units
+    for (int k = 0, n = 0;; ++k, ++n) {
+      Unit x;
+      const bool more = next_valid_unit<2, kItems, true, kBN>(p, tab, k, x);
+      const int slot = n % kUnits;
+      if (n >= kUnits && !__all_sync(kFull, wait_or_abort(&B->unit_empty[slot], ((n / kUnits) - 1) & 1, p))) break;
+      if (lane == 0) {
+        B->unit[slot][0] = make_int4(more ? x.n_kv : 0, x.pos_first, x.ctx, x.delta);
+        B->unit[slot][1] = make_int4(x.rows, x.q0, x.row0, x.h0);
+        B->unit[slot][2] = make_int4(x.s, x.sb, 0, 0);
+        mbar_arrive(&B->unit_full[slot]);
+      }
+      __syncwarp();
+      if (!more) break;
+    }
   } else if (warp >= kConvWarp0) {
     // ----------------------------------------------- V conversion and output
     // Both V tiles bf16 -> fp16 in place, 16 bytes at a time (the swizzle only
@@ -451,9 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       return true;
     };
-    for (int k = 0; ok; ++k) {
+    for (int n = 0; ok; ++n) {
       Unit x;
-      if (!next_unit(k, x)) break;
+      if (!unit_at(n, x)) break;
       for (int j = 0; j < x.n_kv; ++j) {
         if (j == 2 && out.due && !write_out()) break;
         if (!wait(&B->v_full[st], ph)) break;
@@ -512,9 +556,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int units = 0;
     bool ok = true;
 
-    for (int k = 0; ok; ++k, ++units) {
+    for (; ok; ++units) {
       Unit x;
-      if (!next_unit(k, x)) break;
+      if (!unit_at(units, x)) break;
       // positions in the unit's key list
       const int pos_first = x.pos_first - x.delta;
       const int qpos = pos_first + r;
@@ -662,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long u = unit_index(k, c, G);
         if (u >= n_units) break;
         Unit x;
-        unit_info<2, kThreads, true, kBN>(p, tab, static_cast<int>(u), x);
+        unit_info<2, kItems, true, kBN>(p, tab, static_cast<int>(u), x);
         if (x.bad) report(p.status, x.bad_ctx ? TVL_DEV_BAD_CONTEXT_LEN : TVL_DEV_BAD_QUERY_LEN);
       }
     }
@@ -747,7 +791,7 @@ cudaError_t launch_diff_prefill(const DiffPrefillArgs& a, cudaStream_t stream) {
     cudaFuncAttributes fa;
     r = cudaFuncGetAttributes(&fa, diff_prefill_kernel);
     if (r != cudaSuccess) return r;
-    if (fa.numRegs * kThreads < 256 * kRegsSoftmax + 256 * kRegsAux) {
+    if (fa.numRegs * kThreads < 256 * kRegsSoftmax + 384 * kRegsAux) {
       set_last_error("differential prefill register allocation smaller than its register split");
       return cudaErrorInvalidConfiguration;
     }
