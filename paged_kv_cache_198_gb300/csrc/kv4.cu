@@ -12,13 +12,14 @@
 //
 // Bound: HBM bandwidth for a prefill chunk (per token 256 Hkv bytes in, 72 Hkv
 // out, and q both ways), latency for a decode step.  16 chunks of 700 tokens, 32/8
-// heads: 30 us, of which the 121 MB are 18, and 8 for expanding their blocks; at 68
-// registers 37% of the warps' places are used, too few to keep loads and the
-// codes' arithmetic (62% of issue slots) both going.  At 64 registers (8 bytes
-// spilled) 34.6 us for both, against 35.1.  Eight lanes hold a row, 16
-// bytes each; a warp takes 16 rows of a token (q, K and V rows in one list)
-// with all loads in flight, so a token with 48 rows is spread over three warps
-// and a decode step of 64 tokens over 192.
+// heads: 23 us, of which the 121 MB are 18, and 6 for expanding their blocks; issue slots
+// (71% full) hold it back.  Eight lanes hold a row, 16 bytes each; a warp takes 16 q rows
+// or 8 K and V rows of a token (in one list) with all loads in flight, the parts of a
+// token next to each other in the grid, so that q's traffic goes on beside the codes'
+// arithmetic, and a decode step of 64 tokens is spread over 256 warps.  What brought it
+// there, us for write and expansion: packed minima and maxima, codes from one side of the
+// residual, a reciprocal within an ulp and 16 K and V rows in two warps 35.5 -> 31.2; two
+// batches of q rows a warp 29.2; 48 registers (10 CTAs an SM) 28.9.
 #include <cuda_bf16.h>
 
 #include "device.cuh"
@@ -30,7 +31,11 @@ namespace tvl {
 namespace {
 
 constexpr int kWarps = 4;              // per CTA
-constexpr int kRowsPerWarp = 16;
+constexpr int kRowsQ = 16, kRowsKv = 8;   // rows a warp has in flight
+// Beyond this many q rows a warp takes two batches of them with one set of angles: 8192
+// tokens of 32 heads 17.6 us, 18.5 with a batch a warp; 1536 (49152 rows) 6.1 and 5.7,
+// 1024 of 64 (65536) 6.3 and 5.7, 2048 of 32 (65536) 6.6 and 6.9, 1536 of 64 7.1 and 7.4.
+constexpr int kManyRows = 80000;
 
 struct WriteParams {
   __nv_bfloat16* q;
@@ -39,18 +44,43 @@ struct WriteParams {
   uint8_t* cache;
   const int32_t* slots;
   const int32_t* positions;     // [axes, T]; null: no rotation
-  int num_tokens, hq, hkv, parts_q;
+  int num_tokens, hq, hkv, parts_q, parts, batches;
   long long num_slots;
   uint32_t* status;
 };
 
+// A row's minimum and its range, in all eight lanes that hold it; a NaN in the row makes
+// both NaN, an infinity the range infinite or NaN.  The values are bf16, so packed minima
+// are exact; a word holds (min, -max) and one reduction finds both.
+struct RowRange {
+  float mn, range;
+};
+__device__ __forceinline__ RowRange row_range(uint4 w) {
+  auto as = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+  auto bits = [](__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); };
+  const uint32_t lo = bits(__hmin2_nan(__hmin2_nan(as(w.x), as(w.y)), __hmin2_nan(as(w.z), as(w.w))));
+  const uint32_t hi = bits(__hmax2_nan(__hmax2_nan(as(w.x), as(w.y)), __hmax2_nan(as(w.z), as(w.w))));
+  const uint32_t nh = hi ^ 0x80008000u;
+  uint32_t x = bits(__hmin2_nan(as(__byte_perm(lo, nh, 0x5410)), as(__byte_perm(lo, nh, 0x7632))));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) x = bits(__hmin2_nan(as(x), as(__shfl_xor_sync(kFull, x, o))));
+  const float2 e = bf16x2_to_float2(x);
+  return {e.x, -e.y - e.x};
+}
+
 // A row's (s, z) from its extremes, and the codes of this lane's eight values.
 //
-// c = rint(d / s), d = x - z in fp32, ties to even, without a division a value: t = d * inv
-// rounded to an integer is off by at most one, and only next to a tie (inv is
-// within 2^-24 of 1 / s and d / s <= 15).  The residual e = d - t s is exact, so
-// |e| > s / 2, or = with t odd, says that the other neighbour is the nearer or
-// the even one.  Rows whose scale is too small for 1 / s take the division.
+// c = rint(d / s), d = x - z in fp32, ties to even, without a division a value: r =
+// rint((x - (z + s / 2)) / s) is c or c - 1, as what it rounds is off by 2^-10 at most (a
+// row's s is at least 2^-12 of |z|, but for rows of one value).  The residual e = d - r s
+// is exact and in about [0, s] (r = -1: d is about 0 and e about s), and c = r + 1 where
+// e > s / 2, or e = s / 2 and r is odd: positive floats compare as integers, a negative
+// one is a negative integer.  Rows whose scale is too small for 1 / s take the division.
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));    // within one ulp
+  return y;
+}
 __device__ __forceinline__ uint32_t row_codes(const Eight& x, float mn, float s) {
   constexpr float kMagic = 12582912.f;             // 1.5 * 2^23: adding it rounds to an integer
   if (s < 1e-36f) {
@@ -64,23 +94,18 @@ __device__ __forceinline__ uint32_t row_codes(const Eight& x, float mn, float s)
     }
     return code;
   }
-  const float inv = __fdiv_rn(1.0f, s), half = 0.5f * s;
+  const float inv = rcp(s), half = 0.5f * s, low = -(mn + half);
+  const int half_bits = __float_as_int(half);
   float c[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 d = __fadd2_rn(x.v[j], make_float2(-mn, -mn));
-    const float2 t = __ffma2_rn(d, make_float2(inv, inv), make_float2(kMagic, kMagic));
+    const float2 t = __ffma2_rn(__fadd2_rn(x.v[j], make_float2(low, low)), make_float2(inv, inv),
+                                make_float2(kMagic, kMagic));
     const float2 r = __fadd2_rn(t, make_float2(-kMagic, -kMagic));
     const float2 e = __ffma2_rn(r, make_float2(-s, -s), d);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float ev = k ? e.y : e.x;
-      const int odd = __float_as_int(k ? t.y : t.x) & 1;
-      // over > 0, or = +0 with an odd code
-      const float over = fabsf(ev) - half;
-      const bool fix = __float_as_int(over) + odd > 0;
-      c[2 * j + k] = (k ? r.y : r.x) + (fix ? copysignf(1.0f, ev) : 0.0f);
-    }
+    c[2 * j] = r.x + (__float_as_int(e.x) + (__float_as_int(t.x) & 1) > half_bits ? 1.0f : 0.0f);
+    c[2 * j + 1] = r.y + (__float_as_int(e.y) + (__float_as_int(t.y) & 1) > half_bits ? 1.0f : 0.0f);
   }
   // four codes are exact in one float: c0 + 16 c1 + 256 c2 + 4096 c3
   const float lo = fmaf(4096.f, c[3], fmaf(256.f, c[2], fmaf(16.f, c[1], c[0]))) + kMagic;
@@ -88,49 +113,68 @@ __device__ __forceinline__ uint32_t row_codes(const Eight& x, float mn, float s)
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
 }
 
-// Block (x, y): 4 tokens, and of each the 16-row part y: parts_q of q rows, then
-// K and V rows.
-__global__ void __launch_bounds__(kWarps * 32)
+// Block x: kWarps tokens, and of each part x % parts: parts_q of `batches` times kRowsQ q
+// rows, then parts of kRowsKv K and V rows, in one list.
+__global__ void __launch_bounds__(kWarps * 32, 10)
     kv4_write_kernel(const WriteParams p, const RopeTurns turns) {
   __shared__ float2 trig[kWarps][kD / 2];
   grid_dependency_wait();
   grid_dependents_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long t = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  const int step = blockIdx.x / p.parts, part = blockIdx.x - step * p.parts;
+  const long long t = static_cast<long long>(step) * kWarps + warp;
   if (t >= p.num_tokens) return;
   const int c = lane & 7;
-  constexpr int kIt = kRowsPerWarp / 4;
-  const bool is_q = static_cast<int>(blockIdx.y) < p.parts_q;
-  const int row0 = (blockIdx.y - (is_q ? 0 : p.parts_q)) * kRowsPerWarp + (lane >> 3);
-  const int rows = is_q ? p.hq : 2 * p.hkv;
-
+  if (part < p.parts_q) {
+    constexpr int kIt = kRowsQ / 4;
+    uint4* q = reinterpret_cast<uint4*>(p.q + t * p.hq * kD) + c;
+    int row0 = part * p.batches * kRowsQ + (lane >> 3);
+    uint4 w[kIt];
+    auto load = [&]() {
+#pragma unroll
+      for (int i = 0; i < kIt; ++i) {
+        const int r = row0 + 4 * i;
+        w[i] = r < p.hq ? __ldcs(q + r * (kD / 8)) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    load();
+    const Turn turn = token_turn(p.positions, p.num_tokens, t, turns, trig[warp]);
+#pragma unroll 1
+    for (int k = 0;;) {
+#pragma unroll
+      for (int i = 0; i < kIt; ++i) {
+        const int r = row0 + 4 * i;
+        const uint4 y = rotate(w[i], turn);
+        if (r < p.hq) q[r * (kD / 8)] = y;
+      }
+      if (++k == p.batches) break;
+      row0 += kRowsQ;
+      load();
+    }
+    return;
+  }
+  constexpr int kIt = kRowsKv / 4;
+  const int first = (part - p.parts_q) * kRowsKv;
+  const int row0 = first + (lane >> 3);
   uint4 w[kIt];
 #pragma unroll
   for (int i = 0; i < kIt; ++i) {
     const int r = row0 + 4 * i;
-    w[i] = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
-      const __nv_bfloat16* src = is_q        ? p.q + (t * p.hq + r) * kD
-                                 : r < p.hkv ? p.k_new + (t * p.hkv + r) * kD
-                                             : p.v_new + (t * p.hkv + r - p.hkv) * kD;
-      w[i] = __ldcs(reinterpret_cast<const uint4*>(src) + c);
-    }
-  }
-  Turn turn;
-  const bool rope = p.positions != nullptr && row0 - (lane >> 3) < (is_q ? p.hq : p.hkv);
-  if (rope) {
-    turn = token_turn(p.positions, p.num_tokens, t, turns, trig[warp]);
-  }
-  if (is_q) {
-#pragma unroll
-    for (int i = 0; i < kIt; ++i) {
-      const int r = row0 + 4 * i;
-      const uint4 y = rotate(w[i], turn);
-      if (r < rows) reinterpret_cast<uint4*>(p.q + (t * p.hq + r) * kD)[c] = y;
-    }
-    return;
+    const __nv_bfloat16* src = r < p.hkv ? p.k_new + (t * p.hkv + r) * kD
+                                         : p.v_new + (t * p.hkv + r - p.hkv) * kD;
+    w[i] = r < 2 * p.hkv ? __ldcs(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
   }
   const long long slot = p.slots[t];
+  const bool rope = p.positions != nullptr && first < p.hkv;
+  if (rope) {
+    // the K that is quantised is the bf16 row the bf16 cache would hold
+    const Turn turn = token_turn(p.positions, p.num_tokens, t, turns, trig[warp]);
+#pragma unroll
+    for (int i = 0; i < kIt; ++i) {
+      const uint4 y = rotate(w[i], turn);
+      if (row0 + 4 * i < p.hkv) w[i] = y;
+    }
+  }
   if (slot < 0) return;
   if (slot >= p.num_slots) {
     if (lane == 0) report(p.status, TVL_DEV_BAD_SLOT);
@@ -143,35 +187,14 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int i = 0; i < kIt; ++i) {
     const int r = row0 + 4 * i;
     const bool is_v = r >= p.hkv;
-    if (rope && r - (lane >> 3) < p.hkv) {       // the step holds a K row
-      // the K that is quantised is the bf16 row the bf16 cache would hold
-      const uint4 y = rotate(w[i], turn);
-      if (!is_v) w[i] = y;
-    }
-    const Eight x = widen(w[i]);
-    float mn = x.v[0].x, mx = mn;
-    float2 fin = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      mn = fminf(mn, fminf(x.v[j].x, x.v[j].y));
-      mx = fmaxf(mx, fmaxf(x.v[j].x, x.v[j].y));
-      fin = __ffma2_rn(x.v[j], make_float2(0.f, 0.f), fin);    // 0 unless something is not finite
-    }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      mn = fminf(mn, __shfl_xor_sync(kFull, mn, o));
-      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-    }
-    const float range = mx - mn;
-    const bool bad = !(range < INFINITY) || fin.x + fin.y != 0.f;   // NaN != 0
-    const bool row_bad = ((__ballot_sync(kFull, bad) >> (lane & 24)) & 0xffu) != 0;
-    if (r >= rows) continue;
+    const RowRange e = row_range(w[i]);
+    if (r >= 2 * p.hkv) continue;
     uint32_t code = 0;
     uint32_t sz = 0x7fc07fc0u;          // a row that is not finite stands for NaN
-    if (!row_bad) {
-      const uint32_t sb = (__float_as_uint(__fdiv_rn(range, 15.0f)) + 0xffffu) & 0xffff0000u;
-      sz = (sb >> 16) | (__float_as_uint(mn) & 0xffff0000u);
-      code = row_codes(x, mn, __uint_as_float(sb));
+    if (e.range < INFINITY) {
+      const uint32_t sb = (__float_as_uint(__fdiv_rn(e.range, 15.0f)) + 0xffffu) & 0xffff0000u;
+      sz = (sb >> 16) | (__float_as_uint(e.mn) & 0xffff0000u);
+      code = row_codes(widen(w[i]), e.mn, __uint_as_float(sb));
     } else if (c == 0) {
       report(p.status, TVL_DEV_NONFINITE);
     }
@@ -215,14 +238,19 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int k = 0; k < 8; ++k) {
     const int tok = (k & 3) * 4 + g;
     const float2 m = bf16x2_to_float2(sz[k]);
-    float y[8];
+    const uint32_t even = code[k] & 0x0f0f0f0fu, odd = (code[k] >> 4) & 0x0f0f0f0fu;
+    uint32_t y[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      y[j] = fmaf(m.x, static_cast<float>((code[k] >> (4 * j)) & 15u), m.y);
+    for (int b = 0; b < 4; ++b) {        // a code under 2^23's exponent is 2^23 + code
+      const float2 v = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(even, 0x4b000000u, 0x7440 | b)),
+                                              __uint_as_float(__byte_perm(odd, 0x4b000000u, 0x7440 | b))),
+                                  make_float2(-8388608.f, -8388608.f));
+      const float2 u = __ffma2_rn(v, make_float2(m.x, m.x), make_float2(m.y, m.y));
+      y[b] = pack_bf16(u.x, u.y);
+    }
     __nv_bfloat16* out = (k < 4 ? k_cache : v_cache) +
                          ((static_cast<long long>(to) * cpb + sub) * kRecTokens + tok) * hkv * kD + h * kD;
-    reinterpret_cast<uint4*>(out)[c] = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
-                                                  pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+    reinterpret_cast<uint4*>(out)[c] = make_uint4(y[0], y[1], y[2], y[3]);
   }
 }
 
@@ -240,12 +268,15 @@ cudaError_t launch_kv4_write(const Kv4WriteArgs& a, cudaStream_t stream) {
   p.num_tokens = a.num_tokens;
   p.hq = a.q && a.positions ? a.num_q_heads : 0;
   p.hkv = a.num_kv_heads;
-  p.parts_q = (p.hq + kRowsPerWarp - 1) / kRowsPerWarp;
-  const int parts_kv = (2 * p.hkv + kRowsPerWarp - 1) / kRowsPerWarp;
+  p.batches = p.hq > kRowsQ && static_cast<long long>(a.num_tokens) * p.hq > kManyRows ? 2 : 1;
+  p.parts_q = (p.hq + kRowsQ * p.batches - 1) / (kRowsQ * p.batches);
+  p.parts = p.parts_q + (2 * p.hkv + kRowsKv - 1) / kRowsKv;
+  const long long ctas = static_cast<long long>((a.num_tokens - 1) / kWarps + 1) * p.parts;
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   p.num_slots = a.num_slots;
   p.status = a.status;
   static const RopeTurns none = {};
-  return launch_pdl(kv4_write_kernel, dim3((a.num_tokens - 1) / kWarps + 1, p.parts_q + parts_kv),
+  return launch_pdl(kv4_write_kernel, dim3(static_cast<unsigned>(ctas)),
                     dim3(kWarps * 32), 0, stream, p,
                     a.positions ? rope_turns(a.rope_theta, a.axis_of) : none);
 }
