@@ -194,7 +194,7 @@ tvl_status tvl_rope_axes_paged_kv_write(void* q, const void* k_new, const void* 
  * a step without tokens.  A block id outside [0, NB), in the stack or in the table
  * entry of a partly filled block, is reported (TVL_DEV_BAD_BLOCK_ID) and its
  * tokens get slot -1.
- * Any block_size > 0; NB * bs and MB * bs < 2^31.  One or two launches; no
+ * Any block_size > 0; S <= 2^30; NB * bs and MB * bs < 2^31.  One or two launches; no
  * workspace; results do not vary.
  */
 tvl_status tvl_build_step_tables(int32_t* block_tables, int32_t* free_blocks,
@@ -514,7 +514,8 @@ tvl_status tvl_diff_decode_workspace_size(int num_q_heads, int num_kv_heads, int
  *   norm_weight : bf16 [128] (device) or NULL;  norm_eps >= 0
  * context_lens[s] == 0 gives a zero row, and so does d == 0.  One or two launches; no
  * allocation; results do not vary from call to call.
- * Supported: D == 64, Hq and Hkv even, G from 1 to 8, bs in {16, 32, 64, 128}, cached V
+ * Supported: D == 64, Hq and Hkv even, G from 1 to 8, bs in {16, 32, 64, 128}, visible
+ * K finite (one that is not spoils both maps of its pair), cached V
  * below 2^60 in magnitude (the norm's squares), NB * bs < 2^31, Hkv <= 65534, Hq <=
  * 262140.
  */

@@ -586,6 +586,7 @@ tvl_status tvl_build_step_tables(int32_t* block_tables, int32_t* free_blocks,
   if (block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0)
     return fail(TVL_ERR_INVALID_ARG,
                 "block_size, num_blocks and max_blocks_per_seq must be positive");
+  if (num_seqs > 1 << 30) return fail(TVL_ERR_UNSUPPORTED, "num_seqs %d > 2^30", num_seqs);
   if (static_cast<long long>(num_blocks) * block_size > INT_MAX ||
       static_cast<long long>(max_blocks_per_seq) * block_size > INT_MAX)
     return fail(TVL_ERR_UNSUPPORTED, "more than 2^31 - 1 token slots");

@@ -97,3 +97,7 @@ def test_binding_checks(tvl):
     with pytest.raises(ValueError, match="CUDA"):
         tvl.kv4_axes_write(kv[0], kv[0], torch.zeros(2, 1, 2, 1152, dtype=torch.uint8), i32, None,
                            i32.view(1, 4), [32])
+
+
+def test_more_rows_than_the_loops_count_are_refused(tvl):
+    assert _tables(tvl, s=(1 << 30) + 1, mb=1) == tvl.ERR_UNSUPPORTED
