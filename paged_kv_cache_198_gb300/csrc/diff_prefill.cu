@@ -32,7 +32,7 @@
 //
 // What bounds it: a softmax warp's chain of steps a tile, some 1500 cycles (scores seen,
 // loaded, 620 for 64 exponentials with two warps a scheduler, vote, store, arrival), not
-// the tensor pipe (49% active), the exp unit (33%), issue slots (54%) or L2.  Timing copies
+// the tensor pipe (52% active), the exp unit (35%), issue slots (59%) or L2.  Timing copies
 // that leave work out say the same (2 sequences x 4096 rows, window 4096, 396 us then):
 // a quarter of the MMAs 400, no exponentials 369, no V conversion 373.
 // Measured: 16 chunks of 512 rows on prefixes of 0-2k 155 us, 841 TFLOP/s of visible

@@ -12,8 +12,8 @@
 //
 // Bound: HBM bandwidth for a prefill chunk (per token 256 Hkv bytes in, 72 Hkv
 // out, and q both ways), latency for a decode step.  16 chunks of 700 tokens, 32/8
-// heads: 23 us, of which the 121 MB are 18, and 6 for expanding their blocks; issue slots
-// (71% full) hold it back.  Eight lanes hold a row, 16 bytes each; a warp takes 16 q rows
+// heads: 23-24 us, of which the 121 MB are 18, and 6-8 for expanding their blocks; issue slots
+// (72-74% full) hold it back.  Eight lanes hold a row, 16 bytes each; a warp takes 16 q rows
 // or 8 K and V rows of a token (in one list) with all loads in flight, the parts of a
 // token next to each other in the grid, so that q's traffic goes on beside the codes'
 // arithmetic, and a decode step of 64 tokens is spread over 256 warps.  What brought it
